@@ -54,7 +54,8 @@ typedef enum {
     NVFP4_ERR_NULL = 1,        /* a required pointer is NULL */
     NVFP4_ERR_ALIGN = 2,       /* a pointer or leading dimension breaks the 16-byte rule */
     NVFP4_ERR_SHAPE = 3,       /* a size violates the operation's shape rule (see each call) */
-    NVFP4_ERR_ARG = 4,         /* an enum or flag out of range, or inconsistent operands */
+    NVFP4_ERR_ARG = 4,         /* an enum or flag out of range, or inconsistent operands;
+                                  (nvfp4_poll) expert offsets out of order or range */
     NVFP4_ERR_WORKSPACE = 5,   /* workspace NULL */
     NVFP4_ERR_CUDA = 6,        /* a CUDA launch or runtime call failed */
     NVFP4_ERR_NONFINITE = 7,   /* (nvfp4_poll) NaN or Inf seen by an amax pass */
@@ -164,6 +165,13 @@ nvfp4_status nvfp4_quantize_dual_shard(const void* x, int64_t rows, int64_t cols
 nvfp4_status nvfp4_quantize_weight(const void* w, int64_t rows, int64_t cols, int64_t ldw,
                                    nvfp4_tensor* w_q, nvfp4_tensor* w_qt, void* ws,
                                    nvfp4_stream_t stream);
+
+/* nvfp4_quantize_weight without its amax pass: the plain amax word of ws already holds w's amax,
+ * written by the producer of w (nvfp4_adamw with this workspace as the tensor's amax_ws, or
+ * nvfp4_amax with rht = 0).  Results are bit-identical to nvfp4_quantize_weight. */
+nvfp4_status nvfp4_quantize_weight_ready(const void* w, int64_t rows, int64_t cols, int64_t ldw,
+                                         nvfp4_tensor* w_q, nvfp4_tensor* w_qt, void* ws,
+                                         nvfp4_stream_t stream);
 
 /*
  * Transposed layout of a 16x16-quantized tensor without requantizing (gist.science 2.B.3):
@@ -375,8 +383,122 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
                                    int64_t T, int64_t d, int64_t n, void* scratch, void* ws,
                                    nvfp4_stream_t stream);
 
+/*
+ * Products grouped by expert, the BF16 path of a layer with one weight per expert.  Rows of a
+ * token-major operand are sorted by expert: expert e owns rows [offsets[e], offsets[e + 1]).
+ * offsets: int32 [experts + 1] in device memory (4-byte aligned), so the row counts never visit the host.  Entries
+ * ascend within [0, rows]; an expert may own no row, and rows before offsets[0] or from
+ * offsets[experts] on belong to nobody.  Offsets that descend or lie outside [0, rows] are read as
+ * the running maximum of their values clamped to [0, rows] (no access leaves the operands), and
+ * nvfp4_poll(ws) then reports NVFP4_ERR_ARG.
+ *
+ * nvfp4_bf16_gemm_grouped: for every expert e and row t it owns
+ *   D[t][0..N) = A[t][0..K) . B_e^T with B_e [N][K]  (b_kn = 0: fprop, y = x w_e^T), or
+ *   D[t][0..N) = A[t][0..K) . B_e   with B_e [K][N]  (b_kn = 1: dgrad, dx = dy w_e, the same
+ *                                                      weight buffer, no transposed copy).
+ * A [rows][lda] bf16; B_e starts at b + e * stride_b (elements) with leading dimension ldb; D
+ * [rows][ldd] bf16 or fp32.  Rows of D that no expert owns are left as they were.  fp32
+ * accumulation; with fp32 output, partial sums of 512 products are joined in fp32 registers
+ * (round to nearest), since the tensor core truncates as it accumulates.  Each row's result
+ * depends on that row and its expert's weight alone, but for the choice of kernel by `rows`.
+ * Shape rules: 1 <= experts <= 1024; rows >= 0 (0: no-op); N, K >= 8, N % 8 == 0, K % 8 == 0;
+ * lda >= K, ldb >= K (N if b_kn), stride_b >= 0, all multiples of 8; ldd >= N and
+ * ldd * sizeof(out) % 16 == 0; sizes up to 2^30.  ws receives the timeout and offset flags.
+ *
+ * nvfp4_bf16_wgrad_grouped: for every expert e, the weight gradient
+ *   D_e[m][n] (+)= sum over the rows t of e of A[t][m] * B[t][n]   (dw_e = dy^T x, A = dy, B = x)
+ * A [rows][lda], B [rows][ldb] bf16; D_e at d + e * stride_d, fp32, leading dimension ldd.
+ * accumulate = 0 stores (an expert without rows gets zeros); 1 adds to what D holds (each element
+ * once, fp32; an expert without rows is left as it was).  Sums are joined as above.  Shape rules:
+ * as above with M, N multiples of 8; lda >= M, ldb >= N; ldd >= N, stride_d >= 0, both multiples of
+ * 4; with more than one expert stride_d >= M * ldd.  rows == 0 makes every expert one without rows.
+ */
+nvfp4_status nvfp4_bf16_gemm_grouped(const void* a, int64_t lda, int64_t rows, const int32_t* offsets, int experts,
+                                     const void* b, int64_t ldb, int64_t stride_b, int b_kn, int64_t N, int64_t K,
+                                     void* d, int64_t ldd, nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream);
+nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows,
+                                      const int32_t* offsets, int experts, int64_t M, int64_t N, float* d,
+                                      int64_t ldd, int64_t stride_d, int accumulate, void* ws, nvfp4_stream_t stream);
+
+/*
+ * One AdamW step over many tensors in one launch (per 384 tensors), from the gradients the linear
+ * layers' backward calls write to the bf16 weights their next forward call reads.  Per element, in
+ * fp32, each operation rounded once and in this order (products before the sum they enter):
+ *   g = grad * grad_scale
+ *   m = m * beta1 + g * (1 - beta1)
+ *   v = v * beta2 + (g * (1 - beta2)) * g
+ *   p = p * (1 - lr * weight_decay) - (m / (sqrt(v) * c + eps)) * (lr / (1 - beta1^step))
+ *   w = bf16(p), nearest even                              c = 1 / sqrt(1 - beta2^step)
+ * The scalars 1 - beta, 1 - lr * weight_decay, the step size and c are computed in double and
+ * rounded once.
+ *
+ * state = NVFP4_STATE_FP32: m and v are fp32 [n].
+ * state = NVFP4_STATE_FP8: m and sqrt(v) are held as E4M3 codes [n] with one fp32 scale per 256
+ * consecutive elements (m_scale, v_scale: ceil(n / 256) floats; value = code * scale, and v is the
+ * square of that value).  After the update a block of x (m, or sqrt(v)) is encoded with scale =
+ * amax * fp32(1 / 448) and u = |x| * (448 * fp32(1 / amax)); a block with amax < 2^-100 gets scale
+ * 0 and codes 0, a block that holds a NaN or Inf gets a NaN scale.  u is rounded to E4M3, sign kept, at
+ * most 448: mode NVFP4_SR rounds up iff r16 < f * 2^16, f the cut-off part of the step (below 2^-6
+ * the step is 2^-9 and f is taken of fp32(u + 2^-6)), r16 the element's Philox4x32-10 field: key
+ * sr_seed, counter (i/8 lo, i/8 hi, stream, tensor), field i mod 8, i the element's index, tensor
+ * its tensor's index in the call, stream NVFP4_STREAM_MOMENT1 for m and NVFP4_STREAM_MOMENT2 for
+ * sqrt(v).  NVFP4_RNE rounds to nearest even, which stops a slow average from moving once its step
+ * is below half a code: SR, with another seed each step, keeps the averages unbiased.  The weight
+ * update of a step reads m and v before they are encoded.
+ *
+ * amax_ws: if not NULL, a workspace whose plain amax word receives the amax of w (for
+ * nvfp4_quantize_weight_ready); it is reset first, and a NaN or Inf in w raises the non-finite flag
+ * of ws.  w may be NULL (then amax_ws must be too).
+ * dynamic: if not NULL, device memory that holds the step's values in place of lr, weight_decay,
+ * step, grad_scale and sr_seed of the arguments, read when the kernel runs: a captured graph that
+ * is replayed takes the values the caller has put there (nvfp4_adamw_dynamic_values computes them).
+ * Shape rules: count >= 0, 0 <= n <= 2^40 per tensor; every pointer 16-byte aligned, the scales
+ * 4-byte; tensors do not overlap.  beta1, beta2 in [0, 1); eps >= 0; step >= 1; lr, weight_decay, grad_scale finite.
+ */
+typedef enum { NVFP4_STATE_FP32 = 0, NVFP4_STATE_FP8 = 1 } nvfp4_state;
+#define NVFP4_STREAM_MOMENT1 4u
+#define NVFP4_STREAM_MOMENT2 5u
+
+typedef struct {
+    float* p;           /* fp32 master weights [n] */
+    const void* g;      /* gradient [n], bf16 or fp32 */
+    void* w;            /* bf16 weights [n], written; or NULL */
+    void* m;            /* first moment: fp32 [n] or E4M3 codes [n] */
+    void* v;            /* second moment: fp32 [n], or E4M3 codes [n] of its square root */
+    float* m_scale;     /* NVFP4_STATE_FP8: ceil(n / 256) scales */
+    float* v_scale;
+    void* amax_ws;      /* workspace that receives w's amax, or NULL */
+    int64_t n;
+    int32_t g_dtype;    /* nvfp4_dtype */
+    int32_t reserved;
+} nvfp4_adamw_tensor;
+
+typedef struct {
+    float keep;         /* 1 - lr * weight_decay */
+    float step_size;    /* lr / (1 - beta1^step) */
+    float v_fix;        /* 1 / sqrt(1 - beta2^step) */
+    float grad_scale;
+    uint64_t sr_seed;
+    uint64_t reserved;
+} nvfp4_adamw_dynamic;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay, grad_scale;
+    int64_t step;
+    uint64_t sr_seed;
+    int32_t state;      /* nvfp4_state */
+    int32_t mode;       /* nvfp4_round of the FP8 state's codes */
+    const nvfp4_adamw_dynamic* dynamic; /* device memory, or NULL */
+} nvfp4_adamw_args;
+
+nvfp4_status nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int count, const nvfp4_adamw_args* args, void* ws,
+                         nvfp4_stream_t stream);
+/* The values of args as nvfp4_adamw would use them (host memory; no device work). */
+nvfp4_status nvfp4_adamw_dynamic_values(const nvfp4_adamw_args* args, nvfp4_adamw_dynamic* out);
+
 /* Synchronize `stream`, then report (and clear) the device flags of `ws`: NVFP4_ERR_TIMEOUT
- * takes precedence over NVFP4_ERR_NONFINITE; NVFP4_OK when neither is set. */
+ * takes precedence over NVFP4_ERR_ARG (expert offsets out of order), and that over
+ * NVFP4_ERR_NONFINITE; NVFP4_OK when none is set. */
 nvfp4_status nvfp4_poll(void* ws, nvfp4_stream_t stream);
 
 /* Device-side wait budget of the GEMM's mbarrier spins, in nanoseconds (default 2e9).

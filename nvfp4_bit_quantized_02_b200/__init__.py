@@ -8,8 +8,9 @@ no CPU fallback.
 
 The functions carry the C names: ``nvfp4_quantize``, ``nvfp4_quantize_dual``,
 ``nvfp4_quantize_weight``, ``nvfp4_transpose_2d``, ``nvfp4_gemm``, ``nvfp4_linear_fwd``,
-``nvfp4_linear_bwd``, ``nvfp4_gelu_fwd``, ``nvfp4_gelu_bwd``, ``nvfp4_poll``, and for data-parallel
-token shards ``nvfp4_amax``, ``nvfp4_quantize_dual_shard`` (and ``nvfp4_quantize_dual_dp``, which
+``nvfp4_linear_bwd``, ``nvfp4_gelu_fwd``, ``nvfp4_gelu_bwd``, ``nvfp4_poll``, for layers with one weight
+per expert ``nvfp4_bf16_gemm_grouped`` and ``nvfp4_bf16_wgrad_grouped``, for the weight update
+``nvfp4_adamw_step``, and for data-parallel token shards ``nvfp4_amax``, ``nvfp4_quantize_dual_shard`` (and ``nvfp4_quantize_dual_dp``, which
 all-reduces the amax between them).
 """
 from __future__ import annotations
@@ -27,6 +28,8 @@ RNE, SR = 0, 1
 BLOCK_1x16, BLOCK_16x16 = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
 STREAM_DGRAD, STREAM_WGRAD, STREAM_RHT = 1, 2, 3
+STREAM_MOMENT1, STREAM_MOMENT2 = 4, 5
+STATE_FP32, STATE_FP8 = 0, 1
 
 STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_ALIGN", 3: "ERR_SHAPE", 4: "ERR_ARG", 5: "ERR_WORKSPACE", 6: "ERR_CUDA",
           7: "ERR_NONFINITE", 8: "ERR_TIMEOUT", 9: "ERR_UNSUPPORTED", 10: "ERR_LIMIT"}
@@ -56,6 +59,25 @@ class CLinearCtx(ctypes.Structure):
                 ("dx_amax_ws", ctypes.c_void_p), ("dx_rht_seed", ctypes.c_uint64)]
 
 
+class CAdamWTensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("w", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("amax_ws", ctypes.c_void_p), ("n", ctypes.c_int64), ("g_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class CAdamWDynamic(ctypes.Structure):
+    _fields_ = [("keep", ctypes.c_float), ("step_size", ctypes.c_float), ("v_fix", ctypes.c_float),
+                ("grad_scale", ctypes.c_float), ("sr_seed", ctypes.c_uint64), ("reserved", ctypes.c_uint64)]
+
+
+class CAdamWArgs(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("step", ctypes.c_int64), ("sr_seed", ctypes.c_uint64), ("state", ctypes.c_int32),
+                ("mode", ctypes.c_int32), ("dynamic", ctypes.c_void_p)]
+
+
 _L = None
 
 
@@ -77,6 +99,11 @@ def _lib():
             "nvfp4_quantize": ([vp, i64, i64, i64, i32, i32, i32, i32, u64, u64, u32, T, vp, vp], i32),
             "nvfp4_quantize_dual": ([vp, i64, i64, i64, i32, u64, u64, u32, u32, T, T, vp, vp], i32),
             "nvfp4_quantize_weight": ([vp, i64, i64, i64, T, T, vp, vp], i32),
+            "nvfp4_quantize_weight_ready": ([vp, i64, i64, i64, T, T, vp, vp], i32),
+            "nvfp4_bf16_gemm_grouped": ([vp, i64, i64, vp, i32, vp, i64, i64, i32, i64, i64, vp, i64, i32, vp, vp], i32),
+            "nvfp4_bf16_wgrad_grouped": ([vp, i64, vp, i64, i64, vp, i32, i64, i64, vp, i64, i64, i32, vp, vp], i32),
+            "nvfp4_adamw": ([c.POINTER(CAdamWTensor), i32, c.POINTER(CAdamWArgs), vp, vp], i32),
+            "nvfp4_adamw_dynamic_values": ([c.POINTER(CAdamWArgs), c.POINTER(CAdamWDynamic)], i32),
             "nvfp4_amax": ([vp, i64, i64, i64, i32, u64, vp, vp], i32),
             "nvfp4_workspace_amax_offset": ([], c.c_size_t),
             "nvfp4_quantize_dual_shard": ([vp, i64, i64, i64, i64, i64, i32, u64, u64, u32, u32, T, T, vp, vp], i32),
@@ -299,7 +326,10 @@ def nvfp4_quantize_dual_dp(x: torch.Tensor, group, row_offset: int, rows_total: 
 
 
 def nvfp4_quantize_weight(w: torch.Tensor, transposed: bool = True, out: NVFP4Tensor | None = None,
-                          out_t: NVFP4Tensor | None = None, ws: Workspace | None = None, stream=None):
+                          out_t: NVFP4Tensor | None = None, ws: Workspace | None = None, stream=None,
+                          amax_ready: bool = False):
+    """16x16 forms of a weight.  amax_ready: ws holds w's amax already (an AdamW step wrote it with w),
+    and the amax pass is skipped."""
     rows, cols, ld = _bf16_2d(w)
     out = out or NVFP4Tensor.empty(rows, cols, BLOCK_16x16, w.device)
     if transposed:
@@ -307,8 +337,8 @@ def nvfp4_quantize_weight(w: torch.Tensor, transposed: bool = True, out: NVFP4Te
     ws = ws or default_workspace()
     a = out.c()
     b = out_t.c() if transposed else None
-    st = _lib().nvfp4_quantize_weight(_ptr(w), rows, cols, ld, ctypes.byref(a), ctypes.byref(b) if b else None,
-                                      ws.ptr, _stream(stream))
+    fn = _lib().nvfp4_quantize_weight_ready if amax_ready else _lib().nvfp4_quantize_weight
+    st = fn(_ptr(w), rows, cols, ld, ctypes.byref(a), ctypes.byref(b) if b else None, ws.ptr, _stream(stream))
     _check(st, "nvfp4_quantize_weight")
     return (out, out_t) if transposed else out
 
@@ -532,6 +562,252 @@ class LinearBF16:
         _check(_lib().nvfp4_linear_bf16_bwd(_ptr(x), _ptr(w), _ptr(dy), _ptr(dx), _ptr(dw), self.T, self.d, self.n,
                                             _ptr(self.scratch), self.ws.ptr, _stream(stream)), "nvfp4_linear_bf16_bwd")
         return dx, dw
+
+
+# ---------------------------------------------------------------------------------------
+# BF16 products grouped by expert (one weight per expert, token rows sorted by expert)
+# ---------------------------------------------------------------------------------------
+def _on_current_device(*tensors):
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.device.type != "cuda" or t.device.index != dev:
+            raise ValueError(f"expected tensors on the current CUDA device ({dev}), got one on {t.device}")
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty in the pool of the stream the kernel runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _offsets(t: torch.Tensor, experts: int):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != experts + 1 or t.stride(0) != 1:
+        raise ValueError("offsets: contiguous int32 [experts + 1]")
+
+
+def nvfp4_bf16_gemm_grouped(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, b_kn: bool = False,
+                            out_dtype=torch.bfloat16, out: torch.Tensor | None = None, ws: Workspace | None = None,
+                            stream=None) -> torch.Tensor:
+    """out[t] = a[t] . b[e]^T (b [E][N][K]) or a[t] . b[e] (b_kn: b [E][K][N]) for the rows t in
+    [offsets[e], offsets[e + 1]) of each expert e (offsets: int32 [E + 1] on the device).  Rows that
+    no expert owns are left as they were in out (undefined where out is not given)."""
+    if a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16 or a.dim() != 2 or b.dim() != 3:
+        raise TypeError("expected bf16 a [rows][K] and b [E][N][K] (b_kn: [E][K][N])")
+    rows, K = a.shape
+    E = b.shape[0]
+    N, Kb = (b.shape[2], b.shape[1]) if b_kn else (b.shape[1], b.shape[2])
+    if Kb != K:
+        raise ValueError("a and b need the same K")
+    if a.stride(1) != 1 or b.stride(2) != 1:
+        raise ValueError("inner dimensions must be contiguous")
+    _offsets(offsets, E)
+    _on_current_device(a, b, offsets)
+    if out is None:
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("output must be bf16 or fp32")
+        out = _empty((rows, N), out_dtype, a.device, stream)
+    else:
+        if out.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("output must be bf16 or fp32")
+        if out.shape != (rows, N) or out.stride(1) != 1:
+            raise ValueError("out: [rows][N] with a contiguous inner dimension")
+        _on_current_device(out)
+    ws = ws or default_workspace()
+    st = _lib().nvfp4_bf16_gemm_grouped(a.data_ptr(), _ld(a, K), rows, offsets.data_ptr(), E, b.data_ptr(),
+                                        b.stride(1) if b.shape[1] > 1 else b.shape[2], b.stride(0) if E > 1 else 0, int(b_kn), N, K,
+                                        out.data_ptr(), _ld(out, N), OUT_FP32 if out.dtype == torch.float32 else OUT_BF16,
+                                        ws.buf.data_ptr(), _stream(stream))
+    _check(st, "nvfp4_bf16_gemm_grouped")
+    return out
+
+
+def _ld(t: torch.Tensor, width: int) -> int:
+    """Leading dimension of a 2-D tensor; of a single row, whose stride means nothing, its width."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def nvfp4_bf16_wgrad_grouped(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
+                             accumulate: bool = False, ws: Workspace | None = None, stream=None) -> torch.Tensor:
+    """out[e] = dy_e^T . x_e in fp32 over each expert's rows (dy [rows][n], x [rows][d], out
+    [E][n][d]); an expert without rows gets zeros.  accumulate: out[e] += instead."""
+    if dy.dtype != torch.bfloat16 or x.dtype != torch.bfloat16 or dy.dim() != 2 or x.dim() != 2:
+        raise TypeError("expected bf16 dy [rows][n] and x [rows][d]")
+    rows, M = dy.shape
+    N = x.shape[1]
+    if x.shape[0] != rows:
+        raise ValueError("dy and x need the same rows")
+    if dy.stride(1) != 1 or x.stride(1) != 1:
+        raise ValueError("inner dimensions must be contiguous")
+    E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
+    _offsets(offsets, E)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = _empty((max(E, 0), M, N), torch.float32, dy.device, stream)
+    elif out.dtype != torch.float32 or out.shape != (E, M, N) or out.stride(2) != 1:
+        raise ValueError("out: fp32 [E][n][d] with a contiguous inner dimension")
+    _on_current_device(dy, x, offsets, out)
+    ws = ws or default_workspace()
+    st = _lib().nvfp4_bf16_wgrad_grouped(dy.data_ptr(), _ld(dy, M), x.data_ptr(), _ld(x, N), rows, offsets.data_ptr(), E, M,
+                                         N, out.data_ptr(), out.stride(1) if M > 1 else N, out.stride(0) if E > 1 else 0,
+                                         int(accumulate), ws.buf.data_ptr(), _stream(stream))
+    _check(st, "nvfp4_bf16_wgrad_grouped")
+    return out
+
+
+class GroupedLinearBF16:
+    """The BF16 linear layer y = x w_e^T with one weight per expert (w [E][n][d] bf16): rows of x are
+    sorted by expert, expert e owning rows [offsets[e], offsets[e + 1]).  Its workspace holds the
+    device flags of its calls (nvfp4_poll(layer.ws))."""
+
+    def __init__(self, experts: int, d: int, n: int, device=None):
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        self.experts, self.d, self.n = experts, d, n
+        self.ws = Workspace(device)
+
+    def _weight(self, w: torch.Tensor):
+        if w.shape != (self.experts, self.n, self.d):
+            raise ValueError(f"w: [{self.experts}][{self.n}][{self.d}]")
+
+    def fwd(self, x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+        self._weight(w)
+        return nvfp4_bf16_gemm_grouped(x, w, offsets, out=y, ws=self.ws, stream=stream)
+
+    def bwd(self, x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor,
+            dx: torch.Tensor | None = None, dw: torch.Tensor | None = None, accumulate: bool = False, stream=None):
+        """dx [rows][d] bf16 and dw [E][n][d] fp32 (accumulate: added to dw)."""
+        self._weight(w)
+        dx = nvfp4_bf16_gemm_grouped(dy, w, offsets, b_kn=True, out=dx, ws=self.ws, stream=stream)
+        dw = nvfp4_bf16_wgrad_grouped(dy, x, offsets, out=dw, accumulate=accumulate, ws=self.ws, stream=stream)
+        return dx, dw
+
+
+# ---------------------------------------------------------------------------------------
+# AdamW over many tensors
+# ---------------------------------------------------------------------------------------
+class AdamWContext:
+    """The tensors of an AdamW step and their moments.
+
+    params: fp32 master weights; grads: fp32 or bf16 gradients; weights: the bf16 weights the step
+    writes (None, or None entries, for none); all contiguous, entry by entry of one size, held in
+    place from step to step (the context keeps references).  state: STATE_FP32 moments, or STATE_FP8:
+    E4M3 codes with an fp32 scale per 256 elements (m, and the square root of v).  m, v, m_scale and
+    v_scale may be given (resuming from a checkpoint); otherwise they start at zero.  amax_ws: per
+    tensor a Workspace that receives the amax of its new bf16 weights (nvfp4_quantize_weight with
+    amax_ready), or None.
+    """
+
+    BLOCK = 256
+
+    def __init__(self, params, grads, weights=None, m=None, v=None, state: int = STATE_FP32, m_scale=None,
+                 v_scale=None, amax_ws=None, ws: Workspace | None = None):
+        if state not in (STATE_FP32, STATE_FP8):
+            raise ValueError("state is STATE_FP32 or STATE_FP8")
+        k = len(params)
+        fp8 = state == STATE_FP8
+        dt = torch.float8_e4m3fn if fp8 else torch.float32
+        zeros = lambda dtype, size: [torch.zeros(size(p.numel()), dtype=dtype, device=p.device) for p in params]
+        blocks = lambda n: -(-n // self.BLOCK)
+        self.state = state
+        self.params, self.grads = list(params), list(grads)
+        self.weights = [None] * k if weights is None else list(weights)
+        self.m = zeros(dt, lambda n: n) if m is None else list(m)
+        self.v = zeros(dt, lambda n: n) if v is None else list(v)
+        self.m_scale = (zeros(torch.float32, blocks) if m_scale is None else list(m_scale)) if fp8 else [None] * k
+        self.v_scale = (zeros(torch.float32, blocks) if v_scale is None else list(v_scale)) if fp8 else [None] * k
+        self.amax_ws = [None] * k if amax_ws is None else list(amax_ws)
+        self.ws = ws or default_workspace()
+        for name in ("grads", "weights", "m", "v", "m_scale", "v_scale", "amax_ws"):
+            if len(getattr(self, name)) != k:
+                raise ValueError(f"{name}: one entry per parameter")
+        table = (CAdamWTensor * max(k, 1))()
+        for i in range(k):
+            p = self.params[i]
+            n = p.numel()
+            self._tensor(p, n, (torch.float32,), f"params[{i}]")
+            self._tensor(self.grads[i], n, (torch.float32, torch.bfloat16), f"grads[{i}]")
+            self._tensor(self.m[i], n, (dt,), f"m[{i}]")
+            self._tensor(self.v[i], n, (dt,), f"v[{i}]")
+            if fp8:
+                self._tensor(self.m_scale[i], blocks(n), (torch.float32,), f"m_scale[{i}]")
+                self._tensor(self.v_scale[i], blocks(n), (torch.float32,), f"v_scale[{i}]")
+            if self.weights[i] is not None:
+                self._tensor(self.weights[i], n, (torch.bfloat16,), f"weights[{i}]")
+            e = table[i]
+            e.p, e.m, e.v, e.n = p.data_ptr(), self.m[i].data_ptr(), self.v[i].data_ptr(), n
+            e.w = None if self.weights[i] is None else self.weights[i].data_ptr()
+            e.m_scale = self.m_scale[i].data_ptr() if fp8 else None
+            e.v_scale = self.v_scale[i].data_ptr() if fp8 else None
+            e.amax_ws = None if self.amax_ws[i] is None else self.amax_ws[i].buf.data_ptr()
+        self._table, self._count = table, k
+        self._device = self.params[0].device if k else None
+        self._args = CAdamWArgs()
+        self._args.state = state
+        self._args_ref = ctypes.byref(self._args)
+        self.set_grads(self.grads)
+
+    def _tensor(self, t, n, dtypes, name):
+        if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"{name}: expected a contiguous {' or '.join(str(d) for d in dtypes)} tensor of {n} elements")
+        if t.device != self.params[0].device or t.device.type != "cuda":
+            raise ValueError(f"{name}: all tensors live on one CUDA device")
+
+    def set_grads(self, grads):
+        """Gradients of the next steps, where they are not the buffers of the steps before."""
+        grads = list(grads)
+        if len(grads) != self._count:
+            raise ValueError("grads: one entry per parameter")
+        for i, g in enumerate(grads):
+            self._tensor(g, self._table[i].n, (torch.float32, torch.bfloat16), f"grads[{i}]")
+        for e, g in zip(self._table, grads):
+            e.g = g.data_ptr()
+            e.g_dtype = OUT_FP32 if g.dtype == torch.float32 else OUT_BF16
+        self.grads = grads
+
+    def moment(self, i: int, which: str) -> torch.Tensor:
+        """Moment "m" or "v" of tensor i as fp32 values (a copy)."""
+        t = getattr(self, which)[i]
+        if self.state == STATE_FP32:
+            return t.clone()
+        n = t.numel()
+        x = t.reshape(-1).float() * getattr(self, which + "_scale")[i].repeat_interleave(self.BLOCK)[:n]
+        return (x * x if which == "v" else x).view(t.shape)
+
+    def dynamic(self, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.95, weight_decay: float = 0.1,
+                grad_scale: float = 1.0, sr_seed: int = 0) -> torch.Tensor:
+        """A step's values as 32 bytes of host memory: copied into a device buffer that a captured
+        nvfp4_adamw_step reads (its `dynamic`), they are what the next replay uses."""
+        a = CAdamWArgs(lr, beta1, beta2, 0.0, weight_decay, grad_scale, step, sr_seed & 0xFFFFFFFFFFFFFFFF, self.state, RNE, None)
+        out = CAdamWDynamic()
+        _check(_lib().nvfp4_adamw_dynamic_values(ctypes.byref(a), ctypes.byref(out)), "nvfp4_adamw_dynamic_values")
+        return torch.frombuffer(bytearray(bytes(out)), dtype=torch.uint8)
+
+
+def nvfp4_adamw_step(ctx: AdamWContext, lr: float = 0.0, step: int = 1, beta1: float = 0.9, beta2: float = 0.95,
+                     eps: float = 1e-8, weight_decay: float = 0.1, grad_scale: float = 1.0, mode: int = SR,
+                     sr_seed: int = 0, dynamic: torch.Tensor | None = None, stream=None) -> None:
+    """One AdamW step (decoupled weight decay, bias-corrected moments; step counts from 1) over the
+    context's tensors, in place.  mode and sr_seed: rounding of 8-bit moments (give each step
+    another seed).  dynamic: 32 device bytes (AdamWContext.dynamic) that replace lr, step,
+    weight_decay, grad_scale and sr_seed, read when the kernel runs."""
+    if ctx._count == 0:
+        return
+    if ctx._device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors live on {ctx._device}, which is not the current device")
+    a = ctx._args
+    a.lr, a.beta1, a.beta2, a.eps, a.weight_decay, a.grad_scale = lr, beta1, beta2, eps, weight_decay, grad_scale
+    a.step, a.sr_seed, a.mode = step, sr_seed & 0xFFFFFFFFFFFFFFFF, mode
+    if dynamic is not None:
+        if dynamic.dtype != torch.uint8 or dynamic.numel() != 32 or not dynamic.is_contiguous() or dynamic.device != ctx._device:
+            raise ValueError("dynamic: 32 contiguous uint8 on the tensors' device")
+        a.dynamic = dynamic.data_ptr()
+    else:
+        a.dynamic = None
+    _check(_lib().nvfp4_adamw(ctx._table, ctx._count, ctx._args_ref, ctx.ws.buf.data_ptr(), _stream(stream)),
+           "nvfp4_adamw")
 
 
 # ---------------------------------------------------------------------------------------

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -17,6 +18,7 @@ namespace {
 std::atomic<uint64_t> g_budget_ns{2000000000ull};
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // sm_100 check, cached per device
 nvfp4_status check_device() {
@@ -63,6 +65,8 @@ nvfp4_status check_input(const void* x, int64_t rows, int64_t cols, int64_t ld) 
     }
     return NVFP4_OK;
 }
+
+constexpr int64_t kMaxDim = (int64_t)1 << 30;
 
 __global__ void set_f32_kernel(float* p, float v) { *p = v; }
 
@@ -291,8 +295,13 @@ nvfp4_status nvfp4_quantize_dual_shard(const void* x, int64_t rows, int64_t cols
                               stream, row_offset, rows_total, false);
 }
 
-nvfp4_status nvfp4_quantize_weight(const void* wp, int64_t rows, int64_t cols, int64_t ldw, nvfp4_tensor* w_q,
-                                   nvfp4_tensor* w_qt, void* ws, nvfp4_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// run_amax: the amax pass here; otherwise the plain amax word in ws is used as it is
+nvfp4_status quantize_weight_impl(const void* wp, int64_t rows, int64_t cols, int64_t ldw, nvfp4_tensor* w_q,
+                                  nvfp4_tensor* w_qt, void* ws, nvfp4_stream_t stream, bool run_amax) {
     if (nvfp4_status st = check_input(wp, rows, cols, ldw)) return st;
     if (nvfp4_status st = check_form_buffers(w_q, true)) return st;
     if (w_qt)
@@ -315,13 +324,15 @@ nvfp4_status nvfp4_quantize_weight(const void* wp, int64_t rows, int64_t cols, i
         return from_cuda(cudaGetLastError());
     }
     Workspace* w = ws_of(ws);
-    if (cudaError_t e = reset_amax(ws, s)) return from_cuda(e);
+    if (run_amax)
+        if (cudaError_t e = reset_amax(ws, s)) return from_cuda(e);
     if (has_scale_padding(rows, cols))
         if (cudaError_t e = cudaMemsetAsync(w_q->scales, 0, nvfp4_scales_bytes(rows, cols), s)) return from_cuda(e);
     if (w_qt && has_scale_padding(cols, rows))
         if (cudaError_t e = cudaMemsetAsync(w_qt->scales, 0, nvfp4_scales_bytes(cols, rows), s)) return from_cuda(e);
     const uint16_t* xb = reinterpret_cast<const uint16_t*>(wp);
-    if (cudaError_t e = launch_amax_plain(xb, rows, cols, ldw, &w->amax_a, &w->flags, s)) return from_cuda(e);
+    if (run_amax)
+        if (cudaError_t e = launch_amax_plain(xb, rows, cols, ldw, &w->amax_a, &w->flags, s)) return from_cuda(e);
     QuantParams p;
     std::memset(&p, 0, sizeof(p));
     p.x = xb;
@@ -347,6 +358,20 @@ nvfp4_status nvfp4_quantize_weight(const void* wp, int64_t rows, int64_t cols, i
         p.nkt_col = nkt_of(rows);
     }
     return from_cuda(launch_quantize_tiles(p, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status nvfp4_quantize_weight(const void* w, int64_t rows, int64_t cols, int64_t ldw, nvfp4_tensor* w_q,
+                                   nvfp4_tensor* w_qt, void* ws, nvfp4_stream_t stream) {
+    return quantize_weight_impl(w, rows, cols, ldw, w_q, w_qt, ws, stream, true);
+}
+
+nvfp4_status nvfp4_quantize_weight_ready(const void* w, int64_t rows, int64_t cols, int64_t ldw, nvfp4_tensor* w_q,
+                                         nvfp4_tensor* w_qt, void* ws, nvfp4_stream_t stream) {
+    return quantize_weight_impl(w, rows, cols, ldw, w_q, w_qt, ws, stream, false);
 }
 
 nvfp4_status nvfp4_transpose_2d(const nvfp4_tensor* w, nvfp4_tensor* wt, nvfp4_stream_t stream) {
@@ -703,6 +728,164 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
     return NVFP4_OK;
 }
 
+nvfp4_status nvfp4_bf16_gemm_grouped(const void* a, int64_t lda, int64_t rows, const int32_t* offsets, int experts,
+                                     const void* b, int64_t ldb, int64_t stride_b, int b_kn, int64_t N, int64_t K,
+                                     void* d, int64_t ldd, nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream) {
+    if (out_dtype != NVFP4_OUT_BF16 && out_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_ARG;
+    if (b_kn != 0 && b_kn != 1) return NVFP4_ERR_ARG;
+    if (experts < 1 || rows < 0 || N < 8 || K < 8 || N % 8 || K % 8) return NVFP4_ERR_SHAPE;
+    if (lda < K || ldb < (b_kn ? N : K) || stride_b < 0 || ldd < N) return NVFP4_ERR_SHAPE;
+    if (experts > kMaxExperts || rows > kMaxDim || N > kMaxDim || K > kMaxDim || lda > kMaxDim || ldb > kMaxDim ||
+        ldd > kMaxDim || stride_b > (int64_t)1 << 38)
+        return NVFP4_ERR_LIMIT;
+    if (!ws) return NVFP4_ERR_WORKSPACE;
+    if (!offsets || !b || (rows > 0 && (!a || !d))) return NVFP4_ERR_NULL;
+    const int64_t esz = out_dtype == NVFP4_OUT_FP32 ? 4 : 2;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(d) || !aligned4(offsets) || lda % 8 || ldb % 8 || stride_b % 8 ||
+        (ldd * esz) % 16)
+        return NVFP4_ERR_ALIGN;
+    if (nvfp4_status st = check_device()) return st;
+    if (rows == 0) return NVFP4_OK;
+    GroupedGemm g{};
+    g.a = reinterpret_cast<const uint16_t*>(a);
+    g.b = reinterpret_cast<const uint16_t*>(b);
+    g.d = d;
+    g.offsets = offsets;
+    g.lda = lda;
+    g.ldb = ldb;
+    g.stride_b = stride_b;
+    g.ldd = ldd;
+    g.rows = rows;
+    g.N = N;
+    g.K = K;
+    g.experts = experts;
+    g.b_kn = b_kn != 0;
+    g.out_fp32 = out_dtype == NVFP4_OUT_FP32;
+    g.flags = &ws_of(ws)->flags;
+    g.budget_ns = g_budget_ns.load();
+    return from_cuda(launch_gemm_grouped(g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows,
+                                      const int32_t* offsets, int experts, int64_t M, int64_t N, float* d, int64_t ldd,
+                                      int64_t stride_d, int accumulate, void* ws, nvfp4_stream_t stream) {
+    if (accumulate != 0 && accumulate != 1) return NVFP4_ERR_ARG;
+    if (experts < 1 || rows < 0 || M < 8 || N < 8 || M % 8 || N % 8) return NVFP4_ERR_SHAPE;
+    if (lda < M || ldb < N || ldd < N || stride_d < 0) return NVFP4_ERR_SHAPE;
+    if (experts > kMaxExperts || rows > kMaxDim || M > kMaxDim || N > kMaxDim || lda > kMaxDim || ldb > kMaxDim ||
+        ldd > kMaxDim || stride_d > (int64_t)1 << 37)
+        return NVFP4_ERR_LIMIT;
+    if (experts > 1 && stride_d < M * ldd) return NVFP4_ERR_SHAPE;   // the gradients would overlap
+    if (!ws) return NVFP4_ERR_WORKSPACE;
+    if (!offsets || !d || (rows > 0 && (!a || !b))) return NVFP4_ERR_NULL;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(d) || !aligned4(offsets) || lda % 8 || ldb % 8 || ldd % 4 ||
+        stride_d % 4)
+        return NVFP4_ERR_ALIGN;
+    if (nvfp4_status st = check_device()) return st;
+    GroupedWgrad g{};
+    g.a = reinterpret_cast<const uint16_t*>(a);
+    g.b = reinterpret_cast<const uint16_t*>(b);
+    g.d = d;
+    g.offsets = offsets;
+    g.lda = lda;
+    g.ldb = ldb;
+    g.ldd = ldd;
+    g.stride_d = stride_d;
+    g.rows = rows;
+    g.M = M;
+    g.N = N;
+    g.experts = experts;
+    g.accumulate = accumulate != 0;
+    g.flags = &ws_of(ws)->flags;
+    g.budget_ns = g_budget_ns.load();
+    return from_cuda(launch_wgrad_grouped(g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_adamw_dynamic_values(const nvfp4_adamw_args* args, nvfp4_adamw_dynamic* out) {
+    if (!args || !out) return NVFP4_ERR_NULL;
+    if (!(args->beta1 >= 0.0 && args->beta1 < 1.0 && args->beta2 >= 0.0 && args->beta2 < 1.0)) return NVFP4_ERR_ARG;
+    if (args->step < 1 || !std::isfinite(args->lr) || !std::isfinite(args->weight_decay) || !std::isfinite(args->grad_scale))
+        return NVFP4_ERR_ARG;
+    const double step = (double)args->step;
+    out->keep = (float)(1.0 - args->lr * args->weight_decay);
+    out->step_size = (float)(args->lr / (1.0 - std::pow(args->beta1, step)));
+    out->v_fix = (float)(1.0 / std::sqrt(1.0 - std::pow(args->beta2, step)));
+    out->grad_scale = (float)args->grad_scale;
+    out->sr_seed = args->sr_seed;
+    out->reserved = 0;
+    return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int count, const nvfp4_adamw_args* args, void* ws,
+                         nvfp4_stream_t stream) {
+    static_assert(sizeof(nvfp4_adamw_dynamic) == sizeof(AdamwDynamic), "one layout on both sides");
+    if (count < 0) return NVFP4_ERR_SHAPE;
+    if (!args || (count > 0 && !tensors)) return NVFP4_ERR_NULL;
+    if (args->state != NVFP4_STATE_FP32 && args->state != NVFP4_STATE_FP8) return NVFP4_ERR_ARG;
+    if (args->mode != NVFP4_RNE && args->mode != NVFP4_SR) return NVFP4_ERR_ARG;
+    if (!(args->eps >= 0.0) || !std::isfinite(args->eps)) return NVFP4_ERR_ARG;
+    nvfp4_adamw_dynamic v;
+    if (args->dynamic) {   // lr, weight_decay, grad_scale and step are not read
+        nvfp4_adamw_args fixed = *args;
+        fixed.lr = fixed.weight_decay = fixed.grad_scale = 0.0;
+        fixed.step = 1;
+        if (nvfp4_status st = nvfp4_adamw_dynamic_values(&fixed, &v)) return st;
+    } else if (nvfp4_status st = nvfp4_adamw_dynamic_values(args, &v)) {
+        return st;
+    }
+    if (!aligned16(args->dynamic)) return NVFP4_ERR_ALIGN;
+    if (!ws) return NVFP4_ERR_WORKSPACE;
+    const bool fp8 = args->state == NVFP4_STATE_FP8;
+    for (int i = 0; i < count; ++i) {
+        const nvfp4_adamw_tensor& t = tensors[i];
+        if (t.n < 0) return NVFP4_ERR_SHAPE;
+        if (t.n > (int64_t)1 << 40) return NVFP4_ERR_LIMIT;
+        if (t.g_dtype != NVFP4_OUT_BF16 && t.g_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_ARG;
+        if (t.amax_ws && !t.w) return NVFP4_ERR_ARG;
+        if (t.n == 0) continue;
+        if (!t.p || !t.g || !t.m || !t.v || (fp8 && (!t.m_scale || !t.v_scale))) return NVFP4_ERR_NULL;
+        if (!aligned16(t.p) || !aligned16(t.g) || !aligned16(t.w) || !aligned16(t.m) || !aligned16(t.v) ||
+            !aligned16(t.amax_ws) || (fp8 && (!aligned4(t.m_scale) || !aligned4(t.v_scale))))
+            return NVFP4_ERR_ALIGN;
+    }
+    if (nvfp4_status st = check_device()) return st;
+    AdamwScalars sc{};
+    sc.keep = v.keep;
+    sc.step_size = v.step_size;
+    sc.v_fix = v.v_fix;
+    sc.grad_scale = v.grad_scale;
+    sc.beta1 = (float)args->beta1;
+    sc.one_beta1 = (float)(1.0 - args->beta1);
+    sc.beta2 = (float)args->beta2;
+    sc.one_beta2 = (float)(1.0 - args->beta2);
+    sc.eps = (float)args->eps;
+    sc.sr = args->mode == NVFP4_SR;
+    sc.sr_seed = v.sr_seed;
+    sc.dynamic = reinterpret_cast<const AdamwDynamic*>(args->dynamic);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    AdamwEntry entries[kAdamMaxTensors];
+    int held = 0;
+    for (int i = 0; i < count; ++i) {
+        const nvfp4_adamw_tensor& t = tensors[i];
+        uint32_t* amax = t.amax_ws ? &ws_of(t.amax_ws)->amax_a : nullptr;
+        if (t.n == 0) {   // an empty tensor's amax is zero
+            if (amax)
+                if (cudaError_t e = reset_amax(t.amax_ws, s)) return from_cuda(e);
+            continue;
+        }
+        AdamwEntry& e = entries[held++];
+        e = AdamwEntry{t.p, t.g, reinterpret_cast<uint16_t*>(t.w), t.m, t.v, t.m_scale, t.v_scale, amax, t.n, 0u,
+                       (int32_t)((uint32_t)i << 1 | (t.g_dtype == NVFP4_OUT_BF16 ? 1u : 0u))};
+        if (held == kAdamMaxTensors) {
+            if (cudaError_t err = launch_adamw(entries, held, fp8, sc, &ws_of(ws)->flags, s)) return from_cuda(err);
+            held = 0;
+        }
+    }
+    if (held)
+        if (cudaError_t err = launch_adamw(entries, held, fp8, sc, &ws_of(ws)->flags, s)) return from_cuda(err);
+    return NVFP4_OK;
+}
+
 nvfp4_status nvfp4_poll(void* ws, nvfp4_stream_t stream) {
     if (!ws) return NVFP4_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -711,6 +894,7 @@ nvfp4_status nvfp4_poll(void* ws, nvfp4_stream_t stream) {
     if (cudaMemcpy(&flags, ws, sizeof(flags), cudaMemcpyDeviceToHost) != cudaSuccess) return from_cuda(cudaErrorUnknown);
     if (flags && cudaMemset(ws, 0, sizeof(uint32_t)) != cudaSuccess) return from_cuda(cudaErrorUnknown);
     if (flags & kFlagTimeout) return NVFP4_ERR_TIMEOUT;
+    if (flags & kFlagOffsets) return NVFP4_ERR_ARG;
     if (flags & kFlagNonFinite) return NVFP4_ERR_NONFINITE;
     return NVFP4_OK;
 }
@@ -723,7 +907,7 @@ const char* nvfp4_status_string(nvfp4_status s) {
         case NVFP4_ERR_NULL: return "a required pointer is NULL";
         case NVFP4_ERR_ALIGN: return "a pointer or leading dimension is not 16-byte aligned";
         case NVFP4_ERR_SHAPE: return "a size violates the call's shape rule";
-        case NVFP4_ERR_ARG: return "an argument is out of range or operands are inconsistent";
+        case NVFP4_ERR_ARG: return "an argument is out of range or operands (or expert offsets) are inconsistent";
         case NVFP4_ERR_WORKSPACE: return "workspace missing";
         case NVFP4_ERR_CUDA: return "a CUDA launch or runtime call failed";
         case NVFP4_ERR_NONFINITE: return "NaN or Inf in a quantized input";

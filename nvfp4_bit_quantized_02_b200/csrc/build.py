@@ -1,8 +1,8 @@
 """Build libnvfp4.so in-tree for sm_100a (B200) with nvcc.
 
 Each .cu is compiled to an object under _build/, then linked into
-nvfp4_bit_quantized_02_b200/libnvfp4.so.  The quantization and API translation units are
-compiled with -fmad=false: codes and scales must come from single IEEE operations.
+nvfp4_bit_quantized_02_b200/libnvfp4.so.  The quantization, AdamW and API translation
+units are compiled with -fmad=false: codes and scales must come from single IEEE operations.
 """
 import os
 import subprocess
@@ -20,6 +20,8 @@ SOURCES = {
     "api.cu": ["-fmad=false"],
     "gemm_sm100.cu": [],
     "glue.cu": [],
+    "adamw.cu": ["-fmad=false"],
+    "grouped.cu": [],
     "noalloc.cu": [],
 }
 HEADERS = ["nvfp4_device.cuh", "nvfp4_internal.h"]

@@ -18,6 +18,7 @@ static_assert(sizeof(Workspace) == 256, "workspace is 256 bytes");
 
 constexpr uint32_t kFlagNonFinite = 1u;
 constexpr uint32_t kFlagTimeout = 2u;
+constexpr uint32_t kFlagOffsets = 4u;   // expert offsets out of order or range
 
 // the 16 RHT signs as bf16-pair masks (0x80008000 for a -1 sign), a by-value kernel parameter
 struct SignMasks {
@@ -120,6 +121,66 @@ cudaError_t launch_gelu_bwd(const uint16_t* h, const uint16_t* dg, uint16_t* dh,
 cudaError_t launch_gelu_amax(bool bwd, const uint16_t* h, const uint16_t* dg, uint16_t* out, int64_t rows,
                              int64_t cols, uint32_t signs, uint32_t* amax_plain, uint32_t* amax_rht, uint32_t* flags,
                              cudaStream_t s);
+
+// Products grouped by expert.  offsets: device int32 [experts + 1]; expert e owns the rows from the
+// running maximum (clamped to [0, rows]) of offsets[0..e] up to that of offsets[0..e+1].
+constexpr int kMaxExperts = 1024;
+struct GroupedGemm {        // D[t] = A[t] . B_e^T (b_kn = 0, B_e [N][K]) or A[t] . B_e (b_kn = 1, B_e [K][N])
+    const uint16_t* a;
+    const uint16_t* b;
+    void* d;
+    const int32_t* offsets;
+    int64_t lda, ldb, stride_b, ldd;
+    int64_t rows, N, K;
+    int experts;
+    bool b_kn, out_fp32;
+    uint32_t* flags;
+    uint64_t budget_ns;
+};
+struct GroupedWgrad {       // D_e[m][n] (+)= sum over e's rows t of A[t][m] B[t][n]
+    const uint16_t* a;
+    const uint16_t* b;
+    float* d;
+    const int32_t* offsets;
+    int64_t lda, ldb, ldd, stride_d;
+    int64_t rows, M, N;
+    int experts;
+    bool accumulate;
+    uint32_t* flags;
+    uint64_t budget_ns;
+};
+cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s);
+cudaError_t launch_wgrad_grouped(const GroupedWgrad& g, cudaStream_t s);
+
+// AdamW: one tensor of a launch (80 bytes: a launch's table fits the 32764 bytes of kernel parameters)
+constexpr int kAdamMaxTensors = 384;
+constexpr uint32_t kStreamMoment1 = 4u, kStreamMoment2 = 5u;
+struct AdamwEntry {
+    float* p;
+    const void* g;
+    uint16_t* w;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    uint32_t* amax;
+    int64_t n;
+    uint32_t first_chunk;   // set by the launcher
+    int32_t index_g;        // the tensor's index in the call << 1 | (gradient is bf16)
+};
+struct AdamwDynamic {       // nvfp4_adamw_dynamic
+    float keep, step_size, v_fix, grad_scale;
+    uint64_t sr_seed, reserved;
+};
+struct AdamwScalars {
+    float keep, step_size, v_fix, grad_scale;
+    float beta1, one_beta1, beta2, one_beta2, eps;
+    int32_t sr;
+    uint64_t sr_seed;
+    const AdamwDynamic* dynamic;
+};
+cudaError_t launch_adamw(const AdamwEntry* entries, int count, bool fp8, const AdamwScalars& sc, uint32_t* flags,
+                         cudaStream_t s);
 
 // host-side Philox4x32-10 (same algorithm as the device one) for the RHT sign draw
 uint32_t rht_signs_host(uint64_t seed);
