@@ -24,7 +24,7 @@ SOURCES = {
     "grouped.cu": [],
     "noalloc.cu": [],
 }
-HEADERS = ["nvfp4_device.cuh", "nvfp4_internal.h"]
+HEADERS = ["nvfp4_device.cuh", "nvfp4_internal.h", "sm100_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include"), "-I" + HERE]
 

@@ -1,162 +1,579 @@
-// grouped.cu -- bf16 products grouped by expert: D[t] = A[t] . W_e^T and the weight gradients
-// dW_e (+)= sum_t A[t]^T B[t] over each expert's rows.
+// grouped.cu -- bf16 products grouped by expert on the 5th-generation tensor cores (sm_100a):
+//   fprop   D[t] = A[t] . W_e^T      W_e [N][K], rows t of expert e
+//   dgrad   D[t] = A[t] . W_e        W_e [K][N]
+//   wgrad   D_e (+)= sum_t A[t]^T B[t]   over the rows t of expert e
 //
-// First form: one kernel for all three products, 64 x 64 output tiles by 256 threads (4 x 4 fp32
-// sums each), the operands read through their strides into shared memory 16 products deep.
-#include <cuda_runtime.h>
-
-#include <cstdint>
+// One kernel, three instantiations, on SM pairs (clusters of two CTAs, tcgen05.mma.cta_group::2,
+// kind::f16, fp32 accumulators in TMEM).  The operand whose elements lie next to one another in a
+// row of the output is the MMA's M side ("P": the weights of fprop and dgrad, B of wgrad), 256
+// features per tile, 128 per CTA; the other is its N side ("Q": the token rows, A's features of
+// wgrad), up to 256 output rows per tile in steps of 32.  So
+//   - a ragged run of rows costs MMA time for its rows rounded up to 32, not to a tile's 256;
+//   - a TMEM lane is an output feature and a TMEM column an output row: the 32 lanes of an epilogue
+//     warp hold 32 neighbours of one output row, and plain stores are whole 64-byte (bf16) or
+//     128-byte (fp32) pieces.  No staging in shared memory, no output box that could touch another
+//     expert's rows: a row past the run is a predicate.
+// Operands whose reduction index is contiguous (fprop's both, dgrad's A) are K-major in shared
+// memory; the others (dgrad's W_e, both of wgrad) are MN-major, read by TMA as they lie: no
+// transposed copies.
+//
+// Warps: 0 TMA producer (six stages of 64 products, 32 KiB per CTA); 1 MMA issuer in the leader CTA,
+// in the peer it forwards "accumulator drained"; 2-17 epilogue (32 lanes x 64 columns each); 18
+// (wgrad) clears the rows of a run's last stage that belong to the next expert.
+// The accumulator is double-buffered (2 x 256 TMEM columns).  The tensor core truncates as it
+// accumulates (measured on N(0, 1) operands: 5e-7 of the result after 512 products, 9e-6 after 8192,
+// 4e-5 after 32768), so with fp32 output an accumulator holds at most 512 products and the epilogue
+// joins such runs in registers, rounded to nearest, while the next run is under way.
+//
+// The offsets stay on the device: every CTA reads them, takes their running maximum clamped to
+// [0, rows], and numbers the tiles of all experts; a pair walks tiles pair, pair + pairs, ...
+// Every mbarrier wait is bounded by the caller's budget; on expiry the CTA raises the timeout flag,
+// drains its copies and MMAs (bounded again) and frees its TMEM.
+#include <algorithm>
 
 #include "nvfp4_device.cuh"
-#include "nvfp4_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace nvfp4 {
 
-struct SimpleParams {
-    const uint16_t *a, *b;
-    void* d;
+using namespace ptx;
+
+enum : int { kFprop = 0, kDgrad = 1, kWgrad = 2 };
+
+constexpr int kGStages = 6;
+constexpr int kPBytes = 128 * 128;                       // this CTA's 128 features x 64 products
+constexpr int kGStageBytes = 2 * kPBytes;                // and up to 128 output rows x 64 products
+constexpr int kEpiWarps = 16;
+constexpr int kRun = 8;                                  // stages per accumulator with fp32 output: 512 products
+constexpr int kBand = 8;                                 // Q tiles of an expert swept together (L2 reuse)
+constexpr uint64_t kGDrainBudgetNs = 2000000000ull;      // teardown waits, whatever the caller's budget
+
+struct GroupedParams {
     const int32_t* offsets;
-    int64_t a_m, a_k, b_n, b_k;   // element strides of A by output row / product, of B by output column / product
-    int64_t stride_b, ldd, stride_d;
-    int64_t rows, M, N, K;        // M, K: of the dimension that is not the token rows
-    int experts, wgrad, accumulate, out_fp32;
+    void* d;
+    int64_t ldd, stride_d;
+    int32_t rows, experts;
+    int32_t P, Q;           // features of the P side; wgrad: features of the Q side
+    int32_t K;              // fprop, dgrad: the reduction
+    int32_t expert_step;    // 1: expert e reads slice e of the weights' map, 0: always slice 0
+    int32_t out_fp32, accumulate;
     uint32_t* flags;
+    uint64_t budget_ns;
 };
 
-// The rows of expert e as the running maximum of the clamped offsets
-__device__ void expert_rows(const SimpleParams& p, int e, int64_t& lo, int64_t& hi) {
-    int64_t run = 0;
-    bool bad = false;
-    for (int i = 0; i <= e + 1; ++i) {
-        const int64_t o = p.offsets[i];
-        bad |= o < run || o > p.rows || o < 0;
-        lo = run;
-        run = max(run, min(max(o, (int64_t)0), p.rows));
-        if (i == 0) lo = run;
+struct GroupedSmem {        // behind the stages
+    uint64_t full[kGStages];     // leader: a stage's bytes of both CTAs
+    uint64_t empty[kGStages];    // both: the MMAs that read the stage are done
+    uint64_t tail[kGStages];     // each CTA: its bytes of a stage whose rows have to be cleared (wgrad)
+    uint64_t tfull[2];           // both: accumulator ready
+    uint64_t tempty[2];          // leader: both CTAs' epilogues have read it
+    uint64_t edrained[2];        // peer: its epilogue has read it
+    uint64_t done;
+    uint32_t tmem, abort, issued, tails;
+    uint32_t stage_tx[kGStages]; // bytes per CTA of the last use of each stage, 0: a tail
+    int32_t width;               // Q rows per tile at most
+    int32_t pad;
+    int32_t row[kMaxExperts + 4];    // expert e owns rows [row[e], row[e + 1])
+    int32_t tile[kMaxExperts + 4];   // and tiles [tile[e], tile[e + 1])
+};
+constexpr int kGroupedSmem = kGStages * kGStageBytes + (int)sizeof(GroupedSmem) + 1024;
+static_assert(kGroupedSmem <= 232448, "shared memory");
+
+template <int MODE>
+struct Shape {
+    static constexpr bool kPmn = MODE != kFprop;         // P is MN-major
+    static constexpr bool kQmn = MODE == kWgrad;
+    static constexpr int kThreads = MODE == kWgrad ? 608 : 576;
+    static constexpr int kQBox = kQmn ? 8192 : 4096;     // bytes of a Q box: 64 features x 64 rows, or 32 rows x 64
+    static constexpr int kQBoxRows = kQmn ? 64 : 32;     // output rows of a Q box
+};
+
+// One output tile
+struct Tile {
+    int e, p0;          // expert, first feature
+    int q0, qn;         // first output row (wgrad: of D_e) and how many are valid
+    int n;              // the MMA's N: qn rounded up to 32
+    int k0, klen;       // the reduction: first index and length
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ int even_width(int len, int tiles) { return (ceil_div(len, tiles) + 31) & ~31; }
+
+// Walks the tiles of one pair.  Tiles of an expert in bands of kBand Q tiles, within a band along P
+// with Q fastest.
+template <int MODE>
+struct Walk {
+    const GroupedParams& p;
+    const GroupedSmem& sm;
+    int e = 0, np, nq = 0, wq = 0, at = -1;
+    __device__ __forceinline__ Walk(const GroupedParams& p_, const GroupedSmem& sm_) : p(p_), sm(sm_) {
+        np = ceil_div(p.P, 256);
+        if (MODE == kWgrad) {
+            nq = ceil_div(p.Q, 256);
+            wq = even_width(p.Q, nq);
+        }
     }
-    hi = run;
-    if (bad) atomicOr(p.flags, kFlagOffsets);
+    __device__ __forceinline__ Tile get(int t) {
+        while (t >= sm.tile[e + 1]) ++e;
+        Tile r;
+        r.e = e;
+        const int lo = sm.row[e], len = sm.row[e + 1] - lo;
+        if (MODE != kWgrad && at != e) {
+            at = e;
+            nq = ceil_div(len, sm.width);
+            wq = even_width(len, nq);
+        }
+        const int i = t - sm.tile[e];
+        const int band = i / (kBand * np), in_band = i - band * (kBand * np);
+        const int w = min(kBand, nq - band * kBand);
+        const int pt = in_band / w, qt = band * kBand + (in_band - pt * w);
+        r.p0 = pt * 256;
+        const int total = MODE == kWgrad ? p.Q : len;
+        r.q0 = qt * wq;
+        r.qn = max(0, min(wq, total - r.q0));
+        r.n = max(32, (r.qn + 31) & ~31);
+        if (MODE == kWgrad) {
+            r.k0 = lo;
+            r.klen = len;
+        } else {
+            r.q0 += lo;
+            r.k0 = 0;
+            r.klen = p.K;
+        }
+        return r;
+    }
+};
+
+// Fills sm.row, sm.tile and sm.width from the offsets (one warp; raw offsets are in sm.row)
+template <int MODE>
+__device__ void plan_tiles(GroupedSmem& sm, const GroupedParams& p, int pairs) {
+    const int lane = threadIdx.x & 31;
+    int carry = 0;
+    bool bad = false;
+    for (int i = lane; i - lane <= p.experts; i += 32) {
+        const bool in = i <= p.experts;
+        const int o = in ? sm.row[i] : 0;
+        int v = min(max(o, 0), p.rows);
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, v, s);
+            if (lane >= s) v = max(v, u);
+        }
+        v = max(v, carry);
+        bad |= in && o != v;
+        if (in) sm.row[i] = v;
+        carry = __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    if (bad && blockIdx.x == 0) atomicOr(p.flags, kFlagOffsets);
+    __syncwarp();
+    const int np = ceil_div(p.P, 256);
+    int width = 256;
+    if (MODE != kWgrad) {
+        // Rows per tile: of 256, 224, ... 128 the one with the shortest schedule, waves of tiles over
+        // the pairs times a tile's average rows (MMA time is proportional to them; runs are cut evenly)
+        float best = 3.0e38f;
+#pragma unroll 1
+        for (int w = 256; w >= 128; w -= 32) {
+            int tiles = 0;
+            float rows = 0.0f;
+            const float inv = 1.0f / (float)w;
+            for (int e = lane; e < p.experts; e += 32) {
+                const int len = sm.row[e + 1] - sm.row[e];
+                const float nt = ceilf((float)len * inv);
+                tiles += (int)nt;
+                if (len > 0) rows += nt * (32.0f * ceilf((float)len / (32.0f * nt)));
+            }
+            tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) rows += __shfl_xor_sync(0xFFFFFFFFu, rows, s);
+            const float cost = ceilf((float)tiles * np / pairs) * rows / fmaxf((float)tiles, 1.0f);
+            if (cost < best) {
+                best = cost;
+                width = w;
+            }
+        }
+    }
+    const int nq_wgrad = MODE == kWgrad ? ceil_div(p.Q, 256) : 0;
+    int total = 0;
+    for (int i = lane; i - lane < p.experts; i += 32) {
+        int c = 0;
+        if (i < p.experts) {
+            const int len = sm.row[i + 1] - sm.row[i];
+            c = MODE == kWgrad ? (len == 0 && p.accumulate ? 0 : nq_wgrad * np) : ceil_div(len, width) * np;
+        }
+        int v = c;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, v, s);
+            if (lane >= s) v += u;
+        }
+        if (i < p.experts) sm.tile[i] = total + v - c;
+        total += __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    if (lane == 0) {
+        sm.tile[p.experts] = total;
+        sm.width = width;
+    }
 }
 
-__global__ void __launch_bounds__(256) grouped_simple_kernel(const SimpleParams p) {
-    __shared__ float as[16][65], bs[16][65];
-    __shared__ int64_t s_lo, s_hi;
-    __shared__ int s_e;
-    const int64_t n0 = (int64_t)blockIdx.x * 64;
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const GroupedParams p) {
+    using S = Shape<MODE>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    GroupedSmem& sm = *reinterpret_cast<GroupedSmem*>(smem + kGStages * kGStageBytes);
+    volatile uint32_t* abort_flag = &sm.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    for (int i = threadIdx.x; i <= p.experts; i += S::kThreads) sm.row[i] = p.offsets[i];
     if (threadIdx.x == 0) {
-        int64_t lo = 0, hi = 0;
-        if (p.wgrad) {
-            s_e = blockIdx.z;
-            expert_rows(p, blockIdx.z, lo, hi);
-        } else {   // row tile blockIdx.y of the experts' tiles in order
-            int64_t left = blockIdx.y;
-            s_e = -1;
-            for (int e = 0; e < p.experts; ++e) {
-                expert_rows(p, e, lo, hi);
-                const int64_t tiles = (hi - lo + 63) / 64;
-                if (left < tiles) {
-                    s_e = e;
-                    lo += left * 64;
-                    break;
-                }
-                left -= tiles;
-            }
+        for (int s = 0; s < kGStages; ++s) {
+            mbar_init(smem_u32(&sm.full[s]), MODE == kWgrad ? 2 : 1);
+            mbar_init(smem_u32(&sm.empty[s]), 1);
+            mbar_init(smem_u32(&sm.tail[s]), 1);
+            sm.stage_tx[s] = 0;
         }
-        s_lo = lo;
-        s_hi = hi;
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&sm.tfull[b]), 1);
+            mbar_init(smem_u32(&sm.tempty[b]), kEpiWarps + 1);   // and the peer's forwarded arrival
+            mbar_init(smem_u32(&sm.edrained[b]), kEpiWarps);
+        }
+        mbar_init(smem_u32(&sm.done), 1);
+        sm.abort = 0u;
+        sm.issued = 0u;
+        sm.tails = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&tmP);
+        prefetch_map(&tmQ);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     __syncthreads();
-    const int e = s_e;
-    if (e < 0) return;
-    const int64_t lo = s_lo, hi = s_hi;
-    const int64_t m0 = p.wgrad ? (int64_t)blockIdx.y * 64 : lo;
-    const int64_t m_end = p.wgrad ? p.M : hi, k0 = p.wgrad ? lo : 0, k_end = p.wgrad ? hi : p.K;
-    if (p.wgrad && p.accumulate && lo == hi) return;
-    const uint16_t* b = p.b + (p.wgrad ? 0 : e * p.stride_b);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {}, sum[4][4] = {};
-    for (int64_t k = k0; k < k_end; k += 16) {
-        for (int i = threadIdx.x; i < 1024; i += 256) {
-            const int kk = p.wgrad ? i >> 6 : i & 15, r = p.wgrad ? i & 63 : i >> 4;
-            const bool kin = k + kk < k_end;
-            as[kk][r] = kin && m0 + r < m_end ? __uint_as_float((uint32_t)p.a[(m0 + r) * p.a_m + (k + kk) * p.a_k] << 16) : 0.0f;
-            bs[kk][r] = kin && n0 + r < p.N ? __uint_as_float((uint32_t)b[(n0 + r) * p.b_n + (k + kk) * p.b_k] << 16) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[kk][ty + 16 * i], bs[kk][tx + 16 * j], acc[i][j]);
-        __syncthreads();
-        if (((k - k0) & 511) == 496 || k + 16 >= k_end) {   // runs of 512 products are joined
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) {
-                    sum[i][j] += acc[i][j];
-                    acc[i][j] = 0.0f;
+    if (warp == 0) plan_tiles<MODE>(sm, p, pairs);
+    tc_fence_before();
+    cluster_sync_all();   // both CTAs' barriers, TMEM and plans are there
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const int ntiles = sm.tile[p.experts];
+    const int run = p.out_fp32 ? kRun : 1 << 30;   // stages per accumulator
+
+    if (warp == 0) {
+        // ------------------------------- producer (both CTAs) --------------------------------
+        if (lane == 0) {
+            Walk<MODE> walk(p, sm);
+            int g = 0, tails = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < ntiles; t += pairs) {
+                const Tile c = walk.get(t);
+                const int p0 = c.p0 + (int)rank * 128, half = c.n >> 1, q0 = c.q0 + (int)rank * half;
+                const int boxes = ceil_div(half, S::kQBoxRows);
+                const uint32_t tx = (uint32_t)(kPBytes + boxes * S::kQBox);
+                const int z = c.e * p.expert_step;
+                for (int k = 0; k < c.klen; k += 64, ++g) {
+                    const int s = g % kGStages;
+                    if (!mbar_wait(smem_u32(&sm.empty[s]), ((uint32_t)(g / kGStages) & 1u) ^ 1u, abort_flag, p.flags, p.budget_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    uint32_t bar = map_rank(smem_u32(&sm.full[s]), 0);
+                    const bool tail = MODE == kWgrad && (min(64, c.klen - k) & 15) != 0;
+                    if (tail) {
+                        bar = smem_u32(&sm.tail[tails % kGStages]);
+                        mbar_expect_tx(bar, tx);
+                        ++tails;
+                    } else if (rank == 0) {
+                        mbar_expect_tx(smem_u32(&sm.full[s]), 2u * tx);
+                        if (MODE == kWgrad) mbar_arrive(smem_u32(&sm.full[s]));
+                    }
+                    sm.stage_tx[s] = tail ? 0u : tx;
+                    const uint32_t dst = smem_u32(smem + s * kGStageBytes), dq = dst + kPBytes;
+                    const int kk = c.k0 + k;
+                    if (MODE == kFprop) {
+                        tma_load_3d_pair(dst, &tmP, kk, p0, z, bar);
+                    } else if (MODE == kDgrad) {
+                        tma_load_3d_pair(dst, &tmP, p0, kk, z, bar);
+                        tma_load_3d_pair(dst + 8192, &tmP, p0 + 64, kk, z, bar);
+                    } else {
+                        tma_load_2d_pair(dst, &tmP, p0, kk, bar);
+                        tma_load_2d_pair(dst + 8192, &tmP, p0 + 64, kk, bar);
+                    }
+                    for (int b = 0; b < boxes; ++b) {
+                        if (S::kQmn)
+                            tma_load_2d_pair(dq + b * S::kQBox, &tmQ, q0 + 64 * b, kk, bar);
+                        else
+                            tma_load_2d_pair(dq + b * S::kQBox, &tmQ, kk, q0 + 32 * b, bar);
+                    }
                 }
+            }
+            sm.issued = (uint32_t)g;   // read by the drain, after the cluster barrier
+            sm.tails = (uint32_t)tails;
         }
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m >= m_end || n >= p.N) continue;
-            const int64_t at = (p.wgrad ? e * p.stride_d : 0) + m * p.ldd + n;
-            if (!p.out_fp32) {
-                reinterpret_cast<uint16_t*>(p.d)[at] = (uint16_t)f32x2_to_bf16x2(sum[i][j], 0.0f);
-            } else {
-                float* d = reinterpret_cast<float*>(p.d) + at;
-                *d = p.accumulate ? *d + sum[i][j] : sum[i][j];
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ------------------------------- MMA issuer (leader) -----------------------------
+            // the whole warp runs the loop, one elected lane issues
+            const uint32_t base = smem_u32(smem);
+            const uint64_t pdesc = S::kPmn ? desc_mn_major(base, 8192) : desc_k_major(base);
+            const uint64_t qdesc = S::kQmn ? desc_mn_major(base + kPBytes, 8192) : desc_k_major(base + kPBytes);
+            constexpr uint32_t pstep = S::kPmn ? 2048 >> 4 : 32 >> 4, qstep = S::kQmn ? 2048 >> 4 : 32 >> 4;   // 16 products
+            // fp32 accumulator, bf16 operands, transpose bits of the MN-major ones, M = 256
+            constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | (S::kPmn ? 1u << 15 : 0u) |
+                                        (S::kQmn ? 1u << 16 : 0u) | ((uint32_t)(256 >> 4) << 24);
+            Walk<MODE> walk(p, sm);
+            int g = 0, it = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < ntiles; t += pairs) {
+                const Tile c = walk.get(t);
+                const uint32_t idesc = idesc0 | ((uint32_t)(c.n >> 3) << 17);
+                const int stages = ceil_div(c.klen, 64);
+                for (int k = 0; ok && k < stages; ++it) {
+                    const int end = min(stages, k + min(run, stages - k));
+                    const int buf = it & 1;
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.tempty[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag,
+                                                           p.flags, p.budget_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t acc = tmem + 256u * buf;
+                    const int first = k;
+                    for (; k < end; ++k, ++g) {
+                        const int s = g % kGStages;
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.full[s]), (uint32_t)(g / kGStages) & 1u, abort_flag,
+                                                               p.flags, p.budget_ns))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const int steps = min(4, (c.klen - 64 * k + 15) >> 4);
+                        const uint64_t off = (uint64_t)((s * kGStageBytes) >> 4);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (j < steps)
+                                    mma_bf16_pair(acc, pdesc + off + pstep * j, qdesc + off + qstep * j, idesc, (k > first || j > 0) ? 1u : 0u);
+                            mma_commit_pair(smem_u32(&sm.empty[s]));
+                        }
+                        __syncwarp();
+                    }
+                    if (ok && elect_one()) mma_commit_pair(smem_u32(&sm.tfull[buf]));
+                    __syncwarp();
+                }
+            }
+            if (elect_one()) mma_commit_local(smem_u32(&sm.done));
+            __syncwarp();
+            mbar_wait(smem_u32(&sm.done), 0u, abort_flag, p.flags, kGDrainBudgetNs, false);
+        } else {
+            // the peer's drained accumulators as one remote arrival each
+            Walk<MODE> walk(p, sm);
+            int it = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < ntiles; t += pairs) {
+                const int stages = ceil_div(walk.get(t).klen, 64);
+                for (int k = 0; k < stages; k += min(run, stages), ++it) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.edrained[it & 1]), (uint32_t)(it >> 1) & 1u, abort_flag,
+                                                           p.flags, p.budget_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_remote(map_rank(smem_u32(&sm.tempty[it & 1]), 0));
+                    __syncwarp();
+                }
             }
         }
+    } else if (warp < 2 + kEpiWarps) {
+        // ------------------------------- epilogue (both CTAs) --------------------------------
+        const int q = warp & 3, c0 = ((warp - 2) >> 2) * 64;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        Walk<MODE> walk(p, sm);
+        int it = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < ntiles; t += pairs) {
+            const Tile c = walk.get(t);
+            const int stages = ceil_div(c.klen, 64);
+            const bool mine = c0 < c.qn;
+            float acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+            for (int k = 0; k < stages; k += min(run, stages), ++it) {
+                const int buf = it & 1;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, p.flags,
+                                                       p.budget_ns))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (mine) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        float v[16];
+                        tmem_ld16(tmem + lanes + 256u * buf + (uint32_t)(c0 + 16 * h), v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[16 * h + i] += v[i];
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(rank == 0 ? &sm.tempty[buf] : &sm.edrained[buf]));
+            }
+            if (!ok || !mine) continue;
+            const int n = min(64, c.qn - c0);
+            const int f = c.p0 + (int)rank * 128 + q * 32 + lane;
+            const int64_t at = (MODE == kWgrad ? c.e * p.stride_d : 0) + (int64_t)(c.q0 + c0) * p.ldd;
+            if (MODE == kWgrad || p.out_fp32) {
+                float* d = reinterpret_cast<float*>(p.d) + at + f;
+                if (f < p.P) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        if (i < n) {
+                            if (MODE == kWgrad && p.accumulate)
+                                atomicAdd(d, acc[i]);   // one add per element and call: no order to depend on
+                            else
+                                *d = acc[i];
+                        }
+                        d += p.ldd;
+                    }
+                }
+            } else {
+                // neighbouring lanes trade one value of two rows, so that each stores two features of one row
+                const int odd = lane & 1;
+                uint16_t* d = reinterpret_cast<uint16_t*>(p.d) + at + odd * p.ldd + (f - odd);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? acc[i] : acc[i + 1], 1);
+                    const uint32_t w = odd ? f32x2_to_bf16x2(other, acc[i + 1]) : f32x2_to_bf16x2(acc[i], other);
+                    if (i + odd < n && f < p.P) *reinterpret_cast<uint32_t*>(d) = w;
+                    d += 2 * p.ldd;
+                }
+            }
+        }
+    } else {
+        // ------------------------------- tails (wgrad, both CTAs) ----------------------------
+        // A run's last stage holds rows of the next expert behind its own.  MMAs stop at the 16 rows
+        // that hold the last one; the rest of those 16 is cleared, in both operands (0 x NaN).
+        Walk<MODE> walk(p, sm);
+        int g = 0, tails = 0;
+        for (int t = pair; t < ntiles; t += pairs) {
+            const Tile c = walk.get(t);
+            const int stages = ceil_div(c.klen, 64);
+            g += stages;
+            const int last = c.klen & 63;
+            if (!(last & 15)) continue;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.tail[tails % kGStages]), (uint32_t)(tails / kGStages) & 1u,
+                                                   abort_flag, p.flags, p.budget_ns)))
+                break;
+            ++tails;
+            const int s = (g - 1) % kGStages;
+            // a lane clears 16 bytes of each row of one of the stage's four 64 x 64 boxes
+            const uint32_t box = smem_u32(smem + s * kGStageBytes) + (uint32_t)(lane >> 3) * 8192u + (uint32_t)(lane & 7) * 16u;
+            for (int r = last; r & 15; ++r)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + (uint32_t)r * 128u), "r"(0) : "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_release_cluster(map_rank(smem_u32(&sm.full[s]), 0));
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync_all();   // both producers have stopped and published what they issued
+    if (warp == 0 && lane == 0) {
+        // Drain: every copy lands before its CTA exits.  Tails land on the CTA's own barriers; the other
+        // stages of both CTAs on the leader's.  A producer is at most kGStages ahead of the MMAs, so only
+        // the last kGStages uses can be outstanding.  After an abort the counts may differ: a stage
+        // that only the peer issued has its arrivals made here, one that only the leader issued has the
+        // peer's bytes cancelled.  After a normal run every wait returns at once.
+        const int tails = (int)sm.tails;
+        for (int j = max(0, tails - kGStages); j < tails; ++j)
+            mbar_wait(smem_u32(&sm.tail[j % kGStages]), (uint32_t)(j / kGStages) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
+        if (rank == 0) {
+            const int gl = (int)sm.issued, gp = (int)ld_cluster_u32(map_rank(smem_u32(&sm.issued), 1)), gm = max(gl, gp);
+            for (int k = max(0, gm - kGStages); k < gm; ++k) {
+                const int s = k % kGStages;
+                const uint32_t bar = smem_u32(&sm.full[s]);
+                const uint32_t tx = k < gl ? sm.stage_tx[s] : ld_cluster_u32(map_rank(smem_u32(&sm.stage_tx[s]), 1));
+                if (tx == 0) continue;
+                if (k >= gl) {
+                    mbar_expect_tx(bar, tx);
+                    if (MODE == kWgrad) mbar_arrive(bar);
+                } else if (k >= gp) {
+                    mbar_complete_tx(bar, tx);
+                }
+                mbar_wait(bar, (uint32_t)(k / kGStages) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
+            }
+        }
+    }
+    cluster_sync_all();   // both CTAs are done with TMEM, barriers and each other's shared memory
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+template <int MODE>
+static cudaError_t launch(const CUtensorMap& tp, const CUtensorMap& tq, const GroupedParams& p, int64_t most_tiles, cudaStream_t s) {
+    static std::atomic<uint64_t> attr{0};
+    auto kern = grouped_kernel<MODE>;
+    if (cudaError_t e = host::ensure_smem(reinterpret_cast<const void*>(kern), kGroupedSmem, attr)) return e;
+    const int64_t pairs = std::min<int64_t>(std::max<int64_t>(most_tiles, 1), host::sm_count() / 2);
+    kern<<<(unsigned)(2 * pairs), Shape<MODE>::kThreads, kGroupedSmem, s>>>(tp, tq, p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
-    SimpleParams p{};
-    p.a = g.a;
-    p.b = g.b;
-    p.d = g.d;
+    GroupedParams p{};
     p.offsets = g.offsets;
-    p.a_m = g.lda;
-    p.a_k = 1;
-    p.b_n = g.b_kn ? 1 : g.ldb;
-    p.b_k = g.b_kn ? g.ldb : 1;
-    p.stride_b = g.stride_b;
+    p.d = g.d;
     p.ldd = g.ldd;
-    p.rows = g.rows;
-    p.N = g.N;
-    p.K = g.K;
+    p.rows = (int32_t)g.rows;
     p.experts = g.experts;
+    p.P = (int32_t)g.N;
+    p.K = (int32_t)g.K;
     p.out_fp32 = g.out_fp32;
     p.flags = g.flags;
-    const int64_t tiles = g.rows / 64 + (g.rows < g.experts ? g.rows : g.experts);
-    grouped_simple_kernel<<<dim3((unsigned)((g.N + 63) / 64), (unsigned)tiles), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    p.budget_ns = g.budget_ns;
+    // one weight for all experts (stride 0) is one slice of the map
+    const bool many = g.experts > 1 && g.stride_b > 0;
+    p.expert_step = many ? 1 : 0;
+    const int64_t bcols = g.b_kn ? g.N : g.K, brows = g.b_kn ? g.K : g.N;
+    CUtensorMap tp, tq;
+    if (!host::bf16_map(&tp, g.b, bcols, brows, g.ldb, many ? g.experts : 1, many ? g.stride_b : brows * g.ldb, 3,
+                        g.b_kn ? 64u : 128u) ||
+        !host::bf16_map(&tq, g.a, g.K, g.rows, g.lda, 1, 0, 2, 32u))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = ((g.N + 255) / 256) * (g.rows / 128 + std::min<int64_t>(g.rows, g.experts));
+    return g.b_kn ? launch<kDgrad>(tp, tq, p, tiles, s) : launch<kFprop>(tp, tq, p, tiles, s);
 }
 
 cudaError_t launch_wgrad_grouped(const GroupedWgrad& g, cudaStream_t s) {
-    SimpleParams p{};
-    p.a = g.a;
-    p.b = g.b;
-    p.d = g.d;
+    GroupedParams p{};
     p.offsets = g.offsets;
-    p.a_m = 1;
-    p.a_k = g.lda;
-    p.b_n = 1;
-    p.b_k = g.ldb;
+    p.d = g.d;
     p.ldd = g.ldd;
     p.stride_d = g.stride_d;
-    p.rows = g.rows;
-    p.M = g.M;
-    p.N = g.N;
+    p.rows = (int32_t)g.rows;
     p.experts = g.experts;
-    p.wgrad = 1;
-    p.accumulate = g.accumulate;
+    p.P = (int32_t)g.N;
+    p.Q = (int32_t)g.M;
     p.out_fp32 = 1;
+    p.accumulate = g.accumulate;
     p.flags = g.flags;
-    grouped_simple_kernel<<<dim3((unsigned)((g.N + 63) / 64), (unsigned)((g.M + 63) / 64), g.experts), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    p.budget_ns = g.budget_ns;
+    CUtensorMap tp, tq;
+    // without rows nothing is read: the maps then cover the output, which is there
+    const int64_t rows = std::max<int64_t>(g.rows, 1);
+    const void* b = g.rows ? (const void*)g.b : (const void*)g.d;
+    const void* a = g.rows ? (const void*)g.a : (const void*)g.d;
+    if (!host::bf16_map(&tp, b, g.N, rows, g.ldb, 1, 0, 2, 64u) || !host::bf16_map(&tq, a, g.M, rows, g.lda, 1, 0, 2, 64u))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = ((g.N + 255) / 256) * ((g.M + 255) / 256) * g.experts;
+    return launch<kWgrad>(tp, tq, p, tiles, s);
 }
 
 }  // namespace nvfp4
