@@ -44,7 +44,7 @@ constexpr int kGStages = 6;
 constexpr int kPBytes = 128 * 128;                       // this CTA's 128 features x 64 products
 constexpr int kGStageBytes = 2 * kPBytes;                // and up to 128 output rows x 64 products
 constexpr int kEpiWarps = 16;
-constexpr int kRun = 8;                                  // stages per accumulator with fp32 output: 512 products
+constexpr int kRun = 12;                                 // stages per accumulator with fp32 output: 768 products
 constexpr int kBand = 8;                                 // Q tiles of an expert swept together (L2 reuse)
 constexpr uint64_t kGDrainBudgetNs = 2000000000ull;      // teardown waits, whatever the caller's budget
 
@@ -84,8 +84,16 @@ struct Shape {
     static constexpr bool kPmn = MODE != kFprop;         // P is MN-major
     static constexpr bool kQmn = MODE == kWgrad;
     static constexpr int kThreads = MODE == kWgrad ? 608 : 576;
-    static constexpr int kQBox = kQmn ? 8192 : 4096;     // bytes of a Q box: 64 features x 64 rows, or 32 rows x 64
-    static constexpr int kQBoxRows = kQmn ? 64 : 32;     // output rows of a Q box
+};
+
+// The maps of a launch.  A stage is one TMA load per operand and CTA: more, smaller boxes cost their
+// issue (fprop at 8192 x 5120 x 5120: 1519 TFLOP/s with one 128-row box for Q, 1171 with four of 32).
+// K-major Q: boxes of 32, 64 and 128 rows (q[0..2]), the smallest that holds a tile's rows.
+// MN-major operands: a row's features cut into blocks of 64, so that one box holds two blocks (wide);
+// where a tile's 128 features are not all there, or do not start at a block, two boxes of one
+// block each, which end at the tensor's width (p, q[0]).
+struct Maps {
+    CUtensorMap p, p_wide, q[3], q_wide;
 };
 
 // One output tile
@@ -110,7 +118,7 @@ struct Walk {
         np = ceil_div(p.P, 256);
         if (MODE == kWgrad) {
             nq = ceil_div(p.Q, 256);
-            wq = even_width(p.Q, nq);
+            wq = 256;
         }
     }
     __device__ __forceinline__ Tile get(int t) {
@@ -169,8 +177,9 @@ __device__ void plan_tiles(GroupedSmem& sm, const GroupedParams& p, int pairs) {
     const int np = ceil_div(p.P, 256);
     int width = 256;
     if (MODE != kWgrad) {
-        // Rows per tile: of 256, 224, ... 128 the one with the shortest schedule, waves of tiles over
-        // the pairs times a tile's average rows (MMA time is proportional to them; runs are cut evenly)
+        // Rows per tile: of 256, 224, ... 128 the one with the shortest schedule: waves of tiles over the
+        // pairs times a tile's operand rows (256 features and its own rows, evenly cut), since a stage
+        // takes the time its operands need from L2
         float best = 3.0e38f;
 #pragma unroll 1
         for (int w = 256; w >= 128; w -= 32) {
@@ -186,7 +195,7 @@ __device__ void plan_tiles(GroupedSmem& sm, const GroupedParams& p, int pairs) {
             tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) rows += __shfl_xor_sync(0xFFFFFFFFu, rows, s);
-            const float cost = ceilf((float)tiles * np / pairs) * rows / fmaxf((float)tiles, 1.0f);
+            const float cost = ceilf((float)tiles * np / pairs) * (256.0f + rows / fmaxf((float)tiles, 1.0f));
             if (cost < best) {
                 best = cost;
                 width = w;
@@ -218,7 +227,7 @@ __device__ void plan_tiles(GroupedSmem& sm, const GroupedParams& p, int pairs) {
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const GroupedParams p) {
+    grouped_kernel(const __grid_constant__ Maps maps, const GroupedParams p) {
     using S = Shape<MODE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -246,8 +255,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         sm.issued = 0u;
         sm.tails = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        prefetch_map(&tmP);
-        prefetch_map(&tmQ);
+        prefetch_map(S::kPmn ? &maps.p_wide : &maps.p);
+        prefetch_map(S::kQmn ? &maps.q_wide : &maps.q[2]);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "r"(512)
@@ -272,8 +281,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             for (int t = pair; ok && t < ntiles; t += pairs) {
                 const Tile c = walk.get(t);
                 const int p0 = c.p0 + (int)rank * 128, half = c.n >> 1, q0 = c.q0 + (int)rank * half;
-                const int boxes = ceil_div(half, S::kQBoxRows);
-                const uint32_t tx = (uint32_t)(kPBytes + boxes * S::kQBox);
+                // K-major Q: the box that holds the half's rows; MN-major: whether one wide box serves
+                const int qbox = half <= 32 ? 0 : half <= 64 ? 1 : 2;
+                const bool pwide = S::kPmn && p0 + 128 <= p.P, qwide = S::kQmn && half == 128 && q0 + 128 <= p.Q;
+                const uint32_t tx = (uint32_t)kPBytes + (S::kQmn ? (half <= 64 ? 8192u : 16384u) : 4096u << qbox);
                 const int z = c.e * p.expert_step;
                 for (int k = 0; k < c.klen; k += 64, ++g) {
                     const int s = g % kGStages;
@@ -294,20 +305,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                     sm.stage_tx[s] = tail ? 0u : tx;
                     const uint32_t dst = smem_u32(smem + s * kGStageBytes), dq = dst + kPBytes;
                     const int kk = c.k0 + k;
-                    if (MODE == kFprop) {
-                        tma_load_3d_pair(dst, &tmP, kk, p0, z, bar);
-                    } else if (MODE == kDgrad) {
-                        tma_load_3d_pair(dst, &tmP, p0, kk, z, bar);
-                        tma_load_3d_pair(dst + 8192, &tmP, p0 + 64, kk, z, bar);
+                    if (!S::kPmn) {
+                        tma_load_3d_pair(dst, &maps.p, kk, p0, z, bar);
+                    } else if (pwide) {
+                        tma_load_4d_pair(dst, &maps.p_wide, 0, kk, p0 >> 6, z, bar);
                     } else {
-                        tma_load_2d_pair(dst, &tmP, p0, kk, bar);
-                        tma_load_2d_pair(dst + 8192, &tmP, p0 + 64, kk, bar);
+                        tma_load_3d_pair(dst, &maps.p, p0, kk, z, bar);
+                        tma_load_3d_pair(dst + 8192, &maps.p, p0 + 64, kk, z, bar);
                     }
-                    for (int b = 0; b < boxes; ++b) {
-                        if (S::kQmn)
-                            tma_load_2d_pair(dq + b * S::kQBox, &tmQ, q0 + 64 * b, kk, bar);
-                        else
-                            tma_load_2d_pair(dq + b * S::kQBox, &tmQ, kk, q0 + 32 * b, bar);
+                    if (!S::kQmn) {
+                        tma_load_2d_pair(dq, &maps.q[qbox], kk, q0, bar);
+                    } else if (qwide) {
+                        tma_load_4d_pair(dq, &maps.q_wide, 0, kk, q0 >> 6, 0, bar);
+                    } else {
+                        tma_load_3d_pair(dq, &maps.q[0], q0, kk, 0, bar);
+                        if (half > 64) tma_load_3d_pair(dq + 8192, &maps.q[0], q0 + 64, kk, 0, bar);
                     }
                 }
             }
@@ -517,13 +529,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
 }
 
 template <int MODE>
-static cudaError_t launch(const CUtensorMap& tp, const CUtensorMap& tq, const GroupedParams& p, int64_t most_tiles, cudaStream_t s) {
+static cudaError_t launch(const Maps& maps, const GroupedParams& p, int64_t most_tiles, cudaStream_t s) {
     static std::atomic<uint64_t> attr{0};
     auto kern = grouped_kernel<MODE>;
     if (cudaError_t e = host::ensure_smem(reinterpret_cast<const void*>(kern), kGroupedSmem, attr)) return e;
     const int64_t pairs = std::min<int64_t>(std::max<int64_t>(most_tiles, 1), host::sm_count() / 2);
-    kern<<<(unsigned)(2 * pairs), Shape<MODE>::kThreads, kGroupedSmem, s>>>(tp, tq, p);
+    kern<<<(unsigned)(2 * pairs), Shape<MODE>::kThreads, kGroupedSmem, s>>>(maps, p);
     return cudaGetLastError();
+}
+
+// MN-major operand [slices][rows][cols] (row stride ld, slice stride `stride`): one-block boxes up to
+// the width, and two-block boxes over the whole blocks (valid where there are any)
+static bool mn_maps(CUtensorMap* narrow, CUtensorMap* wide, const void* x, int64_t cols, int64_t rows, int64_t ld,
+                    int64_t slices, int64_t stride) {
+    const int64_t dims[4] = {cols, rows, slices, 0}, strides[3] = {ld, stride, 0};
+    const uint32_t box[4] = {64, 64, 1, 0};
+    if (!host::bf16_map(narrow, x, 3, dims, strides, box)) return false;
+    *wide = *narrow;
+    if (cols < 128) return true;
+    const int64_t wdims[4] = {64, rows, cols / 64, slices}, wstrides[3] = {ld, 64, stride};
+    const uint32_t wbox[4] = {64, 64, 2, 1};
+    return host::bf16_map(wide, x, 4, wdims, wstrides, wbox);
 }
 
 cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
@@ -541,14 +567,24 @@ cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
     // one weight for all experts (stride 0) is one slice of the map
     const bool many = g.experts > 1 && g.stride_b > 0;
     p.expert_step = many ? 1 : 0;
-    const int64_t bcols = g.b_kn ? g.N : g.K, brows = g.b_kn ? g.K : g.N;
-    CUtensorMap tp, tq;
-    if (!host::bf16_map(&tp, g.b, bcols, brows, g.ldb, many ? g.experts : 1, many ? g.stride_b : brows * g.ldb, 3,
-                        g.b_kn ? 64u : 128u) ||
-        !host::bf16_map(&tq, g.a, g.K, g.rows, g.lda, 1, 0, 2, 32u))
-        return cudaErrorInvalidValue;
+    const int64_t slices = many ? g.experts : 1, stride = many ? g.stride_b : 8;
+    Maps maps;
+    if (g.b_kn) {
+        if (!mn_maps(&maps.p, &maps.p_wide, g.b, g.N, g.K, g.ldb, slices, stride)) return cudaErrorInvalidValue;
+    } else {
+        const int64_t dims[3] = {g.K, g.N, slices}, strides[2] = {g.ldb, stride};
+        const uint32_t box[3] = {64, 128, 1};
+        if (!host::bf16_map(&maps.p, g.b, 3, dims, strides, box)) return cudaErrorInvalidValue;
+        maps.p_wide = maps.p;
+    }
+    for (int i = 0; i < 3; ++i) {
+        const int64_t dims[2] = {g.K, g.rows}, strides[1] = {g.lda};
+        const uint32_t box[2] = {64, 32u << i};
+        if (!host::bf16_map(&maps.q[i], g.a, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    maps.q_wide = maps.q[0];
     const int64_t tiles = ((g.N + 255) / 256) * (g.rows / 128 + std::min<int64_t>(g.rows, g.experts));
-    return g.b_kn ? launch<kDgrad>(tp, tq, p, tiles, s) : launch<kFprop>(tp, tq, p, tiles, s);
+    return g.b_kn ? launch<kDgrad>(maps, p, tiles, s) : launch<kFprop>(maps, p, tiles, s);
 }
 
 cudaError_t launch_wgrad_grouped(const GroupedWgrad& g, cudaStream_t s) {
@@ -565,15 +601,17 @@ cudaError_t launch_wgrad_grouped(const GroupedWgrad& g, cudaStream_t s) {
     p.accumulate = g.accumulate;
     p.flags = g.flags;
     p.budget_ns = g.budget_ns;
-    CUtensorMap tp, tq;
-    // without rows nothing is read: the maps then cover the output, which is there
+    // without rows nothing is read: the maps then stand over the output, which is there
     const int64_t rows = std::max<int64_t>(g.rows, 1);
     const void* b = g.rows ? (const void*)g.b : (const void*)g.d;
     const void* a = g.rows ? (const void*)g.a : (const void*)g.d;
-    if (!host::bf16_map(&tp, b, g.N, rows, g.ldb, 1, 0, 2, 64u) || !host::bf16_map(&tq, a, g.M, rows, g.lda, 1, 0, 2, 64u))
+    Maps maps;
+    if (!mn_maps(&maps.p, &maps.p_wide, b, g.N, rows, g.ldb, 1, 8) ||
+        !mn_maps(&maps.q[0], &maps.q_wide, a, g.M, rows, g.lda, 1, 8))
         return cudaErrorInvalidValue;
+    maps.q[1] = maps.q[2] = maps.q[0];
     const int64_t tiles = ((g.N + 255) / 256) * ((g.M + 255) / 256) * g.experts;
-    return launch<kWgrad>(tp, tq, p, tiles, s);
+    return launch<kWgrad>(maps, p, tiles, s);
 }
 
 }  // namespace nvfp4

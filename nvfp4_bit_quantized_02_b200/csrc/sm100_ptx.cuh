@@ -126,6 +126,13 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                                 int32_t w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---- tcgen05 --------------------------------------------------------------------------
@@ -193,17 +200,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return f;
 }
 
-// bf16 map [outer][rows][cols] (outer = 1: 2D), box 64 columns (128 bytes) x box_rows, 128-byte
-// swizzle, zero fill past the ends
-inline bool bf16_map(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, int64_t outer,
-                     int64_t stride, int dims, uint32_t box_rows) {
+// bf16 map of `n` dimensions, innermost first, strides in elements from the second dimension on;
+// 128-byte swizzle (an inner box of 64 elements), zero fill past the ends
+inline bool bf16_map(CUtensorMap* map, const void* p, int n, const int64_t* dims, const int64_t* strides, const uint32_t* box) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t d[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)outer};
-    cuuint64_t st[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)(stride * 2)};
-    cuuint32_t box[3] = {64u, box_rows, 1u};
-    cuuint32_t es[3] = {1u, 1u, 1u};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void*>(p), d, st, box, es,
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5], es[5];
+    for (int i = 0; i < n; ++i) {
+        d[i] = (cuuint64_t)dims[i];
+        if (i) st[i - 1] = (cuuint64_t)strides[i - 1] * 2;
+        bx[i] = box[i];
+        es[i] = 1u;
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)n, const_cast<void*>(p), d, st, bx, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
