@@ -32,94 +32,326 @@ struct AdamwTable {
     AdamwEntry t[CAP];
     int32_t count;
     uint32_t chunks;
+    uint32_t key0[10], key1[10];   // Philox round keys of the arguments' seed (constant-bank operands)
 };
 
-// Two E4M3 codes (low byte first) to fp32, exact
-__device__ __forceinline__ void e4m3x2_decode(uint32_t pair, float& lo, float& hi) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(pair & 0xFFFFu));
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
-}
-
-// E4M3 code of x * per (per = 448 * (1 / amax) of the block), sign kept.  For u = |x| * per >= 2^-6 the
-// code is the top bits of u's fp32 pattern; below, u + 2^-6 lies in a binade whose 3-bit step is
-// the subnormal step 2^-9, so the same bits give the subnormal code plus 8.  Adding `round` to the
-// 20 bits that are cut off carries into the code where it rounds up: 2^20 - 1 - 16 r16 does so iff
-// r16 < f * 2^16 (f = the cut-off bits / 2^20), half a step less the parity bit gives nearest even.
-__device__ __forceinline__ uint32_t e4m3_encode(float x, float per, bool sr, uint32_t r16) {
-    const float u = __fmul_rn(fabsf(x), per);
-    const bool low = u < 0.015625f;
-    const uint32_t bits = __float_as_uint(low ? __fadd_rn(u, 0.015625f) : u);
-    const uint32_t round = sr ? 0xFFFFFu - (r16 << 4) : 0x7FFFFu + ((bits >> 20) & 1u);
-    const uint32_t code = min(((bits + round) >> 20) - (low ? 968u : 960u), 0x7Eu);
-    return code | ((__float_as_uint(x) >> 24) & 0x80u);
-}
-
-// The four 16-bit fields of each of a lane's two element quads.  A Philox block serves eight
-// consecutive elements, i.e. the quads of two neighbouring lanes: the even lane computes the block
-// of the pair's j = 0 quads, the odd lane that of the j = 1 quads, and each hands the other half over.
-__device__ __forceinline__ void quad_words(uint32_t (&w)[2][2], uint64_t block_base, uint32_t stream, uint32_t tensor,
-                                           uint32_t k0, uint32_t k1) {
-    const uint32_t lane = threadIdx.x & 31;
-    const uint64_t g = (block_base + 4u * (lane & ~1u) + 128u * (lane & 1u)) >> 3;
-    const U4 r = philox4x32_10((uint32_t)g, (uint32_t)(g >> 32), stream, tensor, k0, k1);
-    const bool odd = lane & 1u;
-    const uint32_t g0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? r.x : r.z, 1);
-    const uint32_t g1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? r.y : r.w, 1);
-    w[0][0] = odd ? g0 : r.x;
-    w[0][1] = odd ? g1 : r.y;
-    w[1][0] = odd ? r.z : g0;
-    w[1][1] = odd ? r.w : g1;
-}
-
-// Encodes one moment's block: the scale, then the lane's two words of four codes
-__device__ __forceinline__ void encode_block(const float (&x)[8], uint32_t (&codes)[2], float& scale, bool sr,
-                                             uint64_t block_base, uint32_t stream, uint32_t tensor, uint32_t k0,
-                                             uint32_t k1) {
-    uint32_t top = 0;
+// Decodes the four codes of a word times `scale`, one rounding each.  A code's exponent and mantissa
+// fields, placed at fp32's, read as its value times 2^-120 (subnormals too), and scale * 2^120 is exact;
+// where that leaves the fp32 range, or a code is NaN, the power of two is applied to the code first.
+template <bool SIGNED>
+__device__ __forceinline__ void decode4(uint32_t w, float scale, float* x) {
+    const float s = __fmul_rn(scale, 0x1p120f);
+    const bool nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    const bool rare = nan || !(fabsf(scale) < 128.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    top = __reduce_max_sync(0xFFFFFFFFu, top);   // magnitudes order as integers, NaN above Inf above the rest
-    const bool finite = top < 0x7F800000u, held = finite && top >= 0x0D800000u;   // 2^-100
-    const float amax = __uint_as_float(top);
-    scale = held ? __fmul_rn(amax, 1.0f / 448.0f) : finite ? 0.0f : __uint_as_float(0x7FC00000u);
-    const float per = held ? __fmul_rn(448.0f, __frcp_rn(amax)) : 0.0f;
-    uint32_t r[2][2] = {};
-    if (sr) quad_words(r, block_base, stream, tensor, k0, k1);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t r16 = (i & 1) ? r[j][i >> 1] >> 16 : r[j][i >> 1] & 0xFFFFu;
-            const float v = finite ? x[4 * j + i] : 0.0f;
-            c |= e4m3_encode(v, per, sr, r16) << (8 * i);
+    for (int i = 0; i < 4; ++i) {
+        uint32_t bits;
+        if (SIGNED)
+            bits = (uint32_t)((int32_t)(w << (24 - 8 * i)) >> 4) & 0x87F00000u;
+        else
+            bits = (i == 3 ? w >> 4 : w << (20 - 8 * i)) & 0x07F00000u;
+        if (!rare) {
+            x[i] = __fmul_rn(__uint_as_float(bits), s);
+        } else {
+            const bool n = (bits & 0x07F00000u) == 0x07F00000u;
+            x[i] = __fmul_rn(n ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float(bits), 0x1p120f), scale);
         }
-        codes[j] = c;
     }
 }
 
-template <bool FP8, int CAP>
-__global__ void __launch_bounds__(kAdamThreads)
+// E4M3 code of u = |x| * per (per = 448 * (1 / amax) of the block), unsigned, in bits 20-26: u * 2^-120
+// has the code's fields at fp32's (below 2^-6 it is an fp32 subnormal, rounded to the step that
+// u + 2^-6 would have).  Adding `cut` to the 20 bits that are cut off carries into the code where it
+// rounds up: 2^20 - 1 - 16 r16 does so iff r16 < f * 2^16 (f = the cut-off bits / 2^20), half a
+// step less the parity bit gives nearest even.
+template <bool SR>
+__device__ __forceinline__ uint32_t e4m3_encode(float x, float per, uint32_t cut) {
+    const uint32_t bits = __float_as_uint(__fmul_rn(__fmul_rn(fabsf(x), per), 0x1p-120f));
+    if (!SR) cut = 0x7FFFFu + ((bits >> 20) & 1u);
+    return min((bits + cut) >> 20, 0x7Eu);
+}
+
+// The Philox words of a lane's two element quads.  A block of four words serves eight consecutive
+// elements, i.e. the quads of two neighbouring lanes: the even lane computes the block of the pair's
+// j = 0 quads, the odd lane that of the j = 1 quads, and each hands the other half over.
+__device__ __forceinline__ void quad_words(uint32_t (&w)[2][2], uint64_t block_base, uint32_t stream, uint32_t tensor,
+                                           const uint32_t* key0, const uint32_t* key1) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t g = (block_base + 4u * (lane & ~1u) + 128u * (lane & 1u)) >> 3;
+    uint32_t c0 = (uint32_t)g, c1 = (uint32_t)(g >> 32), c2 = stream, c3 = tensor;
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
+        const uint32_t n0 = (uint32_t)(p1 >> 32) ^ c1 ^ key0[r], n2 = (uint32_t)(p0 >> 32) ^ c3 ^ key1[r];
+        c1 = (uint32_t)p1;
+        c3 = (uint32_t)p0;
+        c0 = n0;
+        c2 = n2;
+    }
+    const bool odd = lane & 1u;
+    const uint32_t h0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? c0 : c2, 1);
+    const uint32_t h1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? c1 : c3, 1);
+    w[0][0] = odd ? h0 : c0;
+    w[0][1] = odd ? h1 : c1;
+    w[1][0] = odd ? c2 : h0;
+    w[1][1] = odd ? c3 : h1;
+}
+
+// max(a, |b|, |c|), a >= 0, NaN where there is one
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
+}
+
+// Encodes one moment's block: the scale, then the lane's two words of four codes
+template <bool SR, bool SIGNED>
+__device__ __forceinline__ void encode_block(const float (&x)[8], uint32_t (&codes)[2], float& scale, uint64_t block_base,
+                                             uint32_t stream, uint32_t tensor, const uint32_t* key0,
+                                             const uint32_t* key1) {
+    float t0 = max3_abs_nan(fabsf(x[0]), x[1], x[2]), t1 = max3_abs_nan(fabsf(x[3]), x[4], x[5]);
+    t0 = max3_abs_nan(t0, x[6], x[7]);
+    uint32_t top = __float_as_uint(max3_abs_nan(t0, t1, t1)) & 0x7FFFFFFFu;
+    top = __reduce_max_sync(0xFFFFFFFFu, top);   // magnitudes order as integers, NaN above Inf above the rest
+    if (top >= 0x7F800000u) {
+        scale = __uint_as_float(0x7FC00000u);
+        codes[0] = codes[1] = 0u;
+        return;
+    }
+    const bool held = top >= 0x0D800000u;   // 2^-100
+    const float amax = __uint_as_float(top);
+    scale = held ? __fmul_rn(amax, 1.0f / 448.0f) : 0.0f;
+    const float per = held ? __fmul_rn(448.0f, __frcp_rn(amax)) : 0.0f;
+    uint32_t r[2][2] = {};
+    if (SR) quad_words(r, block_base, stream, tensor, key0, key1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // 2^20 - 1 - 16 r16 = 16 (r16's complement) + 15
+            const uint32_t n = ~r[j][i >> 1];
+            const uint32_t cut = (i & 1) ? (n >> 12) | 15u : ((n << 4) & 0xFFFF0u) | 15u;
+            c[i] = e4m3_encode<SR>(x[4 * j + i], per, cut);
+        }
+        codes[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        if (SIGNED) {
+            const uint32_t s01 = __byte_perm(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]), 0x0073);
+            const uint32_t s23 = __byte_perm(__float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]), 0x0073);
+            codes[j] |= __byte_perm(s01, s23, 0x5410) & 0x80808080u;
+        }
+    }
+}
+
+// The step's scalars and the tensor's constants as one chunk uses them
+struct StepValues {
+    float keep, size, fix, gs;
+};
+
+// This thread's places in the current chunk of a tensor: lane l of a warp owns elements 4 l + 128 j +
+// (0..3), j = 0, 1, of the warp's block.  They advance by whole chunks.
+template <bool FP8>
+struct Places {
+    float* p;
+    const uint8_t* g;
+    uint16_t* w;
+    uint8_t *m, *v;            // fp32, or codes
+    float *m_scale, *v_scale;  // of the warp's block
+    bool g_bf16;
+    __device__ __forceinline__ Places(const AdamwEntry& e, int64_t chunk) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int64_t at = chunk * kAdamChunk + warp * kAdamBlock + 4 * lane;
+        g_bf16 = e.index_g & 1;
+        p = e.p + at;
+        g = reinterpret_cast<const uint8_t*>(e.g) + at * (g_bf16 ? 2 : 4);
+        w = e.w ? e.w + at : nullptr;
+        m = reinterpret_cast<uint8_t*>(e.m) + at * (FP8 ? 1 : 4);
+        v = reinterpret_cast<uint8_t*>(e.v) + at * (FP8 ? 1 : 4);
+        m_scale = e.m_scale + chunk * (kAdamChunk / kAdamBlock) + warp;
+        v_scale = e.v_scale + chunk * (kAdamChunk / kAdamBlock) + warp;
+    }
+    __device__ __forceinline__ void next() {
+        p += kAdamChunk;
+        g += kAdamChunk * (g_bf16 ? 2 : 4);
+        if (w) w += kAdamChunk;
+        m += kAdamChunk * (FP8 ? 1 : 4);
+        v += kAdamChunk * (FP8 ? 1 : 4);
+        if (FP8) {
+            m_scale += kAdamChunk / kAdamBlock;
+            v_scale += kAdamChunk / kAdamBlock;
+        }
+    }
+};
+
+// One warp's block.  FULL: all its 256 elements are there; otherwise `left` (> 0) of them, counted
+// from the block's first.  `first` is the block's first element's index, for the random fields.
+template <bool FP8, bool SR, bool FULL>
+__device__ __forceinline__ void block_step(const Places<FP8>& at, int64_t first, int left, uint32_t tensor, const AdamwScalars& sc,
+                                           const StepValues& sv, const uint32_t* key0, const uint32_t* key1, bool amax,
+                                           uint32_t& am) {
+    const int lane = threadIdx.x & 31;
+    const auto in = [&](int i) { return FULL || 4 * lane + 128 * (i >> 2) + (i & 3) < left; };
+    const auto off = [](int i) { return 128 * (i >> 2) + (i & 3); };
+    float p[8], g[8], m[8], v[8];
+    uint32_t mc[2] = {0u, 0u}, vc[2] = {0u, 0u};   // codes of the 8-bit moments
+    if (FULL) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 x = *reinterpret_cast<const float4*>(at.p + 128 * j);
+            p[4 * j] = x.x; p[4 * j + 1] = x.y; p[4 * j + 2] = x.z; p[4 * j + 3] = x.w;
+            if (at.g_bf16) {
+                const uint2 y = *reinterpret_cast<const uint2*>(at.g + 256 * j);
+                g[4 * j] = bf16_lo(y.x); g[4 * j + 1] = bf16_hi(y.x); g[4 * j + 2] = bf16_lo(y.y); g[4 * j + 3] = bf16_hi(y.y);
+            } else {
+                const float4 y = *reinterpret_cast<const float4*>(at.g + 512 * j);
+                g[4 * j] = y.x; g[4 * j + 1] = y.y; g[4 * j + 2] = y.z; g[4 * j + 3] = y.w;
+            }
+            if (FP8) {
+                mc[j] = *reinterpret_cast<const uint32_t*>(at.m + 128 * j);
+                vc[j] = *reinterpret_cast<const uint32_t*>(at.v + 128 * j);
+            } else {
+                const float4 a = *reinterpret_cast<const float4*>(at.m + 512 * j);
+                const float4 b = *reinterpret_cast<const float4*>(at.v + 512 * j);
+                m[4 * j] = a.x; m[4 * j + 1] = a.y; m[4 * j + 2] = a.z; m[4 * j + 3] = a.w;
+                v[4 * j] = b.x; v[4 * j + 1] = b.y; v[4 * j + 2] = b.z; v[4 * j + 3] = b.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool ok = in(i);
+            p[i] = ok ? at.p[off(i)] : 0.0f;
+            g[i] = !ok ? 0.0f : at.g_bf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(at.g)[off(i)] << 16)
+                                          : reinterpret_cast<const float*>(at.g)[off(i)];
+            if (FP8) {
+                mc[i >> 2] |= (ok ? at.m[off(i)] : 0u) << (8 * (i & 3));
+                vc[i >> 2] |= (ok ? at.v[off(i)] : 0u) << (8 * (i & 3));
+            } else {
+                m[i] = ok ? reinterpret_cast<const float*>(at.m)[off(i)] : 0.0f;
+                v[i] = ok ? reinterpret_cast<const float*>(at.v)[off(i)] : 0.0f;
+            }
+        }
+    }
+    if (FP8) {
+        const float ms = *at.m_scale, vs = *at.v_scale;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            decode4<true>(mc[j], ms, m + 4 * j);
+            decode4<false>(vc[j], vs, v + 4 * j);   // the root
+        }
+        if (!FULL) {   // a NaN scale stays out of the padding
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (!in(i)) m[i] = v[i] = 0.0f;
+        }
+    }
+    // Products on pairs (an f32x2 product is two single IEEE products), sums one by one: a pair's
+    // product that feeds a pair's sum would be fused with it, whatever the flags.
+    float root[8];
+    const uint64_t gs2 = f2c(sv.gs), b1 = f2c(sc.beta1), nb1 = f2c(sc.one_beta1), b2 = f2c(sc.beta2), nb2 = f2c(sc.one_beta2);
+    const uint64_t fix2 = f2c(sv.fix), keep2 = f2c(sv.keep), size2 = f2c(sv.size);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        float x0, x1, y0, y1;
+        const uint64_t gi = f2_mul(f2(g[i], g[i + 1]), gs2);
+        f2_split(f2_mul(f2(m[i], m[i + 1]), b1), x0, x1);
+        f2_split(f2_mul(gi, nb1), y0, y1);
+        m[i] = __fadd_rn(x0, y0);
+        m[i + 1] = __fadd_rn(x1, y1);
+        uint64_t vi = f2(v[i], v[i + 1]);
+        if (FP8) vi = f2_mul(vi, vi);
+        f2_split(f2_mul(vi, b2), x0, x1);
+        f2_split(f2_mul(f2_mul(gi, nb2), gi), y0, y1);
+        v[i] = __fadd_rn(x0, y0);
+        v[i + 1] = __fadd_rn(x1, y1);
+        root[i] = __fsqrt_rn(v[i]);
+        root[i + 1] = __fsqrt_rn(v[i + 1]);
+        f2_split(f2_mul(f2(root[i], root[i + 1]), fix2), x0, x1);
+        const uint64_t q = f2(__fdiv_rn(m[i], __fadd_rn(x0, sc.eps)), __fdiv_rn(m[i + 1], __fadd_rn(x1, sc.eps)));
+        f2_split(f2_mul(f2(p[i], p[i + 1]), keep2), x0, x1);
+        f2_split(f2_mul(q, size2), y0, y1);
+        p[i] = __fsub_rn(x0, y0);
+        p[i + 1] = __fsub_rn(x1, y1);
+    }
+    // p and w leave at once: the encode below needs their registers
+    uint32_t wb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wb[i] = f32x2_to_bf16x2(p[2 * i], p[2 * i + 1]);
+    if (FULL) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            *reinterpret_cast<float4*>(at.p + 128 * j) = make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+            if (at.w) *reinterpret_cast<uint2*>(at.w + 128 * j) = make_uint2(wb[2 * j], wb[2 * j + 1]);
+            if (!FP8) {
+                *reinterpret_cast<float4*>(at.m + 512 * j) = make_float4(m[4 * j], m[4 * j + 1], m[4 * j + 2], m[4 * j + 3]);
+                *reinterpret_cast<float4*>(at.v + 512 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (!in(i)) continue;
+            at.p[off(i)] = p[i];
+            if (at.w) at.w[off(i)] = (uint16_t)(wb[i >> 1] >> (16 * (i & 1)));
+            if (!FP8) {
+                reinterpret_cast<float*>(at.m)[off(i)] = m[i];
+                reinterpret_cast<float*>(at.v)[off(i)] = v[i];
+            }
+        }
+    }
+    if (amax) {
+        // elements past the end are masked: their p is 0 - 0 * size, or NaN where eps = 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t b = (wb[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+            am = max(am, in(i) ? b : 0u);
+        }
+    }
+    if (FP8) {
+        float ms, vs;
+        encode_block<SR, true>(m, mc, ms, (uint64_t)first, kStreamMoment1, tensor, key0, key1);
+        encode_block<SR, false>(root, vc, vs, (uint64_t)first, kStreamMoment2, tensor, key0, key1);
+        if (lane == 0) {
+            *at.m_scale = ms;
+            *at.v_scale = vs;
+        }
+        if (FULL) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                *reinterpret_cast<uint32_t*>(at.m + 128 * j) = mc[j];
+                *reinterpret_cast<uint32_t*>(at.v + 128 * j) = vc[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!in(i)) continue;
+                at.m[off(i)] = (uint8_t)(mc[i >> 2] >> (8 * (i & 3)));
+                at.v[off(i)] = (uint8_t)(vc[i >> 2] >> (8 * (i & 3)));
+            }
+        }
+    }
+}
+
+template <bool FP8>
+constexpr int kAdamResident = FP8 ? 4 : 4;   // CTAs per SM
+
+// DYN: the step's values and the seed are read from device memory
+template <bool FP8, bool SR, bool DYN, int CAP>
+__global__ void __launch_bounds__(kAdamThreads, kAdamResident<FP8>)
     adamw_kernel(const __grid_constant__ AdamwTable<CAP> tab, const AdamwScalars sc, uint32_t* flags) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t c0 = (uint32_t)((uint64_t)tab.chunks * blockIdx.x / gridDim.x);
     const uint32_t c1 = (uint32_t)((uint64_t)tab.chunks * (blockIdx.x + 1) / gridDim.x);
     if (c0 >= c1) return;
-    float keep = sc.keep, size = sc.step_size, fix = sc.v_fix, gs = sc.grad_scale;
-    uint32_t k0 = (uint32_t)sc.sr_seed, k1 = (uint32_t)(sc.sr_seed >> 32);
-    if (sc.dynamic) {
+    StepValues sv{sc.keep, sc.step_size, sc.v_fix, sc.grad_scale};
+    PhiloxKeys dyn_keys;
+    if (DYN) {
         const float4 d = __ldg(reinterpret_cast<const float4*>(sc.dynamic));
         const uint2 k = __ldg(reinterpret_cast<const uint2*>(sc.dynamic) + 2);
-        keep = d.x;
-        size = d.y;
-        fix = d.z;
-        gs = d.w;
-        k0 = k.x;
-        k1 = k.y;
+        sv = StepValues{d.x, d.y, d.z, d.w};
+        dyn_keys = philox_keys((uint64_t)k.y << 32 | k.x);
     }
+    const uint32_t *key0 = DYN ? dyn_keys.k0 : tab.key0, *key1 = DYN ? dyn_keys.k1 : tab.key1;
     // the tensor of chunk c0: the last entry whose first chunk is <= c0 (every entry has chunks)
     int ti = 0;
     for (int lo = 0, hi = tab.count; hi - lo > 1;) {
@@ -127,140 +359,24 @@ __global__ void __launch_bounds__(kAdamThreads)
         if (tab.t[mid].first_chunk <= c0) lo = mid; else hi = mid;
         ti = lo;
     }
-    uint32_t am = 0;   // |w| bits of this thread's elements of the current tensor
-    for (uint32_t c = c0; c < c1; ++c) {
-        while (ti + 1 < tab.count && tab.t[ti + 1].first_chunk <= c) ++ti;
+    for (uint32_t c = c0; c < c1; ++ti) {   // this CTA's run, tensor by tensor
         const AdamwEntry& e = tab.t[ti];
-        const int64_t base = (int64_t)(c - e.first_chunk) * kAdamChunk + warp * kAdamBlock;
+        const uint32_t end = min(c1, ti + 1 < tab.count ? tab.t[ti + 1].first_chunk : tab.chunks);
+        const uint32_t tensor = (uint32_t)e.index_g >> 1;
+        const bool amax = e.amax != nullptr;
         const int64_t n = e.n;
-        if (base < n) {
-            const bool full = base + kAdamBlock <= n;
-            const int64_t at = base + 4 * lane;
-            float p[8], g[8], m[8], v[8];
-            if (full) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float4 x = *reinterpret_cast<const float4*>(e.p + at + 128 * j);
-                    p[4 * j] = x.x; p[4 * j + 1] = x.y; p[4 * j + 2] = x.z; p[4 * j + 3] = x.w;
-                    if ((e.index_g & 1)) {
-                        const uint2 y = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(e.g) + at + 128 * j);
-                        g[4 * j] = bf16_lo(y.x); g[4 * j + 1] = bf16_hi(y.x); g[4 * j + 2] = bf16_lo(y.y); g[4 * j + 3] = bf16_hi(y.y);
-                    } else {
-                        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(e.g) + at + 128 * j);
-                        g[4 * j] = y.x; g[4 * j + 1] = y.y; g[4 * j + 2] = y.z; g[4 * j + 3] = y.w;
-                    }
-                    if (!FP8) {
-                        const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(e.m) + at + 128 * j);
-                        const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(e.v) + at + 128 * j);
-                        m[4 * j] = a.x; m[4 * j + 1] = a.y; m[4 * j + 2] = a.z; m[4 * j + 3] = a.w;
-                        v[4 * j] = b.x; v[4 * j + 1] = b.y; v[4 * j + 2] = b.z; v[4 * j + 3] = b.w;
-                    } else {
-                        const uint32_t a = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(e.m) + at + 128 * j);
-                        const uint32_t b = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(e.v) + at + 128 * j);
-                        e4m3x2_decode(a, m[4 * j], m[4 * j + 1]);
-                        e4m3x2_decode(a >> 16, m[4 * j + 2], m[4 * j + 3]);
-                        e4m3x2_decode(b, v[4 * j], v[4 * j + 1]);
-                        e4m3x2_decode(b >> 16, v[4 * j + 2], v[4 * j + 3]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t k = at + 128 * (i >> 2) + (i & 3);
-                    const bool in = k < n;
-                    p[i] = in ? e.p[k] : 0.0f;
-                    g[i] = !in ? 0.0f : (e.index_g & 1) ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(e.g)[k] << 16)
-                                                 : reinterpret_cast<const float*>(e.g)[k];
-                    if (!FP8) {
-                        m[i] = in ? reinterpret_cast<const float*>(e.m)[k] : 0.0f;
-                        v[i] = in ? reinterpret_cast<const float*>(e.v)[k] : 0.0f;
-                    } else {
-                        float unused;
-                        e4m3x2_decode(in ? reinterpret_cast<const uint8_t*>(e.m)[k] : 0u, m[i], unused);
-                        e4m3x2_decode(in ? reinterpret_cast<const uint8_t*>(e.v)[k] : 0u, v[i], unused);
-                    }
-                }
-            }
-            if (FP8) {
-                const float ms = e.m_scale[base / kAdamBlock], vs = e.v_scale[base / kAdamBlock];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool in = full || at + 128 * (i >> 2) + (i & 3) < n;   // a NaN scale stays out of the padding
-                    m[i] = in ? __fmul_rn(m[i], ms) : 0.0f;
-                    const float r = in ? __fmul_rn(v[i], vs) : 0.0f;
-                    v[i] = __fmul_rn(r, r);
-                }
-            }
-            float root[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float gi = __fmul_rn(g[i], gs);
-                m[i] = __fadd_rn(__fmul_rn(m[i], sc.beta1), __fmul_rn(gi, sc.one_beta1));
-                v[i] = __fadd_rn(__fmul_rn(v[i], sc.beta2), __fmul_rn(__fmul_rn(gi, sc.one_beta2), gi));
-                root[i] = __fsqrt_rn(v[i]);
-                const float q = __fdiv_rn(m[i], __fadd_rn(__fmul_rn(root[i], fix), sc.eps));
-                p[i] = __fsub_rn(__fmul_rn(p[i], keep), __fmul_rn(q, size));
-            }
-            uint32_t wb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) wb[i] = f32x2_to_bf16x2(p[2 * i], p[2 * i + 1]);
-            uint32_t mc[2], vc[2];
-            if (FP8) {
-                float ms, vs;
-                const uint32_t tensor = (uint32_t)e.index_g >> 1;
-                encode_block(m, mc, ms, sc.sr, (uint64_t)base, kStreamMoment1, tensor, k0, k1);
-                encode_block(root, vc, vs, sc.sr, (uint64_t)base, kStreamMoment2, tensor, k0, k1);
-                if (lane == 0) {
-                    e.m_scale[base / kAdamBlock] = ms;
-                    e.v_scale[base / kAdamBlock] = vs;
-                }
-            }
-            if (full) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    *reinterpret_cast<float4*>(e.p + at + 128 * j) = make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-                    if (e.w) *reinterpret_cast<uint2*>(e.w + at + 128 * j) = make_uint2(wb[2 * j], wb[2 * j + 1]);
-                    if (!FP8) {
-                        *reinterpret_cast<float4*>(reinterpret_cast<float*>(e.m) + at + 128 * j) =
-                            make_float4(m[4 * j], m[4 * j + 1], m[4 * j + 2], m[4 * j + 3]);
-                        *reinterpret_cast<float4*>(reinterpret_cast<float*>(e.v) + at + 128 * j) =
-                            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                    } else {
-                        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(e.m) + at + 128 * j) = mc[j];
-                        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(e.v) + at + 128 * j) = vc[j];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t k = at + 128 * (i >> 2) + (i & 3);
-                    if (k >= n) continue;
-                    e.p[k] = p[i];
-                    if (e.w) e.w[k] = (uint16_t)(wb[i >> 1] >> (16 * (i & 1)));
-                    if (!FP8) {
-                        reinterpret_cast<float*>(e.m)[k] = m[i];
-                        reinterpret_cast<float*>(e.v)[k] = v[i];
-                    } else {
-                        reinterpret_cast<uint8_t*>(e.m)[k] = (uint8_t)(mc[i >> 2] >> (8 * (i & 3)));
-                        reinterpret_cast<uint8_t*>(e.v)[k] = (uint8_t)(vc[i >> 2] >> (8 * (i & 3)));
-                    }
-                }
-            }
-            if (e.amax) {
-                // elements past n hold p = 0 - 0 * size: no effect on the maximum (or NaN, from
-                // eps = 0, so they are masked)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool in = full || at + 128 * (i >> 2) + (i & 3) < n;
-                    const uint32_t b = (wb[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
-                    am = max(am, in ? b : 0u);
-                }
-            }
+        Places<FP8> at(e, c - e.first_chunk);
+        int64_t first = (int64_t)(c - e.first_chunk) * kAdamChunk + warp * kAdamBlock;
+        uint32_t am = 0;   // |w| bits of this thread's elements
+#pragma unroll 1
+        for (; c < end; ++c, first += kAdamChunk, at.next()) {
+            if (first + kAdamBlock <= n)
+                block_step<FP8, SR, true>(at, first, kAdamBlock, tensor, sc, sv, key0, key1, amax, am);
+            else if (first < n)
+                block_step<FP8, SR, false>(at, first, (int)(n - first), tensor, sc, sv, key0, key1, amax, am);
         }
-        // the run of this tensor ends here: its maximum so far
-        if (e.amax && (c + 1 == c1 || (ti + 1 < tab.count && tab.t[ti + 1].first_chunk == c + 1))) {
+        if (amax) {
             const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, am);
-            am = 0;
             if (lane == 0 && top) {
                 atomicMax(e.amax, top << 16);
                 if (top >= 0x7F80u) atomicOr(flags, kFlagNonFinite);
@@ -282,7 +398,7 @@ static int sm_count_adamw() {
     return n;
 }
 
-template <bool FP8, int CAP>
+template <bool FP8, bool SR, bool DYN, int CAP>
 static cudaError_t launch_table(const AdamwEntry* entries, int count, const AdamwScalars& sc,
                                 uint32_t* flags, cudaStream_t s) {
     AdamwTable<CAP> tab;
@@ -297,20 +413,36 @@ static cudaError_t launch_table(const AdamwEntry* entries, int count, const Adam
     if (chunks > 0xFFFFFFFFull) return cudaErrorInvalidValue;
     tab.count = count;
     tab.chunks = (uint32_t)chunks;
+    for (int r = 0; r < 10; ++r) {   // Weyl sequences of the seed's two words
+        tab.key0[r] = (uint32_t)sc.sr_seed + 0x9E3779B9u * r;
+        tab.key1[r] = (uint32_t)(sc.sr_seed >> 32) + 0xBB67AE85u * r;
+    }
     if (any_amax) adamw_reset_amax_kernel<CAP><<<(CAP + 127) / 128, 128, 0, s>>>(tab);
-    const uint64_t most = (uint64_t)sm_count_adamw() * 4;
-    adamw_kernel<FP8, CAP><<<(unsigned)std::min<uint64_t>(chunks, most), kAdamThreads, 0, s>>>(tab, sc, flags);
+    const uint64_t most = (uint64_t)sm_count_adamw() * kAdamResident<FP8>;   // one wave: a CTA takes its whole run
+    adamw_kernel<FP8, SR, DYN, CAP><<<(unsigned)std::min<uint64_t>(chunks, most), kAdamThreads, 0, s>>>(tab, sc, flags);
     return cudaGetLastError();
 }
 
-cudaError_t launch_adamw(const AdamwEntry* entries, int count, bool fp8, const AdamwScalars& sc, uint32_t* flags, cudaStream_t s) {
+template <bool FP8, bool SR, int CAP>
+static cudaError_t launch_values(const AdamwEntry* entries, int count, const AdamwScalars& sc, uint32_t* flags, cudaStream_t s) {
+    return sc.dynamic ? launch_table<FP8, SR, true, CAP>(entries, count, sc, flags, s)
+                      : launch_table<FP8, SR, false, CAP>(entries, count, sc, flags, s);
+}
+
+template <int CAP>
+static cudaError_t launch_state(const AdamwEntry* entries, int count, bool fp8, const AdamwScalars& sc, uint32_t* flags,
+                                cudaStream_t s) {
+    if (!fp8) return launch_values<false, false, CAP>(entries, count, sc, flags, s);
+    return sc.sr ? launch_values<true, true, CAP>(entries, count, sc, flags, s)
+                 : launch_values<true, false, CAP>(entries, count, sc, flags, s);
+}
+
+cudaError_t launch_adamw(const AdamwEntry* entries, int count, bool fp8, const AdamwScalars& sc, uint32_t* flags,
+                         cudaStream_t s) {
     if (count < 1 || count > kAdamMaxTensors) return cudaErrorInvalidValue;
     // two table sizes: a launch copies its whole parameter block (80 bytes per tensor)
-    if (count <= 16)
-        return fp8 ? launch_table<true, 16>(entries, count, sc, flags, s)
-                   : launch_table<false, 16>(entries, count, sc, flags, s);
-    return fp8 ? launch_table<true, kAdamMaxTensors>(entries, count, sc, flags, s)
-               : launch_table<false, kAdamMaxTensors>(entries, count, sc, flags, s);
+    return count <= 16 ? launch_state<16>(entries, count, fp8, sc, flags, s)
+                       : launch_state<kAdamMaxTensors>(entries, count, fp8, sc, flags, s);
 }
 
 }  // namespace nvfp4

@@ -22,6 +22,7 @@ SOURCES = {
     "glue.cu": [],
     "adamw.cu": ["-fmad=false"],
     "grouped.cu": [],
+    "grouped_few.cu": [],
     "noalloc.cu": [],
 }
 HEADERS = ["nvfp4_device.cuh", "nvfp4_internal.h", "sm100_ptx.cuh"]

@@ -72,7 +72,7 @@ struct GroupedSmem {        // behind the stages
     uint32_t tmem, abort, issued, tails;
     uint32_t stage_tx[kGStages]; // bytes per CTA of the last use of each stage, 0: a tail
     int32_t width;               // Q rows per tile at most
-    int32_t pad;
+    float cost[5];
     int32_t row[kMaxExperts + 4];    // expert e owns rows [row[e], row[e + 1])
     int32_t tile[kMaxExperts + 4];   // and tiles [tile[e], tile[e + 1])
 };
@@ -152,16 +152,23 @@ struct Walk {
     }
 };
 
-// Fills sm.row, sm.tile and sm.width from the offsets (one warp; raw offsets are in sm.row)
+// Rows per tile of fprop and dgrad are the best of kWidths by the plan below
+constexpr int kWidths = 5;   // 256, 224, ... 128
+
+// Warp w < kWidths: the offsets' running maximum (warp 0 writes sm.row), and the cost of a width of
+// 256 - 32 w: waves of tiles over the pairs times a tile's operand rows (256 features and its own
+// rows, evenly cut), since a stage takes the time its operands need from L2.
 template <int MODE>
-__device__ void plan_tiles(GroupedSmem& sm, const GroupedParams& p, int pairs) {
-    const int lane = threadIdx.x & 31;
-    int carry = 0;
+__device__ __forceinline__ void plan_rows(GroupedSmem& sm, const GroupedParams& p, int pairs) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float width = 256.0f - 32.0f * warp, inv = 1.0f / width;
+    int carry = 0, tiles = 0;
+    float rows = 0.0f;
     bool bad = false;
     for (int i = lane; i - lane <= p.experts; i += 32) {
         const bool in = i <= p.experts;
-        const int o = in ? sm.row[i] : 0;
-        int v = min(max(o, 0), p.rows);
+        const int o = in ? __ldg(p.offsets + i) : 0;
+        int v = in ? min(max(o, 0), p.rows) : 0;
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
             const int u = __shfl_up_sync(0xFFFFFFFFu, v, s);
@@ -169,40 +176,43 @@ __device__ void plan_tiles(GroupedSmem& sm, const GroupedParams& p, int pairs) {
         }
         v = max(v, carry);
         bad |= in && o != v;
-        if (in) sm.row[i] = v;
-        carry = __shfl_sync(0xFFFFFFFFu, v, 31);
-    }
-    if (bad && blockIdx.x == 0) atomicOr(p.flags, kFlagOffsets);
-    __syncwarp();
-    const int np = ceil_div(p.P, 256);
-    int width = 256;
-    if (MODE != kWgrad) {
-        // Rows per tile: of 256, 224, ... 128 the one with the shortest schedule: waves of tiles over the
-        // pairs times a tile's operand rows (256 features and its own rows, evenly cut), since a stage
-        // takes the time its operands need from L2
-        float best = 3.0e38f;
-#pragma unroll 1
-        for (int w = 256; w >= 128; w -= 32) {
-            int tiles = 0;
-            float rows = 0.0f;
-            const float inv = 1.0f / (float)w;
-            for (int e = lane; e < p.experts; e += 32) {
-                const int len = sm.row[e + 1] - sm.row[e];
+        if (warp == 0 && in) sm.row[i] = v;
+        if (MODE != kWgrad) {   // the run that ends at this offset
+            int len = v - __shfl_up_sync(0xFFFFFFFFu, v, 1);
+            if (lane == 0) len = i == 0 ? 0 : v - carry;
+            if (in && len > 0) {
                 const float nt = ceilf((float)len * inv);
                 tiles += (int)nt;
-                if (len > 0) rows += nt * (32.0f * ceilf((float)len / (32.0f * nt)));
-            }
-            tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) rows += __shfl_xor_sync(0xFFFFFFFFu, rows, s);
-            const float cost = ceilf((float)tiles * np / pairs) * (256.0f + rows / fmaxf((float)tiles, 1.0f));
-            if (cost < best) {
-                best = cost;
-                width = w;
+                rows += nt * (32.0f * ceilf((float)len / (32.0f * nt)));
             }
         }
+        carry = __shfl_sync(0xFFFFFFFFu, v, 31);
     }
-    const int nq_wgrad = MODE == kWgrad ? ceil_div(p.Q, 256) : 0;
+    if (warp == 0 && bad && blockIdx.x == 0) atomicOr(p.flags, kFlagOffsets);
+    if (MODE != kWgrad) {
+        tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) rows += __shfl_xor_sync(0xFFFFFFFFu, rows, s);
+        if (lane == 0)
+            sm.cost[warp] = ceilf((float)tiles * ceil_div(p.P, 256) / pairs) * (256.0f + rows / fmaxf((float)tiles, 1.0f));
+    }
+}
+
+// Warp 0, after plan_rows: the width, and the experts' first tiles
+template <int MODE>
+__device__ __forceinline__ void plan_tiles(GroupedSmem& sm, const GroupedParams& p) {
+    const int lane = threadIdx.x & 31;
+    int width = 256;
+    if (MODE != kWgrad) {
+        float best = sm.cost[0];
+#pragma unroll
+        for (int w = 1; w < kWidths; ++w)
+            if (sm.cost[w] < best) {
+                best = sm.cost[w];
+                width = 256 - 32 * w;
+            }
+    }
+    const int np = ceil_div(p.P, 256), nq_wgrad = MODE == kWgrad ? ceil_div(p.Q, 256) : 0;
     int total = 0;
     for (int i = lane; i - lane < p.experts; i += 32) {
         int c = 0;
@@ -237,8 +247,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
-    for (int i = threadIdx.x; i <= p.experts; i += S::kThreads) sm.row[i] = p.offsets[i];
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 8 * 32) {
         for (int s = 0; s < kGStages; ++s) {
             mbar_init(smem_u32(&sm.full[s]), MODE == kWgrad ? 2 : 1);
             mbar_init(smem_u32(&sm.empty[s]), 1);
@@ -258,13 +267,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         prefetch_map(S::kPmn ? &maps.p_wide : &maps.p);
         prefetch_map(S::kQmn ? &maps.q_wide : &maps.q[2]);
     }
-    if (warp == 1) {
+    if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    __syncthreads();
-    if (warp == 0) plan_tiles<MODE>(sm, p, pairs);
+    if (warp < (MODE == kWgrad ? 1 : kWidths)) plan_rows<MODE>(sm, p, pairs);
+    if (MODE != kWgrad) __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        plan_tiles<MODE>(sm, p);
+    }
     tc_fence_before();
     cluster_sync_all();   // both CTAs' barriers, TMEM and plans are there
     tc_fence_after();
@@ -410,9 +423,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             const Tile c = walk.get(t);
             const int stages = ceil_div(c.klen, 64);
             const bool mine = c0 < c.qn;
+            const int n = min(64, c.qn - c0);
+            const int f = c.p0 + (int)rank * 128 + q * 32 + lane;
+            const int64_t at = (MODE == kWgrad ? c.e * p.stride_d : 0) + (int64_t)(c.q0 + c0) * p.ldd;
             float acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+            if (MODE == kWgrad && p.accumulate && f < p.P) {
+                // added to what D holds: read while the products are under way (in order, so that one
+                // running address serves), and stored once
+                const float* old = reinterpret_cast<const float*>(p.d) + at + f;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    if (i < n) asm volatile("ld.global.f32 %0, [%1];" : "=f"(acc[i]) : "l"(old));
+                    old += p.ldd;
+                }
+            }
             for (int k = 0; k < stages; k += min(run, stages), ++it) {
                 const int buf = it & 1;
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, p.flags,
@@ -436,20 +462,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                 if (lane == 0) mbar_arrive(smem_u32(rank == 0 ? &sm.tempty[buf] : &sm.edrained[buf]));
             }
             if (!ok || !mine) continue;
-            const int n = min(64, c.qn - c0);
-            const int f = c.p0 + (int)rank * 128 + q * 32 + lane;
-            const int64_t at = (MODE == kWgrad ? c.e * p.stride_d : 0) + (int64_t)(c.q0 + c0) * p.ldd;
             if (MODE == kWgrad || p.out_fp32) {
                 float* d = reinterpret_cast<float*>(p.d) + at + f;
                 if (f < p.P) {
 #pragma unroll
                     for (int i = 0; i < 64; ++i) {
-                        if (i < n) {
-                            if (MODE == kWgrad && p.accumulate)
-                                atomicAdd(d, acc[i]);   // one add per element and call: no order to depend on
-                            else
-                                *d = acc[i];
-                        }
+                        if (i < n) *d = acc[i];
                         d += p.ldd;
                     }
                 }
@@ -522,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         }
     }
     cluster_sync_all();   // both CTAs are done with TMEM, barriers and each other's shared memory
-    if (warp == 1) {
+    if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
@@ -553,6 +571,8 @@ static bool mn_maps(CUtensorMap* narrow, CUtensorMap* wide, const void* x, int64
 }
 
 cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
+    // A few rows only stream the weights: the kernel without set-up (grouped_few.cu).
+    if (!g.b_kn && g.rows <= kFewMaxRows && g.experts <= kFewMaxExperts) return launch_gemm_grouped_few(g, s);
     GroupedParams p{};
     p.offsets = g.offsets;
     p.d = g.d;
