@@ -165,6 +165,11 @@ def _stream(stream=None):
     return torch.cuda.current_stream().cuda_stream
 
 
+# the current device's index without torch.cuda's initialisation check on every call; the public
+# route where this torch does not offer it
+_CUR_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -179,6 +184,7 @@ class Workspace:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.buf = torch.empty(_lib().nvfp4_workspace_bytes(), dtype=torch.uint8, device=device)
         _check(_lib().nvfp4_workspace_init(_ptr(self.buf), _stream()), "nvfp4_workspace_init")
+        self.addr = self.buf.data_ptr()
 
     @property
     def ptr(self):
@@ -567,11 +573,22 @@ class LinearBF16:
 # ---------------------------------------------------------------------------------------
 # BF16 products grouped by expert (one weight per expert, token rows sorted by expert)
 # ---------------------------------------------------------------------------------------
-def _on_current_device(*tensors):
-    dev = torch.cuda.current_device()
+def _on_current_device(*tensors) -> int:
+    """The current device's index, which every tensor has to live on."""
+    dev = _CUR_DEVICE()
     for t in tensors:
-        if t.device.type != "cuda" or t.device.index != dev:
+        if t.get_device() != dev:
             raise ValueError(f"expected tensors on the current CUDA device ({dev}), got one on {t.device}")
+    return dev
+
+
+def _call_context(dev: int, ws, stream):
+    """Addresses of the workspace and the stream of a call on device `dev`."""
+    if ws is None:
+        ws = _DEFAULT_WS.get(dev) or default_workspace()
+    if stream is not None:
+        return ws.addr, stream.cuda_stream
+    return ws.addr, _RAW_STREAM(dev) if _RAW_STREAM is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -583,7 +600,7 @@ def _empty(shape, dtype, device, stream):
 
 
 def _offsets(t: torch.Tensor, experts: int):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != experts + 1 or t.stride(0) != 1:
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != experts + 1 or t.stride(0) != 1:
         raise ValueError("offsets: contiguous int32 [experts + 1]")
 
 
@@ -593,67 +610,72 @@ def nvfp4_bf16_gemm_grouped(a: torch.Tensor, b: torch.Tensor, offsets: torch.Ten
     """out[t] = a[t] . b[e]^T (b [E][N][K]) or a[t] . b[e] (b_kn: b [E][K][N]) for the rows t in
     [offsets[e], offsets[e + 1]) of each expert e (offsets: int32 [E + 1] on the device).  Rows that
     no expert owns are left as they were in out (undefined where out is not given)."""
-    if a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16 or a.dim() != 2 or b.dim() != 3:
+    if a.dtype is not torch.bfloat16 or b.dtype is not torch.bfloat16 or a.dim() != 2 or b.dim() != 3:
         raise TypeError("expected bf16 a [rows][K] and b [E][N][K] (b_kn: [E][K][N])")
     rows, K = a.shape
-    E = b.shape[0]
-    N, Kb = (b.shape[2], b.shape[1]) if b_kn else (b.shape[1], b.shape[2])
+    E, b_rows, b_cols = b.shape
+    N, Kb = (b_cols, b_rows) if b_kn else (b_rows, b_cols)
     if Kb != K:
         raise ValueError("a and b need the same K")
-    if a.stride(1) != 1 or b.stride(2) != 1:
+    a_row, a_col = a.stride()
+    b_expert, b_row, b_col = b.stride()
+    if a_col != 1 or b_col != 1:
         raise ValueError("inner dimensions must be contiguous")
     _offsets(offsets, E)
-    _on_current_device(a, b, offsets)
+    dev = _on_current_device(a, b, offsets)
     if out is None:
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("output must be bf16 or fp32")
         out = _empty((rows, N), out_dtype, a.device, stream)
     else:
-        if out.dtype not in (torch.float32, torch.bfloat16):
+        out_dtype = out.dtype
+        if out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("output must be bf16 or fp32")
         if out.shape != (rows, N) or out.stride(1) != 1:
             raise ValueError("out: [rows][N] with a contiguous inner dimension")
         _on_current_device(out)
-    ws = ws or default_workspace()
-    st = _lib().nvfp4_bf16_gemm_grouped(a.data_ptr(), _ld(a, K), rows, offsets.data_ptr(), E, b.data_ptr(),
-                                        b.stride(1) if b.shape[1] > 1 else b.shape[2], b.stride(0) if E > 1 else 0, int(b_kn), N, K,
-                                        out.data_ptr(), _ld(out, N), OUT_FP32 if out.dtype == torch.float32 else OUT_BF16,
-                                        ws.buf.data_ptr(), _stream(stream))
-    _check(st, "nvfp4_bf16_gemm_grouped")
+    ws_addr, raw = _call_context(dev, ws, stream)
+    # a single row's or slice's stride means nothing: its width, and 0
+    st = _lib().nvfp4_bf16_gemm_grouped(a.data_ptr(), a_row if rows > 1 else K, rows, offsets.data_ptr(), E, b.data_ptr(),
+                                        b_row if b_rows > 1 else b_cols, b_expert if E > 1 else 0, 1 if b_kn else 0, N, K,
+                                        out.data_ptr(), out.stride(0) if rows > 1 else N,
+                                        OUT_FP32 if out_dtype is torch.float32 else OUT_BF16, ws_addr, raw)
+    if st:
+        _check(st, "nvfp4_bf16_gemm_grouped")
     return out
-
-
-def _ld(t: torch.Tensor, width: int) -> int:
-    """Leading dimension of a 2-D tensor; of a single row, whose stride means nothing, its width."""
-    return t.stride(0) if t.shape[0] > 1 else width
 
 
 def nvfp4_bf16_wgrad_grouped(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
                              accumulate: bool = False, ws: Workspace | None = None, stream=None) -> torch.Tensor:
     """out[e] = dy_e^T . x_e in fp32 over each expert's rows (dy [rows][n], x [rows][d], out
     [E][n][d]); an expert without rows gets zeros.  accumulate: out[e] += instead."""
-    if dy.dtype != torch.bfloat16 or x.dtype != torch.bfloat16 or dy.dim() != 2 or x.dim() != 2:
+    if dy.dtype is not torch.bfloat16 or x.dtype is not torch.bfloat16 or dy.dim() != 2 or x.dim() != 2:
         raise TypeError("expected bf16 dy [rows][n] and x [rows][d]")
     rows, M = dy.shape
-    N = x.shape[1]
-    if x.shape[0] != rows:
+    x_rows, N = x.shape
+    if x_rows != rows:
         raise ValueError("dy and x need the same rows")
-    if dy.stride(1) != 1 or x.stride(1) != 1:
+    dy_row, dy_col = dy.stride()
+    x_row, x_col = x.stride()
+    if dy_col != 1 or x_col != 1:
         raise ValueError("inner dimensions must be contiguous")
     E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
     _offsets(offsets, E)
+    dev = _on_current_device(dy, x, offsets)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out = _empty((max(E, 0), M, N), torch.float32, dy.device, stream)
-    elif out.dtype != torch.float32 or out.shape != (E, M, N) or out.stride(2) != 1:
-        raise ValueError("out: fp32 [E][n][d] with a contiguous inner dimension")
-    _on_current_device(dy, x, offsets, out)
-    ws = ws or default_workspace()
-    st = _lib().nvfp4_bf16_wgrad_grouped(dy.data_ptr(), _ld(dy, M), x.data_ptr(), _ld(x, N), rows, offsets.data_ptr(), E, M,
-                                         N, out.data_ptr(), out.stride(1) if M > 1 else N, out.stride(0) if E > 1 else 0,
-                                         int(accumulate), ws.buf.data_ptr(), _stream(stream))
-    _check(st, "nvfp4_bf16_wgrad_grouped")
+    else:
+        if out.dtype is not torch.float32 or out.shape != (E, M, N) or out.stride(2) != 1:
+            raise ValueError("out: fp32 [E][n][d] with a contiguous inner dimension")
+        _on_current_device(out)
+    ws_addr, raw = _call_context(dev, ws, stream)
+    st = _lib().nvfp4_bf16_wgrad_grouped(dy.data_ptr(), dy_row if rows > 1 else M, x.data_ptr(), x_row if rows > 1 else N, rows,
+                                         offsets.data_ptr(), E, M, N, out.data_ptr(), out.stride(1) if M > 1 else N,
+                                         out.stride(0) if E > 1 else 0, 1 if accumulate else 0, ws_addr, raw)
+    if st:
+        _check(st, "nvfp4_bf16_wgrad_grouped")
     return out
 
 
@@ -795,7 +817,8 @@ def nvfp4_adamw_step(ctx: AdamWContext, lr: float = 0.0, step: int = 1, beta1: f
     weight_decay, grad_scale and sr_seed, read when the kernel runs."""
     if ctx._count == 0:
         return
-    if ctx._device.index != torch.cuda.current_device():
+    dev = _CUR_DEVICE()
+    if ctx._device.index != dev:
         raise ValueError(f"the tensors live on {ctx._device}, which is not the current device")
     a = ctx._args
     a.lr, a.beta1, a.beta2, a.eps, a.weight_decay, a.grad_scale = lr, beta1, beta2, eps, weight_decay, grad_scale
@@ -806,8 +829,10 @@ def nvfp4_adamw_step(ctx: AdamWContext, lr: float = 0.0, step: int = 1, beta1: f
         a.dynamic = dynamic.data_ptr()
     else:
         a.dynamic = None
-    _check(_lib().nvfp4_adamw(ctx._table, ctx._count, ctx._args_ref, ctx.ws.buf.data_ptr(), _stream(stream)),
-           "nvfp4_adamw")
+    ws_addr, raw = _call_context(dev, ctx.ws, stream)
+    st = _lib().nvfp4_adamw(ctx._table, ctx._count, ctx._args_ref, ws_addr, raw)
+    if st:
+        _check(st, "nvfp4_adamw")
 
 
 # ---------------------------------------------------------------------------------------

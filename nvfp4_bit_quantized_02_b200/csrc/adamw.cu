@@ -440,9 +440,11 @@ static cudaError_t launch_state(const AdamwEntry* entries, int count, bool fp8, 
 cudaError_t launch_adamw(const AdamwEntry* entries, int count, bool fp8, const AdamwScalars& sc, uint32_t* flags,
                          cudaStream_t s) {
     if (count < 1 || count > kAdamMaxTensors) return cudaErrorInvalidValue;
-    // two table sizes: a launch copies its whole parameter block (80 bytes per tensor)
-    return count <= 16 ? launch_state<16>(entries, count, fp8, sc, flags, s)
-                       : launch_state<kAdamMaxTensors>(entries, count, fp8, sc, flags, s);
+    // Table sizes: a launch copies its whole parameter block, 80 bytes per tensor (24 tensors in the table
+    // of 384 took the host 18 us a call, in that of 64 10 us).
+    if (count <= 16) return launch_state<16>(entries, count, fp8, sc, flags, s);
+    if (count <= 64) return launch_state<64>(entries, count, fp8, sc, flags, s);
+    return launch_state<kAdamMaxTensors>(entries, count, fp8, sc, flags, s);
 }
 
 }  // namespace nvfp4

@@ -272,6 +272,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    // a launch behind another kernel of the stream: what comes before overlaps that kernel's end, what
+    // follows touches memory that it may have written
+    griddep_wait();
+    griddep_launch();
     if (warp < (MODE == kWgrad ? 1 : kWidths)) plan_rows<MODE>(sm, p, pairs);
     if (MODE != kWgrad) __syncthreads();
     if (warp == 0) {
@@ -552,8 +556,17 @@ static cudaError_t launch(const Maps& maps, const GroupedParams& p, int64_t most
     auto kern = grouped_kernel<MODE>;
     if (cudaError_t e = host::ensure_smem(reinterpret_cast<const void*>(kern), kGroupedSmem, attr)) return e;
     const int64_t pairs = std::min<int64_t>(std::max<int64_t>(most_tiles, 1), host::sm_count() / 2);
-    kern<<<(unsigned)(2 * pairs), Shape<MODE>::kThreads, kGroupedSmem, s>>>(maps, p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr_pdl{};
+    attr_pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr_pdl.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(Shape<MODE>::kThreads);
+    cfg.dynamicSmemBytes = kGroupedSmem;
+    cfg.stream = s;
+    cfg.attrs = &attr_pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
 // MN-major operand [slices][rows][cols] (row stride ld, slice stride `stride`): one-block boxes up to

@@ -22,6 +22,9 @@ namespace nvfp4 {
 
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 constexpr int kFewChunks = kFewMaxExperts / 32;
+// CTAs per SM.  48 rows x 14 busy experts of 5120 x 1280 (184 MB): 34.4 us with 4, 36.1 with 2, 3 or 5;
+// unrolling the K loop (more loads in flight per warp, fewer warps) is slower: 35.5 by 2, 37.3 by 4.
+constexpr int kFewResident = 4;
 
 struct FewParams {
     const uint16_t* a;
@@ -87,62 +90,64 @@ __device__ __forceinline__ int busy_expert(const FewParams& p, int j, bool repor
     return found;
 }
 
-// NG: groups of 8 tokens an expert can own at most (8 * NG >= rows of the call)
+// NG: groups of 8 tokens taken in one pass over the weights; an expert with more rows takes more
+// passes (its weights then come from L2)
 template <int NG>
-__global__ void __launch_bounds__(kFewThreads) grouped_few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kFewThreads, kFewResident) grouped_few_kernel(const FewParams p) {
     __shared__ float part[kFewWarps][NG * 8][17];   // [warp][token][feature], padded
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     int lo = 0, hi = 0;
     const int e = busy_expert(p, blockIdx.y, blockIdx.x == 0 && blockIdx.y == 0 && warp == 0, lo, hi);
     if (e < 0) return;
-    const int tokens = hi - lo, groups = (tokens + 7) >> 3;
     const int f0 = blockIdx.x * 16;
-    // rows g and g + 8 of the CTA's features (N % 8 == 0: the second eight may be past the end), token g
-    // of each group
+    // rows g and g + 8 of the CTA's features (N % 8 == 0: the second eight may be past the end)
     const bool upper = f0 + 8 < p.N;
     const uint16_t* w0 = p.b + e * p.stride_b + (int64_t)(f0 + g) * p.ldb + 8 * t;
     const uint16_t* w1 = w0 + (upper ? 8 * p.ldb : 0);
-    const uint16_t* x = p.a + (int64_t)(lo + g) * p.lda + 8 * t;
-    float acc[NG][4] = {};
     const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
-    for (int k = 64 * warp; k < p.K; k += 64 * kFewWarps) {
-        const bool in0 = k + 8 * t < p.K, in1 = k + 32 + 8 * t < p.K;
-        const uint4 a00 = in0 ? ld_stream(w0 + k) : zero, a01 = in1 ? ld_stream(w0 + k + 32) : zero;
-        const uint4 a10 = in0 && upper ? ld_stream(w1 + k) : zero, a11 = in1 && upper ? ld_stream(w1 + k + 32) : zero;
+    for (; lo < hi; lo += 8 * NG) {
+        const int tokens = min(8 * NG, hi - lo), groups = (tokens + 7) >> 3;
+        const uint16_t* x = p.a + (int64_t)(lo + g) * p.lda + 8 * t;   // token g of each group
+        float acc[NG][4] = {};
+#pragma unroll 1
+        for (int k = 64 * warp; k < p.K; k += 64 * kFewWarps) {
+            const bool in0 = k + 8 * t < p.K, in1 = k + 32 + 8 * t < p.K;
+            const uint4 a00 = in0 ? ld_stream(w0 + k) : zero, a01 = in1 ? ld_stream(w0 + k + 32) : zero;
+            const uint4 a10 = in0 && upper ? ld_stream(w1 + k) : zero, a11 = in1 && upper ? ld_stream(w1 + k + 32) : zero;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                if (i >= groups) break;
+                const bool tok = 8 * i + g < tokens;
+                const uint16_t* xi = x + (int64_t)(8 * i) * p.lda + k;
+                const uint4 b0 = tok && in0 ? __ldg(reinterpret_cast<const uint4*>(xi)) : zero;
+                const uint4 b1 = tok && in1 ? __ldg(reinterpret_cast<const uint4*>(xi + 32)) : zero;
+                mma_16n8k16(acc[i], a00.x, a10.x, a00.y, a10.y, b0.x, b0.y);
+                mma_16n8k16(acc[i], a00.z, a10.z, a00.w, a10.w, b0.z, b0.w);
+                mma_16n8k16(acc[i], a01.x, a11.x, a01.y, a11.y, b1.x, b1.y);
+                mma_16n8k16(acc[i], a01.z, a11.z, a01.w, a11.w, b1.z, b1.w);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
             if (i >= groups) break;
-            const bool tok = 8 * i + g < tokens;
-            const uint16_t* xi = x + (int64_t)(8 * i) * p.lda + k;
-            const uint4 b0 = tok && in0 ? __ldg(reinterpret_cast<const uint4*>(xi)) : zero;
-            const uint4 b1 = tok && in1 ? __ldg(reinterpret_cast<const uint4*>(xi + 32)) : zero;
-            mma_16n8k16(acc[i], a00.x, a10.x, a00.y, a10.y, b0.x, b0.y);
-            mma_16n8k16(acc[i], a00.z, a10.z, a00.w, a10.w, b0.z, b0.w);
-            mma_16n8k16(acc[i], a01.x, a11.x, a01.y, a11.y, b1.x, b1.y);
-            mma_16n8k16(acc[i], a01.z, a11.z, a01.w, a11.w, b1.z, b1.w);
+            part[warp][8 * i + 2 * t][g] = acc[i][0];
+            part[warp][8 * i + 2 * t + 1][g] = acc[i][1];
+            part[warp][8 * i + 2 * t][g + 8] = acc[i][2];
+            part[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
         }
-    }
+        __syncthreads();
+        const int f = threadIdx.x & 15, tok = threadIdx.x >> 4;   // 16 tokens at most
+        if (f0 + f < p.N && tok < tokens) {
+            float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-        if (i >= groups) break;
-        part[warp][8 * i + 2 * t][g] = acc[i][0];
-        part[warp][8 * i + 2 * t + 1][g] = acc[i][1];
-        part[warp][8 * i + 2 * t][g + 8] = acc[i][2];
-        part[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
-    }
-    __syncthreads();
-    const int f = threadIdx.x & 15;
-    if (f0 + f >= p.N) return;
-    for (int tok = threadIdx.x >> 4; tok < tokens; tok += kFewThreads / 16) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) s += part[w][tok][f];
-        const int64_t at = (int64_t)(lo + tok) * p.ldd + f0 + f;
-        if (p.out_fp32)
-            reinterpret_cast<float*>(p.d)[at] = s;
-        else
-            reinterpret_cast<uint16_t*>(p.d)[at] = (uint16_t)f32x2_to_bf16x2(s, 0.0f);
+            for (int w = 0; w < kFewWarps; ++w) s += part[w][tok][f];
+            const int64_t at = (int64_t)(lo + tok) * p.ldd + f0 + f;
+            if (p.out_fp32)
+                reinterpret_cast<float*>(p.d)[at] = s;
+            else
+                reinterpret_cast<uint16_t*>(p.d)[at] = (uint16_t)f32x2_to_bf16x2(s, 0.0f);
+        }
+        __syncthreads();   // the next pass writes `part` again
     }
 }
 
@@ -166,12 +171,8 @@ cudaError_t launch_gemm_grouped_few(const GroupedGemm& g, cudaStream_t s) {
     const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)std::min<int64_t>(g.rows, g.experts));
     if (g.rows <= 8)
         grouped_few_kernel<1><<<grid, kFewThreads, 0, s>>>(p);
-    else if (g.rows <= 16)
-        grouped_few_kernel<2><<<grid, kFewThreads, 0, s>>>(p);
-    else if (g.rows <= 32)
-        grouped_few_kernel<4><<<grid, kFewThreads, 0, s>>>(p);
     else
-        grouped_few_kernel<8><<<grid, kFewThreads, 0, s>>>(p);
+        grouped_few_kernel<2><<<grid, kFewThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
