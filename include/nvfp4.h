@@ -398,8 +398,8 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
  *                                                      weight buffer, no transposed copy).
  * A [rows][lda] bf16; B_e starts at b + e * stride_b (elements) with leading dimension ldb; D
  * [rows][ldd] bf16 or fp32.  Rows of D that no expert owns are left as they were.  fp32
- * accumulation; with fp32 output, partial sums of 512 products are joined in fp32 registers
- * (round to nearest), since the tensor core truncates as it accumulates.  Each row's result
+ * accumulation; with fp32 output, partial sums of at most 768 products are joined in fp32
+ * registers (round to nearest), since the tensor core truncates as it accumulates.  Each row's result
  * depends on that row and its expert's weight alone, but for the choice of kernel by `rows`.
  * Shape rules: 1 <= experts <= 1024; rows >= 0 (0: no-op); N, K >= 8, N % 8 == 0, K % 8 == 0;
  * lda >= K, ldb >= K (N if b_kn), stride_b >= 0, all multiples of 8; ldd >= N and
@@ -409,7 +409,8 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
  *   D_e[m][n] (+)= sum over the rows t of e of A[t][m] * B[t][n]   (dw_e = dy^T x, A = dy, B = x)
  * A [rows][lda], B [rows][ldb] bf16; D_e at d + e * stride_d, fp32, leading dimension ldd.
  * accumulate = 0 stores (an expert without rows gets zeros); 1 adds to what D holds (each element
- * once, fp32; an expert without rows is left as it was).  Sums are joined as above.  Shape rules:
+ * once, by the memory system's fp32 add, which rounds to nearest and reads subnormals as zero; an
+ * expert without rows is left as it was).  Sums are joined as above.  Shape rules:
  * as above with M, N multiples of 8; lda >= M, ldb >= N; ldd >= N, stride_d >= 0, both multiples of
  * 4; with more than one expert stride_d >= M * ldd.  rows == 0 makes every expert one without rows.
  */
@@ -446,8 +447,8 @@ nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b,
  * is below half a code: SR, with another seed each step, keeps the averages unbiased.  The weight
  * update of a step reads m and v before they are encoded.
  *
- * amax_ws: if not NULL, a workspace whose plain amax word receives the amax of w (for
- * nvfp4_quantize_weight_ready); it is reset first, and a NaN or Inf in w raises the non-finite flag
+ * amax_ws: if not NULL, a workspace of the tensor's own whose plain amax word receives the amax of w
+ * (for nvfp4_quantize_weight_ready); it is reset first, and a NaN or Inf in w raises the non-finite flag
  * of ws.  w may be NULL (then amax_ws must be too).
  * dynamic: if not NULL, device memory that holds the step's values in place of lr, weight_decay,
  * step, grad_scale and sr_seed of the arguments, read when the kernel runs: a captured graph that

@@ -745,6 +745,9 @@ class AdamWContext:
         for name in ("grads", "weights", "m", "v", "m_scale", "v_scale", "amax_ws"):
             if len(getattr(self, name)) != k:
                 raise ValueError(f"{name}: one entry per parameter")
+        named = [w.addr for w in self.amax_ws if w is not None]
+        if len(set(named)) != len(named):
+            raise ValueError("amax_ws: a workspace of its own for each tensor")
         table = (CAdamWTensor * max(k, 1))()
         for i in range(k):
             p = self.params[i]
@@ -763,7 +766,7 @@ class AdamWContext:
             e.w = None if self.weights[i] is None else self.weights[i].data_ptr()
             e.m_scale = self.m_scale[i].data_ptr() if fp8 else None
             e.v_scale = self.v_scale[i].data_ptr() if fp8 else None
-            e.amax_ws = None if self.amax_ws[i] is None else self.amax_ws[i].buf.data_ptr()
+            e.amax_ws = None if self.amax_ws[i] is None else self.amax_ws[i].addr
         self._table, self._count = table, k
         self._device = self.params[0].device if k else None
         self._args = CAdamWArgs()

@@ -40,11 +40,10 @@ using namespace ptx;
 
 enum : int { kFprop = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kGStages = 6;
-constexpr int kPBytes = 128 * 128;                       // this CTA's 128 features x 64 products
-constexpr int kGStageBytes = 2 * kPBytes;                // and up to 128 output rows x 64 products
+constexpr int kMaxStages = 6;
+constexpr int kRingBytes = 192 * 1024;                   // every instantiation's stages together
 constexpr int kEpiWarps = 16;
-constexpr int kRun = 12;                                 // stages per accumulator with fp32 output: 768 products
+constexpr int kRunK = 768;                               // products per accumulator with fp32 output
 constexpr int kBand = 8;                                 // Q tiles of an expert swept together (L2 reuse)
 constexpr uint64_t kGDrainBudgetNs = 2000000000ull;      // teardown waits, whatever the caller's budget
 
@@ -57,43 +56,56 @@ struct GroupedParams {
     int32_t K;              // fprop, dgrad: the reduction
     int32_t expert_step;    // 1: expert e reads slice e of the weights' map, 0: always slice 0
     int32_t out_fp32, accumulate;
+    int32_t deep;           // dgrad: K is a multiple of 64, Q's boxes hold two blocks of products
     uint32_t* flags;
     uint64_t budget_ns;
 };
 
 struct GroupedSmem {        // behind the stages
-    uint64_t full[kGStages];     // leader: a stage's bytes of both CTAs
-    uint64_t empty[kGStages];    // both: the MMAs that read the stage are done
-    uint64_t tail[kGStages];     // each CTA: its bytes of a stage whose rows have to be cleared (wgrad)
+    uint64_t full[kMaxStages];     // leader: a stage's bytes of both CTAs
+    uint64_t empty[kMaxStages];    // both: the MMAs that read the stage are done
+    uint64_t tail[kMaxStages];     // each CTA: its bytes of a stage whose rows have to be cleared (wgrad)
     uint64_t tfull[2];           // both: accumulator ready
     uint64_t tempty[2];          // leader: both CTAs' epilogues have read it
     uint64_t edrained[2];        // peer: its epilogue has read it
     uint64_t done;
     uint32_t tmem, abort, issued, tails;
-    uint32_t stage_tx[kGStages]; // bytes per CTA of the last use of each stage, 0: a tail
+    uint32_t stage_tx[kMaxStages]; // bytes per CTA of the last use of each stage, 0: a tail
     int32_t width;               // Q rows per tile at most
     float cost[5];
     int32_t row[kMaxExperts + 4];    // expert e owns rows [row[e], row[e + 1])
     int32_t tile[kMaxExperts + 4];   // and tiles [tile[e], tile[e + 1])
 };
-constexpr int kGroupedSmem = kGStages * kGStageBytes + (int)sizeof(GroupedSmem) + 1024;
+constexpr int kGroupedSmem = kRingBytes + (int)sizeof(GroupedSmem) + 1024;
 static_assert(kGroupedSmem <= 232448, "shared memory");
 
+// A stage is one TMA load per operand and CTA, since the TMA engine's rate, not L2's, bounds the
+// loads, and each load has a fixed cost (fprop at 8192 x 5120 x 5120: 1519 TFLOP/s with one 128-row
+// box for Q, 1171 with four of 32).  That cost is higher for the 4-dimensional MN-major boxes, so
+// they are taken deeper: loads alone, 16384 rows x 16 experts x 5120 x 1280, take dgrad 121 us in
+// stages of 128 products and 147 in stages of 64, wgrad 153 and 177 (in all 168 and 172, 197 and 206).  K-major boxes gain little (119
+// and 122) and lose the finer ring (fprop 164 and 158 us in all).
 template <int MODE>
 struct Shape {
     static constexpr bool kPmn = MODE != kFprop;         // P is MN-major
     static constexpr bool kQmn = MODE == kWgrad;
     static constexpr int kThreads = MODE == kWgrad ? 608 : 576;
+    static constexpr int kK = MODE == kFprop ? 64 : 128;   // products per stage
+    static constexpr int kOpBytes = 256 * kK;            // an operand's 128 features or rows
+    static constexpr int kStageBytes = 2 * kOpBytes;
+    static constexpr int kStages = kRingBytes / kStageBytes;
+    static constexpr int kBlock = 128 * kK;              // an MN-major block: 64 features x kK products
+    static_assert(kStages <= kMaxStages && kRunK % kK == 0, "ring");
 };
 
-// The maps of a launch.  A stage is one TMA load per operand and CTA: more, smaller boxes cost their
-// issue (fprop at 8192 x 5120 x 5120: 1519 TFLOP/s with one 128-row box for Q, 1171 with four of 32).
-// K-major Q: boxes of 32, 64 and 128 rows (q[0..2]), the smallest that holds a tile's rows.
+// The maps of a launch.
+// K-major Q: boxes of 32, 64 and 128 rows (q[0..2]), the smallest that holds a tile's rows; the
+// same with two blocks of 64 products (q_deep, where K is a multiple of 64) for dgrad's stages.
 // MN-major operands: a row's features cut into blocks of 64, so that one box holds two blocks (wide);
 // where a tile's 128 features are not all there, or do not start at a block, two boxes of one
 // block each, which end at the tensor's width (p, q[0]).
 struct Maps {
-    CUtensorMap p, p_wide, q[3], q_wide;
+    CUtensorMap p, p_wide, q[3], q_deep[3];
 };
 
 // One output tile
@@ -102,43 +114,56 @@ struct Tile {
     int q0, qn;         // first output row (wgrad: of D_e) and how many are valid
     int n;              // the MMA's N: qn rounded up to 32
     int k0, klen;       // the reduction: first index and length
+    int stages;         // that it takes
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ int even_width(int len, int tiles) { return (ceil_div(len, tiles) + 31) & ~31; }
 
-// Walks the tiles of one pair.  Tiles of an expert in bands of kBand Q tiles, within a band along P
-// with Q fastest.
+// Walks the tiles of one pair: pair, pair + pairs, ...  An expert's tiles go along P row by row of Q
+// tiles, so that a last, partial P tile (little to write) comes to every pair in turn; with more than
+// kBand rows, in bands of kBand Q tiles, within a band along P with Q fastest.
 template <int MODE>
 struct Walk {
     const GroupedParams& p;
     const GroupedSmem& sm;
+    int t, step, total;             // the next tile, their distance, their number
     int e = 0, np, nq = 0, wq = 0, at = -1;
-    __device__ __forceinline__ Walk(const GroupedParams& p_, const GroupedSmem& sm_) : p(p_), sm(sm_) {
+    __device__ __forceinline__ Walk(const GroupedParams& p_, const GroupedSmem& sm_, int first, int step_)
+        : p(p_), sm(sm_), t(first), step(step_), total(sm_.tile[p_.experts]) {
         np = ceil_div(p.P, 256);
         if (MODE == kWgrad) {
             nq = ceil_div(p.Q, 256);
             wq = 256;
         }
     }
-    __device__ __forceinline__ Tile get(int t) {
+    // the next tile, if there is one
+    __device__ __forceinline__ bool next(Tile& r) {
+        if (t >= total) return false;
+        int pt, qt, i = t;
         while (t >= sm.tile[e + 1]) ++e;
-        Tile r;
-        r.e = e;
-        const int lo = sm.row[e], len = sm.row[e + 1] - lo;
         if (MODE != kWgrad && at != e) {
             at = e;
+            const int len = sm.row[e + 1] - sm.row[e];
             nq = ceil_div(len, sm.width);
             wq = even_width(len, nq);
         }
-        const int i = t - sm.tile[e];
-        const int band = i / (kBand * np), in_band = i - band * (kBand * np);
-        const int w = min(kBand, nq - band * kBand);
-        const int pt = in_band / w, qt = band * kBand + (in_band - pt * w);
+        i -= sm.tile[e];
+        if (nq <= kBand) {
+            qt = (int)((uint32_t)i / (uint32_t)np);
+            pt = i - qt * np;
+        } else {
+            const int band = i / (kBand * np), in_band = i - band * (kBand * np);
+            const int w = min(kBand, nq - band * kBand);
+            pt = in_band / w;
+            qt = band * kBand + (in_band - pt * w);
+        }
+        t += step;
+        const int lo = sm.row[e], len = sm.row[e + 1] - lo;
+        r.e = e;
         r.p0 = pt * 256;
-        const int total = MODE == kWgrad ? p.Q : len;
         r.q0 = qt * wq;
-        r.qn = max(0, min(wq, total - r.q0));
+        r.qn = max(0, min(wq, (MODE == kWgrad ? p.Q : len) - r.q0));
         r.n = max(32, (r.qn + 31) & ~31);
         if (MODE == kWgrad) {
             r.k0 = lo;
@@ -148,7 +173,8 @@ struct Walk {
             r.k0 = 0;
             r.klen = p.K;
         }
-        return r;
+        r.stages = ceil_div(r.klen, Shape<MODE>::kK);
+        return true;
     }
 };
 
@@ -235,20 +261,51 @@ __device__ __forceinline__ void plan_tiles(GroupedSmem& sm, const GroupedParams&
     }
 }
 
+// Stores (wgrad: or adds) R output rows of one feature per lane: the first `n` are the tile's.  `at` is
+// the first row's offset in D.
+template <int MODE, int R>
+__device__ __forceinline__ void put_rows(const float (&v)[R], const GroupedParams& p, int64_t at, int f, int n) {
+    if (MODE == kWgrad || p.out_fp32) {
+        float* d = reinterpret_cast<float*>(p.d) + at + f;
+        if (f >= p.P) return;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (i < n) {
+                if (MODE == kWgrad && p.accumulate)
+                    atomicAdd(d, v[i]);   // once per element and call: no order to depend on, no load to wait for
+                else
+                    *d = v[i];
+            }
+            d += p.ldd;
+        }
+    } else {
+        // neighbouring lanes trade one value of two rows, so that each stores two features of one row
+        const int odd = threadIdx.x & 1;
+        uint16_t* d = reinterpret_cast<uint16_t*>(p.d) + at + odd * p.ldd + (f - odd);
+#pragma unroll
+        for (int i = 0; i < R; i += 2) {
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 1);
+            const uint32_t w = odd ? f32x2_to_bf16x2(other, v[i + 1]) : f32x2_to_bf16x2(v[i], other);
+            if (i + odd < n && f < p.P) *reinterpret_cast<uint32_t*>(d) = w;
+            d += 2 * p.ldd;
+        }
+    }
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThreads, 1)
     grouped_kernel(const __grid_constant__ Maps maps, const GroupedParams p) {
     using S = Shape<MODE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    GroupedSmem& sm = *reinterpret_cast<GroupedSmem*>(smem + kGStages * kGStageBytes);
+    GroupedSmem& sm = *reinterpret_cast<GroupedSmem*>(smem + kRingBytes);
     volatile uint32_t* abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 8 * 32) {
-        for (int s = 0; s < kGStages; ++s) {
+        for (int s = 0; s < S::kStages; ++s) {
             mbar_init(smem_u32(&sm.full[s]), MODE == kWgrad ? 2 : 1);
             mbar_init(smem_u32(&sm.empty[s]), 1);
             mbar_init(smem_u32(&sm.tail[s]), 1);
@@ -265,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         sm.tails = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(S::kPmn ? &maps.p_wide : &maps.p);
-        prefetch_map(S::kQmn ? &maps.q_wide : &maps.q[2]);
+        prefetch_map(S::kQmn ? &maps.q_deep[0] : &maps.q[2]);
     }
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "r"(512)
@@ -286,33 +343,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
     cluster_sync_all();   // both CTAs' barriers, TMEM and plans are there
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    const int ntiles = sm.tile[p.experts];
-    const int run = p.out_fp32 ? kRun : 1 << 30;   // stages per accumulator
+    const int run = p.out_fp32 ? kRunK / S::kK : 1 << 30;   // stages per accumulator
 
     if (warp == 0) {
         // ------------------------------- producer (both CTAs) --------------------------------
         if (lane == 0) {
-            Walk<MODE> walk(p, sm);
+            Walk<MODE> walk(p, sm, pair, pairs);
+            Tile c;
             int g = 0, tails = 0;
             bool ok = true;
-            for (int t = pair; ok && t < ntiles; t += pairs) {
-                const Tile c = walk.get(t);
+            while (ok && walk.next(c)) {
                 const int p0 = c.p0 + (int)rank * 128, half = c.n >> 1, q0 = c.q0 + (int)rank * half;
                 // K-major Q: the box that holds the half's rows; MN-major: whether one wide box serves
                 const int qbox = half <= 32 ? 0 : half <= 64 ? 1 : 2;
                 const bool pwide = S::kPmn && p0 + 128 <= p.P, qwide = S::kQmn && half == 128 && q0 + 128 <= p.Q;
-                const uint32_t tx = (uint32_t)kPBytes + (S::kQmn ? (half <= 64 ? 8192u : 16384u) : 4096u << qbox);
+                const uint32_t tx = (uint32_t)(S::kOpBytes + (S::kQmn ? (half <= 64 ? S::kBlock : S::kOpBytes) : (64 * S::kK) << qbox));
                 const int z = c.e * p.expert_step;
-                for (int k = 0; k < c.klen; k += 64, ++g) {
-                    const int s = g % kGStages;
-                    if (!mbar_wait(smem_u32(&sm.empty[s]), ((uint32_t)(g / kGStages) & 1u) ^ 1u, abort_flag, p.flags, p.budget_ns)) {
+                for (int k = 0; k < c.klen; k += S::kK, ++g) {
+                    const int s = g % S::kStages;
+                    if (!mbar_wait(smem_u32(&sm.empty[s]), ((uint32_t)(g / S::kStages) & 1u) ^ 1u, abort_flag, p.flags, p.budget_ns)) {
                         ok = false;
                         break;
                     }
                     uint32_t bar = map_rank(smem_u32(&sm.full[s]), 0);
-                    const bool tail = MODE == kWgrad && (min(64, c.klen - k) & 15) != 0;
+                    const bool tail = MODE == kWgrad && (min(S::kK, c.klen - k) & 15) != 0;
                     if (tail) {
-                        bar = smem_u32(&sm.tail[tails % kGStages]);
+                        bar = smem_u32(&sm.tail[tails % S::kStages]);
                         mbar_expect_tx(bar, tx);
                         ++tails;
                     } else if (rank == 0) {
@@ -320,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                         if (MODE == kWgrad) mbar_arrive(smem_u32(&sm.full[s]));
                     }
                     sm.stage_tx[s] = tail ? 0u : tx;
-                    const uint32_t dst = smem_u32(smem + s * kGStageBytes), dq = dst + kPBytes;
+                    const uint32_t dst = smem_u32(smem + s * S::kStageBytes), dq = dst + S::kOpBytes;
                     const int kk = c.k0 + k;
                     if (!S::kPmn) {
                         tma_load_3d_pair(dst, &maps.p, kk, p0, z, bar);
@@ -328,15 +384,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                         tma_load_4d_pair(dst, &maps.p_wide, 0, kk, p0 >> 6, z, bar);
                     } else {
                         tma_load_3d_pair(dst, &maps.p, p0, kk, z, bar);
-                        tma_load_3d_pair(dst + 8192, &maps.p, p0 + 64, kk, z, bar);
+                        tma_load_3d_pair(dst + S::kBlock, &maps.p, p0 + 64, kk, z, bar);
                     }
-                    if (!S::kQmn) {
+                    if (MODE == kFprop) {
                         tma_load_2d_pair(dq, &maps.q[qbox], kk, q0, bar);
+                    } else if (MODE == kDgrad) {
+                        if (p.deep) {
+                            tma_load_3d_pair(dq, &maps.q_deep[qbox], 0, q0, kk >> 6, bar);
+                        } else {   // products past K read as zero
+                            tma_load_2d_pair(dq, &maps.q[qbox], kk, q0, bar);
+                            tma_load_2d_pair(dq + (4096 << qbox), &maps.q[qbox], kk + 64, q0, bar);
+                        }
                     } else if (qwide) {
-                        tma_load_4d_pair(dq, &maps.q_wide, 0, kk, q0 >> 6, 0, bar);
+                        tma_load_4d_pair(dq, &maps.q_deep[0], 0, kk, q0 >> 6, 0, bar);
                     } else {
                         tma_load_3d_pair(dq, &maps.q[0], q0, kk, 0, bar);
-                        if (half > 64) tma_load_3d_pair(dq + 8192, &maps.q[0], q0 + 64, kk, 0, bar);
+                        if (half > 64) tma_load_3d_pair(dq + S::kBlock, &maps.q[0], q0 + 64, kk, 0, bar);
                     }
                 }
             }
@@ -348,19 +411,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             // ------------------------------- MMA issuer (leader) -----------------------------
             // the whole warp runs the loop, one elected lane issues
             const uint32_t base = smem_u32(smem);
-            const uint64_t pdesc = S::kPmn ? desc_mn_major(base, 8192) : desc_k_major(base);
-            const uint64_t qdesc = S::kQmn ? desc_mn_major(base + kPBytes, 8192) : desc_k_major(base + kPBytes);
-            constexpr uint32_t pstep = S::kPmn ? 2048 >> 4 : 32 >> 4, qstep = S::kQmn ? 2048 >> 4 : 32 >> 4;   // 16 products
+            const uint64_t pdesc = S::kPmn ? desc_mn_major(base, S::kBlock) : desc_k_major(base);
+            const uint64_t qdesc = S::kQmn ? desc_mn_major(base + S::kOpBytes, S::kBlock) : desc_k_major(base + S::kOpBytes);
+            // 16 products further: 16 rows MN-major, 32 bytes K-major (of rows of 64 products: the next
+            // 64 are the next block, of the tile's box rows)
+            constexpr uint32_t mn_step = 2048 >> 4, k_step = 32 >> 4;
             // fp32 accumulator, bf16 operands, transpose bits of the MN-major ones, M = 256
             constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | (S::kPmn ? 1u << 15 : 0u) |
                                         (S::kQmn ? 1u << 16 : 0u) | ((uint32_t)(256 >> 4) << 24);
-            Walk<MODE> walk(p, sm);
+            Walk<MODE> walk(p, sm, pair, pairs);
+            Tile c;
             int g = 0, it = 0;
             bool ok = true;
-            for (int t = pair; ok && t < ntiles; t += pairs) {
-                const Tile c = walk.get(t);
+            while (ok && walk.next(c)) {
                 const uint32_t idesc = idesc0 | ((uint32_t)(c.n >> 3) << 17);
-                const int stages = ceil_div(c.klen, 64);
+                const int stages = c.stages;
+                const uint32_t qblock = (uint32_t)((c.n >> 1) <= 32 ? 4096 : (c.n >> 1) <= 64 ? 8192 : 16384) >> 4;
                 for (int k = 0; ok && k < stages; ++it) {
                     const int end = min(stages, k + min(run, stages - k));
                     const int buf = it & 1;
@@ -373,20 +439,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                     const uint32_t acc = tmem + 256u * buf;
                     const int first = k;
                     for (; k < end; ++k, ++g) {
-                        const int s = g % kGStages;
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.full[s]), (uint32_t)(g / kGStages) & 1u, abort_flag,
+                        const int s = g % S::kStages;
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.full[s]), (uint32_t)(g / S::kStages) & 1u, abort_flag,
                                                                p.flags, p.budget_ns))) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const int steps = min(4, (c.klen - 64 * k + 15) >> 4);
-                        const uint64_t off = (uint64_t)((s * kGStageBytes) >> 4);
+                        const int steps = min(S::kK / 16, (c.klen - S::kK * k + 15) >> 4);
+                        const uint64_t off = (uint64_t)((s * S::kStageBytes) >> 4);
                         if (elect_one()) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
+                            for (int j = 0; j < S::kK / 16; ++j)
                                 if (j < steps)
-                                    mma_bf16_pair(acc, pdesc + off + pstep * j, qdesc + off + qstep * j, idesc, (k > first || j > 0) ? 1u : 0u);
+                                    mma_bf16_pair(acc, pdesc + off + (S::kPmn ? mn_step : k_step) * j,
+                                                  qdesc + off + (S::kQmn ? mn_step * j : (j >> 2) * qblock + k_step * (j & 3)), idesc,
+                                                  (k > first || j > 0) ? 1u : 0u);
                             mma_commit_pair(smem_u32(&sm.empty[s]));
                         }
                         __syncwarp();
@@ -400,11 +468,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             mbar_wait(smem_u32(&sm.done), 0u, abort_flag, p.flags, kGDrainBudgetNs, false);
         } else {
             // the peer's drained accumulators as one remote arrival each
-            Walk<MODE> walk(p, sm);
+            Walk<MODE> walk(p, sm, pair, pairs);
+            Tile c;
             int it = 0;
             bool ok = true;
-            for (int t = pair; ok && t < ntiles; t += pairs) {
-                const int stages = ceil_div(walk.get(t).klen, 64);
+            while (ok && walk.next(c)) {
+                const int stages = c.stages;
                 for (int k = 0; k < stages; k += min(run, stages), ++it) {
                     if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.edrained[it & 1]), (uint32_t)(it >> 1) & 1u, abort_flag,
                                                            p.flags, p.budget_ns))) {
@@ -418,95 +487,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         }
     } else if (warp < 2 + kEpiWarps) {
         // ------------------------------- epilogue (both CTAs) --------------------------------
-        const int q = warp & 3, c0 = ((warp - 2) >> 2) * 64;
+        const int q = warp & 3, group = (warp - 2) >> 2;   // the warp's TMEM lanes; four warps a group
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        Walk<MODE> walk(p, sm);
+        Walk<MODE> walk(p, sm, pair, pairs);
+        Tile c;
         int it = 0;
         bool ok = true;
-        for (int t = pair; ok && t < ntiles; t += pairs) {
-            const Tile c = walk.get(t);
-            const int stages = ceil_div(c.klen, 64);
-            const bool mine = c0 < c.qn;
-            const int n = min(64, c.qn - c0);
+        while (ok && walk.next(c)) {
+            const int stages = c.stages;
             const int f = c.p0 + (int)rank * 128 + q * 32 + lane;
-            const int64_t at = (MODE == kWgrad ? c.e * p.stride_d : 0) + (int64_t)(c.q0 + c0) * p.ldd;
+            const int64_t at = (MODE == kWgrad ? c.e * p.stride_d : 0) + (int64_t)c.q0 * p.ldd;
+            const auto ready = [&](int i) {   // accumulator i of this pair is complete
+                const bool full = mbar_wait(smem_u32(&sm.tfull[i & 1]), (uint32_t)(i >> 1) & 1u, abort_flag, p.flags, p.budget_ns);
+                if (!__all_sync(0xFFFFFFFFu, full)) return false;
+                tc_fence_after();
+                return true;
+            };
+            const auto release = [&](int i) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(rank == 0 ? &sm.tempty[i & 1] : &sm.edrained[i & 1]));
+            };
+            if (stages <= run) {
+                // One run (none: zeros).  Half of the warps take the even accumulators, half the odd ones,
+                // so that the stores of one tile and the reads of the next overlap: 128 columns a warp,
+                // 16 at a time from TMEM to their place.
+                if (stages > 0 && !(ok = ready(it))) break;
+                if ((group >> 1) == (it & 1)) {
+                    const int c0 = (group & 1) * 128;
+#pragma unroll 1
+                    for (int h = c0; h < c0 + 128; h += 16) {
+                        float v[16] = {};
+                        const bool mine = h < c.qn;
+                        if (mine && stages > 0) {
+                            tmem_ld16(tmem + lanes + 256u * (it & 1) + (uint32_t)h, v);
+                            tmem_ld_wait();
+                        }
+                        if (h == c0 + 112 && stages > 0) release(it);
+                        if (mine) put_rows<MODE>(v, p, at + h * p.ldd, f, c.qn - h);
+                    }
+                } else if (stages > 0) {
+                    release(it);
+                }
+                it += stages > 0 ? 1 : 0;
+                continue;
+            }
+            const int c0 = group * 64;
+            const bool mine = c0 < c.qn;
             float acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-            if (MODE == kWgrad && p.accumulate && f < p.P) {
-                // added to what D holds: read while the products are under way (in order, so that one
-                // running address serves), and stored once
-                const float* old = reinterpret_cast<const float*>(p.d) + at + f;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    if (i < n) asm volatile("ld.global.f32 %0, [%1];" : "=f"(acc[i]) : "l"(old));
-                    old += p.ldd;
-                }
-            }
-            for (int k = 0; k < stages; k += min(run, stages), ++it) {
-                const int buf = it & 1;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.tfull[buf]), (uint32_t)(it >> 1) & 1u, abort_flag, p.flags,
-                                                       p.budget_ns))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+            for (int k = 0; k < stages; k += run, ++it) {
+                if (!(ok = ready(it))) break;
                 if (mine) {
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         float v[16];
-                        tmem_ld16(tmem + lanes + 256u * buf + (uint32_t)(c0 + 16 * h), v);
+                        tmem_ld16(tmem + lanes + 256u * (it & 1) + (uint32_t)(c0 + 16 * h), v);
                         tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) acc[16 * h + i] += v[i];
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(rank == 0 ? &sm.tempty[buf] : &sm.edrained[buf]));
+                release(it);
             }
             if (!ok || !mine) continue;
-            if (MODE == kWgrad || p.out_fp32) {
-                float* d = reinterpret_cast<float*>(p.d) + at + f;
-                if (f < p.P) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        if (i < n) *d = acc[i];
-                        d += p.ldd;
-                    }
-                }
-            } else {
-                // neighbouring lanes trade one value of two rows, so that each stores two features of one row
-                const int odd = lane & 1;
-                uint16_t* d = reinterpret_cast<uint16_t*>(p.d) + at + odd * p.ldd + (f - odd);
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? acc[i] : acc[i + 1], 1);
-                    const uint32_t w = odd ? f32x2_to_bf16x2(other, acc[i + 1]) : f32x2_to_bf16x2(acc[i], other);
-                    if (i + odd < n && f < p.P) *reinterpret_cast<uint32_t*>(d) = w;
-                    d += 2 * p.ldd;
-                }
-            }
+            put_rows<MODE>(acc, p, at + c0 * p.ldd, f, c.qn - c0);
         }
     } else {
         // ------------------------------- tails (wgrad, both CTAs) ----------------------------
         // A run's last stage holds rows of the next expert behind its own.  MMAs stop at the 16 rows
         // that hold the last one; the rest of those 16 is cleared, in both operands (0 x NaN).
-        Walk<MODE> walk(p, sm);
+        Walk<MODE> walk(p, sm, pair, pairs);
+        Tile c;
         int g = 0, tails = 0;
-        for (int t = pair; t < ntiles; t += pairs) {
-            const Tile c = walk.get(t);
-            const int stages = ceil_div(c.klen, 64);
-            g += stages;
-            const int last = c.klen & 63;
+        while (walk.next(c)) {
+            g += c.stages;
+            const int last = c.klen % S::kK;
             if (!(last & 15)) continue;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.tail[tails % kGStages]), (uint32_t)(tails / kGStages) & 1u,
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.tail[tails % S::kStages]), (uint32_t)(tails / S::kStages) & 1u,
                                                    abort_flag, p.flags, p.budget_ns)))
                 break;
             ++tails;
-            const int s = (g - 1) % kGStages;
-            // a lane clears 16 bytes of each row of one of the stage's four 64 x 64 boxes
-            const uint32_t box = smem_u32(smem + s * kGStageBytes) + (uint32_t)(lane >> 3) * 8192u + (uint32_t)(lane & 7) * 16u;
+            const int s = (g - 1) % S::kStages;
+            // a lane clears 16 bytes of each row of one of the stage's four blocks
+            const uint32_t box = smem_u32(smem + s * S::kStageBytes) + (uint32_t)(lane >> 3) * (uint32_t)S::kBlock + (uint32_t)(lane & 7) * 16u;
             for (int r = last; r & 15; ++r)
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + (uint32_t)r * 128u), "r"(0) : "memory");
             fence_async_smem();
@@ -519,17 +584,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
     cluster_sync_all();   // both producers have stopped and published what they issued
     if (warp == 0 && lane == 0) {
         // Drain: every copy lands before its CTA exits.  Tails land on the CTA's own barriers; the other
-        // stages of both CTAs on the leader's.  A producer is at most kGStages ahead of the MMAs, so only
-        // the last kGStages uses can be outstanding.  After an abort the counts may differ: a stage
+        // stages of both CTAs on the leader's.  A producer is at most S::kStages ahead of the MMAs, so only
+        // the last S::kStages uses can be outstanding.  After an abort the counts may differ: a stage
         // that only the peer issued has its arrivals made here, one that only the leader issued has the
         // peer's bytes cancelled.  After a normal run every wait returns at once.
         const int tails = (int)sm.tails;
-        for (int j = max(0, tails - kGStages); j < tails; ++j)
-            mbar_wait(smem_u32(&sm.tail[j % kGStages]), (uint32_t)(j / kGStages) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
+        for (int j = max(0, tails - S::kStages); j < tails; ++j)
+            mbar_wait(smem_u32(&sm.tail[j % S::kStages]), (uint32_t)(j / S::kStages) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
         if (rank == 0) {
             const int gl = (int)sm.issued, gp = (int)ld_cluster_u32(map_rank(smem_u32(&sm.issued), 1)), gm = max(gl, gp);
-            for (int k = max(0, gm - kGStages); k < gm; ++k) {
-                const int s = k % kGStages;
+            for (int k = max(0, gm - S::kStages); k < gm; ++k) {
+                const int s = k % S::kStages;
                 const uint32_t bar = smem_u32(&sm.full[s]);
                 const uint32_t tx = k < gl ? sm.stage_tx[s] : ld_cluster_u32(map_rank(smem_u32(&sm.stage_tx[s]), 1));
                 if (tx == 0) continue;
@@ -539,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                 } else if (k >= gp) {
                     mbar_complete_tx(bar, tx);
                 }
-                mbar_wait(bar, (uint32_t)(k / kGStages) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
+                mbar_wait(bar, (uint32_t)(k / S::kStages) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
             }
         }
     }
@@ -570,21 +635,23 @@ static cudaError_t launch(const Maps& maps, const GroupedParams& p, int64_t most
 }
 
 // MN-major operand [slices][rows][cols] (row stride ld, slice stride `stride`): one-block boxes up to
-// the width, and two-block boxes over the whole blocks (valid where there are any)
+// the width, and two-block boxes over the whole blocks (valid where there are any); `depth` products
 static bool mn_maps(CUtensorMap* narrow, CUtensorMap* wide, const void* x, int64_t cols, int64_t rows, int64_t ld,
-                    int64_t slices, int64_t stride) {
+                    int64_t slices, int64_t stride, uint32_t depth) {
     const int64_t dims[4] = {cols, rows, slices, 0}, strides[3] = {ld, stride, 0};
-    const uint32_t box[4] = {64, 64, 1, 0};
+    const uint32_t box[4] = {64, depth, 1, 0};
     if (!host::bf16_map(narrow, x, 3, dims, strides, box)) return false;
     *wide = *narrow;
     if (cols < 128) return true;
     const int64_t wdims[4] = {64, rows, cols / 64, slices}, wstrides[3] = {ld, 64, stride};
-    const uint32_t wbox[4] = {64, 64, 2, 1};
+    const uint32_t wbox[4] = {64, depth, 2, 1};
     return host::bf16_map(wide, x, 4, wdims, wstrides, wbox);
 }
 
 cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
-    // A few rows only stream the weights: the kernel without set-up (grouped_few.cu).
+    // A few rows only stream the weights: the kernel without set-up (grouped_few.cu).  64 rows spread over
+    // 16 experts of 1280 x 5120 take it 44.7 us and the pair kernel 58.6, 256 rows 65 and 59; all 64 rows
+    // with one expert 60 and 28 (16 rows are one pass over the weights), 16 rows 15 and 27.
     if (!g.b_kn && g.rows <= kFewMaxRows && g.experts <= kFewMaxExperts) return launch_gemm_grouped_few(g, s);
     GroupedParams p{};
     p.offsets = g.offsets;
@@ -603,7 +670,7 @@ cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
     const int64_t slices = many ? g.experts : 1, stride = many ? g.stride_b : 8;
     Maps maps;
     if (g.b_kn) {
-        if (!mn_maps(&maps.p, &maps.p_wide, g.b, g.N, g.K, g.ldb, slices, stride)) return cudaErrorInvalidValue;
+        if (!mn_maps(&maps.p, &maps.p_wide, g.b, g.N, g.K, g.ldb, slices, stride, Shape<kDgrad>::kK)) return cudaErrorInvalidValue;
     } else {
         const int64_t dims[3] = {g.K, g.N, slices}, strides[2] = {g.ldb, stride};
         const uint32_t box[3] = {64, 128, 1};
@@ -614,8 +681,14 @@ cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
         const int64_t dims[2] = {g.K, g.rows}, strides[1] = {g.lda};
         const uint32_t box[2] = {64, 32u << i};
         if (!host::bf16_map(&maps.q[i], g.a, 2, dims, strides, box)) return cudaErrorInvalidValue;
+        maps.q_deep[i] = maps.q[i];
+        if (g.b_kn && g.K % 64 == 0) {
+            const int64_t ddims[3] = {64, g.rows, g.K / 64}, dstrides[2] = {g.lda, 64};
+            const uint32_t dbox[3] = {64, 32u << i, 2};
+            if (!host::bf16_map(&maps.q_deep[i], g.a, 3, ddims, dstrides, dbox)) return cudaErrorInvalidValue;
+            p.deep = 1;
+        }
     }
-    maps.q_wide = maps.q[0];
     const int64_t tiles = ((g.N + 255) / 256) * (g.rows / 128 + std::min<int64_t>(g.rows, g.experts));
     return g.b_kn ? launch<kDgrad>(maps, p, tiles, s) : launch<kFprop>(maps, p, tiles, s);
 }
@@ -639,10 +712,10 @@ cudaError_t launch_wgrad_grouped(const GroupedWgrad& g, cudaStream_t s) {
     const void* b = g.rows ? (const void*)g.b : (const void*)g.d;
     const void* a = g.rows ? (const void*)g.a : (const void*)g.d;
     Maps maps;
-    if (!mn_maps(&maps.p, &maps.p_wide, b, g.N, rows, g.ldb, 1, 8) ||
-        !mn_maps(&maps.q[0], &maps.q_wide, a, g.M, rows, g.lda, 1, 8))
+    if (!mn_maps(&maps.p, &maps.p_wide, b, g.N, rows, g.ldb, 1, 8, Shape<kWgrad>::kK) ||
+        !mn_maps(&maps.q[0], &maps.q_deep[0], a, g.M, rows, g.lda, 1, 8, Shape<kWgrad>::kK))
         return cudaErrorInvalidValue;
-    maps.q[1] = maps.q[2] = maps.q[0];
+    maps.q[1] = maps.q[2] = maps.q_deep[1] = maps.q_deep[2] = maps.q[0];   // unused
     const int64_t tiles = ((g.N + 255) / 256) * ((g.M + 255) / 256) * g.experts;
     return launch<kWgrad>(maps, p, tiles, s);
 }

@@ -333,7 +333,8 @@ def test_context_refuses():
                 dict(params=[p], grads=[g], state=2), dict(params=[p], grads=[torch.zeros(16, device="cuda")[::2]]),
                 dict(params=[p], grads=[g], m=[p.view(torch.uint8)[:8]], state=m.STATE_FP8),
                 dict(params=[p], grads=[g], m_scale=[torch.zeros(2, device="cuda")], state=m.STATE_FP8),
-                dict(params=[p.cpu()], grads=[g.cpu()])):
+                dict(params=[p.cpu()], grads=[g.cpu()]),
+                dict(params=[p, g], grads=[g, g], weights=[p.bfloat16(), g.bfloat16()], amax_ws=[m.default_workspace()] * 2)):
         with pytest.raises(ValueError):
             m.AdamWContext(**bad)
     ctx = m.AdamWContext([p], [g])
@@ -348,3 +349,68 @@ def test_context_refuses():
         m.nvfp4_adamw_step(m.AdamWContext([torch.zeros(9, device="cuda")[1:]], [g]), lr=1e-3)
     assert not p.any()
     m.nvfp4_adamw_step(m.AdamWContext([], []), lr=1e-3)
+
+
+@pytest.mark.parametrize("state", ["fp32", "fp8"])
+def test_an_expert_layer_is_trained(state):
+    # the operators as a training step uses them: forward, both gradients, the update of every expert's
+    # weight, the next forward with the new weights; each stage against the values it was given
+    m = nv()
+    g = torch.Generator().manual_seed(2)
+    E, d, n, rows = 4, 136, 72, 300
+    counts = [120, 0, 175, 5]
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32).cuda()
+    lay = m.GroupedLinearBF16(E, d, n)
+    master = torch.randn(E, n, d, generator=g).cuda() * 0.02
+    w = master.bfloat16()
+    dw = torch.zeros(E, n, d, device="cuda")
+    ctx = m.AdamWContext(list(master), list(dw), list(w), state=m.STATE_FP8 if state == "fp8" else m.STATE_FP32, ws=lay.ws)
+    ref = [[master[e].cpu().numpy().reshape(-1), np.zeros(n * d, f32), np.zeros(n * d, f32)] for e in range(E)]
+    for step in (1, 2):
+        x = torch.randn(rows, d, generator=g).bfloat16().cuda()
+        target = torch.randn(rows, n, generator=g).bfloat16().cuda()
+        y = lay.fwd(x, w, off)
+        dy = (y.float() - target.float()).bfloat16()
+        dw.zero_()
+        for lo, hi in ((0, 150), (150, rows)):      # two micro-batches, added
+            part = off.clamp(lo, hi) - lo
+            dx, _ = lay.bwd(x[lo:hi], w, dy[lo:hi], part, dw=dw, accumulate=True)
+        grad = dw.cpu().numpy().copy()
+        for e in range(E):
+            lo, hi = int(off[e]), int(off[e + 1])
+            a, b = dy[lo:hi].double().cpu(), x[lo:hi].double().cpu()
+            bound = 2.0 ** -23 * (hi - lo + 4) * (a.abs().t() @ b.abs()) + 1e-30
+            assert ((torch.from_numpy(grad[e]).double() - a.t() @ b).abs() <= bound).all()
+            yy, ww = y[lo:hi].double().cpu(), w[e].double().cpu()
+            full = b @ ww.t()
+            assert ((yy - full).abs() <= 2.0 ** -8 * full.abs() + 2.0 ** -23 * d * (b.abs() @ ww.abs().t()) + 1e-30).all()
+        m.nvfp4_adamw_step(ctx, step=step, sr_seed=step, **HYPER)
+        assert m.nvfp4_poll(lay.ws) == 0
+        for e in range(E):
+            out = numpy_step(ref[e][0], grad[e].reshape(-1), ref[e][1], ref[e][2], state == "fp8", HYPER, step, 1, step, e)
+            assert same(master[e].cpu().numpy().reshape(-1), out[0]) and torch.equal(w[e].cpu().reshape(-1), out[1])
+            ref[e] = [out[0]] + ([E4M3[c] * s.repeat(256)[:n * d] for c, s in ((out[2], out[3]), (out[4], out[5]))]
+                                 if state == "fp8" else [out[2], out[3]])
+
+
+def test_the_quantized_layer_takes_the_updated_weight():
+    # NVFP4 layer -> its fp32 dw -> AdamW (bf16 weight and its amax) -> the weight's forms without an
+    # amax pass -> a forward pass on the cached forms, equal to one that quantizes the weight itself
+    m = nv()
+    T, d, n = 128, 192, 256
+    g = torch.Generator().manual_seed(3)
+    master = torch.randn(n, d, generator=g).cuda() * 0.02
+    w = master.bfloat16()
+    x, dy = torch.randn(T, d, generator=g).bfloat16().cuda(), (torch.randn(T, n, generator=g) * 1e-2).bfloat16().cuda()
+    lay, check, aw = m.LinearContext(T, d, n), m.LinearContext(T, d, n), m.Workspace()
+    dw = torch.empty(n, d, device="cuda")
+    ctx = m.AdamWContext([master], [dw], [w], state=m.STATE_FP8, amax_ws=[aw])
+    for step in (1, 2):
+        m.nvfp4_linear_fwd(lay, x, w)
+        m.nvfp4_linear_bwd(lay, dy, step, dw=dw)
+        m.nvfp4_adamw_step(ctx, lr=1e-2, step=step, sr_seed=step)
+        m.nvfp4_quantize_weight(w, out=lay.wq, out_t=lay.wqt, ws=aw, amax_ready=True)
+        lay.w_cached = True
+        y = m.nvfp4_linear_fwd(lay, x, None)
+        lay.w_cached = False
+        assert torch.equal(y, m.nvfp4_linear_fwd(check, x, w))

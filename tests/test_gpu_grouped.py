@@ -3,8 +3,8 @@ products of the same bf16 values.
 
 Tolerances (from the arithmetic): bf16 x bf16 products are exact in fp32.  A running fp32 sum of k
 products errs by at most gamma_k * sum |a b|, gamma_k = k u / (1 - k u), u = 2^-23 (one fp32 ulp per
-add: the tensor core may truncate).  With fp32 output the runs are at most 512 products long and
-are joined by rounded fp32 adds: gamma_512 + (number of runs) * 2^-23 covers both.  A bf16 output
+add: the tensor core may truncate).  With fp32 output the runs are at most 768 products long and
+are joined by rounded fp32 adds: gamma_768 + (number of runs) * 2^-23 covers both.  A bf16 output
 adds half a bf16 step, 2^-8 |D| (relative to the value, 2^-9 at best and 2^-8 at worst in a binade)."""
 import numpy as np
 import pytest
@@ -34,7 +34,7 @@ def _inputs(counts, K, N, E=None, before=0, behind=0, seed=0):
 
 def _gamma(K, fp32):
     u = 2.0 ** -23
-    run = min(K, 512) if fp32 else K
+    run = min(K, 768) if fp32 else K
     return run * u / (1 - run * u) + (-(-K // run)) * u
 
 
@@ -218,8 +218,9 @@ def test_wgrad_nonfinite_rows_stay_with_their_expert():
 
 
 def test_wgrad_long_runs_keep_fp32_accuracy():
-    # 20000 products of one sign: a truncating running sum would be off by some 1e-4, joined runs by the
-    # bound of _gamma (6.4e-5 of the sum at worst) and in fact by less than 4e-6
+    # 20000 products of one sign: a truncating running sum would be off by some 1e-4.  A run of 768 takes
+    # 48 adds of 16 products; each loses less than 2^-23 of the partial sum, which is half of the run's
+    # on average: 48 / 2 * 2^-23 = 2.9e-6; the 27 joins add at most 27 / 2 * 2^-24 = 0.8e-6
     m = nv()
     g = torch.Generator().manual_seed(4)
     dy = torch.rand(20000, 64, generator=g).bfloat16()
@@ -345,7 +346,12 @@ def test_streams_graphs_and_two_at_once():
         s.wait_stream(torch.cuda.current_stream())
         g = torch.cuda.CUDAGraph()
 
-        def body():
+        spare = torch.zeros_like(y)
+
+        def body():   # behind a memset, a copy and kernels
+            y.zero_()
+            m.nvfp4_bf16_gemm_grouped(a, w, off, out=y)
+            spare.copy_(y)
             m.nvfp4_bf16_gemm_grouped(a, w, off, out=y)
             dy.copy_(y)
             m.nvfp4_bf16_gemm_grouped(dy, w, off, b_kn=True, out=dx)
@@ -446,3 +452,31 @@ def test_binding_refuses():
         m.nvfp4_bf16_wgrad_grouped(a, a, off, out=torch.zeros(1, 16, 16, device="cuda").expand(2, 16, 16), accumulate=True)
     with pytest.raises(ValueError):
         m.GroupedLinearBF16(2, 16, 16).fwd(a, w, off)
+
+
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+def test_budget_expiry_is_reported_and_the_next_call_is_right(kn):
+    # A bf16 output's accumulator holds the whole reduction: with K = 2^19 it takes over a millisecond,
+    # far longer than the epilogue's first polls, so that with a budget of 1 ns its wait runs out for
+    # certain.  The call drains its copies and MMAs, reports NVFP4_ERR_TIMEOUT (8) and leaves the device
+    # usable.
+    m = nv()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    K, N, rows = 1 << 19, 256, 256
+    a = torch.randn(rows, K, generator=g, device="cuda").bfloat16()
+    w = torch.randn(*((1, K, N) if kn else (1, N, K)), generator=g, device="cuda").bfloat16()
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    ws = m.Workspace()
+    want = m.nvfp4_bf16_gemm_grouped(a, w, off, b_kn=kn, ws=ws)
+    assert m.nvfp4_poll(ws) == 0
+    m.nvfp4_set_wait_budget_ns(1)
+    try:
+        m.nvfp4_bf16_gemm_grouped(a, w, off, b_kn=kn, ws=ws)
+        status = m.nvfp4_poll(ws)
+    finally:
+        m.nvfp4_set_wait_budget_ns(0)     # back to the default
+    assert status == 8 and m.nvfp4_poll(ws) == 0
+    assert torch.equal(m.nvfp4_bf16_gemm_grouped(a, w, off, b_kn=kn, ws=ws), want) and m.nvfp4_poll(ws) == 0
+    del a, w, want
+    _check_gemm([300, 0, 77], 520, 264, kn, torch.float32)
+    _check_wgrad([300, 0, 77], 136, 264)
