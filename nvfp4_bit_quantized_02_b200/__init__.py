@@ -748,48 +748,53 @@ class AdamWContext:
         named = [w.addr for w in self.amax_ws if w is not None]
         if len(set(named)) != len(named):
             raise ValueError("amax_ws: a workspace of its own for each tensor")
-        table = (CAdamWTensor * max(k, 1))()
-        for i in range(k):
-            p = self.params[i]
+        flat = []      # the fields of a CAdamWTensor per tensor, as 64-bit words
+        dev = self.params[0].get_device() if k else -1
+        for i, (p, m, v, w, ws_i) in enumerate(zip(self.params, self.m, self.v, self.weights, self.amax_ws)):
             n = p.numel()
-            self._tensor(p, n, (torch.float32,), f"params[{i}]")
-            self._tensor(self.grads[i], n, (torch.float32, torch.bfloat16), f"grads[{i}]")
-            self._tensor(self.m[i], n, (dt,), f"m[{i}]")
-            self._tensor(self.v[i], n, (dt,), f"v[{i}]")
+            self._tensor(p, n, torch.float32, dev, "params", i)
+            self._tensor(m, n, dt, dev, "m", i)
+            self._tensor(v, n, dt, dev, "v", i)
+            scales = (0, 0)
             if fp8:
-                self._tensor(self.m_scale[i], blocks(n), (torch.float32,), f"m_scale[{i}]")
-                self._tensor(self.v_scale[i], blocks(n), (torch.float32,), f"v_scale[{i}]")
-            if self.weights[i] is not None:
-                self._tensor(self.weights[i], n, (torch.bfloat16,), f"weights[{i}]")
-            e = table[i]
-            e.p, e.m, e.v, e.n = p.data_ptr(), self.m[i].data_ptr(), self.v[i].data_ptr(), n
-            e.w = None if self.weights[i] is None else self.weights[i].data_ptr()
-            e.m_scale = self.m_scale[i].data_ptr() if fp8 else None
-            e.v_scale = self.v_scale[i].data_ptr() if fp8 else None
-            e.amax_ws = None if self.amax_ws[i] is None else self.amax_ws[i].addr
-        self._table, self._count = table, k
-        self._device = self.params[0].device if k else None
+                ms, vs = self.m_scale[i], self.v_scale[i]
+                self._tensor(ms, blocks(n), torch.float32, dev, "m_scale", i)
+                self._tensor(vs, blocks(n), torch.float32, dev, "v_scale", i)
+                scales = (ms.data_ptr(), vs.data_ptr())
+            if w is not None:
+                self._tensor(w, n, torch.bfloat16, dev, "weights", i)
+            flat += (p.data_ptr(), 0, w.data_ptr() if w is not None else 0, m.data_ptr(), v.data_ptr(), *scales,
+                     ws_i.addr if ws_i is not None else 0, n, 0)
+        self._words = (ctypes.c_int64 * max(len(flat), self._WORDS))(*flat)
+        self._table = ctypes.cast(self._words, ctypes.POINTER(CAdamWTensor))
+        self._count, self._dev = k, dev
         self._args = CAdamWArgs()
         self._args.state = state
         self._args_ref = ctypes.byref(self._args)
         self.set_grads(self.grads)
 
-    def _tensor(self, t, n, dtypes, name):
-        if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_contiguous() or t.numel() != n:
-            raise ValueError(f"{name}: expected a contiguous {' or '.join(str(d) for d in dtypes)} tensor of {n} elements")
-        if t.device != self.params[0].device or t.device.type != "cuda":
-            raise ValueError(f"{name}: all tensors live on one CUDA device")
+    _WORDS = ctypes.sizeof(CAdamWTensor) // 8
+
+    @staticmethod
+    def _tensor(t, n, dtype, dev, name, i):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}]: expected a contiguous {dtype} tensor of {n} elements")
+        if dev < 0 or t.get_device() != dev:
+            raise ValueError(f"{name}[{i}]: all tensors live on one CUDA device")
 
     def set_grads(self, grads):
         """Gradients of the next steps, where they are not the buffers of the steps before."""
         grads = list(grads)
         if len(grads) != self._count:
             raise ValueError("grads: one entry per parameter")
+        words = []
         for i, g in enumerate(grads):
-            self._tensor(g, self._table[i].n, (torch.float32, torch.bfloat16), f"grads[{i}]")
-        for e, g in zip(self._table, grads):
-            e.g = g.data_ptr()
-            e.g_dtype = OUT_FP32 if g.dtype == torch.float32 else OUT_BF16
+            bf16 = isinstance(g, torch.Tensor) and g.dtype is torch.bfloat16
+            self._tensor(g, self._words[self._WORDS * i + 8], torch.bfloat16 if bf16 else torch.float32, self._dev, "grads", i)
+            words.append((g.data_ptr(), OUT_BF16 if bf16 else OUT_FP32))
+        for i, (addr, kind) in enumerate(words):
+            self._words[self._WORDS * i + 1] = addr
+            self._words[self._WORDS * i + 9] = kind      # g_dtype, reserved = 0
         self.grads = grads
 
     def moment(self, i: int, which: str) -> torch.Tensor:
@@ -821,13 +826,13 @@ def nvfp4_adamw_step(ctx: AdamWContext, lr: float = 0.0, step: int = 1, beta1: f
     if ctx._count == 0:
         return
     dev = _CUR_DEVICE()
-    if ctx._device.index != dev:
-        raise ValueError(f"the tensors live on {ctx._device}, which is not the current device")
+    if ctx._dev != dev:
+        raise ValueError(f"the tensors live on CUDA device {ctx._dev}, the current device is {dev}")
     a = ctx._args
     a.lr, a.beta1, a.beta2, a.eps, a.weight_decay, a.grad_scale = lr, beta1, beta2, eps, weight_decay, grad_scale
     a.step, a.sr_seed, a.mode = step, sr_seed & 0xFFFFFFFFFFFFFFFF, mode
     if dynamic is not None:
-        if dynamic.dtype != torch.uint8 or dynamic.numel() != 32 or not dynamic.is_contiguous() or dynamic.device != ctx._device:
+        if dynamic.dtype != torch.uint8 or dynamic.numel() != 32 or not dynamic.is_contiguous() or dynamic.get_device() != dev:
             raise ValueError("dynamic: 32 contiguous uint8 on the tensors' device")
         a.dynamic = dynamic.data_ptr()
     else:
