@@ -43,32 +43,38 @@ __device__ __forceinline__ void decode4(uint32_t w, float scale, float* x) {
     const float s = __fmul_rn(scale, 0x1p120f);
     const bool nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
     const bool rare = nan || !(fabsf(scale) < 128.0f);
+    uint32_t bits[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t bits;
         if (SIGNED)
-            bits = (uint32_t)((int32_t)(w << (24 - 8 * i)) >> 4) & 0x87F00000u;
+            bits[i] = (uint32_t)((int32_t)(w << (24 - 8 * i)) >> 4) & 0x87F00000u;
         else
-            bits = (i == 3 ? w >> 4 : w << (20 - 8 * i)) & 0x07F00000u;
-        if (!rare) {
-            x[i] = __fmul_rn(__uint_as_float(bits), s);
-        } else {
-            const bool n = (bits & 0x07F00000u) == 0x07F00000u;
-            x[i] = __fmul_rn(n ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float(bits), 0x1p120f), scale);
+            bits[i] = (i == 3 ? w >> 4 : w << (20 - 8 * i)) & 0x07F00000u;
+    }
+    if (!rare) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            f2_split(f2_mul(f2(__uint_as_float(bits[i]), __uint_as_float(bits[i + 1])), f2c(s)), x[i], x[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool n = (bits[i] & 0x07F00000u) == 0x07F00000u;
+            x[i] = __fmul_rn(n ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float(bits[i]), 0x1p120f), scale);
         }
     }
 }
 
-// E4M3 code of u = |x| * per (per = 448 * (1 / amax) of the block), unsigned, in bits 20-26: u * 2^-120
-// has the code's fields at fp32's (below 2^-6 it is an fp32 subnormal, rounded to the step that
-// u + 2^-6 would have).  Adding `cut` to the 20 bits that are cut off carries into the code where it
-// rounds up: 2^20 - 1 - 16 r16 does so iff r16 < f * 2^16 (f = the cut-off bits / 2^20), half a
-// step less the parity bit gives nearest even.
+// E4M3 code of u = |x| * per (per = 448 * (1 / amax) of the block), unsigned, from the fp32 pattern of
+// x * per * 2^-120, whose bits 20-26 are the code's fields (below 2^-6 the number is an fp32
+// subnormal, rounded to the step that u + 2^-6 would have).  Adding `cut` to the 20 bits that are cut
+// off carries into the code where it rounds up: 2^20 - 1 - 16 r16 does so iff r16 < f * 2^16 (f = the
+// cut-off bits / 2^20), half a step less the parity bit gives nearest even.  All of it one place to
+// the left, where the sign falls out.
 template <bool SR>
-__device__ __forceinline__ uint32_t e4m3_encode(float x, float per, uint32_t cut) {
-    const uint32_t bits = __float_as_uint(__fmul_rn(__fmul_rn(fabsf(x), per), 0x1p-120f));
-    if (!SR) cut = 0x7FFFFu + ((bits >> 20) & 1u);
-    return min((bits + cut) >> 20, 0x7Eu);
+__device__ __forceinline__ uint32_t e4m3_code(float scaled, uint32_t cut2) {
+    const uint32_t bits = __float_as_uint(scaled);
+    if (!SR) cut2 = 0xFFFFEu + 2u * ((bits >> 20) & 1u);
+    return min((2u * bits + cut2) >> 21, 0x7Eu);
 }
 
 // The Philox words of a lane's two element quads.  A block of four words serves eight consecutive
@@ -128,11 +134,13 @@ __device__ __forceinline__ void encode_block(const float (&x)[8], uint32_t (&cod
     for (int j = 0; j < 2; ++j) {
         uint32_t c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // 2^20 - 1 - 16 r16 = 16 (r16's complement) + 15
+        for (int i = 0; i < 4; i += 2) {
+            float lo, hi;
+            f2_split(f2_mul(f2_mul(f2(x[4 * j + i], x[4 * j + i + 1]), f2c(per)), f2c(0x1p-120f)), lo, hi);
+            // 2^20 - 1 - 16 r16 = 16 (r16's complement) + 15, doubled
             const uint32_t n = ~r[j][i >> 1];
-            const uint32_t cut = (i & 1) ? (n >> 12) | 15u : ((n << 4) & 0xFFFF0u) | 15u;
-            c[i] = e4m3_encode<SR>(x[4 * j + i], per, cut);
+            c[i] = e4m3_code<SR>(lo, ((n << 5) & 0x1FFFE0u) | 30u);
+            c[i + 1] = e4m3_code<SR>(hi, ((n >> 11) & 0x1FFFE0u) | 30u);
         }
         codes[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
         if (SIGNED) {
