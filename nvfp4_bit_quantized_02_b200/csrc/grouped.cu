@@ -17,18 +17,28 @@
 // memory; the others (dgrad's W_e, both of wgrad) are MN-major, read by TMA as they lie: no
 // transposed copies.
 //
-// Warps: 0 TMA producer (six stages of 64 products, 32 KiB per CTA); 1 MMA issuer in the leader CTA,
-// in the peer it forwards "accumulator drained"; 2-17 epilogue (32 lanes x 64 columns each); 18
-// (wgrad) clears the rows of a run's last stage that belong to the next expert.
-// The accumulator is double-buffered (2 x 256 TMEM columns).  The tensor core truncates as it
-// accumulates (measured on N(0, 1) operands: 5e-7 of the result after 512 products, 9e-6 after 8192,
-// 4e-5 after 32768), so with fp32 output an accumulator holds at most 512 products and the epilogue
-// joins such runs in registers, rounded to nearest, while the next run is under way.
+// Warps: 0 TMA producer (a ring of 192 KiB per CTA: Shape below); 1 MMA issuer in the leader CTA, in the
+// peer it forwards "accumulator drained"; 2-17 epilogue; 18 (wgrad) clears the rows of a run's last
+// stage that belong to the next expert.
+// The accumulator is double-buffered (2 x 256 TMEM columns).  Where a tile is one accumulator, half of
+// the epilogue warps take the even ones and half the odd ones, 128 columns each.  The tensor core
+// truncates as it accumulates (measured on N(0, 1) operands, relative to the result: 5e-7 after 512
+// products, 2e-6 after 2048, 9e-6 after 8192, 4e-5 after 32768), so with fp32 output an accumulator
+// holds at most 768 products, and the epilogue joins such runs in registers, rounded to nearest, while
+// the next run is under way: all 16 warps, 64 columns each.  A run costs ~700 cycles of tensor time (its
+// reads of TMEM compete with the MMAs).
 //
 // The offsets stay on the device: every CTA reads them, takes their running maximum clamped to
 // [0, rows], and numbers the tiles of all experts; a pair walks tiles pair, pair + pairs, ...
 // Every mbarrier wait is bounded by the caller's budget; on expiry the CTA raises the timeout flag,
 // drains its copies and MMAs (bounded again) and frees its TMEM.
+//
+// Measured (alone, 16384 rows x 16 experts of 5120 x 1280, even counts): fprop 162 us (1.33 PFLOP/s; 4.3
+// tiles a pair, so a fifth wave that is a third full), dgrad 164, wgrad 196; one expert of 8192 x 5120 x
+// 5120: fprop 1.5 PFLOP/s, as cuBLAS.  Tensor pipe 92 % of active cycles there; what bounds all three
+// then is the 1000 W limit (SM clock ~1.5 GHz).  wgrad also writes 419 MB of fp32 and joins two runs
+// a tile.  Without effect: the reduction begun at another stage for each tile, stores with an evict-first
+// policy or spread out by sleeps, bands of 2 to 16 tiles, 4 or 5 stages of 64 products.
 #include <algorithm>
 
 #include "nvfp4_device.cuh"

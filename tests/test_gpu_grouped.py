@@ -347,9 +347,15 @@ def test_streams_graphs_and_two_at_once():
         g = torch.cuda.CUDAGraph()
 
         spare = torch.zeros_like(y)
+        side = torch.cuda.Stream()
 
-        def body():   # behind a memset, a copy and kernels
+        def body():   # behind another stream's work, a memset, a copy and kernels
+            here = torch.cuda.current_stream()
+            side.wait_stream(here)
+            with torch.cuda.stream(side):
+                spare.add_(1)
             y.zero_()
+            here.wait_stream(side)
             m.nvfp4_bf16_gemm_grouped(a, w, off, out=y)
             spare.copy_(y)
             m.nvfp4_bf16_gemm_grouped(a, w, off, out=y)
