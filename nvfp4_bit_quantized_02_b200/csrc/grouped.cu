@@ -24,21 +24,23 @@
 // the epilogue warps take the even ones and half the odd ones, 128 columns each.  The tensor core
 // truncates as it accumulates (measured on N(0, 1) operands, relative to the result: 5e-7 after 512
 // products, 2e-6 after 2048, 9e-6 after 8192, 4e-5 after 32768), so with fp32 output an accumulator
-// holds at most 768 products, and the epilogue joins such runs in registers, rounded to nearest, while
-// the next run is under way: all 16 warps, 64 columns each.  A run costs ~700 cycles of tensor time (its
-// reads of TMEM compete with the MMAs).
+// holds at most 512 products, and the epilogue joins such runs in registers, rounded to nearest, while
+// the next run is under way: all 16 warps, 64 columns each.  That costs little: wgrad below takes 197.7 us
+// in runs of 512, 197.2 of 768, 191.7 in one.
 //
 // The offsets stay on the device: every CTA reads them, takes their running maximum clamped to
 // [0, rows], and numbers the tiles of all experts; a pair walks tiles pair, pair + pairs, ...
 // Every mbarrier wait is bounded by the caller's budget; on expiry the CTA raises the timeout flag,
 // drains its copies and MMAs (bounded again) and frees its TMEM.
 //
-// Measured (alone, 16384 rows x 16 experts of 5120 x 1280, even counts): fprop 162 us (1.33 PFLOP/s; 4.3
-// tiles a pair, so a fifth wave that is a third full), dgrad 164, wgrad 196; one expert of 8192 x 5120 x
-// 5120: fprop 1.5 PFLOP/s, as cuBLAS.  Tensor pipe 92 % of active cycles there; what bounds all three
-// then is the 1000 W limit (SM clock ~1.5 GHz).  wgrad also writes 419 MB of fp32 and joins two runs
-// a tile.  Without effect: the reduction begun at another stage for each tile, stores with an evict-first
-// policy or spread out by sleeps, bands of 2 to 16 tiles, 4 or 5 stages of 64 products.
+// Measured on 16384 rows x 16 experts of 5120 x 1280, even counts, beside cuBLAS' batched product of the
+// same shapes (us; a call by itself / without a pause, where the 1000 W limit holds the SMs at ~1.5 GHz):
+//   fprop 163 / 188, cuBLAS 165 / 191; dgrad 165 / 191, cuBLAS 155 / 181; wgrad 197 / 226, cuBLAS 191 / 221.
+// One expert of 8192 x 5120 x 5120: fprop 1.5 PFLOP/s, as cuBLAS; the tensor pipe is active in 92 % of
+// its cycles.  Here 4.3 tiles a pair make a fifth wave that is a third full, and wgrad writes 419 MB of
+// fp32 (141 us without its stores).  Without effect: the reduction begun at another stage for each tile,
+// stores with an evict-first policy or spread out by sleeps, bands of 2 to 16 tiles, 4 or 5 stages of
+// 64 products, longer suspended waits.
 #include <algorithm>
 
 #include "nvfp4_device.cuh"
@@ -53,7 +55,7 @@ enum : int { kFprop = 0, kDgrad = 1, kWgrad = 2 };
 constexpr int kMaxStages = 6;
 constexpr int kRingBytes = 192 * 1024;                   // every instantiation's stages together
 constexpr int kEpiWarps = 16;
-constexpr int kRunK = 768;                               // products per accumulator with fp32 output
+constexpr int kRunK = 512;                               // products per accumulator with fp32 output
 constexpr int kBand = 8;                                 // Q tiles of an expert swept together (L2 reuse)
 constexpr uint64_t kGDrainBudgetNs = 2000000000ull;      // teardown waits, whatever the caller's budget
 

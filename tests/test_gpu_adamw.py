@@ -210,6 +210,26 @@ def test_against_the_formula_in_64_bits():
     assert (np.abs(ctx.moment(0, "v").cpu().numpy() - V) <= 2.0 ** -24 * 5 * 20 * V + 1e-37).all()
 
 
+def test_a_tensor_past_2_to_the_31_elements():
+    # its last elements against a small tensor of the same values (RNE codes do not depend on the index)
+    m = nv()
+    n, k = 2 ** 31 + 300, 300 + 512
+    p, g = inputs(k, 11, True)
+    big = [torch.zeros(n, dtype=t, device="cuda") for t in (torch.float32, torch.bfloat16, torch.bfloat16)]
+    big[0][-k:] = torch.from_numpy(p).cuda()
+    big[1][-k:] = g.cuda()
+    a = m.AdamWContext([big[0]], [big[1]], [big[2]], state=m.STATE_FP8)
+    b = m.AdamWContext([torch.from_numpy(p).cuda()], [g.cuda()], [torch.zeros(k, dtype=torch.bfloat16, device="cuda")], state=m.STATE_FP8)
+    for c in (a, b):
+        for step in (1, 2):
+            m.nvfp4_adamw_step(c, step=step, mode=m.RNE, **HYPER)
+    assert torch.equal(big[0][-k:], b.params[0]) and torch.equal(big[2][-k:], b.weights[0])
+    assert not big[0][:n - k].any() and not big[2][:n - k].any()
+    for x, y in ((a.m, b.m), (a.v, b.v)):
+        assert torch.equal(x[0].view(torch.uint8)[-k:], y[0].view(torch.uint8))
+    assert torch.equal(a.m_scale[0][-4:], b.m_scale[0]) and torch.equal(a.v_scale[0][-4:], b.v_scale[0])
+
+
 def test_gradients_of_zero_infinity_and_nan():
     m = nv()
     n = 1024

@@ -3,8 +3,8 @@ products of the same bf16 values.
 
 Tolerances (from the arithmetic): bf16 x bf16 products are exact in fp32.  A running fp32 sum of k
 products errs by at most gamma_k * sum |a b|, gamma_k = k u / (1 - k u), u = 2^-23 (one fp32 ulp per
-add: the tensor core may truncate).  With fp32 output the runs are at most 768 products long and
-are joined by rounded fp32 adds: gamma_768 + (number of runs) * 2^-23 covers both.  A bf16 output
+add: the tensor core may truncate).  With fp32 output the runs are at most 512 products long and
+are joined by rounded fp32 adds: gamma_512 + (number of runs) * 2^-23 covers both.  A bf16 output
 adds half a bf16 step, 2^-8 |D| (relative to the value, 2^-9 at best and 2^-8 at worst in a binade)."""
 import numpy as np
 import pytest
@@ -34,7 +34,7 @@ def _inputs(counts, K, N, E=None, before=0, behind=0, seed=0):
 
 def _gamma(K, fp32):
     u = 2.0 ** -23
-    run = min(K, 768) if fp32 else K
+    run = min(K, 512) if fp32 else K
     return run * u / (1 - run * u) + (-(-K // run)) * u
 
 
@@ -218,9 +218,9 @@ def test_wgrad_nonfinite_rows_stay_with_their_expert():
 
 
 def test_wgrad_long_runs_keep_fp32_accuracy():
-    # 20000 products of one sign: a truncating running sum would be off by some 1e-4.  A run of 768 takes
-    # 48 adds of 16 products; each loses less than 2^-23 of the partial sum, which is half of the run's
-    # on average: 48 / 2 * 2^-23 = 2.9e-6; the 27 joins add at most 27 / 2 * 2^-24 = 0.8e-6
+    # 20000 products of one sign: a truncating running sum would be off by some 1e-4.  A run of 512 takes
+    # 32 adds of 16 products; each loses less than 2^-23 of the partial sum, which is half of the run's
+    # on average: 32 / 2 * 2^-23 = 1.9e-6; the 40 joins add at most 40 / 2 * 2^-24 = 1.2e-6
     m = nv()
     g = torch.Generator().manual_seed(4)
     dy = torch.rand(20000, 64, generator=g).bfloat16()
