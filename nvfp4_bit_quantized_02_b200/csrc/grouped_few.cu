@@ -26,6 +26,10 @@ constexpr int kFewChunks = kFewMaxExperts / 32;
 // unrolling the K loop (more loads in flight per warp, fewer warps) is slower: 35.5 by 2, 37.3 by 4.
 constexpr int kFewResident = 4;
 
+// Products a warp accumulates on the tensor core, which truncates, before it joins them in fp32: 65536
+// positive products summed without joining came out 3.5e-5 low, so 8.9e-7.
+constexpr int kFewRun = 512;
+
 struct FewParams {
     const uint16_t* a;
     const uint16_t* b;
@@ -108,32 +112,38 @@ __global__ void __launch_bounds__(kFewThreads, kFewResident) grouped_few_kernel(
     for (; lo < hi; lo += 8 * NG) {
         const int tokens = min(8 * NG, hi - lo), groups = (tokens + 7) >> 3;
         const uint16_t* x = p.a + (int64_t)(lo + g) * p.lda + 8 * t;   // token g of each group
-        float acc[NG][4] = {};
+        // runs of kFewRun products, joined in the warp's own part of shared memory (registers are full)
 #pragma unroll 1
-        for (int k = 64 * warp; k < p.K; k += 64 * kFewWarps) {
-            const bool in0 = k + 8 * t < p.K, in1 = k + 32 + 8 * t < p.K;
-            const uint4 a00 = in0 ? ld_stream(w0 + k) : zero, a01 = in1 ? ld_stream(w0 + k + 32) : zero;
-            const uint4 a10 = in0 && upper ? ld_stream(w1 + k) : zero, a11 = in1 && upper ? ld_stream(w1 + k + 32) : zero;
+        for (int k = 64 * warp, run = 0; run == 0 || k < p.K; ++run) {
+            const int end = min(p.K, k + kFewRun * kFewWarps);
+            float acc[NG][4] = {};
+#pragma unroll 1
+            for (; k < end; k += 64 * kFewWarps) {
+                const bool in0 = k + 8 * t < p.K, in1 = k + 32 + 8 * t < p.K;
+                const uint4 a00 = in0 ? ld_stream(w0 + k) : zero, a01 = in1 ? ld_stream(w0 + k + 32) : zero;
+                const uint4 a10 = in0 && upper ? ld_stream(w1 + k) : zero, a11 = in1 && upper ? ld_stream(w1 + k + 32) : zero;
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    if (i >= groups) break;
+                    const bool tok = 8 * i + g < tokens;
+                    const uint16_t* xi = x + (int64_t)(8 * i) * p.lda + k;
+                    const uint4 b0 = tok && in0 ? __ldg(reinterpret_cast<const uint4*>(xi)) : zero;
+                    const uint4 b1 = tok && in1 ? __ldg(reinterpret_cast<const uint4*>(xi + 32)) : zero;
+                    mma_16n8k16(acc[i], a00.x, a10.x, a00.y, a10.y, b0.x, b0.y);
+                    mma_16n8k16(acc[i], a00.z, a10.z, a00.w, a10.w, b0.z, b0.w);
+                    mma_16n8k16(acc[i], a01.x, a11.x, a01.y, a11.y, b1.x, b1.y);
+                    mma_16n8k16(acc[i], a01.z, a11.z, a01.w, a11.w, b1.z, b1.w);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 if (i >= groups) break;
-                const bool tok = 8 * i + g < tokens;
-                const uint16_t* xi = x + (int64_t)(8 * i) * p.lda + k;
-                const uint4 b0 = tok && in0 ? __ldg(reinterpret_cast<const uint4*>(xi)) : zero;
-                const uint4 b1 = tok && in1 ? __ldg(reinterpret_cast<const uint4*>(xi + 32)) : zero;
-                mma_16n8k16(acc[i], a00.x, a10.x, a00.y, a10.y, b0.x, b0.y);
-                mma_16n8k16(acc[i], a00.z, a10.z, a00.w, a10.w, b0.z, b0.w);
-                mma_16n8k16(acc[i], a01.x, a11.x, a01.y, a11.y, b1.x, b1.y);
-                mma_16n8k16(acc[i], a01.z, a11.z, a01.w, a11.w, b1.z, b1.w);
-            }
-        }
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            if (i >= groups) break;
-            part[warp][8 * i + 2 * t][g] = acc[i][0];
-            part[warp][8 * i + 2 * t + 1][g] = acc[i][1];
-            part[warp][8 * i + 2 * t][g + 8] = acc[i][2];
-            part[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
+                for (int j = 0; j < 4; ++j) {
+                    float& s = part[warp][8 * i + 2 * t + (j & 1)][g + 4 * (j & 2)];
+                    s = run == 0 ? acc[i][j] : s + acc[i][j];
+                }
+            }
         }
         __syncthreads();
         const int f = threadIdx.x & 15, tok = threadIdx.x >> 4;   // 16 tokens at most

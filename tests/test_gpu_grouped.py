@@ -115,6 +115,24 @@ def test_gemm_exact_on_small_integers(kn):
     assert torch.equal(got.cpu().double(), _reference(a, w, off, kn)[0])
 
 
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+@pytest.mark.parametrize("rows", [3, 11, 40, 100])
+def test_gemm_long_runs_are_joined_by_rounding(rows, kn):
+    """Positive integers whose products add to at most 512 * 2^14 < 2^24 in a run of 512: the runs
+    are exact, so only the fp32 adds that join them err, by 2^-24 of the sum each: one per run of
+    512 and one per part of a cut K (8 at most)."""
+    m = nv()
+    K, N, E = 65536 + 8, 24, 2
+    g = torch.Generator().manual_seed(rows)
+    a = torch.randint(1, 129, (rows, K), generator=g).bfloat16()
+    w = torch.randint(1, 129, (E, K, N) if kn else (E, N, K), generator=g).bfloat16()
+    off = _offsets([rows // 2, rows - rows // 2])
+    got = m.nvfp4_bf16_gemm_grouped(a.cuda(), w.cuda(), off.cuda(), b_kn=kn, out_dtype=torch.float32).cpu()
+    ref, _ = _reference(a, w, off, kn)
+    worst = float(((got.double() - ref).abs() / ref).max())
+    assert worst <= (-(-K // 512) + 8) * 2.0 ** -24, worst
+
+
 @pytest.mark.parametrize("rows", [3, 300])
 def test_gemm_strides(rows):
     # leading dimensions past the widths, experts apart from one another, an output inside a wider one
