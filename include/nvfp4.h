@@ -386,8 +386,8 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
 /*
  * Products grouped by expert, the BF16 path of a layer with one weight per expert.  Rows of a
  * token-major operand are sorted by expert: expert e owns rows [offsets[e], offsets[e + 1]).
- * offsets: int32 [experts + 1] in device memory (4-byte aligned), so the row counts never visit the host.  Entries
- * ascend within [0, rows]; an expert may own no row, and rows before offsets[0] or from
+ * offsets: int32 [experts + 1] in device memory (4-byte aligned), so the row counts never visit the
+ * host.  Entries ascend within [0, rows]; an expert may own no row, and rows before offsets[0] or from
  * offsets[experts] on belong to nobody.  Offsets that descend or lie outside [0, rows] are read as
  * the running maximum of their values clamped to [0, rows] (no access leaves the operands), and
  * nvfp4_poll(ws) then reports NVFP4_ERR_ARG.
@@ -399,8 +399,9 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
  * A [rows][lda] bf16; B_e starts at b + e * stride_b (elements) with leading dimension ldb; D
  * [rows][ldd] bf16 or fp32.  Rows of D that no expert owns are left as they were.  fp32
  * accumulation; with fp32 output, partial sums of at most 512 products are joined in fp32
- * registers (round to nearest), since the tensor core truncates as it accumulates.  Each row's result
- * depends on that row and its expert's weight alone, but for the choice of kernel by `rows`.
+ * registers (round to nearest), since the tensor core truncates as it accumulates.  Each row's
+ * result depends on that row and its expert's weight alone, but for the choice of kernel by `rows`.
+ * D overlaps no operand.
  * Shape rules: 1 <= experts <= 1024; rows >= 0 (0: no-op); N, K >= 8, N % 8 == 0, K % 8 == 0;
  * lda >= K, ldb >= K (N if b_kn), stride_b >= 0, all multiples of 8; ldd >= N and
  * ldd * sizeof(out) % 16 == 0; sizes up to 2^30.  ws receives the timeout and offset flags.
@@ -410,8 +411,8 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
  * A [rows][lda], B [rows][ldb] bf16; D_e at d + e * stride_d, fp32, leading dimension ldd.
  * accumulate = 0 stores (an expert without rows gets zeros); 1 adds to what D holds (each element
  * once, by the memory system's fp32 add, which rounds to nearest and reads subnormals as zero; an
- * expert without rows is left as it was).  Sums are joined as above.  Shape rules:
- * as above with M, N multiples of 8; lda >= M, ldb >= N; ldd >= N, stride_d >= 0, both multiples of
+ * expert without rows is left as it was).  Sums are joined as above, D overlaps no operand.  Shape
+ * rules: as above with M, N multiples of 8; lda >= M, ldb >= N; ldd >= N, stride_d >= 0, both multiples of
  * 4; with more than one expert stride_d >= M * ldd.  rows == 0 makes every expert one without rows.
  */
 nvfp4_status nvfp4_bf16_gemm_grouped(const void* a, int64_t lda, int64_t rows, const int32_t* offsets, int experts,

@@ -184,7 +184,7 @@ class Workspace:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.buf = torch.empty(_lib().nvfp4_workspace_bytes(), dtype=torch.uint8, device=device)
         _check(_lib().nvfp4_workspace_init(_ptr(self.buf), _stream()), "nvfp4_workspace_init")
-        self.addr = self.buf.data_ptr()
+        self.addr, self.index = self.buf.data_ptr(), self.buf.get_device()
 
     @property
     def ptr(self):
@@ -586,6 +586,8 @@ def _call_context(dev: int, ws, stream):
     """Addresses of the workspace and the stream of a call on device `dev`."""
     if ws is None:
         ws = _DEFAULT_WS.get(dev) or default_workspace()
+    elif ws.index != dev:
+        raise ValueError(f"the workspace lives on CUDA device {ws.index}, the call runs on {dev}")
     if stream is not None:
         return ws.addr, stream.cuda_stream
     return ws.addr, _RAW_STREAM(dev) if _RAW_STREAM is not None else torch.cuda.current_stream().cuda_stream
@@ -741,7 +743,6 @@ class AdamWContext:
         self.m_scale = (zeros(torch.float32, blocks) if m_scale is None else list(m_scale)) if fp8 else [None] * k
         self.v_scale = (zeros(torch.float32, blocks) if v_scale is None else list(v_scale)) if fp8 else [None] * k
         self.amax_ws = [None] * k if amax_ws is None else list(amax_ws)
-        self.ws = ws or default_workspace()
         for name in ("grads", "weights", "m", "v", "m_scale", "v_scale", "amax_ws"):
             if len(getattr(self, name)) != k:
                 raise ValueError(f"{name}: one entry per parameter")
@@ -749,6 +750,7 @@ class AdamWContext:
         if len(set(named)) != len(named):
             raise ValueError("amax_ws: a workspace of its own for each tensor")
         flat = []      # the fields of a CAdamWTensor per tensor, as 64-bit words
+        written = []   # (first address, end) of what a step writes
         dev = self.params[0].get_device() if k else -1
         for i, (p, m, v, w, ws_i) in enumerate(zip(self.params, self.m, self.v, self.weights, self.amax_ws)):
             n = p.numel()
@@ -761,13 +763,27 @@ class AdamWContext:
                 self._tensor(ms, blocks(n), torch.float32, dev, "m_scale", i)
                 self._tensor(vs, blocks(n), torch.float32, dev, "v_scale", i)
                 scales = (ms.data_ptr(), vs.data_ptr())
+                written += ((ms.data_ptr(), ms.data_ptr() + 4 * blocks(n)), (vs.data_ptr(), vs.data_ptr() + 4 * blocks(n)))
             if w is not None:
                 self._tensor(w, n, torch.bfloat16, dev, "weights", i)
+                written.append((w.data_ptr(), w.data_ptr() + 2 * n))
+            if ws_i is not None and ws_i.index != dev:
+                raise ValueError(f"amax_ws[{i}]: all tensors live on one CUDA device")
+            size = 1 if fp8 else 4
+            written += ((p.data_ptr(), p.data_ptr() + 4 * n), (m.data_ptr(), m.data_ptr() + size * n),
+                        (v.data_ptr(), v.data_ptr() + size * n))
             flat += (p.data_ptr(), 0, w.data_ptr() if w is not None else 0, m.data_ptr(), v.data_ptr(), *scales,
                      ws_i.addr if ws_i is not None else 0, n, 0)
+        written = sorted(r for r in written if r[0] < r[1])
+        if any(a[1] > b[0] for a, b in zip(written, written[1:])):
+            raise ValueError("params, weights and moments: no two of them may overlap")
         self._words = (ctypes.c_int64 * max(len(flat), self._WORDS))(*flat)
         self._table = ctypes.cast(self._words, ctypes.POINTER(CAdamWTensor))
         self._count, self._dev = k, dev
+        if ws is None and k:
+            with torch.cuda.device(dev):
+                ws = default_workspace()
+        self.ws = ws
         self._args = CAdamWArgs()
         self._args.state = state
         self._args_ref = ctypes.byref(self._args)

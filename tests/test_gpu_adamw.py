@@ -2,6 +2,7 @@
 numpy's float32 +, *, / and sqrt are single IEEE operations) and against the update's formula in
 fp64."""
 import math
+import types
 
 import numpy as np
 import pytest
@@ -300,6 +301,26 @@ def test_amax_feeds_the_weight_quantizer():
     assert torch.equal(q.tile_scales, r.tile_scales)
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_amax_of_a_nonfinite_weight(value):
+    """The flag, and the same quantized weight as with the quantizer's own amax pass."""
+    m = nv()
+    torch.manual_seed(6)
+    p = torch.randn(128, 128, device="cuda")
+    p[77, 5] = value
+    w = torch.empty(128, 128, dtype=torch.bfloat16, device="cuda")
+    aws, ws = m.Workspace(), m.Workspace()
+    ctx = m.AdamWContext([p], [torch.zeros_like(p)], weights=[w], amax_ws=[aws], ws=ws)
+    m.nvfp4_adamw_step(ctx, lr=1e-2)
+    assert m.STATUS[m.nvfp4_poll(ws)] == "ERR_NONFINITE"
+    got = m.nvfp4_quantize_weight(w, ws=aws, amax_ready=True)
+    own = m.nvfp4_quantize_weight(w, ws=ws)
+    assert m.STATUS[m.nvfp4_poll(ws)] == "ERR_NONFINITE"
+    for a, b in zip(got, own):
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+        assert torch.equal(a.tensor_scale.view(torch.int32), b.tensor_scale.view(torch.int32)) or (a.tensor_scale.isnan() & b.tensor_scale.isnan()).all()
+
+
 @pytest.mark.parametrize("state", ["fp32", "fp8"])
 def test_captured_step_reads_its_values_when_replayed(state):
     m = nv()
@@ -369,6 +390,25 @@ def test_context_refuses():
         m.nvfp4_adamw_step(m.AdamWContext([torch.zeros(9, device="cuda")[1:]], [g]), lr=1e-3)
     assert not p.any()
     m.nvfp4_adamw_step(m.AdamWContext([], []), lr=1e-3)
+
+
+def test_context_refuses_tensors_twice_and_foreign_workspaces():
+    m = nv()
+    p, g = torch.zeros(512, device="cuda"), torch.zeros(512, device="cuda")
+    other = types.SimpleNamespace(index=p.get_device() + 1, addr=0)     # a workspace of another device
+    for bad in (dict(params=[p, p], grads=[g, g]),                       # the same tensor twice
+                dict(params=[p[:300], p[256:]], grads=[g[:300], g[256:]]),
+                dict(params=[p], grads=[g], m=[p]),
+                dict(params=[p, g], grads=[g, p], v=[torch.zeros(512, device="cuda")] * 2),
+                dict(params=[p], grads=[g], weights=[p.view(torch.bfloat16)[:512]]),
+                dict(params=[p], grads=[g], weights=[p.bfloat16()], amax_ws=[other])):
+        with pytest.raises(ValueError):
+            m.AdamWContext(**bad)
+    with pytest.raises(ValueError):
+        m.nvfp4_adamw_step(m.AdamWContext([p], [g], ws=other), lr=1e-3)
+    # neighbours in one buffer, and empty tensors wherever they lie, do not overlap
+    m.nvfp4_adamw_step(m.AdamWContext([p[:256], p[256:], p[100:100]], [g[:256], g[256:], g[:0]]), lr=1e-3)
+    assert not p.any()
 
 
 @pytest.mark.parametrize("state", ["fp32", "fp8"])

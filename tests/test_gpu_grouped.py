@@ -6,6 +6,8 @@ products errs by at most gamma_k * sum |a b|, gamma_k = k u / (1 - k u), u = 2^-
 add: the tensor core may truncate).  With fp32 output the runs are at most 512 products long and
 are joined by rounded fp32 adds: gamma_512 + (number of runs) * 2^-23 covers both.  A bf16 output
 adds half a bf16 step, 2^-8 |D| (relative to the value, 2^-9 at best and 2^-8 at worst in a binade)."""
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -476,6 +478,17 @@ def test_binding_refuses():
         m.nvfp4_bf16_wgrad_grouped(a, a, off, out=torch.zeros(1, 16, 16, device="cuda").expand(2, 16, 16), accumulate=True)
     with pytest.raises(ValueError):
         m.GroupedLinearBF16(2, 16, 16).fwd(a, w, off)
+
+
+def test_a_workspace_of_another_device_is_refused():
+    m = nv()
+    a = torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    other = types.SimpleNamespace(index=a.get_device() + 1, addr=0)
+    with pytest.raises(ValueError):
+        m.nvfp4_bf16_gemm_grouped(a, torch.zeros(1, 8, 16, dtype=torch.bfloat16, device="cuda"), off, ws=other)
+    with pytest.raises(ValueError):
+        m.nvfp4_bf16_wgrad_grouped(a, a, off, ws=other)
 
 
 @pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
