@@ -21,7 +21,7 @@
 // peer it forwards "accumulator drained"; 2-17 epilogue; 18 (wgrad) clears the rows of a run's last
 // stage that belong to the next expert.
 // The accumulator is double-buffered (2 x 256 TMEM columns).  Where a tile is one accumulator, half of
-// the epilogue warps take the even ones and half the odd ones, 128 columns each.  The tensor core
+// the epilogue warps take the even ones and half the odd ones, 16 columns in turn.  The tensor core
 // truncates as it accumulates (measured on N(0, 1) operands, relative to the result: 5e-7 after 512
 // products, 2e-6 after 2048, 9e-6 after 8192, 4e-5 after 32768), so with fp32 output an accumulator
 // holds at most 512 products, and the epilogue joins such runs in registers, rounded to nearest, while
@@ -56,6 +56,7 @@ constexpr int kMaxStages = 6;
 constexpr int kRingBytes = 192 * 1024;                   // every instantiation's stages together
 constexpr int kEpiWarps = 16;
 constexpr int kRunK = 512;                               // products per accumulator with fp32 output
+constexpr int kWidths = 5;                               // Q rows per tile: 256, 224, ... 128 (the plan below)
 constexpr int kBand = 8;                                 // Q tiles of an expert swept together (L2 reuse)
 constexpr uint64_t kGDrainBudgetNs = 2000000000ull;      // teardown waits, whatever the caller's budget
 
@@ -81,12 +82,11 @@ struct GroupedSmem {        // behind the stages
     uint64_t tempty[2];          // leader: both CTAs' epilogues have read it
     uint64_t edrained[2];        // peer: its epilogue has read it
     uint64_t done;
-    uint32_t tmem, abort, issued, tails;
+    uint32_t tmem, abort, peer_abort, issued, tails;
     uint32_t stage_tx[kMaxStages]; // bytes per CTA of the last use of each stage, 0: a tail
-    int32_t width;               // Q rows per tile at most
-    float cost[5];
-    int32_t row[kMaxExperts + 4];    // expert e owns rows [row[e], row[e + 1])
-    int32_t tile[kMaxExperts + 4];   // and tiles [tile[e], tile[e + 1])
+    uint32_t cost[kWidths];      // fp32 patterns, the last three bits the width's number
+    int32_t row[kMaxExperts + 4];              // expert e owns rows [row[e], row[e + 1])
+    int32_t tile[kWidths][kMaxExperts + 4];    // and Q tiles [tile[w][e], tile[w][e + 1]) at width w
 };
 constexpr int kGroupedSmem = kRingBytes + (int)sizeof(GroupedSmem) + 1024;
 static_assert(kGroupedSmem <= 232448, "shared memory");
@@ -130,7 +130,19 @@ struct Tile {
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-__device__ __forceinline__ int even_width(int len, int tiles) { return (ceil_div(len, tiles) + 31) & ~31; }
+
+// Quotients of the plan, which stands between a launch and its first load: from fp32, set right by
+// the remainder, in a few instructions rather than an integer division's.
+__device__ __forceinline__ int tiles_of(int len, int width, float inv) {   // ceil(len / width)
+    const int q = (int)((float)len * inv), r = len - q * width;            // the floor, or off by 1 (len <= 2^30)
+    return q + (r > 0) + (r > width) - (r <= -width);
+}
+__device__ __forceinline__ int even_width(int len, int tiles, int width) {   // len over tiles, a multiple of 32
+    int c = (int)ceilf(__fdividef((float)len, 32.0f * (float)tiles));
+    c += (int64_t)c * tiles * 32 < len;
+    c -= (int64_t)(c - 1) * tiles * 32 >= len;
+    return min(32 * c, width);   // tiles * width >= len > (tiles - 1) * width
+}
 
 // Walks the tiles of one pair: pair, pair + pairs, ...  An expert's tiles go along P row by row of Q
 // tiles, so that a last, partial P tile (little to write) comes to every pair in turn; with more than
@@ -139,30 +151,35 @@ template <int MODE>
 struct Walk {
     const GroupedParams& p;
     const GroupedSmem& sm;
+    const int32_t* tile;            // the chosen width's Q tiles
     int t, step, total;             // the next tile, their distance, their number
-    int e = 0, np, nq = 0, wq = 0, at = -1;
-    __device__ __forceinline__ Walk(const GroupedParams& p_, const GroupedSmem& sm_, int first, int step_)
-        : p(p_), sm(sm_), t(first), step(step_), total(sm_.tile[p_.experts]) {
-        np = ceil_div(p.P, 256);
-        if (MODE == kWgrad) {
-            nq = ceil_div(p.Q, 256);
-            wq = 256;
-        }
+    int e = -1, np, width, nq = 0, wq = 256;
+    int first = 0, last = 0;        // expert e's tiles
+    __device__ __forceinline__ Walk(const GroupedParams& p_, const GroupedSmem& sm_, int w, int pair, int pairs)
+        : p(p_), sm(sm_), tile(sm_.tile[w]), t(pair), step(pairs), np(ceil_div(p_.P, 256)), width(256 - 32 * w) {
+        total = tile[p.experts] * np;
     }
     // the next tile, if there is one
     __device__ __forceinline__ bool next(Tile& r) {
         if (t >= total) return false;
-        int pt, qt, i = t;
-        while (t >= sm.tile[e + 1]) ++e;
-        if (MODE != kWgrad && at != e) {
-            at = e;
-            const int len = sm.row[e + 1] - sm.row[e];
-            nq = ceil_div(len, sm.width);
-            wq = even_width(len, nq);
+        if (t >= last) {
+            int end = last;   // in Q tiles times np
+            do {
+                ++e;
+                first = end;
+                end = tile[e + 1] * np;
+            } while (t >= end);
+            last = end;
+            nq = tile[e + 1] - tile[e];
+            if (MODE != kWgrad) wq = even_width(sm.row[e + 1] - sm.row[e], nq, width);
         }
-        i -= sm.tile[e];
+        const int i = t - first;
+        t += step;
+        int pt, qt;
         if (nq <= kBand) {
-            qt = (int)((uint32_t)i / (uint32_t)np);
+            qt = (int)__fdividef((float)i, (float)np);   // at most 7, so off by 1 at most
+            qt -= qt * np > i;
+            qt += (qt + 1) * np <= i;
             pt = i - qt * np;
         } else {
             const int band = i / (kBand * np), in_band = i - band * (kBand * np);
@@ -170,13 +187,12 @@ struct Walk {
             pt = in_band / w;
             qt = band * kBand + (in_band - pt * w);
         }
-        t += step;
         const int lo = sm.row[e], len = sm.row[e + 1] - lo;
         r.e = e;
         r.p0 = pt * 256;
         r.q0 = qt * wq;
-        r.qn = max(0, min(wq, (MODE == kWgrad ? p.Q : len) - r.q0));
-        r.n = max(32, (r.qn + 31) & ~31);
+        r.qn = min(wq, (MODE == kWgrad ? p.Q : len) - r.q0);
+        r.n = (r.qn + 31) & ~31;
         if (MODE == kWgrad) {
             r.k0 = lo;
             r.klen = len;
@@ -190,20 +206,18 @@ struct Walk {
     }
 };
 
-// Rows per tile of fprop and dgrad are the best of kWidths by the plan below
-constexpr int kWidths = 5;   // 256, 224, ... 128
-
-// Warp w < kWidths: the offsets' running maximum (warp 0 writes sm.row), and the cost of a width of
-// 256 - 32 w: waves of tiles over the pairs times a tile's operand rows (256 features and its own
-// rows, evenly cut), since a stage takes the time its operands need from L2.
+// Warp w < kWidths: the offsets' running maximum (warp 0 writes sm.row), and, for Q tiles of a width
+// of 256 - 32 w, the experts' first ones and the cost: waves of tiles over the pairs times a tile's
+// operand rows (256 features and its own rows, evenly cut), since a stage takes the time its operands
+// need from L2.  wgrad has one width.
 template <int MODE>
-__device__ __forceinline__ void plan_rows(GroupedSmem& sm, const GroupedParams& p, int pairs) {
+__device__ __forceinline__ void plan(GroupedSmem& sm, const GroupedParams& p, int pairs) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float width = 256.0f - 32.0f * warp, inv = 1.0f / width;
-    int carry = 0, tiles = 0;
-    float rows = 0.0f;
+    const int width = 256 - 32 * warp, nq_wgrad = ceil_div(p.Q, 256);
+    const float inv = __frcp_rn((float)width);
+    int carry = 0, tiles = 0, rows = 0;   // tiles: before this chunk; rows: this lane's
     bool bad = false;
-    for (int i = lane; i - lane <= p.experts; i += 32) {
+    for (int i = lane; i - lane <= p.experts; i += 32) {   // lane: the run that ends at offset i
         const bool in = i <= p.experts;
         const int o = in ? __ldg(p.offsets + i) : 0;
         int v = in ? min(max(o, 0), p.rows) : 0;
@@ -214,93 +228,63 @@ __device__ __forceinline__ void plan_rows(GroupedSmem& sm, const GroupedParams& 
         }
         v = max(v, carry);
         bad |= in && o != v;
-        if (warp == 0 && in) sm.row[i] = v;
-        if (MODE != kWgrad) {   // the run that ends at this offset
-            int len = v - __shfl_up_sync(0xFFFFFFFFu, v, 1);
-            if (lane == 0) len = i == 0 ? 0 : v - carry;
-            if (in && len > 0) {
-                const float nt = ceilf((float)len * inv);
-                tiles += (int)nt;
-                rows += nt * (32.0f * ceilf((float)len / (32.0f * nt)));
+        int len = v - __shfl_up_sync(0xFFFFFFFFu, v, 1);
+        if (lane == 0) len = i == 0 ? 0 : v - carry;
+        int n = 0;
+        if (in && i > 0) {
+            if (MODE == kWgrad)
+                n = len == 0 && p.accumulate ? 0 : nq_wgrad;
+            else if (len > 0) {
+                n = tiles_of(len, width, inv);
+                rows += n * 32 * (int)ceilf(__fdividef((float)len, 32.0f * (float)n));
             }
         }
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, n, s);
+            if (lane >= s) n += u;
+        }
+        if (in) {
+            sm.tile[warp][i] = tiles + n;
+            if (warp == 0) sm.row[i] = v;
+        }
+        tiles += __shfl_sync(0xFFFFFFFFu, n, 31);
         carry = __shfl_sync(0xFFFFFFFFu, v, 31);
     }
     if (warp == 0 && bad && blockIdx.x == 0) atomicOr(p.flags, kFlagOffsets);
     if (MODE != kWgrad) {
-        tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) rows += __shfl_xor_sync(0xFFFFFFFFu, rows, s);
-        if (lane == 0)
-            sm.cost[warp] = ceilf((float)tiles * ceil_div(p.P, 256) / pairs) * (256.0f + rows / fmaxf((float)tiles, 1.0f));
+        rows = __reduce_add_sync(0xFFFFFFFFu, rows);
+        const float cost = ceilf(__fdividef((float)tiles * ceil_div(p.P, 256), (float)pairs)) *
+                           (256.0f + __fdividef((float)rows, fmaxf((float)tiles, 1.0f)));
+        if (lane == 0) sm.cost[warp] = (__float_as_uint(cost) & ~7u) | (uint32_t)warp;
     }
 }
 
-// Warp 0, after plan_rows: the width, and the experts' first tiles
-template <int MODE>
-__device__ __forceinline__ void plan_tiles(GroupedSmem& sm, const GroupedParams& p) {
-    const int lane = threadIdx.x & 31;
-    int width = 256;
-    if (MODE != kWgrad) {
-        float best = sm.cost[0];
-#pragma unroll
-        for (int w = 1; w < kWidths; ++w)
-            if (sm.cost[w] < best) {
-                best = sm.cost[w];
-                width = 256 - 32 * w;
-            }
-    }
-    const int np = ceil_div(p.P, 256), nq_wgrad = MODE == kWgrad ? ceil_div(p.Q, 256) : 0;
-    int total = 0;
-    for (int i = lane; i - lane < p.experts; i += 32) {
-        int c = 0;
-        if (i < p.experts) {
-            const int len = sm.row[i + 1] - sm.row[i];
-            c = MODE == kWgrad ? (len == 0 && p.accumulate ? 0 : nq_wgrad * np) : ceil_div(len, width) * np;
-        }
-        int v = c;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int u = __shfl_up_sync(0xFFFFFFFFu, v, s);
-            if (lane >= s) v += u;
-        }
-        if (i < p.experts) sm.tile[i] = total + v - c;
-        total += __shfl_sync(0xFFFFFFFFu, v, 31);
-    }
-    if (lane == 0) {
-        sm.tile[p.experts] = total;
-        sm.width = width;
-    }
-}
-
-// Stores (wgrad: or adds) R output rows of one feature per lane: the first `n` are the tile's.  `at` is
+// Stores (wgrad: or adds) 16 output rows of one feature per lane: the first `n` are the tile's.  `at` is
 // the first row's offset in D.
-template <int MODE, int R>
-__device__ __forceinline__ void put_rows(const float (&v)[R], const GroupedParams& p, int64_t at, int f, int n) {
-    if (MODE == kWgrad || p.out_fp32) {
-        float* d = reinterpret_cast<float*>(p.d) + at + f;
-        if (f >= p.P) return;
+template <int MODE>
+__device__ __forceinline__ void put_fp32(const float* v, const GroupedParams& p, int64_t at, int f, int n) {
+    float* d = reinterpret_cast<float*>(p.d) + at + f;
+    if (f >= p.P) return;
+    if (MODE == kWgrad && p.accumulate) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (i < n) {
-                if (MODE == kWgrad && p.accumulate)
-                    atomicAdd(d, v[i]);   // once per element and call: no order to depend on, no load to wait for
-                else
-                    *d = v[i];
-            }
-            d += p.ldd;
-        }
+        for (int i = 0; i < 16; ++i, d += p.ldd)   // once per element and call: no order to depend on, no load to wait for
+            if (i < n) atomicAdd(d, v[i]);
     } else {
-        // neighbouring lanes trade one value of two rows, so that each stores two features of one row
-        const int odd = threadIdx.x & 1;
-        uint16_t* d = reinterpret_cast<uint16_t*>(p.d) + at + odd * p.ldd + (f - odd);
 #pragma unroll
-        for (int i = 0; i < R; i += 2) {
-            const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 1);
-            const uint32_t w = odd ? f32x2_to_bf16x2(other, v[i + 1]) : f32x2_to_bf16x2(v[i], other);
-            if (i + odd < n && f < p.P) *reinterpret_cast<uint32_t*>(d) = w;
-            d += 2 * p.ldd;
-        }
+        for (int i = 0; i < 16; ++i, d += p.ldd)
+            if (i < n) *d = v[i];
+    }
+}
+__device__ __forceinline__ void put_bf16(const float* v, const GroupedParams& p, int64_t at, int f, int n) {
+    // neighbouring lanes trade one value of two rows, so that each stores two features of one row
+    const int odd = threadIdx.x & 1;
+    uint16_t* d = reinterpret_cast<uint16_t*>(p.d) + at + odd * p.ldd + (f - odd);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2, d += 2 * p.ldd) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 1);
+        const uint32_t w = odd ? f32x2_to_bf16x2(other, v[i + 1]) : f32x2_to_bf16x2(v[i], other);
+        if (i + odd < n && f < p.P) *reinterpret_cast<uint32_t*>(d) = w;
     }
 }
 
@@ -330,6 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         }
         mbar_init(smem_u32(&sm.done), 1);
         sm.abort = 0u;
+        sm.peer_abort = 0u;
         sm.issued = 0u;
         sm.tails = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -341,26 +326,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    __syncwarp();
+    tc_fence_before();
+    cluster_arrive();   // this CTA's barriers and TMEM are there
     // a launch behind another kernel of the stream: what comes before overlaps that kernel's end, what
     // follows touches memory that it may have written
     griddep_wait();
     griddep_launch();
-    if (warp < (MODE == kWgrad ? 1 : kWidths)) plan_rows<MODE>(sm, p, pairs);
-    if (MODE != kWgrad) __syncthreads();
-    if (warp == 0) {
-        __syncwarp();
-        plan_tiles<MODE>(sm, p);
-    }
-    tc_fence_before();
-    cluster_sync_all();   // both CTAs' barriers, TMEM and plans are there
+    if (warp < (MODE == kWgrad ? 1 : kWidths)) plan<MODE>(sm, p, pairs);
+    __syncthreads();
+    cluster_wait();   // the peer's too
     tc_fence_after();
+    // the width: the least cost, of the first with it
+    const int best = MODE == kWgrad ? 0 : (int)(__reduce_min_sync(0xFFFFFFFFu, lane < kWidths ? sm.cost[lane] : ~0u) & 7u);
     const uint32_t tmem = sm.tmem;
     const int run = p.out_fp32 ? kRunK / S::kK : 1 << 30;   // stages per accumulator
 
     if (warp == 0) {
         // ------------------------------- producer (both CTAs) --------------------------------
         if (lane == 0) {
-            Walk<MODE> walk(p, sm, pair, pairs);
+            Walk<MODE> walk(p, sm, best, pair, pairs);
             Tile c;
             int g = 0, tails = 0;
             bool ok = true;
@@ -417,6 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             }
             sm.issued = (uint32_t)g;   // read by the drain, after the cluster barrier
             sm.tails = (uint32_t)tails;
+            fence_cluster();
         }
     } else if (warp == 1) {
         if (rank == 0) {
@@ -431,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             // fp32 accumulator, bf16 operands, transpose bits of the MN-major ones, M = 256
             constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | (S::kPmn ? 1u << 15 : 0u) |
                                         (S::kQmn ? 1u << 16 : 0u) | ((uint32_t)(256 >> 4) << 24);
-            Walk<MODE> walk(p, sm, pair, pairs);
+            Walk<MODE> walk(p, sm, best, pair, pairs);
             Tile c;
             int g = 0, it = 0;
             bool ok = true;
@@ -480,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             mbar_wait(smem_u32(&sm.done), 0u, abort_flag, p.flags, kGDrainBudgetNs, false);
         } else {
             // the peer's drained accumulators as one remote arrival each
-            Walk<MODE> walk(p, sm, pair, pairs);
+            Walk<MODE> walk(p, sm, best, pair, pairs);
             Tile c;
             int it = 0;
             bool ok = true;
@@ -501,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         // ------------------------------- epilogue (both CTAs) --------------------------------
         const int q = warp & 3, group = (warp - 2) >> 2;   // the warp's TMEM lanes; four warps a group
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        Walk<MODE> walk(p, sm, pair, pairs);
+        Walk<MODE> walk(p, sm, best, pair, pairs);
         Tile c;
         int it = 0;
         bool ok = true;
@@ -526,36 +512,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                 // 16 at a time from TMEM to their place.
                 if (stages > 0 && !(ok = ready(it))) break;
                 if ((group >> 1) == (it & 1)) {
-                    const int c0 = (group & 1) * 128;
+                    const int c0 = (group & 1) * 16;
+                    int h = c0;
 #pragma unroll 1
-                    for (int h = c0; h < c0 + 128; h += 16) {
+                    for (; h < c.qn; h += 32) {
                         float v[16] = {};
-                        const bool mine = h < c.qn;
-                        if (mine && stages > 0) {
+                        if (stages > 0) {
                             tmem_ld16(tmem + lanes + 256u * (it & 1) + (uint32_t)h, v);
                             tmem_ld_wait();
+                            if (h + 32 >= c.qn) release(it);
                         }
-                        if (h == c0 + 112 && stages > 0) release(it);
-                        if (mine) put_rows<MODE>(v, p, at + h * p.ldd, f, c.qn - h);
+                        if (MODE == kWgrad || p.out_fp32)
+                            put_fp32<MODE>(v, p, at + h * p.ldd, f, c.qn - h);
+                        else
+                            put_bf16(v, p, at + h * p.ldd, f, c.qn - h);
                     }
+                    if (h == c0 && stages > 0) release(it);   // none of its own
                 } else if (stages > 0) {
                     release(it);
                 }
                 it += stages > 0 ? 1 : 0;
                 continue;
             }
-            const int c0 = group * 64;
-            const bool mine = c0 < c.qn;
+            const int c0 = group * 16;   // and every 64 further
             float acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
             for (int k = 0; k < stages; k += run, ++it) {
                 if (!(ok = ready(it))) break;
-                if (mine) {
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
+                for (int h = 0; h < 4; ++h) {
+                    if (c0 + 64 * h < c.qn) {
                         float v[16];
-                        tmem_ld16(tmem + lanes + 256u * (it & 1) + (uint32_t)(c0 + 16 * h), v);
+                        tmem_ld16(tmem + lanes + 256u * (it & 1) + (uint32_t)(c0 + 64 * h), v);
                         tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) acc[16 * h + i] += v[i];
@@ -563,14 +552,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                 }
                 release(it);
             }
-            if (!ok || !mine) continue;
-            put_rows<MODE>(acc, p, at + c0 * p.ldd, f, c.qn - c0);
+            if (!ok) continue;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (c0 + 64 * h < c.qn) put_fp32<MODE>(acc + 16 * h, p, at + (c0 + 64 * h) * p.ldd, f, c.qn - (c0 + 64 * h));
         }
     } else {
         // ------------------------------- tails (wgrad, both CTAs) ----------------------------
         // A run's last stage holds rows of the next expert behind its own.  MMAs stop at the 16 rows
         // that hold the last one; the rest of those 16 is cleared, in both operands (0 x NaN).
-        Walk<MODE> walk(p, sm, pair, pairs);
+        Walk<MODE> walk(p, sm, best, pair, pairs);
         Tile c;
         int g = 0, tails = 0;
         while (walk.next(c)) {
@@ -592,14 +583,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         }
     }
 
+    // Each warp hands an abort that it has seen (its own at least) to the leader.  What the barriers
+    // below order is published here and by the producers: released by every thread, they would wait for
+    // the output's stores, which the next kernel waits for anyway.
+    if (lane == 0 && *abort_flag) {
+        if (rank == 1) st_cluster_u32(map_rank(smem_u32(&sm.peer_abort), 0), 1u);
+        fence_cluster();
+    }
+    __syncwarp();
     tc_fence_before();
-    cluster_sync_all();   // both producers have stopped and published what they issued
-    if (warp == 0 && lane == 0) {
-        // Drain: every copy lands before its CTA exits.  Tails land on the CTA's own barriers; the other
-        // stages of both CTAs on the leader's.  A producer is at most S::kStages ahead of the MMAs, so only
-        // the last S::kStages uses can be outstanding.  After an abort the counts may differ: a stage
-        // that only the peer issued has its arrivals made here, one that only the leader issued has the
-        // peer's bytes cancelled.  After a normal run every wait returns at once.
+    cluster_arrive_relaxed();   // both producers have stopped and published what they issued
+    cluster_wait();
+    if (warp == 0 && lane == 0 && (sm.abort || sm.peer_abort)) {
+        // Drain after an abort: every copy lands before its CTA exits.  (Without one it has: the leader's
+        // MMA warp has waited for each stage of both CTAs, each CTA's tail warp for its tails.)  Tails land
+        // on the CTA's own barriers; the other stages of both CTAs on the leader's.  A producer is at most
+        // a ring ahead of the MMAs, so only the last uses of its stages can be outstanding.  The counts
+        // may differ: a stage that only the peer issued has its arrivals made here, one that only the
+        // leader issued has the peer's bytes cancelled.
         const int tails = (int)sm.tails;
         for (int j = max(0, tails - S::kStages); j < tails; ++j)
             mbar_wait(smem_u32(&sm.tail[j % S::kStages]), (uint32_t)(j / S::kStages) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
@@ -620,7 +621,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             }
         }
     }
-    cluster_sync_all();   // both CTAs are done with TMEM, barriers and each other's shared memory
+    __syncwarp();
+    cluster_arrive_relaxed();
+    cluster_wait();   // both CTAs are done with TMEM, barriers and each other's shared memory
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
