@@ -147,33 +147,26 @@ __device__ __forceinline__ int even_width(int len, int tiles, int width) {   // 
 // Walks the tiles of one pair: pair, pair + pairs, ...  An expert's tiles go along P row by row of Q
 // tiles, so that a last, partial P tile (little to write) comes to every pair in turn; with more than
 // kBand rows, in bands of kBand Q tiles, within a band along P with Q fastest.
+// What can be read again from shared memory is: the epilogue has no registers to spare.
 template <int MODE>
 struct Walk {
     const GroupedParams& p;
     const GroupedSmem& sm;
-    const int32_t* tile;            // the chosen width's Q tiles
-    int t, step, total;             // the next tile, their distance, their number
-    int e = -1, np, width, nq = 0, wq = 256;
-    int first = 0, last = 0;        // expert e's tiles
-    __device__ __forceinline__ Walk(const GroupedParams& p_, const GroupedSmem& sm_, int w, int pair, int pairs)
-        : p(p_), sm(sm_), tile(sm_.tile[w]), t(pair), step(pairs), np(ceil_div(p_.P, 256)), width(256 - 32 * w) {
-        total = tile[p.experts] * np;
-    }
+    int w, t, step;          // the width's number, the next tile, their distance
+    int e = -1, wq = 256;    // the tile's expert, and the rows of its Q tiles
+    __device__ __forceinline__ Walk(const GroupedParams& p_, const GroupedSmem& sm_, int w_, int pair, int pairs)
+        : p(p_), sm(sm_), w(MODE == kWgrad ? 0 : w_), t(pair), step(pairs) {}
     // the next tile, if there is one
     __device__ __forceinline__ bool next(Tile& r) {
-        if (t >= total) return false;
-        if (t >= last) {
-            int end = last;   // in Q tiles times np
-            do {
-                ++e;
-                first = end;
-                end = tile[e + 1] * np;
-            } while (t >= end);
-            last = end;
-            nq = tile[e + 1] - tile[e];
-            if (MODE != kWgrad) wq = even_width(sm.row[e + 1] - sm.row[e], nq, width);
+        const int32_t* tile = sm.tile[w];
+        const int np = ceil_div(p.P, 256);
+        if (t >= tile[p.experts] * np) return false;
+        if (e < 0 || t >= tile[e + 1] * np) {
+            do ++e;
+            while (t >= tile[e + 1] * np);
+            if (MODE != kWgrad) wq = even_width(sm.row[e + 1] - sm.row[e], tile[e + 1] - tile[e], 256 - 32 * w);
         }
-        const int i = t - first;
+        const int nq = tile[e + 1] - tile[e], i = t - tile[e] * np;
         t += step;
         int pt, qt;
         if (nq <= kBand) {
@@ -183,9 +176,9 @@ struct Walk {
             pt = i - qt * np;
         } else {
             const int band = i / (kBand * np), in_band = i - band * (kBand * np);
-            const int w = min(kBand, nq - band * kBand);
-            pt = in_band / w;
-            qt = band * kBand + (in_band - pt * w);
+            const int rows = min(kBand, nq - band * kBand);
+            pt = in_band / rows;
+            qt = band * kBand + (in_band - pt * rows);
         }
         const int lo = sm.row[e], len = sm.row[e + 1] - lo;
         r.e = e;
@@ -402,7 +395,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             }
             sm.issued = (uint32_t)g;   // read by the drain, after the cluster barrier
             sm.tails = (uint32_t)tails;
-            fence_cluster();
         }
     } else if (warp == 1) {
         if (rank == 0) {
@@ -543,11 +535,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     if (c0 + 64 * h < c.qn) {
-                        float v[16];
-                        tmem_ld16(tmem + lanes + 256u * (it & 1) + (uint32_t)(c0 + 64 * h), v);
-                        tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[16 * h + i] += v[i];
+                        for (int j = 0; j < 16; j += 8) {
+                            float v[8];
+                            tmem_ld8(tmem + lanes + 256u * (it & 1) + (uint32_t)(c0 + 64 * h + j), v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) acc[16 * h + j + i] += v[i];
+                        }
                     }
                 }
                 release(it);
@@ -583,16 +578,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         }
     }
 
-    // Each warp hands an abort that it has seen (its own at least) to the leader.  What the barriers
-    // below order is published here and by the producers: released by every thread, they would wait for
-    // the output's stores, which the next kernel waits for anyway.
-    if (lane == 0 && *abort_flag) {
-        if (rank == 1) st_cluster_u32(map_rank(smem_u32(&sm.peer_abort), 0), 1u);
-        fence_cluster();
-    }
+    // Each warp hands an abort that it has seen (its own at least) to the leader.  What the drain reads
+    // is released by those warps and by the producers alone: by every warp, it would wait for the output's
+    // stores, which the next kernel waits for anyway.
+    const bool aborted = __any_sync(0xFFFFFFFFu, *abort_flag != 0u);
+    if (aborted && rank == 1 && lane == 0) st_cluster_u32(map_rank(smem_u32(&sm.peer_abort), 0), 1u);
     __syncwarp();
     tc_fence_before();
-    cluster_arrive_relaxed();   // both producers have stopped and published what they issued
+    if (aborted || warp == 0)
+        cluster_arrive();   // both producers have stopped and published what they issued
+    else
+        cluster_arrive_relaxed();
     cluster_wait();
     if (warp == 0 && lane == 0 && (sm.abort || sm.peer_abort)) {
         // Drain after an abort: every copy lands before its CTA exits.  (Without one it has: the leader's
