@@ -78,13 +78,14 @@ struct GroupedSmem {        // behind the stages
     uint64_t full[kMaxStages];     // leader: a stage's bytes of both CTAs
     uint64_t empty[kMaxStages];    // both: the MMAs that read the stage are done
     uint64_t tail[kMaxStages];     // each CTA: its bytes of a stage whose rows have to be cleared (wgrad)
-    uint64_t tfull[2];           // both: accumulator ready
-    uint64_t tempty[2];          // leader: both CTAs' epilogues have read it
-    uint64_t edrained[2];        // peer: its epilogue has read it
+    uint64_t tfull[2];             // both: accumulator ready
+    uint64_t tempty[2];            // leader: both CTAs' epilogues have read it
+    uint64_t edrained[2];          // peer: its epilogue has read it
     uint64_t done;
     uint32_t tmem, abort, peer_abort, issued, tails;
     uint32_t stage_tx[kMaxStages]; // bytes per CTA of the last use of each stage, 0: a tail
-    uint32_t cost[kWidths];      // fp32 patterns, the last three bits the width's number
+    int32_t best;                  // the chosen width's number
+    uint32_t cost[kWidths];        // fp32 patterns, the last three bits the width's number
     int32_t row[kMaxExperts + 4];              // expert e owns rows [row[e], row[e + 1])
     int32_t tile[kWidths][kMaxExperts + 4];    // and Q tiles [tile[w][e], tile[w][e + 1]) at width w
 };
@@ -95,8 +96,8 @@ static_assert(kGroupedSmem <= 232448, "shared memory");
 // loads, and each load has a fixed cost (fprop at 8192 x 5120 x 5120: 1519 TFLOP/s with one 128-row
 // box for Q, 1171 with four of 32).  That cost is higher for the 4-dimensional MN-major boxes, so
 // they are taken deeper: loads alone, 16384 rows x 16 experts x 5120 x 1280, take dgrad 121 us in
-// stages of 128 products and 147 in stages of 64, wgrad 153 and 177 (in all 168 and 172, 197 and 206).  K-major boxes gain little (119
-// and 122) and lose the finer ring (fprop 164 and 158 us in all).
+// stages of 128 products and 147 in stages of 64, wgrad 153 and 177 (in all 168 and 172, 197 and
+// 206).  K-major boxes gain little (119 and 122) and lose the finer ring (fprop 164 and 158 in all).
 template <int MODE>
 struct Shape {
     static constexpr bool kPmn = MODE != kFprop;         // P is MN-major
@@ -152,21 +153,20 @@ template <int MODE>
 struct Walk {
     const GroupedParams& p;
     const GroupedSmem& sm;
-    int w, t, step;          // the width's number, the next tile, their distance
-    int e = -1, wq = 256;    // the tile's expert, and the rows of its Q tiles
-    __device__ __forceinline__ Walk(const GroupedParams& p_, const GroupedSmem& sm_, int w_, int pair, int pairs)
-        : p(p_), sm(sm_), w(MODE == kWgrad ? 0 : w_), t(pair), step(pairs) {}
+    int t, step;             // the next tile, their distance
+    int e = 0;               // the tile's expert
+    __device__ __forceinline__ Walk(const GroupedParams& p_, const GroupedSmem& sm_, int pair, int pairs)
+        : p(p_), sm(sm_), t(pair), step(pairs) {}
     // the next tile, if there is one
     __device__ __forceinline__ bool next(Tile& r) {
+        const int w = sm.best;
         const int32_t* tile = sm.tile[w];
         const int np = ceil_div(p.P, 256);
         if (t >= tile[p.experts] * np) return false;
-        if (e < 0 || t >= tile[e + 1] * np) {
-            do ++e;
-            while (t >= tile[e + 1] * np);
-            if (MODE != kWgrad) wq = even_width(sm.row[e + 1] - sm.row[e], tile[e + 1] - tile[e], 256 - 32 * w);
-        }
+        while (t >= tile[e + 1] * np) ++e;
+        const int lo = sm.row[e], len = sm.row[e + 1] - lo;
         const int nq = tile[e + 1] - tile[e], i = t - tile[e] * np;
+        const int wq = even_width(MODE == kWgrad ? p.Q : len, nq, 256 - 32 * w);
         t += step;
         int pt, qt;
         if (nq <= kBand) {
@@ -180,7 +180,6 @@ struct Walk {
             pt = in_band / rows;
             qt = band * kBand + (in_band - pt * rows);
         }
-        const int lo = sm.row[e], len = sm.row[e + 1] - lo;
         r.e = e;
         r.p0 = pt * 256;
         r.q0 = qt * wq;
@@ -202,11 +201,14 @@ struct Walk {
 // Warp w < kWidths: the offsets' running maximum (warp 0 writes sm.row), and, for Q tiles of a width
 // of 256 - 32 w, the experts' first ones and the cost: waves of tiles over the pairs times a tile's
 // operand rows (256 features and its own rows, evenly cut), since a stage takes the time its operands
-// need from L2.  wgrad has one width.
+// need from L2.  wgrad's Q tiles cut features, the same for every expert (8192 rows, one expert of
+// 1000 x 1000: 54.8 us, with tiles of 256 67.5).
+// All of it stands between a launch and its first load, so it is one pass; the seven microseconds
+// that the smallest launches took were four of this, of waits for stores at the end and of a drain.
 template <int MODE>
 __device__ __forceinline__ void plan(GroupedSmem& sm, const GroupedParams& p, int pairs) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int width = 256 - 32 * warp, nq_wgrad = ceil_div(p.Q, 256);
+    const int width = 256 - 32 * warp;
     const float inv = __frcp_rn((float)width);
     int carry = 0, tiles = 0, rows = 0;   // tiles: before this chunk; rows: this lane's
     bool bad = false;
@@ -224,13 +226,10 @@ __device__ __forceinline__ void plan(GroupedSmem& sm, const GroupedParams& p, in
         int len = v - __shfl_up_sync(0xFFFFFFFFu, v, 1);
         if (lane == 0) len = i == 0 ? 0 : v - carry;
         int n = 0;
-        if (in && i > 0) {
-            if (MODE == kWgrad)
-                n = len == 0 && p.accumulate ? 0 : nq_wgrad;
-            else if (len > 0) {
-                n = tiles_of(len, width, inv);
-                rows += n * 32 * (int)ceilf(__fdividef((float)len, 32.0f * (float)n));
-            }
+        if (in && i > 0 && (len > 0 || (MODE == kWgrad && !p.accumulate))) {
+            if (MODE == kWgrad) len = p.Q;
+            n = tiles_of(len, width, inv);
+            rows += n * 32 * (int)ceilf(__fdividef((float)len, 32.0f * (float)n));
         }
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
@@ -245,12 +244,10 @@ __device__ __forceinline__ void plan(GroupedSmem& sm, const GroupedParams& p, in
         carry = __shfl_sync(0xFFFFFFFFu, v, 31);
     }
     if (warp == 0 && bad && blockIdx.x == 0) atomicOr(p.flags, kFlagOffsets);
-    if (MODE != kWgrad) {
-        rows = __reduce_add_sync(0xFFFFFFFFu, rows);
-        const float cost = ceilf(__fdividef((float)tiles * ceil_div(p.P, 256), (float)pairs)) *
-                           (256.0f + __fdividef((float)rows, fmaxf((float)tiles, 1.0f)));
-        if (lane == 0) sm.cost[warp] = (__float_as_uint(cost) & ~7u) | (uint32_t)warp;
-    }
+    rows = __reduce_add_sync(0xFFFFFFFFu, rows);
+    const float cost = ceilf(__fdividef((float)tiles * ceil_div(p.P, 256), (float)pairs)) *
+                       (256.0f + __fdividef((float)rows, fmaxf((float)tiles, 1.0f)));
+    if (lane == 0) sm.cost[warp] = (__float_as_uint(cost) & ~7u) | (uint32_t)warp;
 }
 
 // Stores (wgrad: or adds) 16 output rows of one feature per lane: the first `n` are the tile's.  `at` is
@@ -326,19 +323,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
     // follows touches memory that it may have written
     griddep_wait();
     griddep_launch();
-    if (warp < (MODE == kWgrad ? 1 : kWidths)) plan<MODE>(sm, p, pairs);
+    if (warp < kWidths) plan<MODE>(sm, p, pairs);
+    __syncthreads();
+    if (warp == 0) {   // the width: the least cost, of the first with it
+        const uint32_t best = __reduce_min_sync(0xFFFFFFFFu, lane < kWidths ? sm.cost[lane] : ~0u) & 7u;
+        if (lane == 0) sm.best = (int)best;
+    }
     __syncthreads();
     cluster_wait();   // the peer's too
     tc_fence_after();
-    // the width: the least cost, of the first with it
-    const int best = MODE == kWgrad ? 0 : (int)(__reduce_min_sync(0xFFFFFFFFu, lane < kWidths ? sm.cost[lane] : ~0u) & 7u);
     const uint32_t tmem = sm.tmem;
     const int run = p.out_fp32 ? kRunK / S::kK : 1 << 30;   // stages per accumulator
 
     if (warp == 0) {
         // ------------------------------- producer (both CTAs) --------------------------------
         if (lane == 0) {
-            Walk<MODE> walk(p, sm, best, pair, pairs);
+            Walk<MODE> walk(p, sm, pair, pairs);
             Tile c;
             int g = 0, tails = 0;
             bool ok = true;
@@ -409,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             // fp32 accumulator, bf16 operands, transpose bits of the MN-major ones, M = 256
             constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | (S::kPmn ? 1u << 15 : 0u) |
                                         (S::kQmn ? 1u << 16 : 0u) | ((uint32_t)(256 >> 4) << 24);
-            Walk<MODE> walk(p, sm, best, pair, pairs);
+            Walk<MODE> walk(p, sm, pair, pairs);
             Tile c;
             int g = 0, it = 0;
             bool ok = true;
@@ -458,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             mbar_wait(smem_u32(&sm.done), 0u, abort_flag, p.flags, kGDrainBudgetNs, false);
         } else {
             // the peer's drained accumulators as one remote arrival each
-            Walk<MODE> walk(p, sm, best, pair, pairs);
+            Walk<MODE> walk(p, sm, pair, pairs);
             Tile c;
             int it = 0;
             bool ok = true;
@@ -479,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         // ------------------------------- epilogue (both CTAs) --------------------------------
         const int q = warp & 3, group = (warp - 2) >> 2;   // the warp's TMEM lanes; four warps a group
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        Walk<MODE> walk(p, sm, best, pair, pairs);
+        Walk<MODE> walk(p, sm, pair, pairs);
         Tile c;
         int it = 0;
         bool ok = true;
@@ -556,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         // ------------------------------- tails (wgrad, both CTAs) ----------------------------
         // A run's last stage holds rows of the next expert behind its own.  MMAs stop at the 16 rows
         // that hold the last one; the rest of those 16 is cleared, in both operands (0 x NaN).
-        Walk<MODE> walk(p, sm, best, pair, pairs);
+        Walk<MODE> walk(p, sm, pair, pairs);
         Tile c;
         int g = 0, tails = 0;
         while (walk.next(c)) {
@@ -727,7 +727,7 @@ cudaError_t launch_wgrad_grouped(const GroupedWgrad& g, cudaStream_t s) {
         !mn_maps(&maps.q[0], &maps.q_deep[0], a, g.M, rows, g.lda, 1, 8, Shape<kWgrad>::kK))
         return cudaErrorInvalidValue;
     maps.q[1] = maps.q[2] = maps.q_deep[1] = maps.q_deep[2] = maps.q[0];   // unused
-    const int64_t tiles = ((g.N + 255) / 256) * ((g.M + 255) / 256) * g.experts;
+    const int64_t tiles = ((g.N + 255) / 256) * ((g.M + 127) / 128) * g.experts;
     return launch<kWgrad>(maps, p, tiles, s);
 }
 
