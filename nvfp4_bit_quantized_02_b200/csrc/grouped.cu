@@ -660,10 +660,13 @@ static bool mn_maps(CUtensorMap* narrow, CUtensorMap* wide, const void* x, int64
 }
 
 cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
-    // A few rows only stream the weights: the kernel without set-up (grouped_few.cu).  64 rows spread over
-    // 16 experts of 1280 x 5120 take it 44.7 us and the pair kernel 58.6, 256 rows 65 and 59; all 64 rows
-    // with one expert 60 and 28 (16 rows are one pass over the weights), 16 rows 15 and 27.
-    if (!g.b_kn && g.rows <= kFewMaxRows && g.experts <= kFewMaxExperts) return launch_gemm_grouped_few(g, s);
+    // A few rows only stream the weights: the kernel without set-up (grouped_few.cu), whose passes over an
+    // expert's weights take 16 rows each.  64 rows spread over 16 experts of 1280 x 5120 take it 40 us and
+    // the pair kernel 55, of 5120 x 1280 42 and 40; all with one of the 16 33 and 25, 17 and 10.  256 rows
+    // spread over 16 take 65 and 55.  With one expert in all the passes are known: 24 rows of 5120 x 1280
+    // take 9.7 and 9.4, 64 rows 16 and 9.8, of 1280 x 5120 (where the pair kernel has five tiles) 21 and 25.
+    const bool passes = g.experts == 1 && g.rows > 24 && g.K < kFewLongK;
+    if (!g.b_kn && g.rows <= kFewMaxRows && g.experts <= kFewMaxExperts && !passes) return launch_gemm_grouped_few(g, s);
     GroupedParams p{};
     p.offsets = g.offsets;
     p.d = g.d;

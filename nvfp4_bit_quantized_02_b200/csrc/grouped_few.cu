@@ -2,7 +2,7 @@
 // D[t] = A[t] . W_e^T, W_e [N][K].
 //
 // The rows cost nothing against the weights, each of which is read once: the work is bound by
-// memory, and at the smallest sizes by latency.  A CTA takes 16 features of one expert; its 8 warps
+// memory, and at the smallest sizes by latency.  A CTA takes 16 features of one expert; its warps
 // cut K into chunks of 64 and join their sums through shared memory, so that even two experts of a
 // few hundred features are spread over most SMs, with no tensor maps, TMEM or clusters to set up.
 // The products run on mma.sync m16n8k16 (features x token groups of 8): at these sizes the tensor
@@ -17,14 +17,17 @@
 
 #include "nvfp4_device.cuh"
 #include "nvfp4_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace nvfp4 {
 
-constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 constexpr int kFewChunks = kFewMaxExperts / 32;
-// CTAs per SM.  48 rows x 14 busy experts of 5120 x 1280 (184 MB): 34.4 us with 4, 36.1 with 2, 3 or 5;
-// unrolling the K loop (more loads in flight per warp, fewer warps) is slower: 35.5 by 2, 37.3 by 4.
-constexpr int kFewResident = 4;
+// Warps that cut K, and so CTAs per SM.  16 serve a K of kFewLongK or more in launches that a single wave
+// of CTAs holds, where a CTA's chain of loads is what counts: one expert of 1280 x 5120, 8 rows 6.8 us with
+// 16 and 10.0 with 8, 64 rows 21.2 and 31.9.  With more CTAs or a shorter K 8 are better: 48 rows x 14 busy
+// experts of 5120 x 1280 (184 MB) 31.4 us, with 16 34.8.  Those take 36.2 with 5 CTAs per SM, and 35.2 with
+// the K loop unrolled by 2 (more loads in flight per warp; 42.2 with the registers that it asks for).
+constexpr int few_resident(int warps) { return 32 / warps; }
 
 // Products a warp accumulates on the tensor core, which truncates, before it joins them in fp32: 65536
 // positive products summed without joining came out 3.5e-5 low, so 8.9e-7.
@@ -96,9 +99,9 @@ __device__ __forceinline__ int busy_expert(const FewParams& p, int j, bool repor
 
 // NG: groups of 8 tokens taken in one pass over the weights; an expert with more rows takes more
 // passes (its weights then come from L2)
-template <int NG>
-__global__ void __launch_bounds__(kFewThreads, kFewResident) grouped_few_kernel(const FewParams p) {
-    __shared__ float part[kFewWarps][NG * 8][17];   // [warp][token][feature], padded
+template <int NG, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, few_resident(WARPS)) grouped_few_kernel(const FewParams p) {
+    __shared__ float part[WARPS][NG * 8][17];   // [warp][token][feature], padded
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     int lo = 0, hi = 0;
     const int e = busy_expert(p, blockIdx.y, blockIdx.x == 0 && blockIdx.y == 0 && warp == 0, lo, hi);
@@ -115,10 +118,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewResident) grouped_few_kernel(
         // runs of kFewRun products, joined in the warp's own part of shared memory (registers are full)
 #pragma unroll 1
         for (int k = 64 * warp, run = 0; run == 0 || k < p.K; ++run) {
-            const int end = min(p.K, k + kFewRun * kFewWarps);
+            const int end = min(p.K, k + kFewRun * WARPS);
             float acc[NG][4] = {};
 #pragma unroll 1
-            for (; k < end; k += 64 * kFewWarps) {
+            for (; k < end; k += 64 * WARPS) {
                 const bool in0 = k + 8 * t < p.K, in1 = k + 32 + 8 * t < p.K;
                 const uint4 a00 = in0 ? ld_stream(w0 + k) : zero, a01 = in1 ? ld_stream(w0 + k + 32) : zero;
                 const uint4 a10 = in0 && upper ? ld_stream(w1 + k) : zero, a11 = in1 && upper ? ld_stream(w1 + k + 32) : zero;
@@ -146,11 +149,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewResident) grouped_few_kernel(
             }
         }
         __syncthreads();
-        const int f = threadIdx.x & 15, tok = threadIdx.x >> 4;   // 16 tokens at most
-        if (f0 + f < p.N && tok < tokens) {
+        for (int i = threadIdx.x; i < 256; i += 32 * WARPS) {   // 16 tokens at most
+            const int f = i & 15, tok = i >> 4;
+            if (tok >= tokens || f0 + f >= p.N) continue;
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kFewWarps; ++w) s += part[w][tok][f];
+            for (int w = 0; w < WARPS; ++w) s += part[w][tok][f];
             const int64_t at = (int64_t)(lo + tok) * p.ldd + f0 + f;
             if (p.out_fp32)
                 reinterpret_cast<float*>(p.d)[at] = s;
@@ -159,6 +163,11 @@ __global__ void __launch_bounds__(kFewThreads, kFewResident) grouped_few_kernel(
         }
         __syncthreads();   // the next pass writes `part` again
     }
+}
+
+template <int NG, int WARPS>
+static void launch_few(const FewParams& p, dim3 grid, cudaStream_t s) {
+    grouped_few_kernel<NG, WARPS><<<grid, 32 * WARPS, 0, s>>>(p);
 }
 
 cudaError_t launch_gemm_grouped_few(const GroupedGemm& g, cudaStream_t s) {
@@ -179,10 +188,11 @@ cudaError_t launch_gemm_grouped_few(const GroupedGemm& g, cudaStream_t s) {
     p.out_fp32 = g.out_fp32;
     p.flags = g.flags;
     const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)std::min<int64_t>(g.rows, g.experts));
+    const bool long_k = p.K >= kFewLongK && (int64_t)grid.x * grid.y <= host::sm_count() * few_resident(16);
     if (g.rows <= 8)
-        grouped_few_kernel<1><<<grid, kFewThreads, 0, s>>>(p);
+        long_k ? launch_few<1, 16>(p, grid, s) : launch_few<1, 8>(p, grid, s);
     else
-        grouped_few_kernel<2><<<grid, kFewThreads, 0, s>>>(p);
+        long_k ? launch_few<2, 16>(p, grid, s) : launch_few<2, 8>(p, grid, s);
     return cudaGetLastError();
 }
 

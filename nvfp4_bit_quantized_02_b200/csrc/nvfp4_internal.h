@@ -150,7 +150,7 @@ struct GroupedWgrad {       // D_e[m][n] (+)= sum over e's rows t of A[t][m] B[t
     uint64_t budget_ns;
 };
 cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s);
-constexpr int kFewMaxRows = 64, kFewMaxExperts = 256;
+constexpr int kFewMaxRows = 64, kFewMaxExperts = 256, kFewLongK = 2048;
 cudaError_t launch_gemm_grouped_few(const GroupedGemm& g, cudaStream_t s);   // within those, b_kn = 0
 cudaError_t launch_wgrad_grouped(const GroupedWgrad& g, cudaStream_t s);
 

@@ -117,6 +117,13 @@ def test_gemm_exact_on_small_integers(kn):
     assert torch.equal(got.cpu().double(), _reference(a, w, off, kn)[0])
 
 
+@pytest.mark.parametrize("counts", [[1], [8], [24], [25], [64], [1, 0, 7], [9, 5]], ids=lambda c: f"{len(c)}x{sum(c)}")
+@pytest.mark.parametrize("K,N", [(1032, 712), (2040, 40), (2056, 264), (5000, 136)])
+def test_gemm_few_rows_of_a_long_reduction(counts, K, N):
+    for dtype in (torch.bfloat16, torch.float32):
+        _check_gemm(counts, K, N, False, dtype, before=1, behind=1, seed=K + sum(counts))
+
+
 @pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
 @pytest.mark.parametrize("rows", [3, 11, 40, 100])
 def test_gemm_long_runs_are_joined_by_rounding(rows, kn):
