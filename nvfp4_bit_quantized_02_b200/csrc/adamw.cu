@@ -44,46 +44,36 @@ struct AdamwTable {
     uint32_t key0[10], key1[10];   // Philox round keys of the arguments' seed (constant-bank operands)
 };
 
-// Decodes the four codes of a word times `scale`, one rounding each.  A code's exponent and mantissa
-// fields, placed at fp32's, read as its value times 2^-120 (subnormals too), and scale * 2^120 is exact;
-// where that leaves the fp32 range, or a code is NaN, the power of two is applied to the code first.
-template <bool SIGNED>
+// Decodes the four codes of a word times `scale`, one rounding each (a code is exact in fp16).
 __device__ __forceinline__ void decode4(uint32_t w, float scale, float* x) {
-    const float s = __fmul_rn(scale, 0x1p120f);
-    const bool nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-    const bool rare = nan || !(fabsf(scale) < 128.0f);
-    uint32_t bits[4];
+    uint32_t h[2];
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(h[0]), "=r"(h[1])
+        : "r"(w));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (SIGNED)
-            bits[i] = (uint32_t)((int32_t)(w << (24 - 8 * i)) >> 4) & 0x87F00000u;
-        else
-            bits[i] = (i == 3 ? w >> 4 : w << (20 - 8 * i)) & 0x07F00000u;
-    }
-    if (!rare) {
-#pragma unroll
-        for (int i = 0; i < 4; i += 2)
-            f2_split(f2_mul(f2(__uint_as_float(bits[i]), __uint_as_float(bits[i + 1])), f2c(s)), x[i], x[i + 1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool n = (bits[i] & 0x07F00000u) == 0x07F00000u;
-            x[i] = __fmul_rn(n ? __uint_as_float(0x7FC00000u) : __fmul_rn(__uint_as_float(bits[i]), 0x1p120f), scale);
-        }
+    for (int i = 0; i < 2; ++i) {
+        float lo, hi;
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(lo), "=f"(hi) : "r"(h[i]));
+        f2_split(f2_mul(f2(lo, hi), f2c(scale)), x[2 * i], x[2 * i + 1]);
     }
 }
 
-// E4M3 code of u = |x| * per (per = 448 * (1 / amax) of the block), unsigned, from the fp32 pattern of
-// x * per * 2^-120, whose bits 20-26 are the code's fields (below 2^-6 the number is an fp32
-// subnormal, rounded to the step that u + 2^-6 would have).  Adding `cut` to the 20 bits that are cut
-// off carries into the code where it rounds up: 2^20 - 1 - 16 r16 does so iff r16 < f * 2^16 (f = the
-// cut-off bits / 2^20), half a step less the parity bit gives nearest even.  All of it one place to
-// the left, where the sign falls out.
+// E4M3 code of u = |x| * per (per = 448 * (1 / amax) of the block) in the top byte, from the fp32
+// pattern of x * per * 2^-120, whose bits 20-26 are the code's fields (below 2^-6 the number is an fp32
+// subnormal, rounded to the step that u + 2^-6 would have).  Four places to the left, where the sign
+// falls out, 24 bits are cut off.  Adding `cut` to them carries into the code where it rounds up:
+// 2^24 - 1 - 256 r16 does so iff r16 < f * 2^16 (f = the cut-off bits / 2^24), half a step less the
+// parity bit gives nearest even.
 template <bool SR>
-__device__ __forceinline__ uint32_t e4m3_code(float scaled, uint32_t cut2) {
+__device__ __forceinline__ uint32_t e4m3_code(float scaled, uint32_t cut) {
     const uint32_t bits = __float_as_uint(scaled);
-    if (!SR) cut2 = 0xFFFFEu + 2u * ((bits >> 20) & 1u);
-    return min((2u * bits + cut2) >> 21, 0x7Eu);
+    if (!SR) cut = 0x7FFFFFu + ((bits >> 20) & 1u);
+    return 16u * bits + cut;
+}
+// The top bytes of four codes, at most 0x7E (u may exceed 448 by its rounding)
+__device__ __forceinline__ uint32_t pack_codes(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {
+    const uint32_t lo = __vminu2(__byte_perm(c0, c1, 0x7632), 0x7EFF7EFFu), hi = __vminu2(__byte_perm(c2, c3, 0x7632), 0x7EFF7EFFu);
+    return __byte_perm(lo, hi, 0x7531);
 }
 
 // The Philox words of a lane's two element quads.  A block of four words serves eight consecutive
@@ -146,12 +136,12 @@ __device__ __forceinline__ void encode_block(const float (&x)[8], uint32_t (&cod
         for (int i = 0; i < 4; i += 2) {
             float lo, hi;
             f2_split(f2_mul(f2_mul(f2(x[4 * j + i], x[4 * j + i + 1]), f2c(per)), f2c(0x1p-120f)), lo, hi);
-            // 2^20 - 1 - 16 r16 = 16 (r16's complement) + 15, doubled
+            // 2^24 - 1 - 256 r16: r16's complement and a byte of ones
             const uint32_t n = ~r[j][i >> 1];
-            c[i] = e4m3_code<SR>(lo, ((n << 5) & 0x1FFFE0u) | 30u);
-            c[i + 1] = e4m3_code<SR>(hi, ((n >> 11) & 0x1FFFE0u) | 30u);
+            c[i] = e4m3_code<SR>(lo, __byte_perm(n, 0xFFu, 0x5104));
+            c[i + 1] = e4m3_code<SR>(hi, __byte_perm(n, 0xFFu, 0x5324));
         }
-        codes[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        codes[j] = pack_codes(c[0], c[1], c[2], c[3]);
         if (SIGNED) {
             const uint32_t s01 = __byte_perm(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]), 0x0073);
             const uint32_t s23 = __byte_perm(__float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]), 0x0073);
@@ -253,8 +243,8 @@ __device__ __forceinline__ void block_step(const Places<FP8>& at, int64_t first,
         const float ms = *at.m_scale, vs = *at.v_scale;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            decode4<true>(mc[j], ms, m + 4 * j);
-            decode4<false>(vc[j], vs, v + 4 * j);   // the root
+            decode4(mc[j], ms, m + 4 * j);
+            decode4(vc[j], vs, v + 4 * j);   // the root
         }
         if (!FULL) {   // a NaN scale stays out of the padding
 #pragma unroll
