@@ -573,13 +573,8 @@ class LinearBF16:
 # ---------------------------------------------------------------------------------------
 # BF16 products grouped by expert (one weight per expert, token rows sorted by expert)
 # ---------------------------------------------------------------------------------------
-def _on_current_device(*tensors) -> int:
-    """The current device's index, which every tensor has to live on."""
-    dev = _CUR_DEVICE()
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"expected tensors on the current CUDA device ({dev}), got one on {t.device}")
-    return dev
+def _elsewhere(dev: int, *tensors):
+    raise ValueError(f"expected tensors on the current CUDA device ({dev}), got them on {[str(t.device) for t in tensors]}")
 
 
 def _call_context(dev: int, ws, stream):
@@ -624,23 +619,25 @@ def nvfp4_bf16_gemm_grouped(a: torch.Tensor, b: torch.Tensor, offsets: torch.Ten
     if a_col != 1 or b_col != 1:
         raise ValueError("inner dimensions must be contiguous")
     _offsets(offsets, E)
-    dev = _on_current_device(a, b, offsets)
-    if out is None:
-        if out_dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError("output must be bf16 or fp32")
-        out = _empty((rows, N), out_dtype, a.device, stream)
-    else:
+    if out is not None:
         out_dtype = out.dtype
-        if out_dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError("output must be bf16 or fp32")
-        if out.shape != (rows, N) or out.stride(1) != 1:
-            raise ValueError("out: [rows][N] with a contiguous inner dimension")
-        _on_current_device(out)
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise TypeError("output must be bf16 or fp32")
+    if out is None:
+        out = _empty((rows, N), out_dtype, a.device, stream)
+    elif out.shape != (rows, N):
+        raise ValueError("out: [rows][N] with a contiguous inner dimension")
+    out_row, out_col = out.stride()
+    if out_col != 1:
+        raise ValueError("out: [rows][N] with a contiguous inner dimension")
+    dev = _CUR_DEVICE()
+    if a.get_device() != dev or b.get_device() != dev or offsets.get_device() != dev or out.get_device() != dev:
+        _elsewhere(dev, a, b, offsets, out)
     ws_addr, raw = _call_context(dev, ws, stream)
     # a single row's or slice's stride means nothing: its width, and 0
     st = _lib().nvfp4_bf16_gemm_grouped(a.data_ptr(), a_row if rows > 1 else K, rows, offsets.data_ptr(), E, b.data_ptr(),
                                         b_row if b_rows > 1 else b_cols, b_expert if E > 1 else 0, 1 if b_kn else 0, N, K,
-                                        out.data_ptr(), out.stride(0) if rows > 1 else N,
+                                        out.data_ptr(), out_row if rows > 1 else N,
                                         OUT_FP32 if out_dtype is torch.float32 else OUT_BF16, ws_addr, raw)
     if st:
         _check(st, "nvfp4_bf16_gemm_grouped")
@@ -663,19 +660,22 @@ def nvfp4_bf16_wgrad_grouped(dy: torch.Tensor, x: torch.Tensor, offsets: torch.T
         raise ValueError("inner dimensions must be contiguous")
     E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
     _offsets(offsets, E)
-    dev = _on_current_device(dy, x, offsets)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out = _empty((max(E, 0), M, N), torch.float32, dy.device, stream)
-    else:
-        if out.dtype is not torch.float32 or out.shape != (E, M, N) or out.stride(2) != 1:
-            raise ValueError("out: fp32 [E][n][d] with a contiguous inner dimension")
-        _on_current_device(out)
+    elif out.dtype is not torch.float32 or out.shape != (E, M, N):
+        raise ValueError("out: fp32 [E][n][d] with a contiguous inner dimension")
+    out_expert, out_row, out_col = out.stride()
+    if out_col != 1:
+        raise ValueError("out: fp32 [E][n][d] with a contiguous inner dimension")
+    dev = _CUR_DEVICE()
+    if dy.get_device() != dev or x.get_device() != dev or offsets.get_device() != dev or out.get_device() != dev:
+        _elsewhere(dev, dy, x, offsets, out)
     ws_addr, raw = _call_context(dev, ws, stream)
     st = _lib().nvfp4_bf16_wgrad_grouped(dy.data_ptr(), dy_row if rows > 1 else M, x.data_ptr(), x_row if rows > 1 else N, rows,
-                                         offsets.data_ptr(), E, M, N, out.data_ptr(), out.stride(1) if M > 1 else N,
-                                         out.stride(0) if E > 1 else 0, 1 if accumulate else 0, ws_addr, raw)
+                                         offsets.data_ptr(), E, M, N, out.data_ptr(), out_row if M > 1 else N,
+                                         out_expert if E > 1 else 0, 1 if accumulate else 0, ws_addr, raw)
     if st:
         _check(st, "nvfp4_bf16_wgrad_grouped")
     return out

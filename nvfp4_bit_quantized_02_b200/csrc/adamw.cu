@@ -9,12 +9,13 @@
 // threads per SM.  The tensor table travels in the kernel's parameters (constant bank): no device
 // copy that a captured graph or a second call could share.
 //
-// Measured: 2 x 104857600 elements, fp32 moments, 1037 us, 6.07 TB/s, 93 % of the copy bandwidth: bound by
-// memory.  200 tensors of 1000 to 4.8 M elements (107 M in all), E4M3 moments, bf16 gradients, 426 us,
-// 4.3 TB/s: bound by instruction issue, ~97 an element at 2.7 per cycle and SM (Philox and the
-// rounding's random bits 23, square root and quotient 23).  Without effect there: loads one block
-// ahead in registers (530 us then, registers cost CTAs) or by an L2 prefetch (481), the approximate
-// quotient (435); 4 CTAs of 256 threads 443, 6 of 128 440.
+// Measured: 2 x 104857600 elements, fp32 moments, 1040 us, 6.05 TB/s, 92 % of the copy bandwidth: bound by
+// memory.  200 tensors of 1000 to 4.8 M elements (107 M in all), E4M3 moments, bf16 gradients, 384 us,
+// 4.8 TB/s: bound by instruction issue and load latency together, ~81 instructions an element (Philox and
+// the rounding's random bits 19, square root and quotient 23), two thirds of the issue slots taken.
+// Without effect there: the next block's loads ahead in registers (530 us when the rest took 443), by an
+// L2 prefetch (481) or by asynchronous copies into shared memory (425 when the rest took 384), streaming
+// loads and stores (387), the approximate quotient (2 %); 7 or 9 CTAs per SM 394, 4 of 256 threads 4 % more.
 //
 // A warp owns a block of 256 consecutive elements, lane l the elements 4 l + 128 j + (0..3),
 // j = 0, 1: every fp32 access is one 16-byte piece per lane and 512 consecutive bytes per warp, the

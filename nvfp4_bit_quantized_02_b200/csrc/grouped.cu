@@ -25,8 +25,9 @@
 // truncates as it accumulates (measured on N(0, 1) operands, relative to the result: 5e-7 after 512
 // products, 2e-6 after 2048, 9e-6 after 8192, 4e-5 after 32768), so with fp32 output an accumulator
 // holds at most 512 products, and the epilogue joins such runs in registers, rounded to nearest, while
-// the next run is under way: all 16 warps, 64 columns each.  That costs little: wgrad below takes 197.7 us
-// in runs of 512, 197.2 of 768, 191.7 in one.
+// the next run is under way: all 16 warps, 16 columns in turn, 64 at most.  That costs little: wgrad below
+// took 197.7 us in runs of 512, 197.2 of 768, 191.7 in one.  The 64 sums leave no register to spare (five
+// warps share a scheduler's 16384): read 16 columns at a time they spill, and wgrad takes 3 us more.
 //
 // The offsets stay on the device: every CTA reads them, takes their running maximum clamped to
 // [0, rows], and numbers the tiles of all experts; a pair walks tiles pair, pair + pairs, ...
@@ -35,12 +36,12 @@
 //
 // Measured on 16384 rows x 16 experts of 5120 x 1280, even counts, beside cuBLAS' batched product of the
 // same shapes (us; a call by itself / without a pause, where the 1000 W limit holds the SMs at ~1.5 GHz):
-//   fprop 163 / 188, cuBLAS 165 / 191; dgrad 165 / 191, cuBLAS 155 / 181; wgrad 197 / 226, cuBLAS 191 / 221.
-// One expert of 8192 x 5120 x 5120: fprop 1.5 PFLOP/s, as cuBLAS; the tensor pipe is active in 92 % of
-// its cycles.  Here 4.3 tiles a pair make a fifth wave that is a third full, and wgrad writes 419 MB of
-// fp32 (141 us without its stores).  Without effect: the reduction begun at another stage for each tile,
-// stores with an evict-first policy or spread out by sleeps, bands of 2 to 16 tiles, 4 or 5 stages of
-// 64 products, longer suspended waits.
+//   fprop 152 / 183, cuBLAS 161 / 193; dgrad 155 / 187, cuBLAS 150 / 181; wgrad 187 / 223, cuBLAS 184 / 221.
+// One expert of 8192 x 5120 x 5120: fprop 273 / 323 (1.57 PFLOP/s), cuBLAS 277 / 327; the tensor pipe is
+// active in 92 % of its cycles.  Here 4.3 tiles a pair make a fifth wave that is a third full, and wgrad
+// writes 419 MB of fp32 (of 197 us 56 were its stores).  Without effect: the last wave's tiles cut into row
+// parts, the reduction begun at another stage for each tile, stores with an evict-first policy or spread
+// out by sleeps, bands of 2 to 16 tiles, 4 or 5 stages of 64 products, longer suspended waits.
 #include <algorithm>
 
 #include "nvfp4_device.cuh"
@@ -203,8 +204,9 @@ struct Walk {
 // operand rows (256 features and its own rows, evenly cut), since a stage takes the time its operands
 // need from L2.  wgrad's Q tiles cut features, the same for every expert (8192 rows, one expert of
 // 1000 x 1000: 54.8 us, with tiles of 256 67.5).
-// All of it stands between a launch and its first load, so it is one pass; the seven microseconds
-// that the smallest launches took were four of this, of waits for stores at the end and of a drain.
+// All of it stands between a launch and its first load, hence one pass without integer divisions: a
+// launch of one small tile takes 4.9 us, and took 6.8 with two passes, a drain at every end and barriers
+// there that wait for the stores.
 template <int MODE>
 __device__ __forceinline__ void plan(GroupedSmem& sm, const GroupedParams& p, int pairs) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
