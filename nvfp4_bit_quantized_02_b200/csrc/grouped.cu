@@ -339,10 +339,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
 
     if (warp == 0) {
         // ------------------------------- producer (both CTAs) --------------------------------
-        if (lane == 0) {
+        if (elect_one()) {
             Walk<MODE> walk(p, sm, pair, pairs);
             Tile c;
-            int g = 0, tails = 0;
+            int g = 0, tails = 0, s = 0;   // stages issued, the next one's slot
+            uint32_t parity = 1;           // of the slot's `empty`: at first there is no use to wait for
+            const uint32_t base = smem_u32(smem), empty = smem_u32(&sm.empty[0]), full = smem_u32(&sm.full[0]),
+                           leader_full = map_rank(full, 0);
             bool ok = true;
             while (ok && walk.next(c)) {
                 const int p0 = c.p0 + (int)rank * 128, half = c.n >> 1, q0 = c.q0 + (int)rank * half;
@@ -351,24 +354,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                 const bool pwide = S::kPmn && p0 + 128 <= p.P, qwide = S::kQmn && half == 128 && q0 + 128 <= p.Q;
                 const uint32_t tx = (uint32_t)(S::kOpBytes + (S::kQmn ? (half <= 64 ? S::kBlock : S::kOpBytes) : (64 * S::kK) << qbox));
                 const int z = c.e * p.expert_step;
-                for (int k = 0; k < c.klen; k += S::kK, ++g) {
-                    const int s = g % S::kStages;
-                    if (!mbar_wait(smem_u32(&sm.empty[s]), ((uint32_t)(g / S::kStages) & 1u) ^ 1u, abort_flag, p.flags, p.budget_ns)) {
+                for (int k = 0; k < c.klen; k += S::kK) {
+                    if (!mbar_wait(empty + 8u * s, parity, abort_flag, p.flags, p.budget_ns)) {
                         ok = false;
                         break;
                     }
-                    uint32_t bar = map_rank(smem_u32(&sm.full[s]), 0);
+                    uint32_t bar = leader_full + 8u * s;
                     const bool tail = MODE == kWgrad && (min(S::kK, c.klen - k) & 15) != 0;
                     if (tail) {
                         bar = smem_u32(&sm.tail[tails % S::kStages]);
                         mbar_expect_tx(bar, tx);
                         ++tails;
                     } else if (rank == 0) {
-                        mbar_expect_tx(smem_u32(&sm.full[s]), 2u * tx);
-                        if (MODE == kWgrad) mbar_arrive(smem_u32(&sm.full[s]));
+                        mbar_expect_tx(full + 8u * s, 2u * tx);
+                        if (MODE == kWgrad) mbar_arrive(full + 8u * s);
                     }
                     sm.stage_tx[s] = tail ? 0u : tx;
-                    const uint32_t dst = smem_u32(smem + s * S::kStageBytes), dq = dst + S::kOpBytes;
+                    const uint32_t dst = base + (uint32_t)(s * S::kStageBytes), dq = dst + S::kOpBytes;
+                    ++g;
+                    if (++s == S::kStages) {
+                        s = 0;
+                        parity ^= 1u;
+                    }
                     const int kk = c.k0 + k;
                     if (!S::kPmn) {
                         tma_load_3d_pair(dst, &maps.p, kk, p0, z, bar);
@@ -401,63 +408,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
     } else if (warp == 1) {
         if (rank == 0) {
             // ------------------------------- MMA issuer (leader) -----------------------------
-            // the whole warp runs the loop, one elected lane issues
-            const uint32_t base = smem_u32(smem);
-            const uint64_t pdesc = S::kPmn ? desc_mn_major(base, S::kBlock) : desc_k_major(base);
-            const uint64_t qdesc = S::kQmn ? desc_mn_major(base + S::kOpBytes, S::kBlock) : desc_k_major(base + S::kOpBytes);
-            // 16 products further: 16 rows MN-major, 32 bytes K-major (of rows of 64 products: the next
-            // 64 are the next block, of the tile's box rows)
-            constexpr uint32_t mn_step = 2048 >> 4, k_step = 32 >> 4;
-            // fp32 accumulator, bf16 operands, transpose bits of the MN-major ones, M = 256
-            constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | (S::kPmn ? 1u << 15 : 0u) |
-                                        (S::kQmn ? 1u << 16 : 0u) | ((uint32_t)(256 >> 4) << 24);
-            Walk<MODE> walk(p, sm, pair, pairs);
-            Tile c;
-            int g = 0, it = 0;
-            bool ok = true;
-            while (ok && walk.next(c)) {
-                const uint32_t idesc = idesc0 | ((uint32_t)(c.n >> 3) << 17);
-                const int stages = c.stages;
-                const uint32_t qblock = (uint32_t)((c.n >> 1) <= 32 ? 4096 : (c.n >> 1) <= 64 ? 8192 : 16384) >> 4;
-                for (int k = 0; ok && k < stages; ++it) {
-                    const int end = min(stages, k + min(run, stages - k));
-                    const int buf = it & 1;
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.tempty[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag,
-                                                           p.flags, p.budget_ns))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t acc = tmem + 256u * buf;
-                    const int first = k;
-                    for (; k < end; ++k, ++g) {
-                        const int s = g % S::kStages;
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.full[s]), (uint32_t)(g / S::kStages) & 1u, abort_flag,
-                                                               p.flags, p.budget_ns))) {
+            if (elect_one()) {
+                const uint32_t base = smem_u32(smem);
+                const uint64_t pdesc = S::kPmn ? desc_mn_major(base, S::kBlock) : desc_k_major(base);
+                const uint64_t qdesc = S::kQmn ? desc_mn_major(base + S::kOpBytes, S::kBlock) : desc_k_major(base + S::kOpBytes);
+                // 16 products further: 16 rows MN-major, 32 bytes K-major (of rows of 64 products: the next
+                // 64 are the next block, of the tile's box rows)
+                constexpr uint32_t mn_step = 2048 >> 4, k_step = 32 >> 4;
+                // fp32 accumulator, bf16 operands, transpose bits of the MN-major ones, M = 256
+                constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | (S::kPmn ? 1u << 15 : 0u) |
+                                            (S::kQmn ? 1u << 16 : 0u) | ((uint32_t)(256 >> 4) << 24);
+                Walk<MODE> walk(p, sm, pair, pairs);
+                Tile c;
+                int it = 0, s = 0;
+                uint32_t parity = 0;   // of the slot's `full`
+                const uint32_t full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
+                bool ok = true;
+                while (ok && walk.next(c)) {
+                    const uint32_t idesc = idesc0 | ((uint32_t)(c.n >> 3) << 17);
+                    const uint32_t qblock = (uint32_t)((c.n >> 1) <= 32 ? 4096 : (c.n >> 1) <= 64 ? 8192 : 16384) >> 4;
+                    for (int k = 0; k < c.stages; ++it) {
+                        const int end = min(c.stages, k + min(run, c.stages - k));
+                        const int buf = it & 1;
+                        if (!mbar_wait<true>(smem_u32(&sm.tempty[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, p.flags, p.budget_ns)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const int steps = min(S::kK / 16, (c.klen - S::kK * k + 15) >> 4);
-                        const uint64_t off = (uint64_t)((s * S::kStageBytes) >> 4);
-                        if (elect_one()) {
+                        const uint32_t acc = tmem + 256u * buf;
+                        uint32_t add = 0;   // an accumulator's first MMA stores
+                        for (; k < end; ++k) {
+                            if (!mbar_wait<MODE == kWgrad>(full + 8u * s, parity, abort_flag, p.flags, p.budget_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint64_t off = (uint64_t)((uint32_t)(s * S::kStageBytes) >> 4);
+                            const uint64_t pd = pdesc + off, qd = qdesc + off;
+                            const auto mma = [&](int j) {
+                                mma_bf16_pair(acc, pd + (S::kPmn ? mn_step : k_step) * j,
+                                              qd + (S::kQmn ? mn_step * j : (j >> 2) * qblock + k_step * (j & 3)), idesc, j ? 1u : add);
+                            };
+                            const int left = c.klen - S::kK * k;
+                            if (left >= S::kK) {
 #pragma unroll
-                            for (int j = 0; j < S::kK / 16; ++j)
-                                if (j < steps)
-                                    mma_bf16_pair(acc, pdesc + off + (S::kPmn ? mn_step : k_step) * j,
-                                                  qdesc + off + (S::kQmn ? mn_step * j : (j >> 2) * qblock + k_step * (j & 3)), idesc,
-                                                  (k > first || j > 0) ? 1u : 0u);
-                            mma_commit_pair(smem_u32(&sm.empty[s]));
+                                for (int j = 0; j < S::kK / 16; ++j) mma(j);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < S::kK / 16; ++j)
+                                    if (16 * j < left) mma(j);
+                            }
+                            add = 1;
+                            mma_commit_pair(empty + 8u * s);
+                            if (++s == S::kStages) {
+                                s = 0;
+                                parity ^= 1u;
+                            }
                         }
-                        __syncwarp();
+                        if (!ok) break;
+                        mma_commit_pair(smem_u32(&sm.tfull[buf]));
                     }
-                    if (ok && elect_one()) mma_commit_pair(smem_u32(&sm.tfull[buf]));
-                    __syncwarp();
                 }
+                mma_commit_local(smem_u32(&sm.done));
+                mbar_wait(smem_u32(&sm.done), 0u, abort_flag, p.flags, kGDrainBudgetNs, false);
             }
-            if (elect_one()) mma_commit_local(smem_u32(&sm.done));
             __syncwarp();
-            mbar_wait(smem_u32(&sm.done), 0u, abort_flag, p.flags, kGDrainBudgetNs, false);
         } else {
             // the peer's drained accumulators as one remote arrival each
             Walk<MODE> walk(p, sm, pair, pairs);
