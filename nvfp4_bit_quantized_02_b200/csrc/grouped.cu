@@ -36,12 +36,15 @@
 //
 // Measured on 16384 rows x 16 experts of 5120 x 1280, even counts, beside cuBLAS' batched product of the
 // same shapes (us; a call by itself / without a pause, where the 1000 W limit holds the SMs at ~1.5 GHz):
-//   fprop 152 / 183, cuBLAS 161 / 193; dgrad 155 / 187, cuBLAS 150 / 181; wgrad 187 / 223, cuBLAS 184 / 221.
-// One expert of 8192 x 5120 x 5120: fprop 273 / 323 (1.57 PFLOP/s), cuBLAS 277 / 327; the tensor pipe is
+//   fprop 153 / 186, cuBLAS 161 / 195; dgrad 154 / 190, cuBLAS 151 / 184; wgrad 187 / 226, cuBLAS 184 / 223.
+// One expert of 8192 x 5120 x 5120: fprop 271 / 320 (1.58 PFLOP/s), cuBLAS 278 / 329; the tensor pipe is
 // active in 92 % of its cycles.  Here 4.3 tiles a pair make a fifth wave that is a third full, and wgrad
 // writes 419 MB of fp32 (of 197 us 56 were its stores).  Without effect: the last wave's tiles cut into row
 // parts, the reduction begun at another stage for each tile, stores with an evict-first policy or spread
 // out by sleeps, bands of 2 to 16 tiles, 4 or 5 stages of 64 products, longer suspended waits.
+// The producer's and the MMA issuer's loops are one elected lane's and kept short: a stage of 64 products
+// takes them 320 cycles, less than 256 rows' MMAs (512); at 465 they bound every narrower tile (256 rows x
+// 5120 x 1280 25.0 us, now 19.2).
 #include <algorithm>
 
 #include "nvfp4_device.cuh"
@@ -676,14 +679,19 @@ static bool mn_maps(CUtensorMap* narrow, CUtensorMap* wide, const void* x, int64
     return host::bf16_map(wide, x, 4, wdims, wstrides, wbox);
 }
 
+constexpr int kFewManyN = 4096, kFewOneN = 2048;   // features from which the pair kernel has tiles enough
+
 cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
     // A few rows only stream the weights: the kernel without set-up (grouped_few.cu), whose passes over an
-    // expert's weights take 16 rows each.  64 rows spread over 16 experts of 1280 x 5120 take it 40 us and
-    // the pair kernel 55, of 5120 x 1280 42 and 40; all with one of the 16 33 and 25, 17 and 10.  256 rows
-    // spread over 16 take 65 and 55.  With one expert in all the passes are known: 24 rows of 5120 x 1280
-    // take 9.7 and 9.4, 64 rows 16 and 9.8, of 1280 x 5120 (where the pair kernel has five tiles) 21 and 25.
-    const bool passes = g.experts == 1 && g.rows > 24 && g.K < kFewLongK;
-    if (!g.b_kn && g.rows <= kFewMaxRows && g.experts <= kFewMaxExperts && !passes) return launch_gemm_grouped_few(g, s);
+    // expert's weights take 16 rows each.  Rows spread over many experts are one pass: 64 rows over 16
+    // experts of N x K = 1280 x 5120 take it 40 us and the pair kernel (80 tiles for 74 pairs) 50, 2816 x
+    // 2048 34.1 and 35.5; with 4096 features the pair kernel's tiles go round: 4096 x 1408 35.8 and 33.7,
+    // and all rows with one of the 16 16.6 and 8.7 (16 rows 8.6 and 8.3, 8 rows 5.6 and 8.3).
+    // With one expert in all the passes are known: 24 rows of 4096 x 4096 16.1 and 17.3, 32 rows 17.8
+    // and 17.4, 2048 x 512 3.8 and 5.4, 5.4 and 5.4; where the pair kernel has few and long tiles, 1280 x
+    // 5120, 48 rows 17.0 and 18.6.
+    const int64_t most = g.experts > 1 ? (g.N < kFewManyN ? kFewMaxRows : 8) : (g.N < kFewOneN && g.K >= kFewLongK ? kFewMaxRows : 24);
+    if (!g.b_kn && g.rows <= most && g.experts <= kFewMaxExperts) return launch_gemm_grouped_few(g, s);
     GroupedParams p{};
     p.offsets = g.offsets;
     p.d = g.d;

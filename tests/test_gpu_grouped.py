@@ -118,7 +118,7 @@ def test_gemm_exact_on_small_integers(kn):
 
 
 @pytest.mark.parametrize("counts", [[1], [8], [24], [25], [64], [1, 0, 7], [9, 5]], ids=lambda c: f"{len(c)}x{sum(c)}")
-@pytest.mark.parametrize("K,N", [(1032, 712), (2040, 40), (2056, 264), (5000, 136)])
+@pytest.mark.parametrize("K,N", [(1032, 712), (2040, 40), (2056, 264), (5000, 136), (136, 4104)])
 def test_gemm_few_rows_of_a_long_reduction(counts, K, N):
     for dtype in (torch.bfloat16, torch.float32):
         _check_gemm(counts, K, N, False, dtype, before=1, behind=1, seed=K + sum(counts))
