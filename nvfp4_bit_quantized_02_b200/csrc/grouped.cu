@@ -87,6 +87,7 @@ struct GroupedSmem {        // behind the stages
     uint64_t edrained[2];          // peer: its epilogue has read it
     uint64_t done;
     uint32_t tmem, abort, peer_abort, issued, tails;
+    uint32_t consumed, runs;       // leader: stages and accumulators that the MMA issuer has committed
     uint32_t stage_tx[kMaxStages]; // bytes per CTA of the last use of each stage, 0: a tail
     int32_t best;                  // the chosen width's number
     uint32_t cost[kWidths];        // fp32 patterns, the last three bits the width's number
@@ -312,6 +313,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         sm.peer_abort = 0u;
         sm.issued = 0u;
         sm.tails = 0u;
+        sm.consumed = 0u;
+        sm.runs = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(S::kPmn ? &maps.p_wide : &maps.p);
         prefetch_map(S::kQmn ? &maps.q_deep[0] : &maps.q[2]);
@@ -407,6 +410,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             }
             sm.issued = (uint32_t)g;   // read by the drain, after the cluster barrier
             sm.tails = (uint32_t)tails;
+            // the releases of the last stages, which the leader's MMAs signal in both CTAs, land before the end
+            for (int k = max(0, g - S::kStages); ok && k < g; ++k)
+                ok = mbar_wait(empty + 8u * (k % S::kStages), (uint32_t)(k / S::kStages) & 1u, abort_flag, p.flags, p.budget_ns);
         }
     } else if (warp == 1) {
         if (rank == 0) {
@@ -424,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                 Walk<MODE> walk(p, sm, pair, pairs);
                 Tile c;
                 int it = 0, s = 0;
-                uint32_t parity = 0;   // of the slot's `full`
+                uint32_t parity = 0, consumed = 0;   // of the slot's `full`; stages committed
                 const uint32_t full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
                 bool ok = true;
                 while (ok && walk.next(c)) {
@@ -463,6 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                             }
                             add = 1;
                             mma_commit_pair(empty + 8u * s);
+                            ++consumed;
                             if (++s == S::kStages) {
                                 s = 0;
                                 parity ^= 1u;
@@ -474,6 +481,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
                 }
                 mma_commit_local(smem_u32(&sm.done));
                 mbar_wait(smem_u32(&sm.done), 0u, abort_flag, p.flags, kGDrainBudgetNs, false);
+                sm.consumed = consumed;
+                sm.runs = (uint32_t)it;
             }
             __syncwarp();
         } else {
@@ -598,14 +607,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         }
     }
 
-    // Each warp hands an abort that it has seen (its own at least) to the leader.  What the drain reads
-    // is released by those warps and by the producers alone: by every warp, it would wait for the output's
-    // stores, which the next kernel waits for anyway.
+    // Each warp hands an abort that it has seen (its own at least) to the leader.  No arrival may land in
+    // a CTA that has ended.  Those that the MMAs signal are waited for: by the producers and the epilogues,
+    // after an abort by the drain.  Those that the peer makes on the leader's barriers (warp 1's for a
+    // pair's last accumulators are waited for by nobody) are ordered before the leader's end by a release
+    // here, as is what the drain reads.  Only the epilogue arrives without one, since it makes no such
+    // arrival and a release would wait for its stores of the output, which the next kernel waits for anyway.
     const bool aborted = __any_sync(0xFFFFFFFFu, *abort_flag != 0u);
     if (aborted && rank == 1 && lane == 0) st_cluster_u32(map_rank(smem_u32(&sm.peer_abort), 0), 1u);
     __syncwarp();
     tc_fence_before();
-    if (aborted || warp == 0)
+    if (aborted || warp < 2 || warp >= 2 + kEpiWarps)
         cluster_arrive();   // both producers have stopped and published what they issued
     else
         cluster_arrive_relaxed();
@@ -620,6 +632,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         const int tails = (int)sm.tails;
         for (int j = max(0, tails - S::kStages); j < tails; ++j)
             mbar_wait(smem_u32(&sm.tail[j % S::kStages]), (uint32_t)(j / S::kStages) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
+        // what the MMA issuer has committed signals both CTAs
+        const int consumed = (int)ld_cluster_u32(map_rank(smem_u32(&sm.consumed), 0)), runs = (int)ld_cluster_u32(map_rank(smem_u32(&sm.runs), 0));
+        for (int k = max(0, consumed - S::kStages); k < consumed; ++k)
+            mbar_wait(smem_u32(&sm.empty[k % S::kStages]), (uint32_t)(k / S::kStages) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
+        for (int i = max(0, runs - 2); i < runs; ++i)
+            mbar_wait(smem_u32(&sm.tfull[i & 1]), (uint32_t)(i >> 1) & 1u, abort_flag, p.flags, kGDrainBudgetNs, false);
         if (rank == 0) {
             const int gl = (int)sm.issued, gp = (int)ld_cluster_u32(map_rank(smem_u32(&sm.issued), 1)), gm = max(gl, gp);
             for (int k = max(0, gm - S::kStages); k < gm; ++k) {
