@@ -220,7 +220,7 @@ __device__ __forceinline__ void plan(GroupedSmem& sm, const GroupedParams& p, in
     bool bad = false;
     for (int i = lane; i - lane <= p.experts; i += 32) {   // lane: the run that ends at offset i
         const bool in = i <= p.experts;
-        const int o = in ? __ldg(p.offsets + i) : 0;
+        const int o = in ? ld_global_s32(p.offsets + i) : 0;
         int v = in ? min(max(o, 0), p.rows) : 0;
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {

@@ -53,3 +53,23 @@ def test_short_launches_behind_one_another():
     for got, ref in zip(runs[0], want):
         assert torch.equal(got.cpu().double(), ref)
     assert all(torch.equal(p, q) for r in runs[1:] for p, q in zip(runs[0], r))
+
+
+def test_offsets_written_by_the_kernel_before():
+    # the call's set-up overlaps the end of the kernel that writes its offsets: they are read behind it
+    m = nv()
+    g = torch.Generator().manual_seed(2)
+    K, N = 72, 136
+    a, w = _ints(g, 200, K), _ints(g, 3, N, K)
+    offs = [_off(c) for c in ([200, 0, 0], [0, 150, 50], [20, 60, 120])]
+    want = [_products(a, w, o, False) for o in offs]
+    a, w, offs = a.cuda(), w.cuda(), [o.cuda() for o in offs]
+    off = torch.zeros_like(offs[0])
+    ws = m.Workspace()
+    outs = []
+    for i in range(60):
+        off.copy_(offs[i % 3])
+        outs.append(m.nvfp4_bf16_gemm_grouped(a, w, off, out_dtype=torch.float32, ws=ws))
+    assert m.nvfp4_poll(ws) == 0
+    for i, out in enumerate(outs):
+        assert torch.equal(out.cpu().double(), want[i % 3]), i
