@@ -62,6 +62,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
             : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {   // without suspending the thread
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ uint64_t cycles() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%clock64;" : "=l"(t));
@@ -70,18 +81,17 @@ __device__ __forceinline__ uint64_t cycles() {
 // Bounded wait.  False if the CTA aborted (another role ran out of time) or this wait ran out of its
 // budget (it then raises the abort and the timeout flag).  honor_abort = false: the drain after
 // an abort, which must still see copies land.  The budget is counted in SM cycles, 2 per
-// nanosecond.
+// nanosecond.  A try_wait that fails has suspended its thread for 7800 cycles, whatever time it is given
+// as a hint, so a budget near that (kBriefNs) polls with test_wait.
+constexpr uint64_t kBriefNs = 20000;
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, uint32_t* flags,
                                           uint64_t budget_ns, bool honor_abort = true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
+    const bool brief = budget_ns < kBriefNs;
+    if (!brief && mbar_try_wait<CLUSTER>(bar, parity)) return true;
     const uint64_t t0 = cycles(), limit = 2 * budget_ns;
     while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
+        if (brief ? mbar_test_wait(bar, parity) : mbar_try_wait<CLUSTER>(bar, parity)) return true;
         if (honor_abort && *abort) return false;
         if (cycles() - t0 > limit) {
             *abort = 1u;

@@ -73,3 +73,48 @@ def test_offsets_written_by_the_kernel_before():
     assert m.nvfp4_poll(ws) == 0
     for i, out in enumerate(outs):
         assert torch.equal(out.cpu().double(), want[i % 3]), i
+
+
+def _expired(m, ws, call):
+    """The status of a call whose waits have a nanosecond."""
+    m.nvfp4_set_wait_budget_ns(1)
+    try:
+        call()
+        return m.nvfp4_poll(ws)
+    finally:
+        m.nvfp4_set_wait_budget_ns(0)     # back to the default
+
+
+@pytest.mark.parametrize("op", ["fprop", "dgrad", "wgrad"])
+@pytest.mark.parametrize("counts", [[300, 0, 77, 1], [129] * 90], ids=["few tiles", "many tiles"])
+def test_an_expired_call_drains_and_the_next_is_right(op, counts):
+    # the first wait for a load takes far more than a nanosecond: the call stops with copies in flight and
+    # lets them land.  fp32 output, i.e. short accumulators; wgrad's tails land on barriers of their own
+    m = nv()
+    g = torch.Generator().manual_seed(3)
+    K, N, off = 520, 264, _off(counts)
+    w, x, dy = _ints(g, len(counts), N, K), _ints(g, sum(counts), K), _ints(g, sum(counts), N)
+    want = {"fprop": lambda: _products(x, w, off, False), "dgrad": lambda: _products(dy, w, off, True), "wgrad": lambda: _wgrads(dy, x, off)}[op]()
+    w, x, dy, off = (t.cuda() for t in (w, x, dy, off))
+    ws = m.Workspace()
+    call = {"fprop": lambda: m.nvfp4_bf16_gemm_grouped(x, w, off, out_dtype=torch.float32, ws=ws),
+            "dgrad": lambda: m.nvfp4_bf16_gemm_grouped(dy, w, off, b_kn=True, out_dtype=torch.float32, ws=ws),
+            "wgrad": lambda: m.nvfp4_bf16_wgrad_grouped(dy, x, off, ws=ws)}[op]
+    assert torch.equal(call().cpu().double(), want) and m.nvfp4_poll(ws) == 0
+    for _ in range(10):
+        assert _expired(m, ws, call) == 8 and m.nvfp4_poll(ws) == 0
+        assert torch.equal(call().cpu().double(), want) and m.nvfp4_poll(ws) == 0
+
+
+def test_an_expired_wgrad_of_a_long_run():
+    m = nv()
+    g = torch.Generator().manual_seed(4)
+    rows = 2 ** 18 + 77
+    dy, x = _ints(g, rows, 256, top=1), _ints(g, rows, 256, top=1)
+    want = (dy.float().t() @ x.float()).double()[None]        # |sums| <= 2^19: exact
+    dy, x, off = dy.cuda(), x.cuda(), torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    ws = m.Workspace()
+    call = lambda: m.nvfp4_bf16_wgrad_grouped(dy, x, off, ws=ws)
+    for _ in range(3):
+        assert _expired(m, ws, call) == 8
+        assert torch.equal(call().cpu().double(), want) and m.nvfp4_poll(ws) == 0
