@@ -587,15 +587,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
         // that hold the last one; the rest of those 16 is cleared, in both operands (0 x NaN).
         Walk<MODE> walk(p, sm, pair, pairs);
         Tile c;
-        int g = 0, tails = 0;
+        // From one tail to the next may be the whole launch: a budget for each stage between them.
+        int g = 0, tails = 0, waited = 0;
         while (walk.next(c)) {
             g += c.stages;
             const int last = c.klen % S::kK;
             if (!(last & 15)) continue;
+            const uint64_t budget = min(p.budget_ns, (uint64_t)1 << 40) * (uint32_t)(g - waited);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.tail[tails % S::kStages]), (uint32_t)(tails / S::kStages) & 1u,
-                                                   abort_flag, p.flags, p.budget_ns)))
+                                                   abort_flag, p.flags, budget)))
                 break;
             ++tails;
+            waited = g;
             const int s = (g - 1) % S::kStages;
             // a lane clears 16 bytes of each row of one of the stage's four blocks
             const uint32_t box = smem_u32(smem + s * S::kStageBytes) + (uint32_t)(lane >> 3) * (uint32_t)S::kBlock + (uint32_t)(lane & 7) * 16u;

@@ -118,3 +118,27 @@ def test_an_expired_wgrad_of_a_long_run():
     for _ in range(3):
         assert _expired(m, ws, call) == 8
         assert torch.equal(call().cpu().double(), want) and m.nvfp4_poll(ws) == 0
+
+
+def test_a_tail_behind_a_long_run_is_waited_for():
+    # Two experts of 64 tiles: the first one's are over a millisecond long and end at a whole stage, most
+    # pairs then take one of the second's, whose single stage is a tail.  No single load or product takes
+    # long, so a budget of 0.25 ms suffices.
+    m = nv()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    counts = [2 ** 19, 17]
+    dy, x = (torch.randint(-1, 2, (sum(counts), 2048), generator=g, device="cuda", dtype=torch.int8).bfloat16() for _ in range(2))
+    off = _off(counts).cuda()
+    ws = m.Workspace()
+    out = torch.empty(2, 2048, 2048, device="cuda")
+    m.nvfp4_bf16_wgrad_grouped(dy, x, off, out=out, ws=ws)
+    assert m.nvfp4_poll(ws) == 0
+    out.zero_()
+    m.nvfp4_set_wait_budget_ns(250000)
+    try:
+        m.nvfp4_bf16_wgrad_grouped(dy, x, off, out=out, ws=ws)
+        assert m.nvfp4_poll(ws) == 0
+    finally:
+        m.nvfp4_set_wait_budget_ns(0)
+    for e, (lo, hi) in enumerate(((0, counts[0]), (counts[0], sum(counts)))):
+        assert torch.equal(out[e], dy[lo:hi].float().t() @ x[lo:hi].float()), e     # integers up to 2^19
