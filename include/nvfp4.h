@@ -398,7 +398,7 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
  *                                                      weight buffer, no transposed copy).
  * A [rows][lda] bf16; B_e starts at b + e * stride_b (elements) with leading dimension ldb; D
  * [rows][ldd] bf16 or fp32.  Rows of D that no expert owns are left as they were.  fp32
- * accumulation; with fp32 output, partial sums of at most 512 products are joined in fp32
+ * accumulation; partial sums of at most 512 products (bf16 output: 1024) are joined in fp32
  * registers (round to nearest), since the tensor core truncates as it accumulates.  Each row's
  * result depends on that row and its expert's weight alone, but for the choice of kernel by `rows`.
  * D overlaps no operand.

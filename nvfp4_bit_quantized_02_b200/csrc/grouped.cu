@@ -23,11 +23,14 @@
 // The accumulator is double-buffered (2 x 256 TMEM columns).  Where a tile is one accumulator, half of
 // the epilogue warps take the even ones and half the odd ones, 16 columns in turn.  The tensor core
 // truncates as it accumulates (measured on N(0, 1) operands, relative to the result: 5e-7 after 512
-// products, 2e-6 after 2048, 9e-6 after 8192, 4e-5 after 32768), so with fp32 output an accumulator
-// holds at most 512 products, and the epilogue joins such runs in registers, rounded to nearest, while
-// the next run is under way: all 16 warps, 16 columns in turn, 64 at most.  That costs little: wgrad below
-// took 197.7 us in runs of 512, 197.2 of 768, 191.7 in one.  The 64 sums leave no register to spare (five
-// warps share a scheduler's 16384): read 16 columns at a time they spill, and wgrad takes 3 us more.
+// products, 2e-6 after 2048, 9e-6 after 8192, 4e-5 after 32768; positive operands, 6e-3 after 2^20), so
+// an accumulator holds at most 512 products with fp32 output and 1024 with bf16, whose half step is 2e-3
+// at least, and the epilogue joins such runs in registers, rounded to nearest, while the next run is under
+// way: all 16 warps, 16 columns in turn, 64 at most.  fp32 runs of 512 cost wgrad of the shapes below 3 %
+// over one accumulator.  bf16 runs of 1024 cost 0 to 3 %: fprop of those shapes 157.7 us in one, 158.3 in
+// runs of 1024; 8 experts of 4096 x 5120 x 5120 called without a pause 1201 and 1240; runs of 512 are
+// 2 % slower again.  The 64 sums leave no register to spare (five warps share a scheduler's 16384): read
+// 16 columns at a time they spill, and wgrad takes 3 us more.
 //
 // The offsets stay on the device: every CTA reads them, takes their running maximum clamped to
 // [0, rows], and numbers the tiles of all experts; a pair walks tiles pair, pair + pairs, ...
@@ -60,6 +63,7 @@ constexpr int kMaxStages = 6;
 constexpr int kRingBytes = 192 * 1024;                   // every instantiation's stages together
 constexpr int kEpiWarps = 16;
 constexpr int kRunK = 512;                               // products per accumulator with fp32 output
+constexpr int kRunBf16 = 1024;                           // and with bf16 output
 constexpr int kWidths = 5;                               // Q rows per tile: 256, 224, ... 128 (the plan below)
 constexpr int kBand = 8;                                 // Q tiles of an expert swept together (L2 reuse)
 constexpr uint64_t kGDrainBudgetNs = 2000000000ull;      // teardown waits, whatever the caller's budget
@@ -341,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
     cluster_wait();   // the peer's too
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    const int run = p.out_fp32 ? kRunK / S::kK : 1 << 30;   // stages per accumulator
+    const int run = (p.out_fp32 ? kRunK : kRunBf16) / S::kK;   // stages per accumulator
 
     if (warp == 0) {
         // ------------------------------- producer (both CTAs) --------------------------------
@@ -578,8 +582,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MODE>::kThread
             }
             if (!ok) continue;
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-                if (c0 + 64 * h < c.qn) put_fp32<MODE>(acc + 16 * h, p, at + (c0 + 64 * h) * p.ldd, f, c.qn - (c0 + 64 * h));
+            for (int h = 0; h < 4; ++h) {
+                if (c0 + 64 * h >= c.qn) break;
+                if (MODE == kWgrad || p.out_fp32)
+                    put_fp32<MODE>(acc + 16 * h, p, at + (c0 + 64 * h) * p.ldd, f, c.qn - (c0 + 64 * h));
+                else
+                    put_bf16(acc + 16 * h, p, at + (c0 + 64 * h) * p.ldd, f, c.qn - (c0 + 64 * h));
+            }
         }
     } else {
         // ------------------------------- tails (wgrad, both CTAs) ----------------------------

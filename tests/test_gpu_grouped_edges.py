@@ -142,3 +142,29 @@ def test_a_tail_behind_a_long_run_is_waited_for():
         m.nvfp4_set_wait_budget_ns(0)
     for e, (lo, hi) in enumerate(((0, counts[0]), (counts[0], sum(counts)))):
         assert torch.equal(out[e], dy[lo:hi].float().t() @ x[lo:hi].float()), e     # integers up to 2^19
+
+
+@pytest.mark.parametrize("rows", [5, 40, 65, 300])
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+def test_bf16_output_of_a_long_reduction(rows, kn):
+    """Positive operands, K = 2^20, on both sides of the rule for few rows.  A run of 1024 products takes
+    64 adds of 16; each truncates by less than 2^-23 of the partial sum, half of the run's on
+    average: 32 * 2^-23.  The K / 512 joins at most, rounded, add K / 512 / 2 * 2^-24.  The rest is half
+    a bf16 step of the sum itself.  (In one accumulator the sums come out some 6e-3 low, up to two
+    steps.)"""
+    m = nv()
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    K, N = 2 ** 20, 8
+    a = torch.rand(rows, K, generator=g, device="cuda").bfloat16()
+    w = torch.rand(*((2, K, N) if kn else (2, N, K)), generator=g, device="cuda").bfloat16()
+    off = _off([rows // 2, rows - rows // 2])
+    ws = m.Workspace()
+    got = m.nvfp4_bf16_gemm_grouped(a, w, off.cuda(), b_kn=kn, ws=ws)
+    assert got.dtype == torch.bfloat16 and m.nvfp4_poll(ws) == 0
+    for e in range(2):
+        lo, hi = int(off[e]), int(off[e + 1])
+        ref = a[lo:hi].double() @ (w[e].double() if kn else w[e].double().t())
+        half = torch.ldexp(torch.ones_like(ref), torch.frexp(ref)[1] - 9)       # of a step: 8 bits from the leading one
+        bound = half + ref * (32 * 2.0 ** -23 + K / 1024 * 2.0 ** -24)
+        err = (got[lo:hi].double() - ref).abs()
+        assert (err <= bound).all(), f"{int((err > bound).sum())} of {err.numel()}, worst {float((err / half).max()):.3f} half steps"
