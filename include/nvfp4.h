@@ -431,6 +431,7 @@ nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b,
  *   v = v * beta2 + (g * (1 - beta2)) * g
  *   p = p * (1 - lr * weight_decay) - (m / (sqrt(v) * c + eps)) * (lr / (1 - beta1^step))
  *   w = bf16(p), nearest even                              c = 1 / sqrt(1 - beta2^step)
+ * (8-bit state: see below for a sqrt(v) of zero.)
  * The scalars 1 - beta, 1 - lr * weight_decay, the step size and c are computed in double and
  * rounded once.
  *
@@ -446,7 +447,11 @@ nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b,
  * its tensor's index in the call, stream NVFP4_STREAM_MOMENT1 for m and NVFP4_STREAM_MOMENT2 for
  * sqrt(v).  NVFP4_RNE rounds to nearest even, which stops a slow average from moving once its step
  * is below half a code: SR, with another seed each step, keeps the averages unbiased.  The weight
- * update of a step reads m and v before they are encoded.
+ * update of a step reads m and v before they are encoded.  A root below one code (2^-9 of the scale,
+ * 4.4e-6 of its block's largest) may be held as zero while m is not.  Where sqrt(v) is zero, the update
+ * divides by v_scale * 2^-9 (the scale as read) in its place, so a zero gradient does not leave
+ * m / eps; where the gradient is not zero but far below what it was, the update exceeds that of fp32
+ * moments by up to the quotient of the two.
  *
  * amax_ws: if not NULL, a workspace of the tensor's own whose plain amax word receives the amax of w
  * (for nvfp4_quantize_weight_ready); it is reset first, and a NaN or Inf in w raises the non-finite flag

@@ -10,7 +10,7 @@
 // copy that a captured graph or a second call could share.
 //
 // Measured: 2 x 104857600 elements, fp32 moments, 1040 us, 6.05 TB/s, 92 % of the copy bandwidth: bound by
-// memory.  200 tensors of 1000 to 4.8 M elements (107 M in all), E4M3 moments, bf16 gradients, 384 us,
+// memory.  200 tensors of 1000 to 4.8 M elements (107 M in all), E4M3 moments, bf16 gradients, 385 us,
 // 4.8 TB/s: bound by instruction issue and load latency together, ~81 instructions an element (Philox and
 // the rounding's random bits 19, square root and quotient 23), two thirds of the issue slots taken.
 // Without effect there: the next block's loads ahead in registers (530 us when the rest took 443), by an
@@ -274,7 +274,26 @@ __device__ __forceinline__ void block_step(const Places<FP8>& at, int64_t first,
         v[i + 1] = __fadd_rn(x1, y1);
         root[i] = __fsqrt_rn(v[i]);
         root[i + 1] = __fsqrt_rn(v[i + 1]);
-        f2_split(f2_mul(f2(root[i], root[i + 1]), fix2), x0, x1);
+    }
+    // The divisor's roots.  A root below one code may have been held as zero while its m was not, and with
+    // a zero gradient the quotient would be m / eps: such a root divides as the smallest code it can have
+    // been held as.  (The search for one costs 2 us of the 385 above, a select per element 9.)
+    float r[8], low = 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        r[i] = root[i];
+        low = fminf(low, root[i]);
+    }
+    if (FP8 && low == 0.0f) {
+        const float code = *at.v_scale * 0x1p-9f;   // the old scale: the new one is written below
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (root[i] == 0.0f) r[i] = code;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        float x0, x1, y0, y1;
+        f2_split(f2_mul(f2(r[i], r[i + 1]), fix2), x0, x1);
         const uint64_t q = f2(__fdiv_rn(m[i], __fadd_rn(x0, sc.eps)), __fdiv_rn(m[i + 1], __fadd_rn(x1, sc.eps)));
         f2_split(f2_mul(f2(p[i], p[i + 1]), keep2), x0, x1);
         f2_split(f2_mul(q, size2), y0, y1);

@@ -1,0 +1,69 @@
+"""The AdamW step where its 8-bit moments, its amax and its checks of arguments have edges."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import nv
+
+pytestmark = pytest.mark.gpu
+
+f32 = np.float32
+
+
+def test_a_root_held_as_zero_beside_a_moment_that_is_not():
+    """One step from given codes, bit for bit: where sqrt(v) comes out as zero, the smallest code of the
+    block's scale divides in its place; everywhere else the formula is the header's."""
+    m = nv()
+    n = 600                              # two whole blocks and a part of one
+    r = np.random.default_rng(1)
+    p = (0.02 * r.standard_normal(n)).astype(f32)
+    g = np.where(r.random(n) < 0.5, 0, 1e-6 * r.standard_normal(n)).astype(f32)
+    mc = r.integers(0, 0x60, n).astype(np.uint8) | (r.integers(0, 2, n) << 7).astype(np.uint8)
+    vc = np.where(r.random(n) < 0.5, 0, r.integers(0, 0x60, n)).astype(np.uint8)
+    ms, vs = (np.array(x, f32) for x in ([3e-6, 1e-4, 2e-3], [2e-6, 0.0, 1e-3]))
+    vc[256:512] = 0                      # a block whose scale is zero: there only eps is left to divide by
+    values = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
+    M, R = values[mc] * ms.repeat(256)[:n], values[vc] * vs.repeat(256)[:n]
+    h = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1)
+    step = 40
+    codes = lambda c: torch.from_numpy(c).cuda().view(torch.float8_e4m3fn)
+    ctx = m.AdamWContext([torch.from_numpy(p).cuda()], [torch.from_numpy(g).cuda()], m=[codes(mc)], v=[codes(vc)], state=m.STATE_FP8,
+                         m_scale=[torch.from_numpy(ms).cuda()], v_scale=[torch.from_numpy(vs).cuda()])
+    m.nvfp4_adamw_step(ctx, step=step, sr_seed=3, **h)
+    M = M * f32(0.9) + g * f32(1 - 0.9)
+    R = np.sqrt(R * R * f32(0.95) + (g * f32(1 - 0.95)) * g)
+    lost = R == 0
+    assert 100 < lost.sum() < n and (lost & (M != 0)).sum() > 100
+    R = np.where(lost, vs.repeat(256)[:n] * f32(2.0 ** -9), R)
+    fix, size = f32(1 / math.sqrt(1 - 0.95 ** step)), f32(1e-3 / (1 - 0.9 ** step))
+    want = p * f32(1 - 1e-3 * 0.1) - (M / (R * fix + f32(1e-8))) * size
+    assert np.array_equal(ctx.params[0].cpu().numpy(), want)
+    # the codes are those of the root itself: zero stays zero
+    assert not ctx.moment(0, "v").cpu().numpy()[lost].any()
+
+
+@pytest.mark.parametrize("scale", [1.0, 1e-2])
+def test_small_elements_of_a_wide_block_take_bounded_steps(scale):
+    """Gradients of +-G = 1e-5 of the block's largest, zero in half of the steps.  With the block's largest
+    gradient A in every step, a code of m is at most A / 229376 = 0.436 G and a code of the root times the
+    correction at least 0.6 of that (0.716 from the correction of the step before, the rest its
+    rounding).  Each step rounds |m| up by at most a code: |m| <= (1 - beta1^t) / 0.1 * (0.9 * 0.436 G + 0.1 G)
+    = 4.9 G (1 - beta1^t).  The root is at least a code, or as a zero divides as one, or at least
+    sqrt(0.05) G: the update is at most 4.9 / min(0.6 * 0.436, 0.95 * 0.6 * 0.436, 0.22) = 23 lr."""
+    m = nv()
+    n, lr = 4096, 1e-3
+    gen = torch.Generator(device="cuda").manual_seed(int(1 / scale))
+    small = torch.arange(n, device="cuda") % 4 != 0
+    p, g = torch.zeros(n, device="cuda"), torch.empty(n, device="cuda")
+    ctx = m.AdamWContext([p], [g], state=m.STATE_FP8)
+    sign = lambda: torch.randint(0, 2, (n,), generator=gen, device="cuda").float() * 2 - 1
+    worst = 0.0
+    for step in range(1, 301):
+        some = torch.randint(0, 2, (n,), generator=gen, device="cuda").float()
+        g.copy_(scale * torch.where(small, 1e-5 * some, 1.0) * sign())
+        before = p.clone()
+        m.nvfp4_adamw_step(ctx, lr=lr, step=step, weight_decay=0.0, sr_seed=step)
+        worst = max(worst, float((p - before)[small].abs().max()) / lr)
+    assert worst <= 23, worst
