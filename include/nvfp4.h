@@ -455,7 +455,7 @@ nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b,
  *
  * amax_ws: if not NULL, a workspace of the tensor's own whose plain amax word receives the amax of w
  * (for nvfp4_quantize_weight_ready); it is reset first, and a NaN or Inf in w raises the non-finite flag
- * of ws.  w may be NULL (then amax_ws must be too).
+ * of ws.  w may be NULL (then amax_ws must be too, but for a tensor with n = 0, whose amax is zero).
  * dynamic: if not NULL, device memory that holds the step's values in place of lr, weight_decay,
  * step, grad_scale and sr_seed of the arguments, read when the kernel runs: a captured graph that
  * is replayed takes the values the caller has put there (nvfp4_adamw_dynamic_values computes them).

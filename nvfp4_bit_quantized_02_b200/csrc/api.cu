@@ -841,11 +841,12 @@ nvfp4_status nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int count, const nvf
         if (t.n < 0) return NVFP4_ERR_SHAPE;
         if (t.n > (int64_t)1 << 40) return NVFP4_ERR_LIMIT;
         if (t.g_dtype != NVFP4_OUT_BF16 && t.g_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_ARG;
+        if (!aligned16(t.amax_ws)) return NVFP4_ERR_ALIGN;
+        if (t.n == 0) continue;   // an empty tensor may have no addresses
         if (t.amax_ws && !t.w) return NVFP4_ERR_ARG;
-        if (t.n == 0) continue;
         if (!t.p || !t.g || !t.m || !t.v || (fp8 && (!t.m_scale || !t.v_scale))) return NVFP4_ERR_NULL;
         if (!aligned16(t.p) || !aligned16(t.g) || !aligned16(t.w) || !aligned16(t.m) || !aligned16(t.v) ||
-            !aligned16(t.amax_ws) || (fp8 && (!aligned4(t.m_scale) || !aligned4(t.v_scale))))
+            (fp8 && (!aligned4(t.m_scale) || !aligned4(t.v_scale))))
             return NVFP4_ERR_ALIGN;
     }
     if (nvfp4_status st = check_device()) return st;

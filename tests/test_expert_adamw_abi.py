@@ -108,3 +108,12 @@ def test_offsets_rule():
         assert run[0] >= 0 and run[-1] <= rows and (np.diff(run) >= 0).all()
         good = off[0] >= 0 and off[-1] <= rows and (np.diff(off) >= 0).all()
         assert not good or np.array_equal(run, off)
+
+
+def test_adamw_refuses_a_misplaced_amax_of_an_empty_tensor(L):
+    import nvfp4_bit_quantized_02_b200 as nv
+    e = nv.CAdamWTensor(None, None, None, None, None, None, None, 72, 0, 1, 0)
+    assert L.nvfp4_adamw(ctypes.byref(e), 1, ctypes.byref(_adamw_args(nv)), P, None) == 2
+    e.n, e.amax_ws = 10, 64
+    e.p = e.g = e.m = e.v = 64
+    assert L.nvfp4_adamw(ctypes.byref(e), 1, ctypes.byref(_adamw_args(nv)), P, None) == 4     # an amax without a weight

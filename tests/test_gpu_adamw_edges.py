@@ -67,3 +67,22 @@ def test_small_elements_of_a_wide_block_take_bounded_steps(scale):
         m.nvfp4_adamw_step(ctx, lr=lr, step=step, weight_decay=0.0, sr_seed=step)
         worst = max(worst, float((p - before)[small].abs().max()) / lr)
     assert worst <= 23, worst
+
+
+@pytest.mark.parametrize("state", ["fp32", "fp8"])
+def test_an_empty_weight_with_an_amax(state):
+    # an empty tensor has no address, and the amax zero
+    m = nv()
+    p = [torch.randn(300, device="cuda"), torch.empty(0, device="cuda"), torch.randn(7, device="cuda")]
+    g = [torch.randn_like(t) for t in p]
+    w = [torch.zeros_like(t, dtype=torch.bfloat16) for t in p]
+    ws = [m.Workspace() for _ in p]
+    for x in ws:
+        x.amax_words()[0] = 0x7F000000       # what an earlier call left
+    ctx = m.AdamWContext(p, g, w, state=m.STATE_FP8 if state == "fp8" else m.STATE_FP32, amax_ws=ws)
+    before = [t.clone() for t in p]
+    m.nvfp4_adamw_step(ctx, lr=1e-2, step=1)
+    assert int(ws[1].amax_words()[0]) == 0
+    for i in (0, 2):
+        assert (p[i] != before[i]).all() and torch.equal(w[i], p[i].bfloat16())
+        assert int(ws[i].amax_words()[0]) == int(w[i].abs().max().float().view(torch.int32))
