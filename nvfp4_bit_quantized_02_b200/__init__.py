@@ -336,6 +336,8 @@ def nvfp4_quantize_weight(w: torch.Tensor, transposed: bool = True, out: NVFP4Te
                           amax_ready: bool = False):
     """16x16 forms of a weight.  amax_ready: ws holds w's amax already (an AdamW step wrote it with w),
     and the amax pass is skipped."""
+    if amax_ready and ws is None:
+        raise ValueError("amax_ready needs ws, the workspace that holds w's amax")
     rows, cols, ld = _bf16_2d(w)
     out = out or NVFP4Tensor.empty(rows, cols, BLOCK_16x16, w.device)
     if transposed:

@@ -117,3 +117,11 @@ def test_adamw_refuses_a_misplaced_amax_of_an_empty_tensor(L):
     e.n, e.amax_ws = 10, 64
     e.p = e.g = e.m = e.v = 64
     assert L.nvfp4_adamw(ctypes.byref(e), 1, ctypes.byref(_adamw_args(nv)), P, None) == 4     # an amax without a weight
+
+
+def test_a_weight_whose_amax_is_ready_needs_its_workspace(L):
+    # the default workspace holds what some other call left there
+    import torch
+    import nvfp4_bit_quantized_02_b200 as nv
+    with pytest.raises(ValueError):
+        nv.nvfp4_quantize_weight(torch.zeros(16, 16, dtype=torch.bfloat16), amax_ready=True)
