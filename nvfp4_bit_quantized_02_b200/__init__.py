@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from bisect import bisect_left
 from dataclasses import dataclass
 
 import torch
@@ -719,7 +720,8 @@ class AdamWContext:
 
     params: fp32 master weights; grads: fp32 or bf16 gradients; weights: the bf16 weights the step
     writes (None, or None entries, for none); all contiguous, entry by entry of one size, held in
-    place from step to step (the context keeps references).  state: STATE_FP32 moments, or STATE_FP8:
+    place from step to step (the context keeps references).  What a step writes overlaps no other
+    tensor of it; gradients may share memory among themselves.  state: STATE_FP32 moments, or STATE_FP8:
     E4M3 codes with an fp32 scale per 256 elements (m, and the square root of v).  m, v, m_scale and
     v_scale may be given (resuming from a checkpoint); otherwise they start at zero.  amax_ws: per
     tensor a Workspace that receives the amax of its new bf16 weights (nvfp4_quantize_weight with
@@ -779,6 +781,7 @@ class AdamWContext:
         written = sorted(r for r in written if r[0] < r[1])
         if any(a[1] > b[0] for a, b in zip(written, written[1:])):
             raise ValueError("params, weights and moments: no two of them may overlap")
+        self._written = [r[0] for r in written], [r[1] for r in written]
         self._words = (ctypes.c_int64 * max(len(flat), self._WORDS))(*flat)
         self._table = ctypes.cast(self._words, ctypes.POINTER(CAdamWTensor))
         self._count, self._dev = k, dev
@@ -806,10 +809,16 @@ class AdamWContext:
         if len(grads) != self._count:
             raise ValueError("grads: one entry per parameter")
         words = []
+        starts, ends = self._written
         for i, g in enumerate(grads):
             bf16 = isinstance(g, torch.Tensor) and g.dtype is torch.bfloat16
-            self._tensor(g, self._words[self._WORDS * i + 8], torch.bfloat16 if bf16 else torch.float32, self._dev, "grads", i)
-            words.append((g.data_ptr(), OUT_BF16 if bf16 else OUT_FP32))
+            n = self._words[self._WORDS * i + 8]
+            self._tensor(g, n, torch.bfloat16 if bf16 else torch.float32, self._dev, "grads", i)
+            addr = g.data_ptr()
+            at = bisect_left(starts, addr + (2 if bf16 else 4) * n)     # what is written before the gradient's end
+            if n and at and ends[at - 1] > addr:
+                raise ValueError(f"grads[{i}]: overlaps a tensor that the step writes")
+            words.append((addr, OUT_BF16 if bf16 else OUT_FP32))
         for i, (addr, kind) in enumerate(words):
             self._words[self._WORDS * i + 1] = addr
             self._words[self._WORDS * i + 9] = kind      # g_dtype, reserved = 0

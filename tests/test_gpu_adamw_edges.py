@@ -86,3 +86,33 @@ def test_an_empty_weight_with_an_amax(state):
     for i in (0, 2):
         assert (p[i] != before[i]).all() and torch.equal(w[i], p[i].bfloat16())
         assert int(ws[i].amax_words()[0]) == int(w[i].abs().max().float().view(torch.int32))
+
+
+def test_gradients_that_overlap_what_a_step_writes_are_refused():
+    m = nv()
+    flat = torch.zeros(2048, device="cuda")
+    p, g = flat[:512], torch.ones(512, device="cuda")
+    w, v = flat[1024:1280].view(torch.bfloat16), flat[1536:2048]
+    mk = lambda grad, **k: m.AdamWContext([p], [grad], [w], m=[torch.zeros(512, device="cuda")], v=[v], **k)
+    bad = [flat[256:768], flat[511:1023], p, flat[1028:1284].view(torch.bfloat16), flat[800:1312], flat[1100:1612], v, flat[1400:1912]]
+    for grad in bad:
+        with pytest.raises(ValueError):
+            mk(grad)
+    ctx = mk(g)
+    for grad in bad:
+        with pytest.raises(ValueError):
+            ctx.set_grads([grad])
+    assert ctx.grads[0] is g
+    ctx.set_grads([flat[512:1024]])      # between two of them
+    m.nvfp4_adamw_step(ctx, lr=1e-3)
+    assert not flat.any()                # the gradient is zero there
+    q = [torch.zeros(512, device="cuda") for _ in range(2)]
+    both = m.AdamWContext(q, [g, g])     # one gradient for two tensors
+    m.nvfp4_adamw_step(both, lr=1e-3)
+    assert torch.equal(q[0], q[1]) and q[0].all()
+    one = torch.zeros(512, device="cuda")
+    m.nvfp4_adamw_step(m.AdamWContext([one], [g], v=[torch.zeros(512, device="cuda")]), lr=1e-3)
+    assert torch.equal(one, q[0])
+    codes = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):      # 8-bit moments and their scales
+        m.AdamWContext([torch.zeros(128, device="cuda")], [codes[64:320].view(torch.bfloat16)], m=[codes[:128].view(torch.float8_e4m3fn)], state=m.STATE_FP8)
