@@ -440,7 +440,8 @@ nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b,
  * consecutive elements (m_scale, v_scale: ceil(n / 256) floats; value = code * scale, and v is the
  * square of that value).  After the update a block of x (m, or sqrt(v)) is encoded with scale =
  * amax * fp32(1 / 448) and u = |x| * (448 * fp32(1 / amax)); a block with amax < 2^-100 gets scale
- * 0 and codes 0, a block that holds a NaN or Inf gets a NaN scale.  u is rounded to E4M3, sign kept, at
+ * 0 and codes of zero with the elements' signs (0x00 or 0x80), a block that holds a NaN or Inf gets a
+ * NaN scale and codes 0x00.  u is rounded to E4M3, sign kept, at
  * most 448: mode NVFP4_SR rounds up iff r16 < f * 2^16, f the cut-off part of the step (below 2^-6
  * the step is 2^-9 and f is taken of fp32(u + 2^-6)), r16 the element's Philox4x32-10 field: key
  * sr_seed, counter (i/8 lo, i/8 hi, stream, tensor), field i mod 8, i the element's index, tensor

@@ -116,3 +116,22 @@ def test_gradients_that_overlap_what_a_step_writes_are_refused():
     codes = torch.zeros(512, dtype=torch.uint8, device="cuda")
     with pytest.raises(ValueError):      # 8-bit moments and their scales
         m.AdamWContext([torch.zeros(128, device="cuda")], [codes[64:320].view(torch.bfloat16)], m=[codes[:128].view(torch.float8_e4m3fn)], state=m.STATE_FP8)
+
+
+@pytest.mark.parametrize("mode", [0, 1], ids=["rne", "sr"])
+def test_codes_of_blocks_held_as_zero_or_not_finite(mode):
+    # a block below 2^-100: scale 0, codes 0x00 or, where m is negative, 0x80; one with a NaN: codes 0x00
+    m = nv()
+    g = torch.zeros(768)
+    g[:256] = torch.where(torch.arange(256) % 3 == 0, -1e-31, 1e-31)
+    g[256:512] = -1.0
+    g[300] = float("nan")
+    g[512:] = -1.0
+    ctx = m.AdamWContext([torch.zeros(768, device="cuda")], [g.cuda()], state=m.STATE_FP8)
+    m.nvfp4_adamw_step(ctx, lr=1e-3, mode=mode)
+    mc, vc = (t[0].view(torch.uint8).cpu() for t in (ctx.m, ctx.v))
+    assert torch.equal(mc[:256], torch.where(g[:256] < 0, 0x80, 0).to(torch.uint8)) and not vc[:256].any()
+    assert not mc[256:512].any() and not vc[256:512].any()
+    assert (mc[512:] == 0xFE).all() and (vc[512:] == 0x7E).all()
+    for s in (ctx.m_scale[0].cpu(), ctx.v_scale[0].cpu()):
+        assert s[0] == 0 and torch.isnan(s[1]) and s[2] > 0
