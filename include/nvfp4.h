@@ -410,8 +410,8 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
  *   D_e[m][n] (+)= sum over the rows t of e of A[t][m] * B[t][n]   (dw_e = dy^T x, A = dy, B = x)
  * A [rows][lda], B [rows][ldb] bf16; D_e at d + e * stride_d, fp32, leading dimension ldd.
  * accumulate = 0 stores (an expert without rows gets zeros); 1 adds to what D holds (each element
- * once, by the memory system's fp32 add, which rounds to nearest and reads subnormals as zero; an
- * expert without rows is left as it was).  Sums are joined as above, D overlaps no operand.  Shape
+ * once, by the memory system's fp32 add, which rounds to nearest; a subnormal number in D and a
+ * subnormal sum may become zero; an expert without rows is left as it was).  Sums are joined as above, D overlaps no operand.  Shape
  * rules: as above with M, N multiples of 8; lda >= M, ldb >= N; ldd >= N, stride_d >= 0, both multiples of
  * 4; with more than one expert stride_d >= M * ldd.  rows == 0 makes every expert one without rows.
  */

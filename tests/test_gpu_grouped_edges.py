@@ -168,3 +168,22 @@ def test_bf16_output_of_a_long_reduction(rows, kn):
         bound = half + ref * (32 * 2.0 ** -23 + K / 1024 * 2.0 ** -24)
         err = (got[lo:hi].double() - ref).abs()
         assert (err <= bound).all(), f"{int((err > bound).sum())} of {err.numel()}, worst {float((err / half).max()):.3f} half steps"
+
+
+def test_added_gradients_near_the_subnormal_range():
+    # exact but where D, the product or the sum is subnormal, each of which may become zero: two of them at
+    # most (D and the product, or one and the sum), each below the smallest normal number
+    m = nv()
+    tiny = 2.0 ** -126
+    start = torch.tensor([0.0, 0.5, 1.5, -0.25, -1.0, 3.0, -3.0, 2.0 ** -23], dtype=torch.float64) * tiny
+    dy = torch.full((1, 8), 2.0 ** -63).bfloat16()
+    x = torch.tensor([[-1.0, 1.0, -0.75, 0.0, 2.0, 1.0, 0.5, -2.0]]).mul(2.0 ** -63).bfloat16()
+    out = start[:, None].expand(8, 8).float().contiguous()[None].cuda()
+    assert torch.equal(out[0].cpu().double(), start[:, None].expand(8, 8))
+    off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    m.nvfp4_bf16_wgrad_grouped(dy.cuda(), x.cuda(), off, out=out, accumulate=True)
+    want = start[:, None] + dy.double().t() @ x.double()
+    err = (out[0].cpu().double() - want).abs()
+    held = lambda t: (t.abs() >= tiny) | (t == 0)
+    exact = held(start)[:, None] & held(x.double() * 2.0 ** -63) & held(want)
+    assert (err < 2 * tiny).all() and (err[exact] == 0).all() and exact.any()
