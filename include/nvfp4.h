@@ -400,8 +400,9 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
  * [rows][ldd] bf16 or fp32.  Rows of D that no expert owns are left as they were.  fp32
  * accumulation; partial sums of at most 512 products (bf16 output: 1024) are joined in fp32
  * registers (round to nearest), since the tensor core truncates as it accumulates.  Each row's
- * result depends on that row and its expert's weight alone, but for the choice of kernel by `rows`.
- * D overlaps no operand.
+ * result depends on that row and its expert's weight alone, in an order of summation that the call's
+ * sizes choose (rows, experts, N, K and b_kn: they choose the kernel, and how it cuts K); neither the
+ * offsets nor the other rows change it.  D overlaps no operand.
  * Shape rules: 1 <= experts <= 1024; rows >= 0 (0: no-op); N, K >= 8, N % 8 == 0, K % 8 == 0;
  * lda >= K, ldb >= K (N if b_kn), stride_b >= 0, all multiples of 8; ldd >= N and
  * ldd * sizeof(out) % 16 == 0; sizes up to 2^30.  ws receives the timeout and offset flags.

@@ -187,3 +187,22 @@ def test_added_gradients_near_the_subnormal_range():
     held = lambda t: (t.abs() >= tiny) | (t == 0)
     exact = held(start)[:, None] & held(x.double() * 2.0 ** -63) & held(want)
     assert (err < 2 * tiny).all() and (err[exact] == 0).all() and exact.any()
+
+
+@pytest.mark.parametrize("rows,K,N", [(6, 520, 264), (24, 4104, 72), (64, 2056, 4104), (65, 520, 264), (700, 1160, 2056)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_a_row_does_not_depend_on_the_offsets_or_other_rows(rows, K, N, dtype):
+    # one weight for all of four experts: however the rows are dealt out, in whatever order, each comes out
+    # with the same bits
+    m = nv()
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    a = torch.randn(rows, K, generator=g, device="cuda").bfloat16()
+    w = torch.randn(1, N, K, generator=g, device="cuda").bfloat16().expand(4, N, K).contiguous()
+    for kn in (False, True):
+        b = w.transpose(1, 2).contiguous() if kn else w
+        run = lambda x, counts: m.nvfp4_bf16_gemm_grouped(x, b, _off(counts).cuda(), b_kn=kn, out_dtype=dtype)
+        first = run(a, [rows, 0, 0, 0])
+        for counts in ([0, 0, 0, rows], [rows // 3, 0, rows - rows // 3, 0], [1, rows - 3, 1, 1], [rows // 4] * 3 + [rows - 3 * (rows // 4)]):
+            assert torch.equal(run(a, counts), first), (kn, counts)
+            order = torch.randperm(rows, generator=g, device="cuda")
+            assert torch.equal(run(a[order], counts), first[order]), (kn, counts)
