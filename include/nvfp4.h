@@ -510,8 +510,8 @@ nvfp4_status nvfp4_adamw_dynamic_values(const nvfp4_adamw_args* args, nvfp4_adam
  * NVFP4_ERR_NONFINITE; NVFP4_OK when none is set. */
 nvfp4_status nvfp4_poll(void* ws, nvfp4_stream_t stream);
 
-/* Device-side wait budget of the GEMM's mbarrier spins, in nanoseconds (default 2e9).
- * Process-wide; 0 restores the default. */
+/* Device-side wait budget of the GEMMs' mbarrier spins (those grouped by expert too), in nanoseconds
+ * (default 2e9).  Process-wide; 0 restores the default. */
 void nvfp4_set_wait_budget_ns(uint64_t ns);
 
 const char* nvfp4_status_string(nvfp4_status s);

@@ -713,10 +713,19 @@ constexpr int kFewManyN = 4096, kFewOneN = 2048;   // features from which the pa
 
 cudaError_t launch_gemm_grouped(const GroupedGemm& g, cudaStream_t s) {
     // A few rows only stream the weights: the kernel without set-up (grouped_few.cu), whose passes over an
-    // expert's weights take 16 rows each.  Rows spread over many experts are one pass: 64 rows over 16
-    // experts of N x K = 1280 x 5120 take it 40 us and the pair kernel (80 tiles for 74 pairs) 50, 2816 x
-    // 2048 34.1 and 35.5; with 4096 features the pair kernel's tiles go round: 4096 x 1408 35.8 and 33.7,
-    // and all rows with one of the 16 16.6 and 8.7 (16 rows 8.6 and 8.3, 8 rows 5.6 and 8.3).
+    // expert's weights take 16 rows each.  How the rows lie over several experts is known on the device
+    // alone, so there the rule looks at N.  16 experts of N x K, rows spread evenly, then all with one
+    // expert, that kernel and the pair kernel in us:
+    //   8 rows:  2048 x 1280 10.5 and 11.1, 3.7 and 7.8; 2560 x 5120 39.4 and 49.5, 11.5 and 19.0;
+    //            4096 x 1408 19.7 and 19.0, 5.6 and 8.3
+    //   16 rows: 2048 x 1280 19.2 and 17.8, 5.0 and 7.7; 2560 x 5120 69.6 and 78.6, 14.3 and 18.9;
+    //            4096 x 1408 34.9 and 33.2, 8.6 and 8.3
+    //   64 rows: 1280 x 5120 spread 40 and 50; 2048 x 1280 19.6 and 17.8, 12.8 and 8.1; 2048 x 2048 26.6 and
+    //            25.9, 16.4 and 10.3; 2816 x 2048 34.1 and 35.5, 16.9 and 10.3; 2560 x 5120 70.8 and 79.1,
+    //            37.7 and 19.4; 4096 x 1408 35.8 and 33.7, 16.6 and 8.7
+    // So below 4096 features it gains up to a quarter where rows are spread and the pair kernel's tiles are
+    // few and long, and loses up to half where more than 24 of them lie with one expert, a tenth at 2048 x
+    // 1280 spread.  A rule from the number of tiles, the pairs and K would be closer; this one is not.
     // With one expert in all the passes are known: 24 rows of 4096 x 4096 16.1 and 17.3, 32 rows 17.8
     // and 17.4, 2048 x 512 3.8 and 5.4, 5.4 and 5.4; where the pair kernel has few and long tiles, 1280 x
     // 5120, 48 rows 17.0 and 18.6.
