@@ -30,6 +30,7 @@
 
 #include "nvfp4_device.cuh"
 #include "nvfp4_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace nvfp4 {
 
@@ -417,13 +418,6 @@ __global__ void adamw_reset_amax_kernel(const __grid_constant__ AdamwTable<CAP> 
     if (i < tab.count && tab.t[i].amax) *tab.t[i].amax = 0u;
 }
 
-static int sm_count_adamw() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        return 148;
-    return n;
-}
-
 template <bool FP8, bool SR, bool DYN, int CAP>
 static cudaError_t launch_table(const AdamwEntry* entries, int count, const AdamwScalars& sc,
                                 uint32_t* flags, cudaStream_t s) {
@@ -444,7 +438,7 @@ static cudaError_t launch_table(const AdamwEntry* entries, int count, const Adam
         tab.key1[r] = (uint32_t)(sc.sr_seed >> 32) + 0xBB67AE85u * r;
     }
     if (any_amax) adamw_reset_amax_kernel<CAP><<<(CAP + 127) / 128, 128, 0, s>>>(tab);
-    const uint64_t most = (uint64_t)sm_count_adamw() * kAdamResident;   // one wave: a CTA takes its whole run
+    const uint64_t most = (uint64_t)host::sm_count() * kAdamResident;   // one wave: a CTA takes its whole run
     adamw_kernel<FP8, SR, DYN, CAP><<<(unsigned)std::min<uint64_t>(chunks, most), kAdamThreads, 0, s>>>(tab, sc, flags);
     return cudaGetLastError();
 }

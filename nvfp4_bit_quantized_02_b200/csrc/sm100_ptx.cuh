@@ -1,5 +1,5 @@
 // sm100_ptx.cuh -- PTX wrappers (mbarriers, TMA, tcgen05, cluster) and host helpers of the products
-// grouped by expert.  The block-scaled GEMMs hold their own copies: the DRAM counters quoted for
+// grouped by expert (sm_count: of the AdamW step too).  The block-scaled GEMMs hold their own copies: the DRAM counters quoted for
 // them are keyed on the text of their source files.
 #pragma once
 
