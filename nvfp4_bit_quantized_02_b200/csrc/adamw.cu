@@ -11,8 +11,9 @@
 //
 // Measured: 2 x 104857600 elements, fp32 moments, 1040 us, 6.05 TB/s, 92 % of the copy bandwidth: bound by
 // memory.  200 tensors of 1000 to 4.8 M elements (107 M in all), E4M3 moments, bf16 gradients, 385 us,
-// 4.8 TB/s: bound by instruction issue and load latency together, ~81 instructions an element (Philox and
-// the rounding's random bits 19, square root and quotient 23), two thirds of the issue slots taken.
+// 4.8 TB/s (rounded to nearest 371): bound by instruction issue and load latency together, ~83 instructions
+// an element (Philox and the rounding's random bits 19, square root and quotient 23), two thirds of the
+// issue slots taken.  These are replays after a pause; a call among others takes 1056 to 1064 and 411 to 418.
 // Without effect there: the next block's loads ahead in registers (530 us when the rest took 443), by an
 // L2 prefetch (481) or by asynchronous copies into shared memory (425 when the rest took 384), streaming
 // loads and stores (387), the approximate quotient (2 %); 7 or 9 CTAs per SM 394, 4 of 256 threads 4 % more.

@@ -38,13 +38,16 @@
 // drains its copies and MMAs (bounded again) and frees its TMEM.
 //
 // Measured on 16384 rows x 16 experts of 5120 x 1280, even counts, beside cuBLAS' batched product of the
-// same shapes (us; a call by itself / without a pause, where the 1000 W limit holds the SMs at ~1.5 GHz):
-//   fprop 153 / 186, cuBLAS 161 / 195; dgrad 154 / 190, cuBLAS 151 / 184; wgrad 187 / 226, cuBLAS 184 / 223.
-// One expert of 8192 x 5120 x 5120: fprop 271 / 320 (1.58 PFLOP/s), cuBLAS 278 / 329; the tensor pipe is
-// active in 92 % of its cycles.  Here 4.3 tiles a pair make a fifth wave that is a third full, and wgrad
-// writes 419 MB of fp32 (of 197 us 56 were its stores).  Without effect: the last wave's tiles cut into row
-// parts, the reduction begun at another stage for each tile, stores with an evict-first policy or spread
-// out by sleeps, bands of 2 to 16 tiles, 4 or 5 stages of 64 products, longer suspended waits.
+// same shapes (us; a call after a pause / one of thousands in a row, where the 1000 W limit holds the SMs
+// at ~1.5 GHz), in one run:
+//   fprop 157 / 192, cuBLAS 164 / 200; dgrad 160 / 198, cuBLAS 152 / 187; wgrad 192 / 232, cuBLAS 186 / 227.
+// One expert of 8192 x 5120 x 5120: fprop 280 / 331 (1.53 PFLOP/s), cuBLAS 281 / 335.  The tensor pipe is
+// active in 86 % of fprop's cycles, 77 % of dgrad's and 62 % of wgrad's, which writes 419 MB of fp32 (without
+// its stores it took a quarter less).  With uneven counts (log-normal, sigma 0.6) the tiles of the longest
+// expert count: dealt out by number, the busiest pair has 1.06 of the mean in fprop, 1.03 in dgrad and 1.06
+// to 1.20 in wgrad.  Without effect: the last wave's tiles cut into row parts, the reduction begun at
+// another stage for each tile, stores with an evict-first policy or spread out by sleeps, bands of 2 to 16
+// tiles, 4 or 5 stages of 64 products, longer suspended waits.
 // The producer's and the MMA issuer's loops are one elected lane's and kept short: a stage of 64 products
 // takes them 320 cycles, less than 256 rows' MMAs (512); at 465 they bound every narrower tile (256 rows x
 // 5120 x 1280 25.0 us, now 19.2).
@@ -105,8 +108,8 @@ static_assert(kGroupedSmem <= 232448, "shared memory");
 // loads, and each load has a fixed cost (fprop at 8192 x 5120 x 5120: 1519 TFLOP/s with one 128-row
 // box for Q, 1171 with four of 32).  That cost is higher for the 4-dimensional MN-major boxes, so
 // they are taken deeper: loads alone, 16384 rows x 16 experts x 5120 x 1280, take dgrad 121 us in
-// stages of 128 products and 147 in stages of 64, wgrad 153 and 177 (in all 168 and 172, 197 and
-// 206).  K-major boxes gain little (119 and 122) and lose the finer ring (fprop 164 and 158 in all).
+// stages of 128 products and 147 in stages of 64, wgrad 153 and 177 (the whole kernels were 2 and 4 %
+// faster).  K-major boxes gain little (119 and 122) and lose the finer ring (fprop 4 % slower).
 template <int MODE>
 struct Shape {
     static constexpr bool kPmn = MODE != kFprop;         // P is MN-major

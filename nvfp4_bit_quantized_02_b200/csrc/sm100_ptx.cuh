@@ -1,6 +1,6 @@
 // sm100_ptx.cuh -- PTX wrappers (mbarriers, TMA, tcgen05, cluster) and host helpers of the products
-// grouped by expert (sm_count: of the AdamW step too).  The block-scaled GEMMs hold their own copies: the DRAM counters quoted for
-// them are keyed on the text of their source files.
+// grouped by expert (sm_count: of the AdamW step too).  The block-scaled GEMMs hold their own copies:
+// the DRAM counters quoted for them are keyed on the text of their source files.
 #pragma once
 
 #include <cuda.h>
