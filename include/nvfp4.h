@@ -412,9 +412,10 @@ nvfp4_status nvfp4_linear_bf16_bwd(const void* x, const void* w, const void* dy,
  * A [rows][lda], B [rows][ldb] bf16; D_e at d + e * stride_d, fp32, leading dimension ldd.
  * accumulate = 0 stores (an expert without rows gets zeros); 1 adds to what D holds (each element
  * once, by the memory system's fp32 add, which rounds to nearest; a subnormal number in D and a
- * subnormal sum may become zero; an expert without rows is left as it was).  Sums are joined as above, D overlaps no operand.  Shape
- * rules: as above with M, N multiples of 8; lda >= M, ldb >= N; ldd >= N, stride_d >= 0, both multiples of
- * 4; with more than one expert stride_d >= M * ldd.  rows == 0 makes every expert one without rows.
+ * subnormal sum may become zero; an expert without rows is left as it was).  Sums are joined as above,
+ * D overlaps no operand.  Shape rules: as above with M, N multiples of 8; lda >= M, ldb >= N; ldd >= N,
+ * stride_d >= 0, both multiples of 4; with more than one expert stride_d >= M * ldd.  rows == 0 makes
+ * every expert one without rows.
  */
 nvfp4_status nvfp4_bf16_gemm_grouped(const void* a, int64_t lda, int64_t rows, const int32_t* offsets, int experts,
                                      const void* b, int64_t ldb, int64_t stride_b, int b_kn, int64_t N, int64_t K,
@@ -511,7 +512,7 @@ nvfp4_status nvfp4_adamw_dynamic_values(const nvfp4_adamw_args* args, nvfp4_adam
 nvfp4_status nvfp4_poll(void* ws, nvfp4_stream_t stream);
 
 /* Device-side wait budget of the GEMMs' mbarrier spins (those grouped by expert too), in nanoseconds
- * (default 2e9).  Process-wide; 0 restores the default. */
+ * (default 2e9; 2^62 at most).  Process-wide; 0 restores the default. */
 void nvfp4_set_wait_budget_ns(uint64_t ns);
 
 const char* nvfp4_status_string(nvfp4_status s);

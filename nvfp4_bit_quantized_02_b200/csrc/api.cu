@@ -900,7 +900,10 @@ nvfp4_status nvfp4_poll(void* ws, nvfp4_stream_t stream) {
     return NVFP4_OK;
 }
 
-void nvfp4_set_wait_budget_ns(uint64_t ns) { g_budget_ns.store(ns ? ns : 2000000000ull); }
+void nvfp4_set_wait_budget_ns(uint64_t ns) {
+    // the kernels count two cycles a nanosecond in 64 bits
+    g_budget_ns.store(ns == 0 ? 2000000000ull : ns < 1ull << 62 ? ns : 1ull << 62);
+}
 
 const char* nvfp4_status_string(nvfp4_status s) {
     switch (s) {

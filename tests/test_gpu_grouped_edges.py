@@ -206,3 +206,23 @@ def test_a_row_does_not_depend_on_the_offsets_or_other_rows(rows, K, N, dtype):
             assert torch.equal(run(a, counts), first), (kn, counts)
             order = torch.randperm(rows, generator=g, device="cuda")
             assert torch.equal(run(a[order], counts), first[order]), (kn, counts)
+
+
+@pytest.mark.parametrize("budget", [2 ** 62, 2 ** 63, 2 ** 64 - 1])
+def test_the_longest_budgets_do_not_run_out_at_once(budget):
+    # a GEMM whose epilogue waits about a millisecond for its accumulator, and a product grouped by expert
+    from test_gpu_wait_budget import _long_k_operand
+    m = nv()
+    a, b = _long_k_operand(m, 128, 1 << 19, 1), _long_k_operand(m, 256, 1 << 19, 2)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, w = torch.randn(256, 2 ** 17, generator=g, device="cuda").bfloat16(), torch.randn(1, 256, 2 ** 17, generator=g, device="cuda").bfloat16()
+    off = torch.tensor([0, 256], dtype=torch.int32, device="cuda")
+    ws = m.Workspace()
+    m.nvfp4_set_wait_budget_ns(budget)
+    try:
+        m.nvfp4_gemm(a, b, out_dtype=torch.float32, ws=ws)
+        assert m.nvfp4_poll(ws) == 0
+        m.nvfp4_bf16_gemm_grouped(x, w, off, ws=ws)
+        assert m.nvfp4_poll(ws) == 0
+    finally:
+        m.nvfp4_set_wait_budget_ns(0)
