@@ -425,6 +425,85 @@ nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b,
                                       int64_t ldd, int64_t stride_d, int accumulate, void* ws, nvfp4_stream_t stream);
 
 /*
+ * Routing of tokens to experts: the offsets and the order of rows that the grouped products take.
+ * logits [tokens][ld] (bf16 or fp32, `experts` wide).  For each token, with s = softmax(logits) or
+ * s = 1 / (1 + e^-logit) (args->score) and b the bias (fp32 [experts], or NULL; it moves the choice
+ * and not the weights):
+ *   c = s + b, or the logit itself where bias is NULL;
+ *   with groups > 1 the experts are cut into `groups` runs of experts / groups; a group's score is
+ *   its largest c (group_top 1), or the sum of its two largest (group_top 2; without a bias c is s
+ *   there), and the top_groups groups of highest score stay, the lowest index first among equals;
+ *   the k experts of largest c in what stays are chosen, in descending order, the lowest index first
+ *   among equals.  c is compared as evaluated in fp64, whatever the logits' type.
+ *   weight = scale * s, with renormalize scale * s / (the sum of s over the chosen).
+ * An expert whose logit is -inf or NaN, or whose c is -inf or NaN, is never chosen (its s is 0, so
+ * masking by -inf takes it out of the softmax; masking by the type's lowest value leaves it eligible),
+ * and a group whose score is not above -inf does not stay.  +inf counts as the largest fp32 number.
+ * NaN and +inf raise the non-finite flag of ws.  Where fewer than k experts can be chosen, and for
+ * tokens with valid[t] == 0 (uint8 [tokens], or NULL), chosen is -1, row -1 and weight 0.
+ * Outputs, contiguous: chosen, rows int32 [tokens][k], weights fp32 [tokens][k], sources int32
+ * [tokens * k], offsets int32 [experts + 1].  The choices are sorted by expert and, within one, by
+ * token: expert e owns rows [offsets[e], offsets[e + 1]), rows[t][j] is the row of token t's j-th
+ * choice, sources[row] = t * k + j, and sources behind the last row are -1.
+ * scratch: nvfp4_route_scratch_bytes(experts) bytes of the caller's, used while the call runs (calls
+ * that may overlap need one each).
+ * Shape rules: 0 <= tokens, tokens * k <= 2^30 (0 tokens: the offsets are zeros); 1 <= experts <= 1024;
+ * 1 <= k <= 32; 1 <= top_groups <= groups <= 32, experts % groups == 0; group_top 1 or 2, at most
+ * experts / groups; k <= top_groups * experts / groups; scale finite; ld >= experts; logits and scratch 16-byte
+ * aligned, the other pointers to the size of their elements.  No two buffers overlap.
+ *
+ * nvfp4_route_bwd: the gradient of the logits from that of the weights (fp32 [tokens][k]), for the
+ * choices `chosen` of a nvfp4_route call with the same score, renormalize and scale (k and the
+ * rest of args as there; weights are recomputed from the logits, +inf and NaN as above):
+ *   softmax: dl_i = s_i (g_i - sum_j g_j s_j), g = scale * dweights at the chosen and 0 elsewhere;
+ *   sigmoid: dl_j = g_j s_j (1 - s_j);
+ *   renormalized, n = weights / scale: softmax dl_j = n_j (g_j - sum_i g_i n_i), sigmoid that times 1 - s_j.
+ * The choice itself has no gradient, nor has the bias.  dlogits [tokens][ldd] has the logits' type and
+ * is written whole (rows of tokens without a choice: zeros); indices outside [0, experts) are no choice.
+ */
+typedef enum { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 } nvfp4_score;
+typedef struct {
+    int32_t k;
+    int32_t score;         /* nvfp4_score */
+    int32_t groups, top_groups, group_top;
+    int32_t renormalize;   /* 0 or 1 */
+    float scale;
+    int32_t reserved;
+} nvfp4_route_args;
+
+size_t nvfp4_route_scratch_bytes(int experts);
+nvfp4_status nvfp4_route(const void* logits, nvfp4_dtype dtype, int64_t ld, int64_t tokens, int experts,
+                         const nvfp4_route_args* args, const float* bias, const uint8_t* valid, int32_t* chosen,
+                         float* weights, int32_t* rows, int32_t* sources, int32_t* offsets, void* scratch, void* ws,
+                         nvfp4_stream_t stream);
+nvfp4_status nvfp4_route_bwd(const float* dweights, const void* logits, nvfp4_dtype dtype, int64_t ld, int64_t tokens,
+                             int experts, const nvfp4_route_args* args, const int32_t* chosen, void* dlogits,
+                             int64_t ldd, nvfp4_stream_t stream);
+
+/*
+ * Token rows into the experts' order and back.  rows: int32 [tokens][k] as nvfp4_route writes them;
+ * a choice whose row is not in [0, rows_total) is skipped, no two choices name one row.
+ *   dispatch:    xs[rows[t][j]] = x[t]
+ *   combine:     y[t] = residual[t] + sum over j of weights[t][j] * ys[rows[t][j]]
+ *                (weights NULL: 1, which is dispatch's gradient; residual NULL: 0), in fp32, in the
+ *                order of j, rounded once
+ *   combine_bwd: dys[rows[t][j]] = weights[t][j] * dy[t], dweights[t][j] = dy[t] . ys[rows[t][j]]
+ *                (fp32, 0 for a choice without a row); the residual's gradient is dy itself
+ * x, xs, dy, dys bf16; ys bf16 or fp32; y bf16 or fp32, residual of y's type.  Rows of xs and dys that
+ * no choice names are left as they were.  y may be the residual; nothing else overlaps.
+ * Shape rules: tokens >= 0 (0: no-op), d % 8 == 0, 8 <= d <= 2^24; 1 <= k <= 32; tokens * k <= rows_total <=
+ * 2^30; leading dimensions >= d with rows of a multiple of 16 bytes; tensors 16-byte aligned.
+ */
+nvfp4_status nvfp4_dispatch(const void* x, int64_t ldx, int64_t tokens, int64_t d, const int32_t* rows, int k, void* xs,
+                            int64_t ldxs, int64_t rows_total, nvfp4_stream_t stream);
+nvfp4_status nvfp4_combine(const void* ys, int64_t ldys, nvfp4_dtype ys_dtype, int64_t rows_total, const int32_t* rows,
+                           const float* weights, int k, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                           nvfp4_dtype y_dtype, int64_t tokens, int64_t d, nvfp4_stream_t stream);
+nvfp4_status nvfp4_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t ldys, nvfp4_dtype ys_dtype,
+                               int64_t rows_total, const int32_t* rows, const float* weights, int k, void* dys,
+                               int64_t lddys, float* dweights, int64_t tokens, int64_t d, nvfp4_stream_t stream);
+
+/*
  * One AdamW step over many tensors in one launch (per 384 tensors), from the gradients the linear
  * layers' backward calls write to the bf16 weights their next forward call reads.  Per element, in
  * fp32, each operation rounded once and in this order (products before the sum they enter):

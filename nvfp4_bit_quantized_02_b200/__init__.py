@@ -9,7 +9,8 @@ no CPU fallback.
 The functions carry the C names: ``nvfp4_quantize``, ``nvfp4_quantize_dual``,
 ``nvfp4_quantize_weight``, ``nvfp4_transpose_2d``, ``nvfp4_gemm``, ``nvfp4_linear_fwd``,
 ``nvfp4_linear_bwd``, ``nvfp4_gelu_fwd``, ``nvfp4_gelu_bwd``, ``nvfp4_poll``, for layers with one weight
-per expert ``nvfp4_bf16_gemm_grouped`` and ``nvfp4_bf16_wgrad_grouped``, for the weight update
+per expert ``nvfp4_bf16_gemm_grouped`` and ``nvfp4_bf16_wgrad_grouped``, around them ``nvfp4_route``,
+``nvfp4_dispatch`` and ``nvfp4_combine`` with their gradients, for the weight update
 ``nvfp4_adamw_step``, and for data-parallel token shards ``nvfp4_amax``, ``nvfp4_quantize_dual_shard`` (and ``nvfp4_quantize_dual_dp``, which
 all-reduces the amax between them).
 """
@@ -31,6 +32,7 @@ OUT_BF16, OUT_FP32 = 0, 1
 STREAM_DGRAD, STREAM_WGRAD, STREAM_RHT = 1, 2, 3
 STREAM_MOMENT1, STREAM_MOMENT2 = 4, 5
 STATE_FP32, STATE_FP8 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_ALIGN", 3: "ERR_SHAPE", 4: "ERR_ARG", 5: "ERR_WORKSPACE", 6: "ERR_CUDA",
           7: "ERR_NONFINITE", 8: "ERR_TIMEOUT", 9: "ERR_UNSUPPORTED", 10: "ERR_LIMIT"}
@@ -79,6 +81,12 @@ class CAdamWArgs(ctypes.Structure):
                 ("mode", ctypes.c_int32), ("dynamic", ctypes.c_void_p)]
 
 
+class CRouteArgs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_int32), ("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
 _L = None
 
 
@@ -105,6 +113,12 @@ def _lib():
             "nvfp4_bf16_wgrad_grouped": ([vp, i64, vp, i64, i64, vp, i32, i64, i64, vp, i64, i64, i32, vp, vp], i32),
             "nvfp4_adamw": ([c.POINTER(CAdamWTensor), i32, c.POINTER(CAdamWArgs), vp, vp], i32),
             "nvfp4_adamw_dynamic_values": ([c.POINTER(CAdamWArgs), c.POINTER(CAdamWDynamic)], i32),
+            "nvfp4_route_scratch_bytes": ([i32], c.c_size_t),
+            "nvfp4_route": ([vp, i32, i64, i64, i32, c.POINTER(CRouteArgs), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
+            "nvfp4_route_bwd": ([vp, vp, i32, i64, i64, i32, c.POINTER(CRouteArgs), vp, vp, i64, vp], i32),
+            "nvfp4_dispatch": ([vp, i64, i64, i64, vp, i32, vp, i64, i64, vp], i32),
+            "nvfp4_combine": ([vp, i64, i32, i64, vp, vp, i32, vp, i64, vp, i64, i32, i64, i64, vp], i32),
+            "nvfp4_combine_bwd": ([vp, i64, vp, i64, i32, i64, vp, vp, i32, vp, i64, vp, i64, i64, vp], i32),
             "nvfp4_amax": ([vp, i64, i64, i64, i32, u64, vp, vp], i32),
             "nvfp4_workspace_amax_offset": ([], c.c_size_t),
             "nvfp4_quantize_dual_shard": ([vp, i64, i64, i64, i64, i64, i32, u64, u64, u32, u32, T, T, vp, vp], i32),
@@ -710,6 +724,228 @@ class GroupedLinearBF16:
         dx = nvfp4_bf16_gemm_grouped(dy, w, offsets, b_kn=True, out=dx, ws=self.ws, stream=stream)
         dw = nvfp4_bf16_wgrad_grouped(dy, x, offsets, out=dw, accumulate=accumulate, ws=self.ws, stream=stream)
         return dx, dw
+
+
+# ---------------------------------------------------------------------------------------
+# routing of tokens to experts, and their rows into the experts' order and back
+# ---------------------------------------------------------------------------------------
+@dataclass
+class Routes:
+    """A route's buffers (owned by torch): what nvfp4_route writes, and the grouped products, nvfp4_dispatch
+    and nvfp4_combine take."""
+    experts: torch.Tensor        # int32 [tokens][k]: the chosen experts in descending order, -1 for none
+    weights: torch.Tensor        # fp32 [tokens][k]
+    rows: torch.Tensor           # int32 [tokens][k]: the row of each choice in the experts' order, -1 for none
+    sources: torch.Tensor        # int32 [tokens * k]: token * k + choice of each row, -1 behind the last
+    offsets: torch.Tensor        # int32 [experts + 1]: expert e owns rows [offsets[e], offsets[e + 1])
+    scratch: torch.Tensor | None = None   # of nvfp4_route; routes whose calls may overlap have one each
+
+    def __post_init__(self):
+        shape = self.experts.shape
+        if len(shape) != 2:
+            raise ValueError("experts: int32 [tokens][k]")
+        self.tokens, self.k = shape
+        self.count = self.offsets.numel() - 1
+        self.index = self.experts.get_device()
+        for name, dtype, want in (("experts", torch.int32, shape), ("weights", torch.float32, shape), ("rows", torch.int32, shape),
+                                  ("sources", torch.int32, (shape[0] * shape[1],)), ("offsets", torch.int32, (self.count + 1,))):
+            t = getattr(self, name)
+            if t.dtype is not dtype or t.shape != want or not t.is_contiguous() or t.get_device() != self.index:
+                raise ValueError(f"{name}: contiguous {dtype} {list(want)}, all on one device")
+
+    @staticmethod
+    def empty(tokens: int, experts: int, k: int, device=None) -> "Routes":
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        make = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=device)
+        scratch = make(torch.uint8, max(_lib().nvfp4_route_scratch_bytes(experts), 16))
+        return Routes(make(torch.int32, tokens, k), make(torch.float32, tokens, k), make(torch.int32, tokens, k),
+                      make(torch.int32, tokens * k), make(torch.int32, experts + 1), scratch)
+
+
+def _logits(x: torch.Tensor):
+    """A [tokens][experts] tensor's dtype code and row stride."""
+    if x.dtype is not torch.float32 and x.dtype is not torch.bfloat16 or x.dim() != 2:
+        raise TypeError("expected fp32 or bf16 [tokens][experts]")
+    row, col = x.stride()
+    tokens, experts = x.shape
+    if col != 1 and experts > 1:
+        raise ValueError("inner dimension must be contiguous")
+    return OUT_FP32 if x.dtype is torch.float32 else OUT_BF16, row if tokens > 1 else -(-experts // 8) * 8
+
+
+def nvfp4_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None, groups: int = 1,
+                top_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+                valid: torch.Tensor | None = None, out: Routes | None = None, ws: Workspace | None = None,
+                stream=None) -> Routes:
+    """The k experts of each token of logits [tokens][experts] (fp32 or bf16), their weights, and the order of
+    the chosen rows by expert (Routes).  score: softmax over the experts, or sigmoid.  bias: fp32 [experts], added
+    to the score for the choice alone.  groups, top_groups, group_top: the choice is made in the top_groups best of
+    `groups` runs of experts, a group counting as its best expert or as the sum of its two best.  weights: scale *
+    score, with renormalize over the sum of the chosen.  valid: bool [tokens], False for padding, which chooses
+    nobody.  Ties go to the lowest index; experts of logit -inf are never chosen."""
+    dtype, ld = _logits(logits)
+    tokens, experts = logits.shape
+    if out is None:
+        if stream is None:
+            out = Routes.empty(tokens, experts, k, logits.device)
+        else:
+            with torch.cuda.stream(stream):
+                out = Routes.empty(tokens, experts, k, logits.device)
+    elif out.tokens != tokens or out.k != k or out.count != experts:
+        raise ValueError(f"out: Routes of {tokens} tokens, {experts} experts, k = {k}")
+    if out.scratch is None:
+        out.scratch = _empty((max(_lib().nvfp4_route_scratch_bytes(experts), 16),), torch.uint8, logits.device, stream)
+    dev = _CUR_DEVICE()
+    if logits.get_device() != dev or out.index != dev:
+        _elsewhere(dev, logits, out.experts)
+    bias_addr = valid_addr = None
+    if bias is not None:
+        if bias.dtype is not torch.float32 or bias.shape != (experts,) or not bias.is_contiguous() or bias.get_device() != dev:
+            raise ValueError("bias: contiguous fp32 [experts] on the logits' device")
+        bias_addr = bias.data_ptr()
+    if valid is not None:
+        if valid.dtype is not torch.bool and valid.dtype is not torch.uint8 or valid.shape != (tokens,) or not valid.is_contiguous() or valid.get_device() != dev:
+            raise ValueError("valid: contiguous bool [tokens] on the logits' device")
+        valid_addr = valid.data_ptr()
+    ws_addr, raw = _call_context(dev, ws, stream)
+    args = CRouteArgs(k, score, groups, top_groups, group_top, 1 if renormalize else 0, scale, 0)
+    st = _lib().nvfp4_route(logits.data_ptr(), dtype, ld, tokens, experts, ctypes.byref(args), bias_addr, valid_addr,
+                            out.experts.data_ptr(), out.weights.data_ptr(), out.rows.data_ptr(), out.sources.data_ptr(),
+                            out.offsets.data_ptr(), out.scratch.data_ptr(), ws_addr, raw)
+    if st:
+        _check(st, "nvfp4_route")
+    return out
+
+
+def nvfp4_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, routes: Routes, score: int = SCORE_SOFTMAX,
+                    renormalize: bool = True, scale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of the logits (of their type) from that of the weights of a route with the same score,
+    renormalize and scale."""
+    dtype, ld = _logits(logits)
+    tokens, experts = logits.shape
+    if routes.tokens != tokens or routes.count != experts:
+        raise ValueError("routes: of these logits")
+    if dweights.dtype is not torch.float32 or dweights.shape != routes.experts.shape or not dweights.is_contiguous():
+        raise ValueError("dweights: contiguous fp32 [tokens][k]")
+    if out is None:
+        out = _empty((tokens, experts), logits.dtype, logits.device, stream)
+    elif out.dtype is not logits.dtype or out.shape != logits.shape:
+        raise ValueError("out: of the logits' type and shape")
+    ldd = _logits(out)[1]
+    dev = _CUR_DEVICE()
+    if logits.get_device() != dev or routes.index != dev or dweights.get_device() != dev or out.get_device() != dev:
+        _elsewhere(dev, logits, routes.experts, dweights, out)
+    raw = stream.cuda_stream if stream is not None else _stream()
+    args = CRouteArgs(routes.k, score, 1, 1, 1, 1 if renormalize else 0, scale, 0)
+    st = _lib().nvfp4_route_bwd(dweights.data_ptr(), logits.data_ptr(), dtype, ld, tokens, experts, ctypes.byref(args),
+                                routes.experts.data_ptr(), out.data_ptr(), ldd, raw)
+    if st:
+        _check(st, "nvfp4_route_bwd")
+    return out
+
+
+def _row_stride(x: torch.Tensor, what: str):
+    """The row stride of a 2-D tensor with a contiguous inner dimension (a single row's: its width)."""
+    if x.dim() != 2:
+        raise ValueError(f"{what}: two dimensions")
+    row, col = x.stride()
+    if col != 1:
+        raise ValueError(f"{what}: inner dimension must be contiguous")
+    return row if x.shape[0] > 1 else x.shape[1]
+
+
+def nvfp4_dispatch(x: torch.Tensor, routes: Routes, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[row] = x[token] for every choice of the routes (x [tokens][d] bf16, out [tokens * k][d]): the rows the
+    grouped products take.  Rows that no expert owns are left as they were (undefined where out is not given)."""
+    if x.dtype is not torch.bfloat16:
+        raise TypeError("expected bf16 [tokens][d]")
+    ldx = _row_stride(x, "x")
+    tokens, d = x.shape
+    if tokens != routes.tokens:
+        raise ValueError("x: a row for each token of the routes")
+    if out is None:
+        out = _empty((tokens * routes.k, d), torch.bfloat16, x.device, stream)
+    elif out.dtype is not torch.bfloat16 or out.dim() != 2 or out.shape[1] != d or out.shape[0] < tokens * routes.k:
+        raise ValueError("out: bf16 [tokens * k][d]")
+    ldo = _row_stride(out, "out")
+    dev = _CUR_DEVICE()
+    if x.get_device() != dev or routes.index != dev or out.get_device() != dev:
+        _elsewhere(dev, x, routes.rows, out)
+    raw = stream.cuda_stream if stream is not None else _stream()
+    st = _lib().nvfp4_dispatch(x.data_ptr(), ldx, tokens, d, routes.rows.data_ptr(), routes.k, out.data_ptr(), ldo, out.shape[0], raw)
+    if st:
+        _check(st, "nvfp4_dispatch")
+    return out
+
+
+def nvfp4_combine(ys: torch.Tensor, routes: Routes, residual: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                  out: torch.Tensor | None = None, weighted: bool = True, stream=None) -> torch.Tensor:
+    """out[token] = residual[token] + sum of weight * ys[row] over the token's choices (ys [tokens * k][d] bf16 or
+    fp32, out and residual [tokens][d] of one type).  weighted=False takes every weight as 1: the gradient of
+    nvfp4_dispatch.  out may be the residual."""
+    if ys.dtype is not torch.bfloat16 and ys.dtype is not torch.float32:
+        raise TypeError("expected bf16 or fp32 rows")
+    ldys = _row_stride(ys, "ys")
+    total, d = ys.shape
+    tokens = routes.tokens
+    if total < tokens * routes.k:
+        raise ValueError("ys: [tokens * k][d]")
+    if out is None:
+        out = _empty((tokens, d), out_dtype if residual is None else residual.dtype, ys.device, stream)
+    if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+        raise TypeError("output must be bf16 or fp32")
+    if out.shape != (tokens, d):
+        raise ValueError("out: [tokens][d]")
+    ldo, ldr = _row_stride(out, "out"), 0
+    if residual is not None:
+        if residual.dtype is not out.dtype or residual.shape != out.shape:
+            raise ValueError("residual: of the output's type and shape")
+        ldr = _row_stride(residual, "residual")
+    dev = _CUR_DEVICE()
+    if residual is not None and residual.get_device() != dev:
+        _elsewhere(dev, residual)
+    if ys.get_device() != dev or routes.index != dev or out.get_device() != dev:
+        _elsewhere(dev, ys, routes.rows, out)
+    raw = stream.cuda_stream if stream is not None else _stream()
+    st = _lib().nvfp4_combine(ys.data_ptr(), ldys, OUT_FP32 if ys.dtype is torch.float32 else OUT_BF16, total, routes.rows.data_ptr(),
+                              routes.weights.data_ptr() if weighted else None, routes.k,
+                              residual.data_ptr() if residual is not None else None, ldr, out.data_ptr(), ldo,
+                              OUT_FP32 if out.dtype is torch.float32 else OUT_BF16, tokens, d, raw)
+    if st:
+        _check(st, "nvfp4_combine")
+    return out
+
+
+def nvfp4_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, routes: Routes, dys: torch.Tensor | None = None,
+                      dweights: torch.Tensor | None = None, stream=None):
+    """The gradients of nvfp4_combine's rows (dys [tokens * k][d] bf16; rows that no expert owns are left as they
+    were) and weights (fp32 [tokens][k], for nvfp4_route_bwd) from dy [tokens][d] bf16.  The residual's is dy."""
+    if dy.dtype is not torch.bfloat16 or ys.dtype is not torch.bfloat16 and ys.dtype is not torch.float32:
+        raise TypeError("expected bf16 dy and bf16 or fp32 ys")
+    lddy, ldys = _row_stride(dy, "dy"), _row_stride(ys, "ys")
+    tokens, d = dy.shape
+    total = ys.shape[0]
+    if tokens != routes.tokens or ys.shape[1] != d or total < tokens * routes.k:
+        raise ValueError("dy: [tokens][d], ys: [tokens * k][d]")
+    if dys is None:
+        dys = _empty((total, d), torch.bfloat16, dy.device, stream)
+    elif dys.dtype is not torch.bfloat16 or dys.shape != ys.shape:
+        raise ValueError("dys: bf16, of ys' shape")
+    if dweights is None:
+        dweights = _empty((tokens, routes.k), torch.float32, dy.device, stream)
+    elif dweights.dtype is not torch.float32 or dweights.shape != routes.experts.shape or not dweights.is_contiguous():
+        raise ValueError("dweights: contiguous fp32 [tokens][k]")
+    lddys = _row_stride(dys, "dys")
+    dev = _CUR_DEVICE()
+    if dy.get_device() != dev or ys.get_device() != dev or routes.index != dev or dys.get_device() != dev or dweights.get_device() != dev:
+        _elsewhere(dev, dy, ys, routes.rows, dys, dweights)
+    raw = stream.cuda_stream if stream is not None else _stream()
+    st = _lib().nvfp4_combine_bwd(dy.data_ptr(), lddy, ys.data_ptr(), ldys, OUT_FP32 if ys.dtype is torch.float32 else OUT_BF16, total,
+                                  routes.rows.data_ptr(), routes.weights.data_ptr(), routes.k, dys.data_ptr(), lddys,
+                                  dweights.data_ptr(), tokens, d, raw)
+    if st:
+        _check(st, "nvfp4_combine_bwd")
+    return dys, dweights
 
 
 # ---------------------------------------------------------------------------------------

@@ -801,6 +801,170 @@ nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b,
     return from_cuda(launch_wgrad_grouped(g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t nvfp4_route_scratch_bytes(int experts) {
+    return experts >= 1 && experts <= kMaxExperts ? (size_t)kRouteBlocks * experts * sizeof(int32_t) : 0;
+}
+
+static bool is_dtype(nvfp4_dtype t) { return t == NVFP4_OUT_BF16 || t == NVFP4_OUT_FP32; }
+
+// what nvfp4_route and its gradient both take
+static nvfp4_status check_route(nvfp4_dtype dtype, int64_t ld, int64_t tokens, int experts, const nvfp4_route_args* args) {
+    if (!args) return NVFP4_ERR_NULL;
+    if (!is_dtype(dtype)) return NVFP4_ERR_ARG;
+    if (args->score != NVFP4_SCORE_SOFTMAX && args->score != NVFP4_SCORE_SIGMOID) return NVFP4_ERR_ARG;
+    if (args->renormalize != 0 && args->renormalize != 1) return NVFP4_ERR_ARG;
+    if (!std::isfinite(args->scale)) return NVFP4_ERR_ARG;
+    if (tokens < 0 || experts < 1 || args->k < 1 || ld < experts) return NVFP4_ERR_SHAPE;
+    if (args->groups < 1 || args->top_groups < 1 || args->top_groups > args->groups) return NVFP4_ERR_SHAPE;
+    if (experts > kMaxExperts || args->k > kRouteMaxK || args->groups > kRouteMaxGroups || tokens > kMaxDim ||
+        tokens * args->k > kMaxDim || ld > kMaxDim)
+        return NVFP4_ERR_LIMIT;
+    const int size = experts / args->groups;
+    if (experts % args->groups || args->k > args->top_groups * size) return NVFP4_ERR_SHAPE;
+    if (args->group_top < 1 || args->group_top > 2 || args->group_top > size) return NVFP4_ERR_SHAPE;
+    return NVFP4_OK;
+}
+
+static RouteProblem route_problem(const void* logits, nvfp4_dtype dtype, int64_t ld, int64_t tokens, int experts,
+                                  const nvfp4_route_args* args) {
+    RouteProblem r{};
+    r.logits = logits;
+    r.ld = ld;
+    r.tokens = (int32_t)tokens;
+    r.experts = experts;
+    r.k = args->k;
+    r.groups = args->groups;
+    r.top_groups = args->top_groups;
+    r.group_top = args->group_top;
+    r.bf16 = dtype == NVFP4_OUT_BF16;
+    r.sigmoid = args->score == NVFP4_SCORE_SIGMOID;
+    r.renormalize = args->renormalize != 0;
+    r.scale = args->scale;
+    return r;
+}
+
+nvfp4_status nvfp4_route(const void* logits, nvfp4_dtype dtype, int64_t ld, int64_t tokens, int experts,
+                         const nvfp4_route_args* args, const float* bias, const uint8_t* valid, int32_t* chosen,
+                         float* weights, int32_t* rows, int32_t* sources, int32_t* offsets, void* scratch, void* ws,
+                         nvfp4_stream_t stream) {
+    if (nvfp4_status st = check_route(dtype, ld, tokens, experts, args)) return st;
+    if (!ws) return NVFP4_ERR_WORKSPACE;
+    if (!offsets || !scratch || (tokens > 0 && (!logits || !chosen || !weights || !rows || !sources))) return NVFP4_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(scratch) || !aligned4(bias) || !aligned4(chosen) || !aligned4(weights) ||
+        !aligned4(rows) || !aligned4(sources) || !aligned4(offsets))
+        return NVFP4_ERR_ALIGN;
+    if (nvfp4_status st = check_device()) return st;
+    RouteProblem r = route_problem(logits, dtype, ld, tokens, experts, args);
+    r.bias = bias;
+    r.valid = valid;
+    r.chosen = chosen;
+    r.weights = weights;
+    r.rows = rows;
+    r.sources = sources;
+    r.offsets = offsets;
+    r.scratch = reinterpret_cast<int32_t*>(scratch);
+    r.flags = &ws_of(ws)->flags;
+    return from_cuda(launch_route(r, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_route_bwd(const float* dweights, const void* logits, nvfp4_dtype dtype, int64_t ld, int64_t tokens,
+                             int experts, const nvfp4_route_args* args, const int32_t* chosen, void* dlogits,
+                             int64_t ldd, nvfp4_stream_t stream) {
+    if (nvfp4_status st = check_route(dtype, ld, tokens, experts, args)) return st;
+    if (ldd < experts) return NVFP4_ERR_SHAPE;
+    if (ldd > kMaxDim) return NVFP4_ERR_LIMIT;
+    if (tokens > 0 && (!dweights || !logits || !chosen || !dlogits)) return NVFP4_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(dlogits) || !aligned4(dweights) || !aligned4(chosen)) return NVFP4_ERR_ALIGN;
+    if (nvfp4_status st = check_device()) return st;
+    if (tokens == 0) return NVFP4_OK;
+    RouteBwd p{};
+    p.r = route_problem(logits, dtype, ld, tokens, experts, args);
+    p.r.chosen = const_cast<int32_t*>(chosen);
+    p.dweights = dweights;
+    p.dlogits = dlogits;
+    p.ldd = ldd;
+    return from_cuda(launch_route_bwd(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// what dispatch, combine and its gradient all take
+static nvfp4_status check_token_rows(int64_t tokens, int64_t d, int k, int64_t rows_total, const int32_t* rows) {
+    if (tokens < 0 || d < 8 || d % 8 || k < 1 || rows_total < 0) return NVFP4_ERR_SHAPE;
+    if (tokens > kMaxDim || d > (int64_t)1 << 24 || k > kRouteMaxK || rows_total > kMaxDim) return NVFP4_ERR_LIMIT;
+    if (tokens * k > rows_total) return NVFP4_ERR_SHAPE;
+    if (tokens > 0 && !rows) return NVFP4_ERR_NULL;
+    return aligned4(rows) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+// a tensor of rows of d elements
+static nvfp4_status check_rows(const void* p, int64_t ld, int64_t d, nvfp4_dtype dtype, bool needed) {
+    if (ld < d) return NVFP4_ERR_SHAPE;
+    if (ld > kMaxDim) return NVFP4_ERR_LIMIT;
+    if (needed && !p) return NVFP4_ERR_NULL;
+    if (!aligned16(p) || ld * (dtype == NVFP4_OUT_FP32 ? 4 : 2) % 16) return NVFP4_ERR_ALIGN;
+    return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_dispatch(const void* x, int64_t ldx, int64_t tokens, int64_t d, const int32_t* rows, int k, void* xs,
+                            int64_t ldxs, int64_t rows_total, nvfp4_stream_t stream) {
+    if (nvfp4_status st = check_token_rows(tokens, d, k, rows_total, rows)) return st;
+    if (nvfp4_status st = check_rows(x, ldx, d, NVFP4_OUT_BF16, tokens > 0)) return st;
+    if (nvfp4_status st = check_rows(xs, ldxs, d, NVFP4_OUT_BF16, tokens > 0)) return st;
+    if (nvfp4_status st = check_device()) return st;
+    if (tokens == 0) return NVFP4_OK;
+    const TokenRows m{rows, nullptr, k, tokens, d, rows_total};
+    return from_cuda(launch_dispatch(m, reinterpret_cast<const uint16_t*>(x), ldx, reinterpret_cast<uint16_t*>(xs), ldxs,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_combine(const void* ys, int64_t ldys, nvfp4_dtype ys_dtype, int64_t rows_total, const int32_t* rows,
+                           const float* weights, int k, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                           nvfp4_dtype y_dtype, int64_t tokens, int64_t d, nvfp4_stream_t stream) {
+    if (!is_dtype(ys_dtype) || !is_dtype(y_dtype)) return NVFP4_ERR_ARG;
+    if (nvfp4_status st = check_token_rows(tokens, d, k, rows_total, rows)) return st;
+    if (nvfp4_status st = check_rows(ys, ldys, d, ys_dtype, tokens > 0)) return st;
+    if (nvfp4_status st = check_rows(y, ldy, d, y_dtype, tokens > 0)) return st;
+    if (residual)
+        if (nvfp4_status st = check_rows(residual, ldr, d, y_dtype, true)) return st;
+    if (!aligned4(weights)) return NVFP4_ERR_ALIGN;
+    if (nvfp4_status st = check_device()) return st;
+    if (tokens == 0) return NVFP4_OK;
+    Combine c{};
+    c.m = TokenRows{rows, weights, k, tokens, d, rows_total};
+    c.ys = ys;
+    c.residual = residual;
+    c.y = y;
+    c.ldys = ldys;
+    c.ldr = ldr;
+    c.ldy = ldy;
+    c.ys_fp32 = ys_dtype == NVFP4_OUT_FP32;
+    c.y_fp32 = y_dtype == NVFP4_OUT_FP32;
+    return from_cuda(launch_combine(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t ldys, nvfp4_dtype ys_dtype,
+                               int64_t rows_total, const int32_t* rows, const float* weights, int k, void* dys,
+                               int64_t lddys, float* dweights, int64_t tokens, int64_t d, nvfp4_stream_t stream) {
+    if (!is_dtype(ys_dtype)) return NVFP4_ERR_ARG;
+    if (nvfp4_status st = check_token_rows(tokens, d, k, rows_total, rows)) return st;
+    if (nvfp4_status st = check_rows(dy, lddy, d, NVFP4_OUT_BF16, tokens > 0)) return st;
+    if (nvfp4_status st = check_rows(ys, ldys, d, ys_dtype, tokens > 0)) return st;
+    if (nvfp4_status st = check_rows(dys, lddys, d, NVFP4_OUT_BF16, tokens > 0)) return st;
+    if (tokens > 0 && (!weights || !dweights)) return NVFP4_ERR_NULL;
+    if (!aligned4(weights) || !aligned4(dweights)) return NVFP4_ERR_ALIGN;
+    if (nvfp4_status st = check_device()) return st;
+    if (tokens == 0) return NVFP4_OK;
+    CombineBwd c{};
+    c.m = TokenRows{rows, weights, k, tokens, d, rows_total};
+    c.dy = reinterpret_cast<const uint16_t*>(dy);
+    c.ys = ys;
+    c.dys = reinterpret_cast<uint16_t*>(dys);
+    c.dweights = dweights;
+    c.lddy = lddy;
+    c.ldys = ldys;
+    c.lddys = lddys;
+    c.ys_fp32 = ys_dtype == NVFP4_OUT_FP32;
+    return from_cuda(launch_combine_bwd(c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 nvfp4_status nvfp4_adamw_dynamic_values(const nvfp4_adamw_args* args, nvfp4_adamw_dynamic* out) {
     if (!args || !out) return NVFP4_ERR_NULL;
     if (!(args->beta1 >= 0.0 && args->beta1 < 1.0 && args->beta2 >= 0.0 && args->beta2 < 1.0)) return NVFP4_ERR_ARG;

@@ -23,6 +23,8 @@ SOURCES = {
     "adamw.cu": ["-fmad=false"],
     "grouped.cu": [],
     "grouped_few.cu": [],
+    "route.cu": [],
+    "tokens.cu": [],
     "noalloc.cu": [],
 }
 HEADERS = ["nvfp4_device.cuh", "nvfp4_internal.h", "sm100_ptx.cuh"]

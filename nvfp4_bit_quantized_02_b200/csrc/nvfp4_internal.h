@@ -154,6 +154,64 @@ constexpr int kFewMaxRows = 64, kFewMaxExperts = 256, kFewLongK = 2048;
 cudaError_t launch_gemm_grouped_few(const GroupedGemm& g, cudaStream_t s);   // within those, b_kn = 0
 cudaError_t launch_wgrad_grouped(const GroupedWgrad& g, cudaStream_t s);
 
+// Routing of tokens to experts (the arguments of nvfp4_route, checked)
+constexpr int kRouteMaxK = 32, kRouteMaxGroups = 32;
+constexpr int kRouteBlocks = 148;   // counts [blocks][experts] of the scratch
+struct RouteProblem {
+    const void* logits;
+    int64_t ld;
+    const float* bias;
+    const uint8_t* valid;
+    int32_t tokens, experts, k, groups, top_groups, group_top;
+    bool bf16, sigmoid, renormalize;
+    float scale;
+    int32_t* chosen;
+    float* weights;
+    int32_t* rows;
+    int32_t* sources;
+    int32_t* offsets;
+    int32_t* scratch;
+    uint32_t* flags;
+};
+struct RouteBwd {
+    RouteProblem r;             // its logits, sizes, score, renormalize, scale and chosen
+    const float* dweights;
+    void* dlogits;
+    int64_t ldd;
+    int32_t vec;                // set by the launcher
+};
+cudaError_t launch_route(const RouteProblem& r, cudaStream_t s);
+cudaError_t launch_route_bwd(const RouteBwd& p, cudaStream_t s);
+
+// Token rows into the experts' order and back.  rows[t * k + j]: the row of token t's j-th choice, skipped
+// where it is not within [0, rows_total).
+struct TokenRows {
+    const int32_t* rows;
+    const float* weights;       // or NULL: 1
+    int32_t k;
+    int64_t tokens, d, rows_total;
+};
+struct Combine {
+    TokenRows m;
+    const void* ys;
+    const void* residual;       // of y's type, or NULL
+    void* y;
+    int64_t ldys, ldr, ldy;
+    bool ys_fp32, y_fp32;
+};
+struct CombineBwd {
+    TokenRows m;
+    const uint16_t* dy;
+    const void* ys;
+    uint16_t* dys;
+    float* dweights;
+    int64_t lddy, ldys, lddys;
+    bool ys_fp32;
+};
+cudaError_t launch_dispatch(const TokenRows& m, const uint16_t* x, int64_t ldx, uint16_t* xs, int64_t ldxs, cudaStream_t s);
+cudaError_t launch_combine(const Combine& c, cudaStream_t s);
+cudaError_t launch_combine_bwd(const CombineBwd& c, cudaStream_t s);
+
 // AdamW: one tensor of a launch (80 bytes: a launch's table fits the 32764 bytes of kernel parameters)
 constexpr int kAdamMaxTensors = 384;
 constexpr uint32_t kStreamMoment1 = 4u, kStreamMoment2 = 5u;
