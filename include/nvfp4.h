@@ -504,6 +504,44 @@ nvfp4_status nvfp4_combine_bwd(const void* dy, int64_t lddy, const void* ys, int
                                int64_t lddys, float* dweights, int64_t tokens, int64_t d, nvfp4_stream_t stream);
 
 /*
+ * The BF16 product with its neighbours in the epilogue:
+ *   h = A[M][K] . B[N][K]^T + bias,   D[M][N] = act(h) + residual,   pre = h
+ * A, B bf16 row-major with leading dimensions lda, ldb; bias fp32 [N] or NULL; residual [M][ldr], bf16
+ * or fp32 (residual_dtype), or NULL; pre bf16 [M][ldpre], written for nvfp4_act_bwd, or NULL; D bf16 or
+ * fp32 with leading dimension ldd.  act: relu2 is max(h, 0)^2, gelu the erf form, silu h / (1 + e^-h).
+ * Everything after the sums is fp32, act taken of the unrounded h, D rounded once; the sums are joined
+ * from runs of at most 512 products (bf16 output: 1024) in fp32 registers, rounded to nearest, since the tensor
+ * core truncates as it accumulates.  A row's result depends on that row alone, in an order of summation
+ * that M, N, K choose.  D may be the residual (one address, leading dimension and type); nothing else overlaps.
+ * Shape rules: M >= 0 (0: no-op), N >= 1, K >= 8, K % 8 == 0; lda >= K, ldb >= K, multiples of 8;
+ * ldd, ldr, ldpre >= N; sizes up to 2^30, ceil(M / 32) * ceil(N / 256) up to 2^28; pointers 16-byte
+ * aligned (bias 4-byte).  Even leading dimensions of D, pre and the residual let a bf16 D take whole words.
+ * ws receives the timeout flag.
+ *
+ * nvfp4_act_bwd: dh = dy * act'(pre) in bf16 (dh may be NULL, or dy itself) and dbias[f] (+)= the sum over the rows
+ * of dy * act'(pre) before its rounding, in fp32 in a fixed order (dbias may be NULL; accumulate = 1 adds to what it
+ * holds).  relu' and relu2' are 0 at 0.  pre may be NULL with NVFP4_ACT_NONE, and is not read there.  scratch:
+ * nvfp4_act_bwd_scratch_bytes(n) bytes of the caller's, used while the call runs (needed with dbias).  Shape rules: rows >= 0 (0: dh untouched,
+ * dbias zero unless accumulated), n >= 8, n % 8 == 0, leading dimensions >= n, multiples of 8; pointers 16-byte aligned (dbias 4-byte).
+ */
+typedef enum {
+    NVFP4_ACT_NONE = 0,
+    NVFP4_ACT_RELU = 1,
+    NVFP4_ACT_RELU2 = 2,
+    NVFP4_ACT_GELU = 3,
+    NVFP4_ACT_SILU = 4
+} nvfp4_act;
+
+nvfp4_status nvfp4_bf16_gemm_act(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                                 const float* bias, nvfp4_act act, const void* residual, int64_t ldr,
+                                 nvfp4_dtype residual_dtype, void* pre, int64_t ldpre, void* d, int64_t ldd,
+                                 nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream);
+size_t nvfp4_act_bwd_scratch_bytes(int64_t n);
+nvfp4_status nvfp4_act_bwd(const void* dy, int64_t lddy, const void* pre, int64_t ldpre, int64_t rows, int64_t n,
+                           nvfp4_act act, void* dh, int64_t lddh, float* dbias, int accumulate, void* scratch,
+                           nvfp4_stream_t stream);
+
+/*
  * One AdamW step over many tensors in one launch (per 384 tensors), from the gradients the linear
  * layers' backward calls write to the bf16 weights their next forward call reads.  Per element, in
  * fp32, each operation rounded once and in this order (products before the sum they enter):

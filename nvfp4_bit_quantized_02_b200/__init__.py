@@ -10,7 +10,8 @@ The functions carry the C names: ``nvfp4_quantize``, ``nvfp4_quantize_dual``,
 ``nvfp4_quantize_weight``, ``nvfp4_transpose_2d``, ``nvfp4_gemm``, ``nvfp4_linear_fwd``,
 ``nvfp4_linear_bwd``, ``nvfp4_gelu_fwd``, ``nvfp4_gelu_bwd``, ``nvfp4_poll``, for layers with one weight
 per expert ``nvfp4_bf16_gemm_grouped`` and ``nvfp4_bf16_wgrad_grouped``, around them ``nvfp4_route``,
-``nvfp4_dispatch`` and ``nvfp4_combine`` with their gradients, for the weight update
+``nvfp4_dispatch`` and ``nvfp4_combine`` with their gradients, for dense layers with bias, activation and
+residual ``nvfp4_bf16_gemm_act`` and ``nvfp4_act_bwd``, for the weight update
 ``nvfp4_adamw_step``, and for data-parallel token shards ``nvfp4_amax``, ``nvfp4_quantize_dual_shard`` (and ``nvfp4_quantize_dual_dp``, which
 all-reduces the amax between them).
 """
@@ -33,6 +34,7 @@ STREAM_DGRAD, STREAM_WGRAD, STREAM_RHT = 1, 2, 3
 STREAM_MOMENT1, STREAM_MOMENT2 = 4, 5
 STATE_FP32, STATE_FP8 = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_NONE, ACT_RELU, ACT_RELU2, ACT_GELU, ACT_SILU = 0, 1, 2, 3, 4
 
 STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_ALIGN", 3: "ERR_SHAPE", 4: "ERR_ARG", 5: "ERR_WORKSPACE", 6: "ERR_CUDA",
           7: "ERR_NONFINITE", 8: "ERR_TIMEOUT", 9: "ERR_UNSUPPORTED", 10: "ERR_LIMIT"}
@@ -119,6 +121,9 @@ def _lib():
             "nvfp4_dispatch": ([vp, i64, i64, i64, vp, i32, vp, i64, i64, vp], i32),
             "nvfp4_combine": ([vp, i64, i32, i64, vp, vp, i32, vp, i64, vp, i64, i32, i64, i64, vp], i32),
             "nvfp4_combine_bwd": ([vp, i64, vp, i64, i32, i64, vp, vp, i32, vp, i64, vp, i64, i64, vp], i32),
+            "nvfp4_bf16_gemm_act": ([vp, i64, vp, i64, i64, i64, i64, vp, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp], i32),
+            "nvfp4_act_bwd_scratch_bytes": ([i64], c.c_size_t),
+            "nvfp4_act_bwd": ([vp, i64, vp, i64, i64, i64, i32, vp, i64, vp, i32, vp, vp], i32),
             "nvfp4_amax": ([vp, i64, i64, i64, i32, u64, vp, vp], i32),
             "nvfp4_workspace_amax_offset": ([], c.c_size_t),
             "nvfp4_quantize_dual_shard": ([vp, i64, i64, i64, i64, i64, i32, u64, u64, u32, u32, T, T, vp, vp], i32),
@@ -727,6 +732,165 @@ class GroupedLinearBF16:
 
 
 # ---------------------------------------------------------------------------------------
+# the BF16 product with bias, activation and residual in its epilogue
+# ---------------------------------------------------------------------------------------
+def _row_stride(x: torch.Tensor, what: str):
+    """The row stride of a 2-D tensor with a contiguous inner dimension (a single row's: its width)."""
+    if x.dim() != 2:
+        raise ValueError(f"{what}: two dimensions")
+    row, col = x.stride()
+    rows, cols = x.shape
+    if col != 1 and cols > 1:
+        raise ValueError(f"{what}: inner dimension must be contiguous")
+    return row if rows > 1 else cols
+
+
+def nvfp4_bf16_gemm_act(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None, act: int = ACT_NONE,
+                        residual: torch.Tensor | None = None, pre: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                        out: torch.Tensor | None = None, ws: Workspace | None = None, stream=None) -> torch.Tensor:
+    """out = act(a . b^T + bias) + residual for bf16 a [M][K], b [N][K] (fp32 accumulation, one rounding).  bias:
+    fp32 [N]; residual: bf16 or fp32 [M][N], may be out; pre: bf16 [M][N], receives a . b^T + bias for nvfp4_act_bwd."""
+    if a.dtype is not torch.bfloat16 or b.dtype is not torch.bfloat16 or a.dim() != 2 or b.dim() != 2:
+        raise TypeError("expected bf16 a [M][K] and b [N][K]")
+    M, K = a.shape
+    N, Kb = b.shape
+    if Kb != K:
+        raise ValueError("a and b need the same K")
+    a_row, a_col = a.stride()
+    b_row, b_col = b.stride()
+    if a_col != 1 or b_col != 1:
+        raise ValueError("inner dimensions must be contiguous")
+    if out is None:
+        out = _empty((M, N), out_dtype, a.device, stream)
+    elif out.shape != (M, N):
+        raise ValueError("out: [M][N]")
+    out_dtype = out.dtype
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise TypeError("output must be bf16 or fp32")
+    ldd, ldr, ldpre = _row_stride(out, "out"), 0, 0
+    bias_addr = res_addr = pre_addr = None
+    res_fp32 = 0
+    dev = None
+    if bias is not None:
+        if bias.dtype is not torch.float32 or bias.shape != (N,) or not bias.is_contiguous():
+            raise ValueError("bias: contiguous fp32 [N]")
+        bias_addr = bias.data_ptr()
+    if residual is not None:
+        if residual.dtype is not torch.bfloat16 and residual.dtype is not torch.float32 or residual.shape != (M, N):
+            raise ValueError("residual: bf16 or fp32 [M][N]")
+        ldr, res_addr, res_fp32 = _row_stride(residual, "residual"), residual.data_ptr(), OUT_FP32 if residual.dtype is torch.float32 else OUT_BF16
+    if pre is not None:
+        if pre.dtype is not torch.bfloat16 or pre.shape != (M, N):
+            raise ValueError("pre: bf16 [M][N]")
+        ldpre, pre_addr = _row_stride(pre, "pre"), pre.data_ptr()
+    dev = _CUR_DEVICE()
+    for t in (a, b, out, bias, residual, pre):
+        if t is not None and t.get_device() != dev:
+            _elsewhere(dev, *(u for u in (a, b, out, bias, residual, pre) if u is not None))
+    ws_addr, raw = _call_context(dev, ws, stream)
+    st = _lib().nvfp4_bf16_gemm_act(a.data_ptr(), a_row if M > 1 else K, b.data_ptr(), b_row if N > 1 else K, M, N, K, bias_addr, act,
+                                    res_addr, ldr, res_fp32, pre_addr, ldpre, out.data_ptr(), ldd,
+                                    OUT_FP32 if out_dtype is torch.float32 else OUT_BF16, ws_addr, raw)
+    if st:
+        _check(st, "nvfp4_bf16_gemm_act")
+    return out
+
+
+def nvfp4_act_bwd(dy: torch.Tensor, pre: torch.Tensor | None, act: int, out: torch.Tensor | None = None,
+                  dbias: torch.Tensor | None = None, accumulate: bool = False, scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dy * act'(pre) (bf16 [rows][n]; out may be dy) and, where dbias (fp32 [n]) is given, its sum over the rows, which
+    is stored or, with accumulate, added.  scratch: uint8, nvfp4_act_bwd_scratch_bytes(n), used while the call runs."""
+    if dy.dtype is not torch.bfloat16 or (pre is not None and pre.dtype is not torch.bfloat16):
+        raise TypeError("expected bf16 dy and pre [rows][n]")
+    lddy = _row_stride(dy, "dy")
+    rows, n = dy.shape
+    if act != ACT_NONE and (pre is None or pre.shape != dy.shape):
+        raise ValueError("pre: of dy's shape")
+    if out is None:
+        out = _empty((rows, n), torch.bfloat16, dy.device, stream)
+    elif out.dtype is not torch.bfloat16 or out.shape != dy.shape:
+        raise ValueError("out: bf16, of dy's shape")
+    if dbias is not None and (dbias.dtype is not torch.float32 or dbias.shape != (n,) or not dbias.is_contiguous()):
+        raise ValueError("dbias: contiguous fp32 [n]")
+    _act_bwd(dy, lddy, pre, act, out, dbias, accumulate, scratch, stream)
+    return out
+
+
+def _act_bwd(dy, lddy, pre, act, out, dbias, accumulate, scratch, stream):
+    """nvfp4_act_bwd on checked tensors; out=None for the bias' gradient alone."""
+    rows, n = dy.shape
+    need = _lib().nvfp4_act_bwd_scratch_bytes(n) if dbias is not None else 0
+    if need and scratch is None:
+        scratch = _empty((need,), torch.uint8, dy.device, stream)
+    elif need and (scratch.dtype is not torch.uint8 or scratch.numel() < need or not scratch.is_contiguous()):
+        raise ValueError(f"scratch: {need} contiguous uint8")
+    reads = act != ACT_NONE
+    ldpre = _row_stride(pre, "pre") if reads else 0
+    dev = _CUR_DEVICE()
+    for t in (dy, pre if reads else None, out, dbias, scratch if need else None):
+        if t is not None and t.get_device() != dev:
+            _elsewhere(dev, t)
+    raw = stream.cuda_stream if stream is not None else _stream()
+    st = _lib().nvfp4_act_bwd(dy.data_ptr(), lddy, pre.data_ptr() if reads else None, ldpre, rows, n, act,
+                              None if out is None else out.data_ptr(), 0 if out is None else _row_stride(out, "out"),
+                              None if dbias is None else dbias.data_ptr(), 1 if accumulate else 0,
+                              scratch.data_ptr() if need else None, raw)
+    if st:
+        _check(st, "nvfp4_act_bwd")
+
+
+class LinearActBF16:
+    """The BF16 layer y = act(x w^T + bias) + residual of T rows (x [T][d], w [n][d] bf16, bias fp32 [n]), with the
+    buffers of its backward pass.  Its workspace holds the device flags of its calls (nvfp4_poll(layer.ws))."""
+
+    def __init__(self, T: int, d: int, n: int, act: int = ACT_GELU, device=None):
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        self.T, self.d, self.n, self.act = T, d, n, act
+        self.dh = torch.empty((T, n), dtype=torch.bfloat16, device=device) if act != ACT_NONE else None
+        self.scratch = torch.empty(max(_lib().nvfp4_act_bwd_scratch_bytes(n), 16), dtype=torch.uint8, device=device)
+        self.offsets = torch.tensor([0, T], dtype=torch.int32, device=device)
+        self.ws = Workspace(device)
+
+    def _shapes(self, x, w, *rows):
+        if x.shape != (self.T, self.d) or w.shape != (self.n, self.d):
+            raise ValueError(f"x: [{self.T}][{self.d}], w: [{self.n}][{self.d}]")
+        for t in rows:
+            if t is not None and t.shape != (self.T, self.n):
+                raise ValueError(f"expected [{self.T}][{self.n}]")
+
+    def fwd(self, x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+            pre: torch.Tensor | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """y; pre (bf16 [T][n]) receives x w^T + bias, which bwd takes."""
+        self._shapes(x, w, residual, pre, y)
+        return nvfp4_bf16_gemm_act(x, w, bias, self.act, residual, pre, out=y, ws=self.ws, stream=stream)
+
+    def bwd(self, x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, pre: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+            dw: torch.Tensor | None = None, dbias: torch.Tensor | None = None, accumulate: bool = False, stream=None):
+        """dx [T][d] bf16, dw [n][d] and dbias [n] fp32 (accumulate: both added to; they must be given).  The residual's
+        gradient is dy."""
+        self._shapes(x, w, dy, pre)
+        if dy.dtype is not torch.bfloat16:
+            raise TypeError("expected bf16 dy")
+        if self.act != ACT_NONE and (pre is None or pre.dtype is not torch.bfloat16):
+            raise TypeError("expected bf16 pre")
+        if accumulate and (dw is None or dbias is None):
+            raise ValueError("accumulate needs dw and dbias")
+        if dbias is None:
+            dbias = _empty((self.n,), torch.float32, dy.device, stream)
+        elif dbias.dtype is not torch.float32 or dbias.shape != (self.n,) or not dbias.is_contiguous():
+            raise ValueError("dbias: contiguous fp32 [n]")
+        if dw is None:
+            dw = _empty((self.n, self.d), torch.float32, dy.device, stream)
+        elif dw.shape != (self.n, self.d):
+            raise ValueError(f"dw: [{self.n}][{self.d}]")
+        _act_bwd(dy, _row_stride(dy, "dy"), pre, self.act, self.dh, dbias, accumulate, self.scratch, stream)
+        dh = dy if self.dh is None else self.dh
+        dx = nvfp4_bf16_gemm_grouped(dh, w.unsqueeze(0), self.offsets, b_kn=True, out=dx, ws=self.ws, stream=stream)
+        nvfp4_bf16_wgrad_grouped(dh, x, self.offsets, out=dw.unsqueeze(0), accumulate=accumulate, ws=self.ws, stream=stream)
+        return dx, dw, dbias
+
+
+# ---------------------------------------------------------------------------------------
 # routing of tokens to experts, and their rows into the experts' order and back
 # ---------------------------------------------------------------------------------------
 @dataclass
@@ -842,16 +1006,6 @@ def nvfp4_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, routes: Routes
     if st:
         _check(st, "nvfp4_route_bwd")
     return out
-
-
-def _row_stride(x: torch.Tensor, what: str):
-    """The row stride of a 2-D tensor with a contiguous inner dimension (a single row's: its width)."""
-    if x.dim() != 2:
-        raise ValueError(f"{what}: two dimensions")
-    row, col = x.stride()
-    if col != 1:
-        raise ValueError(f"{what}: inner dimension must be contiguous")
-    return row if x.shape[0] > 1 else x.shape[1]
 
 
 def nvfp4_dispatch(x: torch.Tensor, routes: Routes, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:

@@ -1,0 +1,131 @@
+// act.cuh -- the activations of the products' epilogues and their slopes, in fp32.
+//
+//   relu  max(h, 0)      relu2  max(h, 0)^2      gelu  h Phi(h)      silu  h / (1 + e^-h)
+//
+// Two evaluations.  `wide` (fp32 results): CUDA's normcdff, expf and IEEE quotients.  Otherwise, for bf16
+// results: the approximate reciprocal and 2^x, Phi from the Chebyshev fit of erfc published by Press,
+// Teukolsky, Vetterling and Flannery (Numerical Recipes, 2nd ed., section 6.2), relative error
+// below 1.2e-7, whose exponential's argument, rounded to fp32, makes it 1e-6 for |h| < 3 and 1e-5 at 12: a bf16 half
+// step is 2e-3.  Below -30 all of gelu and its slope are zero in fp32 (Phi(-30) = 5e-198).
+#pragma once
+
+#include <cstdint>
+
+#include "nvfp4_device.cuh"
+
+namespace nvfp4 {
+
+enum : int { kActNone = 0, kActRelu = 1, kActRelu2 = 2, kActGelu = 3, kActSilu = 4 };
+
+namespace act {
+
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float exp2a(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// of a pair: a = min(|h|, 30), NaN kept; erfc(a / sqrt 2), and m2 = -a^2 / 2
+__device__ __forceinline__ uint64_t erfc_of(float al, float ah, uint64_t& m2) {
+    const uint64_t a = f2(al, ah);
+    float dl, dh;
+    f2_split(f2_fma(a, f2c(0.35355339059327376f), f2c(1.0f)), dl, dh);
+    const uint64_t t = f2(rcp(dl), rcp(dh));   // 1 / (1 + z / 2), z = a / sqrt 2
+    uint64_t p = f2c(0.17087277f);
+    p = f2_fma(t, p, f2c(-0.82215223f));
+    p = f2_fma(t, p, f2c(1.48851587f));
+    p = f2_fma(t, p, f2c(-1.13520398f));
+    p = f2_fma(t, p, f2c(0.27886807f));
+    p = f2_fma(t, p, f2c(-0.18628806f));
+    p = f2_fma(t, p, f2c(0.09678418f));
+    p = f2_fma(t, p, f2c(0.37409196f));
+    p = f2_fma(t, p, f2c(1.00002368f));
+    m2 = f2_mul(f2_mul(a, f2c(-0.5f)), a);
+    float xl, xh;
+    f2_split(f2_mul(f2_add(f2_fma(t, p, f2c(-1.26551223f)), m2), f2c(kLog2e)), xl, xh);
+    return f2_mul(t, f2(exp2a(xl), exp2a(xh)));
+}
+__device__ __forceinline__ float capped(float h) {
+    const float a = fabsf(h);
+    return a > 30.0f ? 30.0f : a;
+}
+
+// a pair of activations, in place
+template <int ACT>
+__device__ __forceinline__ void pair(float& x, float& y) {
+    if (ACT == kActRelu || ACT == kActRelu2) {
+        x = x < 0.0f ? 0.0f : x;
+        y = y < 0.0f ? 0.0f : y;
+        if (ACT == kActRelu2) {
+            x *= x;
+            y *= y;
+        }
+    } else if (ACT == kActGelu) {   // max(h, 0) - |h| erfc(|h| / sqrt 2) / 2
+        const float al = capped(x), ah = capped(y);
+        uint64_t m2;
+        const uint64_t e = erfc_of(al, ah, m2);
+        f2_split(f2_fma(f2(-0.5f * al, -0.5f * ah), e, f2(x > 0.0f ? x : 0.0f, y > 0.0f ? y : 0.0f)), x, y);
+    } else if (ACT == kActSilu) {
+        x = x * rcp(1.0f + exp2a(x * -kLog2e));
+        y = y * rcp(1.0f + exp2a(y * -kLog2e));
+    }
+}
+// one activation, as exact as fp32 has it
+template <int ACT>
+__device__ __forceinline__ float wide(float h) {
+    if (ACT == kActRelu) return h < 0.0f ? 0.0f : h;
+    if (ACT == kActRelu2) return h < 0.0f ? 0.0f : h * h;
+    if (ACT == kActGelu) return h * normcdff(h);
+    if (ACT == kActSilu) return h / (1.0f + expf(-h));
+    return h;
+}
+__device__ __forceinline__ float wide(int act, float h) {
+    switch (act) {
+        case kActRelu: return wide<kActRelu>(h);
+        case kActRelu2: return wide<kActRelu2>(h);
+        case kActGelu: return wide<kActGelu>(h);
+        case kActSilu: return wide<kActSilu>(h);
+    }
+    return h;
+}
+
+// a pair of slopes
+template <int ACT>
+__device__ __forceinline__ void slope_pair(float& x, float& y) {
+    if (ACT == kActNone) {
+        x = y = 1.0f;
+    } else if (ACT == kActRelu) {
+        x = x > 0.0f ? 1.0f : (x <= 0.0f ? 0.0f : x);
+        y = y > 0.0f ? 1.0f : (y <= 0.0f ? 0.0f : y);
+    } else if (ACT == kActRelu2) {
+        x = x < 0.0f ? 0.0f : 2.0f * x;
+        y = y < 0.0f ? 0.0f : 2.0f * y;
+    } else if (ACT == kActGelu) {   // Phi(h) + h phi(h)
+        const float al = capped(x), ah = capped(y);
+        uint64_t m2;
+        const uint64_t e = erfc_of(al, ah, m2);
+        const uint64_t cdf = f2_fma(f2(x >= 0.0f ? -0.5f : 0.5f, y >= 0.0f ? -0.5f : 0.5f), e,
+                                    f2(x >= 0.0f ? 1.0f : 0.0f, y >= 0.0f ? 1.0f : 0.0f));
+        float ml, mh;
+        f2_split(f2_mul(m2, f2c(kLog2e)), ml, mh);
+        const uint64_t hc = f2_mul(f2(x < 0.0f ? -al : al, y < 0.0f ? -ah : ah), f2c(0.39894228040143268f));
+        f2_split(f2_fma(hc, f2(exp2a(ml), exp2a(mh)), cdf), x, y);
+    } else {                        // s (1 + h (1 - s)), s = 1 / (1 + e^-h); h (1 - s) = h e^-|h| / (1 + e^-|h|) where it is small
+        const float el = exp2a(fabsf(x) * -kLog2e), eh = exp2a(fabsf(y) * -kLog2e);
+        const float rl = rcp(1.0f + el), rh = rcp(1.0f + eh);
+        const float cl = x > 100.0f ? 100.0f : (x < -100.0f ? -100.0f : x), ch = y > 100.0f ? 100.0f : (y < -100.0f ? -100.0f : y);
+        const float sl = (x >= 0.0f ? 1.0f : el) * rl, sh = (y >= 0.0f ? 1.0f : eh) * rh;
+        const float ol = (x >= 0.0f ? el : 1.0f) * rl, oh = (y >= 0.0f ? eh : 1.0f) * rh;
+        x = sl * fmaf(cl, ol, 1.0f);
+        y = sh * fmaf(ch, oh, 1.0f);
+    }
+}
+
+}  // namespace act
+}  // namespace nvfp4

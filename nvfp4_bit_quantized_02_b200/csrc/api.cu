@@ -965,6 +965,83 @@ nvfp4_status nvfp4_combine_bwd(const void* dy, int64_t lddy, const void* ys, int
     return from_cuda(launch_combine_bwd(c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static bool is_act(nvfp4_act a) { return a >= NVFP4_ACT_NONE && a <= NVFP4_ACT_SILU; }
+
+nvfp4_status nvfp4_bf16_gemm_act(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                                 const float* bias, nvfp4_act act, const void* residual, int64_t ldr,
+                                 nvfp4_dtype residual_dtype, void* pre, int64_t ldpre, void* d, int64_t ldd,
+                                 nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream) {
+    if (!is_dtype(out_dtype) || !is_act(act) || (residual && !is_dtype(residual_dtype))) return NVFP4_ERR_ARG;
+    if (M < 0 || N < 1 || K < 8 || K % 8 || lda < K || ldb < K || ldd < N) return NVFP4_ERR_SHAPE;
+    if ((residual && ldr < N) || (pre && ldpre < N)) return NVFP4_ERR_SHAPE;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim || lda > kMaxDim || ldb > kMaxDim || ldd > kMaxDim ||
+        (residual && ldr > kMaxDim) || (pre && ldpre > kMaxDim) || ((M + 31) / 32) * ((N + 255) / 256) > (int64_t)1 << 28)
+        return NVFP4_ERR_LIMIT;
+    if (!ws) return NVFP4_ERR_WORKSPACE;
+    if (!b || (M > 0 && (!a || !d))) return NVFP4_ERR_NULL;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(d) || !aligned16(residual) || !aligned16(pre) || !aligned4(bias) || lda % 8 ||
+        ldb % 8)
+        return NVFP4_ERR_ALIGN;
+    if (nvfp4_status st = check_device()) return st;
+    if (M == 0) return NVFP4_OK;
+    GemmAct g{};
+    g.a = reinterpret_cast<const uint16_t*>(a);
+    g.b = reinterpret_cast<const uint16_t*>(b);
+    g.bias = bias;
+    g.residual = residual;
+    g.pre = reinterpret_cast<uint16_t*>(pre);
+    g.d = d;
+    g.lda = lda;
+    g.ldb = ldb;
+    g.ldr = ldr;
+    g.ldpre = ldpre;
+    g.ldd = ldd;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.act = act;
+    g.out_fp32 = out_dtype == NVFP4_OUT_FP32;
+    g.res_fp32 = residual && residual_dtype == NVFP4_OUT_FP32;
+    g.flags = &ws_of(ws)->flags;
+    g.budget_ns = g_budget_ns.load();
+    return from_cuda(launch_gemm_act(g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_act_bwd_scratch_bytes(int64_t n) {
+    return n > 0 && n <= kMaxDim ? (size_t)kActBwdRuns * (size_t)n * sizeof(float) : 0;
+}
+
+nvfp4_status nvfp4_act_bwd(const void* dy, int64_t lddy, const void* pre, int64_t ldpre, int64_t rows, int64_t n,
+                           nvfp4_act act, void* dh, int64_t lddh, float* dbias, int accumulate, void* scratch,
+                           nvfp4_stream_t stream) {
+    if (!is_act(act) || (accumulate != 0 && accumulate != 1)) return NVFP4_ERR_ARG;
+    const bool reads_pre = act != NVFP4_ACT_NONE;
+    if (rows < 0 || n < 8 || n % 8 || lddy < n || (reads_pre && ldpre < n) || (dh && lddh < n)) return NVFP4_ERR_SHAPE;
+    if (rows > kMaxDim || n > kMaxDim || lddy > kMaxDim || (reads_pre && ldpre > kMaxDim) || (dh && lddh > kMaxDim))
+        return NVFP4_ERR_LIMIT;
+    if ((!dh && !dbias) || (dbias && !scratch) || (rows > 0 && (!dy || (reads_pre && !pre)))) return NVFP4_ERR_NULL;
+    if (!aligned16(dy) || !aligned16(dh) || !aligned4(dbias) || !aligned16(scratch) || lddy % 8 || (dh && lddh % 8) ||
+        (reads_pre && (!aligned16(pre) || ldpre % 8)))
+        return NVFP4_ERR_ALIGN;
+    if (nvfp4_status st = check_device()) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows == 0) return dbias && !accumulate ? from_cuda(cudaMemsetAsync(dbias, 0, n * sizeof(float), s)) : NVFP4_OK;
+    ActBwd p{};
+    p.dy = reinterpret_cast<const uint16_t*>(dy);
+    p.pre = reinterpret_cast<const uint16_t*>(pre);
+    p.dh = reinterpret_cast<uint16_t*>(dh);
+    p.dbias = dbias;
+    p.scratch = reinterpret_cast<float*>(scratch);
+    p.lddy = lddy;
+    p.ldpre = ldpre;
+    p.lddh = lddh;
+    p.rows = rows;
+    p.n = n;
+    p.act = act;
+    p.accumulate = accumulate != 0;
+    return from_cuda(launch_act_bwd(p, s));
+}
+
 nvfp4_status nvfp4_adamw_dynamic_values(const nvfp4_adamw_args* args, nvfp4_adamw_dynamic* out) {
     if (!args || !out) return NVFP4_ERR_NULL;
     if (!(args->beta1 >= 0.0 && args->beta1 < 1.0 && args->beta2 >= 0.0 && args->beta2 < 1.0)) return NVFP4_ERR_ARG;

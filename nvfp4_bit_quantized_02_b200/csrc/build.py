@@ -25,9 +25,10 @@ SOURCES = {
     "grouped_few.cu": [],
     "route.cu": [],
     "tokens.cu": [],
+    "gemm_act.cu": [],
     "noalloc.cu": [],
 }
-HEADERS = ["nvfp4_device.cuh", "nvfp4_internal.h", "sm100_ptx.cuh"]
+HEADERS = ["act.cuh", "nvfp4_device.cuh", "nvfp4_internal.h", "sm100_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include"), "-I" + HERE]
 

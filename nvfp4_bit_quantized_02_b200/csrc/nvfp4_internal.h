@@ -212,6 +212,36 @@ cudaError_t launch_dispatch(const TokenRows& m, const uint16_t* x, int64_t ldx, 
 cudaError_t launch_combine(const Combine& c, cudaStream_t s);
 cudaError_t launch_combine_bwd(const CombineBwd& c, cudaStream_t s);
 
+// D = act(A . B^T + bias) + residual (the arguments of nvfp4_bf16_gemm_act, checked)
+struct GemmAct {
+    const uint16_t* a;
+    const uint16_t* b;
+    const float* bias;          // or NULL
+    const void* residual;       // or NULL; may be d
+    uint16_t* pre;              // or NULL
+    void* d;
+    int64_t lda, ldb, ldr, ldpre, ldd;
+    int64_t M, N, K;
+    int act;
+    bool out_fp32, res_fp32;
+    uint32_t* flags;
+    uint64_t budget_ns;
+};
+constexpr int kActBwdRuns = 64;   // runs of rows whose sums the scratch holds [runs][n]
+struct ActBwd {
+    const uint16_t* dy;
+    const uint16_t* pre;        // NULL: no activation
+    uint16_t* dh;               // or NULL
+    float* dbias;               // or NULL
+    float* scratch;
+    int64_t lddy, ldpre, lddh;
+    int64_t rows, n;
+    int act;
+    bool accumulate;
+};
+cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s);
+cudaError_t launch_act_bwd(const ActBwd& p, cudaStream_t s);
+
 // AdamW: one tensor of a launch (80 bytes: a launch's table fits the 32764 bytes of kernel parameters)
 constexpr int kAdamMaxTensors = 384;
 constexpr uint32_t kStreamMoment1 = 4u, kStreamMoment2 = 5u;
