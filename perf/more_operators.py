@@ -234,7 +234,9 @@ def run_own(s, case):
     if op == "dispatch":
         return nv.nvfp4_dispatch(s["x"], own_routes(nv, s), out=s["out"])
     if op == "combine":
-        return nv.nvfp4_combine(s["ys"], own_routes(nv, s), residual=s["residual"], out=s["out"])
+        # an fp32 residual is the running sum itself, as in the plain form
+        out = s["residual"] if case["residual"] and case["out"] == "fp32" else s["out"]
+        return nv.nvfp4_combine(s["ys"], own_routes(nv, s), residual=s["residual"], out=out)
     return list(nv.nvfp4_combine_bwd(s["dy"], s["ys"], own_routes(nv, s), dys=s["dys"], dweights=s["dweights"]))
 
 
