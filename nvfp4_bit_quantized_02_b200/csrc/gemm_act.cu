@@ -36,7 +36,7 @@ constexpr int kGaStageBytes = 2 * kGaOpBytes;
 constexpr int kGaRing = kGaStages * kGaStageBytes;       // 192 KiB
 constexpr int kGaEpiWarps = 16;
 constexpr int kGaThreads = 64 + 32 * kGaEpiWarps;
-constexpr int kGaRunK = 512, kGaRunBf16 = 1024;          // products per accumulator with fp32, bf16 output
+constexpr int kGaRunK = 512, kGaRunBf16 = 4096;          // products per accumulator with fp32, bf16 output
 constexpr int kGaBand = 8;                               // row tiles swept together along the features (L2 reuse)
 constexpr uint64_t kGaDrainNs = 2000000000ull;           // teardown waits, whatever the caller's budget
 
@@ -47,7 +47,7 @@ struct GemmActParams {
     void* d;
     int64_t ldr, ldpre, ldd;
     int32_t M, N;
-    int32_t stages;         // of K
+    int32_t stages, run;    // of K, and of an accumulator
     int32_t np, nq, wq;     // feature tiles, row tiles and their width
     int32_t act, out_fp32, res_fp32;
     int32_t pairs;          // D, pre and the residual can be taken two features at a time
@@ -95,22 +95,27 @@ __device__ __forceinline__ void commit_pair(uint32_t bar, uint32_t leader) {
         "h"((uint16_t)(3u << leader))
         : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(r[0]), "f"(r[1]),
+                 "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
 // ---------------------------------------------------------------------------------------
-// epilogue: 16 rows of one feature per lane, from sums to their places
+// epilogue: 8 rows of one feature per lane, from sums to their places
 // ---------------------------------------------------------------------------------------
 template <int ACT>
-__device__ __forceinline__ void act16(float* v, bool wide) {
-    if (ACT == kActNone) return;
+__device__ __forceinline__ void act8(float* v, bool wide) {
     if (wide) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = act::wide<ACT>(v[i]);
+        for (int i = 0; i < 8; ++i) v[i] = act::wide<ACT>(v[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) act::pair<ACT>(v[i], v[i + 1]);
+        for (int i = 0; i < 8; i += 2) act::pair<ACT>(v[i], v[i + 1]);
     }
 }
 
@@ -126,93 +131,93 @@ __device__ __forceinline__ void put_pair(uint16_t* at, float2 v, int left) {   /
     else if (left > 0) *at = (uint16_t)w;
 }
 
-// v: sums of rows row0 .. row0 + 15 of feature f, the first n of which exist
-__device__ __forceinline__ void finish16(float* v, const GemmActParams& p, int row0, int n, int f, float bias) {
-    const int odd = threadIdx.x & 1;
+// v: sums of rows row0 .. row0 + 7 of feature f, the first n of which exist
+__device__ __forceinline__ void finish8(float* v, const GemmActParams& p, int row0, int n, int f, float bias) {
+    const int odd = threadIdx.x & 1, fe = f - odd, left = p.N - fe;
+    // the residual first: its loads are under way during the rest, and are widened where they are added
+    float2 w[4];
+    uint32_t u[4];
     const bool pairs = p.pairs && !p.out_fp32;
-    const int fe = f - odd;
+    if (p.residual) {
+        if (pairs && p.res_fp32) {
+            const float* r = reinterpret_cast<const float*>(p.residual) + (int64_t)(row0 + odd) * p.ldr + fe;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += bias;
+            for (int i = 0; i < 4; ++i, r += 2 * p.ldr) {
+                w[i] = make_float2(0.0f, 0.0f);
+                if (2 * i + odd < n) {
+                    if (left > 1) w[i] = *reinterpret_cast<const float2*>(r);
+                    else if (left > 0) w[i].x = *r;
+                }
+            }
+        } else if (pairs) {
+            const uint16_t* r = reinterpret_cast<const uint16_t*>(p.residual) + (int64_t)(row0 + odd) * p.ldr + fe;
+#pragma unroll
+            for (int i = 0; i < 4; ++i, r += 2 * p.ldr) {
+                u[i] = 0;
+                if (2 * i + odd < n) {
+                    if (left > 1) u[i] = *reinterpret_cast<const uint32_t*>(r);
+                    else if (left > 0) u[i] = *r;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float one = 0.0f;
+                if (i < n && f < p.N) {
+                    const int64_t at = (int64_t)(row0 + i) * p.ldr + f;
+                    one = p.res_fp32 ? reinterpret_cast<const float*>(p.residual)[at]
+                                   : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p.residual)[at] << 16);
+                }
+                if (i & 1) w[i >> 1].y = one;
+                else w[i >> 1].x = one;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += bias;
     if (p.pre) {
         if (p.pairs) {
             uint16_t* at = p.pre + (int64_t)(row0 + odd) * p.ldpre + fe;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2, at += 2 * p.ldpre) {
+            for (int i = 0; i < 8; i += 2, at += 2 * p.ldpre) {
                 const float2 t = traded(v[i], v[i + 1], odd);
-                if (i + odd < n) put_pair(at, t, p.N - fe);
+                if (i + odd < n) put_pair(at, t, left);
             }
         } else if (f < p.N) {
             uint16_t* at = p.pre + (int64_t)row0 * p.ldpre + f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i, at += p.ldpre)
+            for (int i = 0; i < 8; ++i, at += p.ldpre)
                 if (i < n) *at = (uint16_t)f32x2_to_bf16x2(v[i], 0.0f);
         }
     }
     switch (p.act) {
-        case kActRelu: act16<kActRelu>(v, p.out_fp32); break;
-        case kActRelu2: act16<kActRelu2>(v, p.out_fp32); break;
-        case kActGelu: act16<kActGelu>(v, p.out_fp32); break;
-        case kActSilu: act16<kActSilu>(v, p.out_fp32); break;
+        case kActRelu: act8<kActRelu>(v, p.out_fp32); break;
+        case kActRelu2: act8<kActRelu2>(v, p.out_fp32); break;
+        case kActGelu: act8<kActGelu>(v, p.out_fp32); break;
+        case kActSilu: act8<kActSilu>(v, p.out_fp32); break;
     }
     if (pairs) {
         uint16_t* at = reinterpret_cast<uint16_t*>(p.d) + (int64_t)(row0 + odd) * p.ldd + fe;
-        const bool two = fe + 1 < p.N, one = fe < p.N;
-        if (p.residual && !p.res_fp32) {
-            const uint16_t* r = reinterpret_cast<const uint16_t*>(p.residual) + (int64_t)(row0 + odd) * p.ldr + fe;
-            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i, r += 2 * p.ldr) {
-                w[i] = 0;
-                if (2 * i + odd < n) w[i] = two ? *reinterpret_cast<const uint32_t*>(r) : one ? (uint32_t)*r : 0u;
+        for (int i = 0; i < 4; ++i, at += 2 * p.ldd) {
+            float2 t = traded(v[2 * i], v[2 * i + 1], odd);
+            if (p.residual) {
+                t.x += p.res_fp32 ? w[i].x : bf16_lo(u[i]);
+                t.y += p.res_fp32 ? w[i].y : bf16_hi(u[i]);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i, at += 2 * p.ldd) {
-                float2 t = traded(v[2 * i], v[2 * i + 1], odd);
-                t.x += bf16_lo(w[i]);
-                t.y += bf16_hi(w[i]);
-                if (2 * i + odd < n) put_pair(at, t, p.N - fe);
-            }
-        } else {
-            const float* r = reinterpret_cast<const float*>(p.residual) + (int64_t)(row0 + odd) * p.ldr + fe;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float2 w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i, r += 2 * p.ldr) {
-                    w[i] = make_float2(0.0f, 0.0f);
-                    if (p.residual && 8 * h + 2 * i + odd < n) {
-                        if (two) w[i] = *reinterpret_cast<const float2*>(r);
-                        else if (one) w[i].x = *r;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i, at += 2 * p.ldd) {
-                    float2 t = traded(v[8 * h + 2 * i], v[8 * h + 2 * i + 1], odd);
-                    t.x += w[i].x;
-                    t.y += w[i].y;
-                    if (8 * h + 2 * i + odd < n) put_pair(at, t, p.N - fe);
-                }
-            }
+            if (2 * i + odd < n) put_pair(at, t, left);
         }
         return;
     }
     if (f >= p.N) return;
-    float w[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        w[i] = 0.0f;
-        if (p.residual && i < n) {
-            const int64_t at = (int64_t)(row0 + i) * p.ldr + f;
-            w[i] = p.res_fp32 ? reinterpret_cast<const float*>(p.residual)[at]
-                              : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p.residual)[at] << 16);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
+        float y = v[i];
+        if (p.residual) y += i & 1 ? w[i >> 1].y : w[i >> 1].x;
         if (i < n) {
             const int64_t at = (int64_t)(row0 + i) * p.ldd + f;
-            if (p.out_fp32) reinterpret_cast<float*>(p.d)[at] = v[i] + w[i];
-            else reinterpret_cast<uint16_t*>(p.d)[at] = (uint16_t)f32x2_to_bf16x2(v[i] + w[i], 0.0f);
+            if (p.out_fp32) reinterpret_cast<float*>(p.d)[at] = y;
+            else reinterpret_cast<uint16_t*>(p.d)[at] = (uint16_t)f32x2_to_bf16x2(y, 0.0f);
         }
     }
 }
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
     cluster_wait();     // and the others'
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    const int run = (p.out_fp32 ? kGaRunK : kGaRunBf16) / kGaK;   // stages per accumulator
+    const int run = p.run;   // stages per accumulator
 
     if (warp == 0) {
         // ------------------------------- producer (both CTAs) --------------------------------
@@ -364,6 +369,8 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
             bool ok = true;
             for (int t = unit; ok && t < tiles; t += units) {
                 for (int k = s0; k < s1; k += run, ++it) {
+                    // a cluster's one tile: its last accumulator is read behind barriers that this warp takes part in
+                    if (SPLIT > 1 && k + run >= s1) break;
                     if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.edrained[it & 1]), (uint32_t)(it >> 1) & 1u, abort_flag,
                                                            p.flags, p.budget_ns))) {
                         ok = false;
@@ -376,99 +383,119 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
         }
     }
     // ------------------------------- epilogue (both CTAs) ------------------------------------
-    // Warps 2-17: the warp's TMEM lanes are 32 q .. 32 q + 31, its columns 16 c0 and every 64 further.
+    // Warps 2-17: the warp's TMEM lanes are 32 q .. 32 q + 31, its columns 16 from c0 and from every 64 further.
+    // Sums that take several runs (or parts) are joined in registers and put back where the last run stood, so that
+    // the tile is finished from TMEM, 8 columns at a time: with the 64 sums of a warp still in registers, those of
+    // the epilogue do not fit, and what is spilled goes to L2 with the output (8192 x 20480 x 5120: 1235 us).
     const bool epilogue = warp >= 2;
     const int q = warp & 3, c0 = ((warp - 2) >> 2) * 16;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     int it = 0;
     bool ok = true;
     // with SPLIT > 1 every warp comes by once, for the cluster's barriers
     for (int t = unit; (epilogue || SPLIT > 1) && ok && t < tiles; t += units) {
         const GaTile c = ga_tile(p, t);
-        const int f = c.p0 + (int)rank * 128 + q * 32 + lane;
-        float acc[64];
-        if (epilogue) {
-            const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        const auto ready = [&]() {   // the next accumulator is complete
+            const bool full = mbar_wait(smem_u32(&sm.tfull[it & 1]), (uint32_t)(it >> 1) & 1u, abort_flag, p.flags, p.budget_ns);
+            if (!__all_sync(0xFFFFFFFFu, full)) return false;
+            tc_fence_after();
+            return true;
+        };
+        const auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(rank == 0 ? &sm.tempty[it & 1] : &sm.edrained[it & 1]));
+            ++it;
+        };
+        if (SPLIT > 1 || s1 - s0 > run) {
+            float acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-            for (int k = s0; k < s1; k += run, ++it) {
-                const bool full = mbar_wait(smem_u32(&sm.tfull[it & 1]), (uint32_t)(it >> 1) & 1u, abort_flag, p.flags, p.budget_ns);
-                if (!__all_sync(0xFFFFFFFFu, full)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+            if (epilogue)
+                for (int k = s0; k < s1; k += run) {
+                    if (!(ok = ready())) break;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (c0 + 64 * h < c.qn) {
+                    for (int h = 0; h < 8; ++h) {
+                        const int at = c0 + 64 * (h >> 1) + 8 * (h & 1);
+                        if (at >= c.qn) break;
+                        float v[8];
+                        tmem_ld8(lanes + 256u * (it & 1) + (uint32_t)at, v);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 16; j += 8) {
-                            float v[8];
-                            tmem_ld8(tmem + lanes + 256u * (it & 1) + (uint32_t)(c0 + 64 * h + j), v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) acc[16 * h + j + i] += v[i];
-                        }
+                        for (int i = 0; i < 8; ++i) acc[8 * h + i] += v[i];
                     }
+                    if (k + run < s1) release();
                 }
-                tc_fence_before();
+            if constexpr (SPLIT > 1) {
+                // chunk (c0 / 16) + 4 h of 16 rows is finished by part (c0 / 16 + h) % SPLIT, in whose shared memory the
+                // others' sums of it stand at [sender][h * 4 / SPLIT + c0 / 16 / SPLIT][row][feature]
+                constexpr uint32_t kChunk = 16 * 128 * 4;
+                const int group = c0 >> 4;
+                const uint32_t mine = (uint32_t)(q * 32 + lane) * 4u;
+                const auto place = [&](int owner, int sender, int h) {
+                    const int slot = sender < owner ? sender : sender - 1;
+                    return smem_u32(smem) + (uint32_t)(slot * (16 / SPLIT) + h * (4 / SPLIT) + group / SPLIT) * kChunk + mine;
+                };
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(rank == 0 ? &sm.tempty[it & 1] : &sm.edrained[it & 1]));
-            }
-        }
-        if constexpr (SPLIT > 1) {
-            // chunk (c0 / 16) + 4 h of 16 rows is finished by part (c0 / 16 + h) % SPLIT, in whose shared memory the others'
-            // sums of it stand at [sender][h * 4 / SPLIT + c0 / 16 / SPLIT][row][feature]
-            constexpr uint32_t kChunk = 16 * 128 * 4;
-            const int group = c0 >> 4;
-            const uint32_t mine = (uint32_t)(q * 32 + lane) * 4u;
-            const auto place = [&](int owner, int sender, int h) {
-                const int slot = sender < owner ? sender : sender - 1;
-                return smem_u32(smem) + (uint32_t)(slot * (16 / SPLIT) + h * (4 / SPLIT) + group / SPLIT) * kChunk + mine;
-            };
-            __syncwarp();
-            cluster_arrive();
-            cluster_wait();      // the products of all parts are done: the rings are free
-            if (epilogue && ok) {
+                cluster_arrive();
+                cluster_wait();      // the products of all parts are done: the rings are free
+                if (epilogue && ok) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int owner = (group + h) % SPLIT;
-                    if (c0 + 64 * h >= c.qn || owner == part) continue;
-                    const uint32_t at = map_rank(place(owner, part, h), (uint32_t)(2 * owner) + rank);
+                    for (int h = 0; h < 4; ++h) {
+                        const int owner = (group + h) % SPLIT;
+                        if (c0 + 64 * h >= c.qn || owner == part) continue;
+                        const uint32_t at = map_rank(place(owner, part, h), (uint32_t)(2 * owner) + rank);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) st_cluster_f32(at + 512u * i, acc[16 * h + i]);
+                        for (int i = 0; i < 16; ++i) st_cluster_f32(at + 512u * i, acc[16 * h + i]);
+                    }
                 }
-            }
-            __syncwarp();
-            cluster_arrive();
-            cluster_wait();      // and what each part finishes is there
-            if (epilogue && ok) {
+                __syncwarp();
+                cluster_arrive();
+                cluster_wait();      // and what each part finishes is there
+                if (epilogue && ok) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (c0 + 64 * h >= c.qn || (group + h) % SPLIT != part) continue;
+                    for (int h = 0; h < 4; ++h) {
+                        if (c0 + 64 * h >= c.qn || (group + h) % SPLIT != part) continue;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float sum = 0.0f;
+                        for (int i = 0; i < 16; ++i) {
+                            float sum = 0.0f;
 #pragma unroll
-                        for (int s = 0; s < SPLIT; ++s) {   // in the order of the parts
-                            float v = acc[16 * h + i];
-                            if (s != part) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(place(part, s, h) + 512u * i));
-                            sum = s == 0 ? v : sum + v;
+                            for (int s = 0; s < SPLIT; ++s) {   // in the order of the parts
+                                float v = acc[16 * h + i];
+                                if (s != part) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(place(part, s, h) + 512u * i));
+                                sum = s == 0 ? v : sum + v;
+                            }
+                            acc[16 * h + i] = sum;
                         }
-                        acc[16 * h + i] = sum;
                     }
                 }
             }
-        }
-        if (epilogue && ok) {
-            const float bias = p.bias && f < p.N ? p.bias[f] : 0.0f;
-#pragma unroll 1
-            for (int h = 0; c0 + 64 * h < c.qn; ++h) {   // one copy of its code: the next 16 sums move up
-                if (SPLIT == 1 || ((c0 >> 4) + h) % SPLIT == part)
-                    finish16(acc, p, c.q0 + c0 + 64 * h, c.qn - (c0 + 64 * h), f, bias);
+            if (epilogue && ok) {
 #pragma unroll
-                for (int i = 0; i < 48; ++i) acc[i] = acc[i + 16];
+                for (int h = 0; h < 8; ++h) {
+                    const int at = c0 + 64 * (h >> 1) + 8 * (h & 1);
+                    if (at >= c.qn) break;
+                    tmem_st8(lanes + 256u * (it & 1) + (uint32_t)at, acc + 8 * h);
+                }
+                tmem_st_wait();
             }
+        } else {
+            ok = ready();
         }
+        if (!epilogue || !ok) continue;
+        const int f = c.p0 + (int)rank * 128 + q * 32 + lane;
+        const float bias = p.bias && f < p.N ? p.bias[f] : 0.0f;
+#pragma unroll 1
+        for (int h = 0; h < 8; ++h) {
+            const int at = c0 + 64 * (h >> 1) + 8 * (h & 1);
+            if (at >= c.qn) break;
+            if (SPLIT > 1 && ((c0 >> 4) + (h >> 1)) % SPLIT != part) continue;
+            float v[8];
+            tmem_ld8(lanes + 256u * (it & 1) + (uint32_t)at, v);
+            tmem_ld_wait();
+            finish8(v, p, c.q0 + at, c.qn - at, f, bias);
+        }
+        release();
     }
 
     // Each warp hands an abort that it has seen to the pair's leader.  No arrival may land in a CTA that has ended: those that
@@ -703,6 +730,10 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
     const int64_t stages = (g.K + kGaK - 1) / kGaK;
     const GaPlan plan = ga_plan(g.M, g.N, stages, sms);
     p.stages = (int32_t)stages;
+    // even runs: a tile is finished under the first run of the next one
+    const int64_t part = (stages + plan.split - 1) / plan.split, most = (g.out_fp32 ? kGaRunK : kGaRunBf16) / kGaK;
+    const int64_t runs = (part + most - 1) / most;
+    p.run = (int32_t)((part + runs - 1) / runs);
     p.wq = plan.wq;
     p.np = (int32_t)((g.N + 255) / 256);
     p.nq = (int32_t)((g.M + plan.wq - 1) / plan.wq);
