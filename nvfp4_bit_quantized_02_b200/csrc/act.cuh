@@ -6,7 +6,7 @@
 // results: the approximate reciprocal and 2^x, Phi from the Chebyshev fit of erfc published by Press,
 // Teukolsky, Vetterling and Flannery (Numerical Recipes, 2nd ed., section 6.2), relative error
 // below 1.2e-7, whose exponential's argument, rounded to fp32, makes it 1e-6 for |h| < 3 and 1e-5 at 12: a bf16 half
-// step is 2e-3.  Below -30 all of gelu and its slope are zero in fp32 (Phi(-30) = 5e-198).
+// step is 2e-3 at least.  Below -30 all of gelu and its slope are zero in fp32 (Phi(-30) = 5e-198).
 #pragma once
 
 #include <cstdint>
@@ -31,29 +31,32 @@ __device__ __forceinline__ float exp2a(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// of a pair: a = min(|h|, 30), NaN kept; erfc(a / sqrt 2), and m2 = -a^2 / 2
-__device__ __forceinline__ uint64_t erfc_of(float al, float ah, uint64_t& m2) {
+// min(|h|, 30), NaN kept
+__device__ __forceinline__ float capped(float h) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(h)), "f"(30.0f));
+    return r;
+}
+// erfc(a / sqrt 2) of a pair, a = capped(h): t e^(-a^2 / 2 + c(t)), t = 1 / (1 + a / sqrt 8); the fit's coefficients
+// times log2 e, for 2^x
+__device__ __forceinline__ uint64_t erfc_of(float al, float ah) {
     const uint64_t a = f2(al, ah);
     float dl, dh;
     f2_split(f2_fma(a, f2c(0.35355339059327376f), f2c(1.0f)), dl, dh);
-    const uint64_t t = f2(rcp(dl), rcp(dh));   // 1 / (1 + z / 2), z = a / sqrt 2
-    uint64_t p = f2c(0.17087277f);
-    p = f2_fma(t, p, f2c(-0.82215223f));
-    p = f2_fma(t, p, f2c(1.48851587f));
-    p = f2_fma(t, p, f2c(-1.13520398f));
-    p = f2_fma(t, p, f2c(0.27886807f));
-    p = f2_fma(t, p, f2c(-0.18628806f));
-    p = f2_fma(t, p, f2c(0.09678418f));
-    p = f2_fma(t, p, f2c(0.37409196f));
-    p = f2_fma(t, p, f2c(1.00002368f));
-    m2 = f2_mul(f2_mul(a, f2c(-0.5f)), a);
+    const uint64_t t = f2(rcp(dl), rcp(dh));
+    uint64_t p = f2c((float)(0.17087277 * 1.4426950408889634));
+    p = f2_fma(t, p, f2c((float)(-0.82215223 * 1.4426950408889634)));
+    p = f2_fma(t, p, f2c((float)(1.48851587 * 1.4426950408889634)));
+    p = f2_fma(t, p, f2c((float)(-1.13520398 * 1.4426950408889634)));
+    p = f2_fma(t, p, f2c((float)(0.27886807 * 1.4426950408889634)));
+    p = f2_fma(t, p, f2c((float)(-0.18628806 * 1.4426950408889634)));
+    p = f2_fma(t, p, f2c((float)(0.09678418 * 1.4426950408889634)));
+    p = f2_fma(t, p, f2c((float)(0.37409196 * 1.4426950408889634)));
+    p = f2_fma(t, p, f2c((float)(1.00002368 * 1.4426950408889634)));
+    p = f2_fma(t, p, f2c((float)(-1.26551223 * 1.4426950408889634)));
     float xl, xh;
-    f2_split(f2_mul(f2_add(f2_fma(t, p, f2c(-1.26551223f)), m2), f2c(kLog2e)), xl, xh);
+    f2_split(f2_fma(f2_mul(a, f2c(-0.5f * kLog2e)), a, p), xl, xh);
     return f2_mul(t, f2(exp2a(xl), exp2a(xh)));
-}
-__device__ __forceinline__ float capped(float h) {
-    const float a = fabsf(h);
-    return a > 30.0f ? 30.0f : a;
 }
 
 // a pair of activations, in place
@@ -68,9 +71,7 @@ __device__ __forceinline__ void pair(float& x, float& y) {
         }
     } else if (ACT == kActGelu) {   // max(h, 0) - |h| erfc(|h| / sqrt 2) / 2
         const float al = capped(x), ah = capped(y);
-        uint64_t m2;
-        const uint64_t e = erfc_of(al, ah, m2);
-        f2_split(f2_fma(f2(-0.5f * al, -0.5f * ah), e, f2(x > 0.0f ? x : 0.0f, y > 0.0f ? y : 0.0f)), x, y);
+        f2_split(f2_fma(f2_mul(f2(al, ah), f2c(-0.5f)), erfc_of(al, ah), f2(fmaxf(x, 0.0f), fmaxf(y, 0.0f))), x, y);
     } else if (ACT == kActSilu) {
         x = x * rcp(1.0f + exp2a(x * -kLog2e));
         y = y * rcp(1.0f + exp2a(y * -kLog2e));
@@ -108,12 +109,11 @@ __device__ __forceinline__ void slope_pair(float& x, float& y) {
         y = y < 0.0f ? 0.0f : 2.0f * y;
     } else if (ACT == kActGelu) {   // Phi(h) + h phi(h)
         const float al = capped(x), ah = capped(y);
-        uint64_t m2;
-        const uint64_t e = erfc_of(al, ah, m2);
+        const uint64_t e = erfc_of(al, ah), a = f2(al, ah);
         const uint64_t cdf = f2_fma(f2(x >= 0.0f ? -0.5f : 0.5f, y >= 0.0f ? -0.5f : 0.5f), e,
                                     f2(x >= 0.0f ? 1.0f : 0.0f, y >= 0.0f ? 1.0f : 0.0f));
         float ml, mh;
-        f2_split(f2_mul(m2, f2c(kLog2e)), ml, mh);
+        f2_split(f2_mul(f2_mul(a, f2c(-0.5f * kLog2e)), a), ml, mh);
         const uint64_t hc = f2_mul(f2(x < 0.0f ? -al : al, y < 0.0f ? -ah : ah), f2c(0.39894228040143268f));
         f2_split(f2_fma(hc, f2(exp2a(ml), exp2a(mh)), cdf), x, y);
     } else {                        // s (1 + h (1 - s)), s = 1 / (1 + e^-h); h (1 - s) = h e^-|h| / (1 + e^-|h|) where it is small

@@ -106,119 +106,109 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
 }
 
 // ---------------------------------------------------------------------------------------
-// epilogue: 8 rows of one feature per lane, from sums to their places
+// epilogue: 16 rows of one feature per lane, from sums to their places
+//
+// bf16 words hold two features of a row, so neighbouring lanes trade: a lane packs its feature of rows i and i + 1,
+// and of its own word and its neighbour's the even lane keeps row i's halves, the odd one row i + 1's.
 // ---------------------------------------------------------------------------------------
 template <int ACT>
-__device__ __forceinline__ void act8(float* v, bool wide) {
+__device__ __forceinline__ void act16(float* v, bool wide) {
     if (wide) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act::wide<ACT>(v[i]);
+        for (int i = 0; i < 16; ++i) v[i] = act::wide<ACT>(v[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) act::pair<ACT>(v[i], v[i + 1]);
+        for (int i = 0; i < 16; i += 2) act::pair<ACT>(v[i], v[i + 1]);
     }
 }
-
-// Two features of one row per lane, out of one feature of two rows: neighbouring lanes trade one value
-__device__ __forceinline__ float2 traded(float a, float b, int odd) {
-    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
-    return odd ? make_float2(other, b) : make_float2(a, other);
+__device__ __forceinline__ void act16(int act, float* v, bool wide) {
+    switch (act) {
+        case kActRelu: act16<kActRelu>(v, wide); break;
+        case kActRelu2: act16<kActRelu2>(v, wide); break;
+        case kActGelu: act16<kActGelu>(v, wide); break;
+        case kActSilu: act16<kActSilu>(v, wide); break;
+    }
+}
+// the trade, its own inverse: halves {own row i, own row i + 1} <-> {feature even, feature odd} of row i + odd
+__device__ __forceinline__ uint32_t traded(uint32_t w, uint32_t select) {
+    return __byte_perm(w, __shfl_xor_sync(0xFFFFFFFFu, w, 1), select);
+}
+// 16 rows of bf16 words from row0 + odd on, two features a lane
+__device__ __forceinline__ void put_words(uint16_t* at, int64_t ld, const float* v, uint32_t select) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2, at += 2 * ld) *reinterpret_cast<uint32_t*>(at) = traded(f32x2_to_bf16x2(v[i], v[i + 1]), select);
 }
 
-__device__ __forceinline__ void put_pair(uint16_t* at, float2 v, int left) {   // left: features from here to the end
-    const uint32_t w = f32x2_to_bf16x2(v.x, v.y);
-    if (left > 1) *reinterpret_cast<uint32_t*>(at) = w;
-    else if (left > 0) *at = (uint16_t)w;
-}
-
-// v: sums of rows row0 .. row0 + 7 of feature f, the first n of which exist
-__device__ __forceinline__ void finish8(float* v, const GemmActParams& p, int row0, int n, int f, float bias) {
-    const int odd = threadIdx.x & 1, fe = f - odd, left = p.N - fe;
-    // the residual first: its loads are under way during the rest, and are widened where they are added
-    float2 w[4];
-    uint32_t u[4];
-    const bool pairs = p.pairs && !p.out_fp32;
+// v: sums of rows row0 .. row0 + 15 of feature f.  All of the rows and of the warp's 32 features exist, and leading
+// dimensions are even.
+__device__ __forceinline__ void finish16(float* v, const GemmActParams& p, int row0, int f, float bias) {
+    const int odd = threadIdx.x & 1, fe = f - odd;
+    const uint32_t select = odd ? 0x3276u : 0x5410u;
+    // the residual first: its loads are under way during the rest
+    float w[16];
     if (p.residual) {
-        if (pairs && p.res_fp32) {
-            const float* r = reinterpret_cast<const float*>(p.residual) + (int64_t)(row0 + odd) * p.ldr + fe;
+        if (p.res_fp32) {
+            const float* r = reinterpret_cast<const float*>(p.residual) + row0 * p.ldr + f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i, r += 2 * p.ldr) {
-                w[i] = make_float2(0.0f, 0.0f);
-                if (2 * i + odd < n) {
-                    if (left > 1) w[i] = *reinterpret_cast<const float2*>(r);
-                    else if (left > 0) w[i].x = *r;
-                }
-            }
-        } else if (pairs) {
-            const uint16_t* r = reinterpret_cast<const uint16_t*>(p.residual) + (int64_t)(row0 + odd) * p.ldr + fe;
+            for (int i = 0; i < 16; ++i, r += p.ldr) w[i] = *r;
+        } else {
+            const uint16_t* r = reinterpret_cast<const uint16_t*>(p.residual) + (row0 + odd) * p.ldr + fe;
 #pragma unroll
-            for (int i = 0; i < 4; ++i, r += 2 * p.ldr) {
-                u[i] = 0;
-                if (2 * i + odd < n) {
-                    if (left > 1) u[i] = *reinterpret_cast<const uint32_t*>(r);
-                    else if (left > 0) u[i] = *r;
-                }
-            }
+            for (int i = 0; i < 8; ++i, r += 2 * p.ldr) w[i] = __uint_as_float(*reinterpret_cast<const uint32_t*>(r));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += bias;
+    if (p.pre) put_words(p.pre + (row0 + odd) * p.ldpre + fe, p.ldpre, v, select);
+    act16(p.act, v, p.out_fp32);
+    if (p.residual) {
+        if (p.res_fp32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += w[i];
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float one = 0.0f;
-                if (i < n && f < p.N) {
-                    const int64_t at = (int64_t)(row0 + i) * p.ldr + f;
-                    one = p.res_fp32 ? reinterpret_cast<const float*>(p.residual)[at]
-                                   : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p.residual)[at] << 16);
-                }
-                if (i & 1) w[i >> 1].y = one;
-                else w[i >> 1].x = one;
+                const uint32_t u = traded(__float_as_uint(w[i]), select);
+                v[2 * i] += bf16_lo(u);
+                v[2 * i + 1] += bf16_hi(u);
             }
         }
     }
+    if (p.out_fp32) {
+        float* at = reinterpret_cast<float*>(p.d) + row0 * p.ldd + f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += bias;
-    if (p.pre) {
-        if (p.pairs) {
-            uint16_t* at = p.pre + (int64_t)(row0 + odd) * p.ldpre + fe;
-#pragma unroll
-            for (int i = 0; i < 8; i += 2, at += 2 * p.ldpre) {
-                const float2 t = traded(v[i], v[i + 1], odd);
-                if (i + odd < n) put_pair(at, t, left);
-            }
-        } else if (f < p.N) {
-            uint16_t* at = p.pre + (int64_t)row0 * p.ldpre + f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i, at += p.ldpre)
-                if (i < n) *at = (uint16_t)f32x2_to_bf16x2(v[i], 0.0f);
-        }
+        for (int i = 0; i < 16; ++i, at += p.ldd) *at = v[i];
+    } else {
+        put_words(reinterpret_cast<uint16_t*>(p.d) + (row0 + odd) * p.ldd + fe, p.ldd, v, select);
     }
-    switch (p.act) {
-        case kActRelu: act8<kActRelu>(v, p.out_fp32); break;
-        case kActRelu2: act8<kActRelu2>(v, p.out_fp32); break;
-        case kActGelu: act8<kActGelu>(v, p.out_fp32); break;
-        case kActSilu: act8<kActSilu>(v, p.out_fp32); break;
-    }
-    if (pairs) {
-        uint16_t* at = reinterpret_cast<uint16_t*>(p.d) + (int64_t)(row0 + odd) * p.ldd + fe;
-#pragma unroll
-        for (int i = 0; i < 4; ++i, at += 2 * p.ldd) {
-            float2 t = traded(v[2 * i], v[2 * i + 1], odd);
-            if (p.residual) {
-                t.x += p.res_fp32 ? w[i].x : bf16_lo(u[i]);
-                t.y += p.res_fp32 ? w[i].y : bf16_hi(u[i]);
-            }
-            if (2 * i + odd < n) put_pair(at, t, left);
-        }
-        return;
-    }
+}
+
+// The same at the edges of the output, or where a leading dimension is odd: the first n rows, element by element
+__device__ __noinline__ void finish_edge(float v0, float v1, float v2, float v3, const GemmActParams& p, int64_t row0, int n, int f, float bias) {
+    float v[4] = {v0 + bias, v1 + bias, v2 + bias, v3 + bias};
     if (f >= p.N) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float y = v[i];
-        if (p.residual) y += i & 1 ? w[i >> 1].y : w[i >> 1].x;
-        if (i < n) {
-            const int64_t at = (int64_t)(row0 + i) * p.ldd + f;
-            if (p.out_fp32) reinterpret_cast<float*>(p.d)[at] = y;
-            else reinterpret_cast<uint16_t*>(p.d)[at] = (uint16_t)f32x2_to_bf16x2(y, 0.0f);
+    for (int i = 0; i < 4; ++i) {
+        if (i >= n) break;
+        const int64_t row = row0 + i;
+        if (p.pre) p.pre[row * p.ldpre + f] = (uint16_t)f32x2_to_bf16x2(v[i], 0.0f);
+        float y;
+        if (p.out_fp32) {
+            y = act::wide(p.act, v[i]);
+        } else {
+            float z = y = v[i];
+            switch (p.act) {
+                case kActRelu: act::pair<kActRelu>(y, z); break;
+                case kActRelu2: act::pair<kActRelu2>(y, z); break;
+                case kActGelu: act::pair<kActGelu>(y, z); break;
+                case kActSilu: act::pair<kActSilu>(y, z); break;
+            }
         }
+        if (p.residual)
+            y += p.res_fp32 ? reinterpret_cast<const float*>(p.residual)[row * p.ldr + f]
+                            : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p.residual)[row * p.ldr + f] << 16);
+        if (p.out_fp32) reinterpret_cast<float*>(p.d)[row * p.ldd + f] = y;
+        else reinterpret_cast<uint16_t*>(p.d)[row * p.ldd + f] = (uint16_t)f32x2_to_bf16x2(y, 0.0f);
     }
 }
 
@@ -226,7 +216,7 @@ __device__ __forceinline__ void finish8(float* v, const GemmActParams& p, int ro
 // the kernel
 // ---------------------------------------------------------------------------------------
 template <int SPLIT>
-__global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_constant__ GemmActMaps maps, const GemmActParams p) {
+__global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_constant__ GemmActMaps maps, const __grid_constant__ GemmActParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     GemmActSmem& sm = *reinterpret_cast<GemmActSmem*>(smem + kGaRing);
@@ -385,7 +375,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
     // ------------------------------- epilogue (both CTAs) ------------------------------------
     // Warps 2-17: the warp's TMEM lanes are 32 q .. 32 q + 31, its columns 16 from c0 and from every 64 further.
     // Sums that take several runs (or parts) are joined in registers and put back where the last run stood, so that
-    // the tile is finished from TMEM, 8 columns at a time: with the 64 sums of a warp still in registers, those of
+    // the tile is finished from TMEM, 16 columns at a time: with the 64 sums of a warp still in registers, those of
     // the epilogue do not fit, and what is spilled goes to L2 with the output (8192 x 20480 x 5120: 1235 us).
     const bool epilogue = warp >= 2;
     const int q = warp & 3, c0 = ((warp - 2) >> 2) * 16;
@@ -485,15 +475,22 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
         if (!epilogue || !ok) continue;
         const int f = c.p0 + (int)rank * 128 + q * 32 + lane;
         const float bias = p.bias && f < p.N ? p.bias[f] : 0.0f;
+        const bool whole = p.pairs && f - lane + 32 <= p.N;
 #pragma unroll 1
-        for (int h = 0; h < 8; ++h) {
-            const int at = c0 + 64 * (h >> 1) + 8 * (h & 1);
+        for (int h = 0; h < 4; ++h) {
+            const int at = c0 + 64 * h;
             if (at >= c.qn) break;
-            if (SPLIT > 1 && ((c0 >> 4) + (h >> 1)) % SPLIT != part) continue;
-            float v[8];
-            tmem_ld8(lanes + 256u * (it & 1) + (uint32_t)at, v);
+            if (SPLIT > 1 && ((c0 >> 4) + h) % SPLIT != part) continue;
+            float v[16];
+            tmem_ld16(lanes + 256u * (it & 1) + (uint32_t)at, v);
             tmem_ld_wait();
-            finish8(v, p, c.q0 + at, c.qn - at, f, bias);
+            if (whole && at + 16 <= c.qn) {
+                finish16(v, p, c.q0 + at, f, bias);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    if (at + i < c.qn) finish_edge(v[i], v[i + 1], v[i + 2], v[i + 3], p, c.q0 + at + i, c.qn - (at + i), f, bias);
+            }
         }
         release();
     }
