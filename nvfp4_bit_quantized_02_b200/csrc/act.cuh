@@ -2,11 +2,11 @@
 //
 //   relu  max(h, 0)      relu2  max(h, 0)^2      gelu  h Phi(h)      silu  h / (1 + e^-h)
 //
-// Two evaluations.  `wide` (fp32 results): CUDA's normcdff, expf and IEEE quotients.  Otherwise, for bf16
-// results: the approximate reciprocal and 2^x, Phi from the Chebyshev fit of erfc published by Press,
-// Teukolsky, Vetterling and Flannery (Numerical Recipes, 2nd ed., section 6.2), relative error
-// below 1.2e-7, whose exponential's argument, rounded to fp32, makes it 1e-6 for |h| < 3 and 1e-5 at 12: a bf16 half
-// step is 2e-3 at least.  Below -30 all of gelu and its slope are zero in fp32 (Phi(-30) = 5e-198).
+// By the approximate reciprocal and 2^x, Phi from the Chebyshev fit of erfc published by Press, Teukolsky, Vetterling
+// and Flannery (Numerical Recipes, 2nd ed., section 6.2), relative error below 1.2e-7.  The exponential's argument, rounded to
+// fp32, makes it 1e-6 for |h| < 3 and 1e-5 at 12, of a term that has become small there: gelu and silu err by less than 2^-20 |h|, for
+// fp32 outputs too (expf, normcdff and IEEE quotients took a tile of 16 rows 1.2 to 4 us longer, the quotient of a zero most of
+// all).  Below -30 all of gelu and its slope are zero in fp32 (Phi(-30) = 5e-198).
 #pragma once
 
 #include <cstdint>
@@ -77,21 +77,13 @@ __device__ __forceinline__ void pair(float& x, float& y) {
         y = y * rcp(1.0f + exp2a(y * -kLog2e));
     }
 }
-// one activation, as exact as fp32 has it
-template <int ACT>
-__device__ __forceinline__ float wide(float h) {
-    if (ACT == kActRelu) return h < 0.0f ? 0.0f : h;
-    if (ACT == kActRelu2) return h < 0.0f ? 0.0f : h * h;
-    if (ACT == kActGelu) return h * normcdff(h);
-    if (ACT == kActSilu) return h / (1.0f + expf(-h));
-    return h;
-}
-__device__ __forceinline__ float wide(int act, float h) {
+__device__ __forceinline__ float one(int act, float h) {
+    float z = 0.0f;
     switch (act) {
-        case kActRelu: return wide<kActRelu>(h);
-        case kActRelu2: return wide<kActRelu2>(h);
-        case kActGelu: return wide<kActGelu>(h);
-        case kActSilu: return wide<kActSilu>(h);
+        case kActRelu: pair<kActRelu>(h, z); break;
+        case kActRelu2: pair<kActRelu2>(h, z); break;
+        case kActGelu: pair<kActGelu>(h, z); break;
+        case kActSilu: pair<kActSilu>(h, z); break;
     }
     return h;
 }

@@ -1,25 +1,30 @@
 // gemm_act.cu -- the bf16 product with bias, activation and residual in its epilogue (sm_100a):
 //   h[t][f] = sum_k A[t][k] B[f][k] + bias[f],   D = act(h) + residual,   pre = h in bf16
+// and the gradients of activation and bias.
 //
-// On SM pairs (tcgen05.mma.cta_group::2, kind::f16, fp32 accumulators in TMEM).  The features are the MMA's M side, 256
+// Three kernels for the product: SM pairs for many rows, one CTA per tile where there are few or small tiles, one without
+// tensor memory for up to 16 rows (the rules stand at ga_plan and kGfRows).
+//
+// SM pairs (tcgen05.mma.cta_group::2, kind::f16, fp32 accumulators in TMEM).  The features are the MMA's M side, 256
 // per tile, 128 per CTA; the rows are its N side, up to 256 per tile in steps of 32.  So few rows cost few MMA cycles, a
 // TMEM lane is a feature and the epilogue's bias a register, and the 32 lanes of a warp hold 32 neighbours of one output
 // row: bias, activation, residual and stores are done from registers, with no staging in shared memory.
 //
 // Warps: 0 TMA producer (6 stages of 64 products, 192 KiB per CTA), 1 MMA issuer in the pair's leader, in the other CTA it
 // forwards "accumulator read"; 2-17 epilogue.  The accumulator is double-buffered (2 x 256 TMEM columns).  The tensor
-// core truncates as it accumulates, so an accumulator holds at most 512 products with fp32 output and 1024 with bf16
-// output (errors of 5e-7 and 1e-6), and the epilogue joins such runs in registers, rounded to nearest, while the next
-// one is under way; the activations and stores of one tile run under the products of the next.
+// core truncates as it accumulates (5e-7 after 512 products, 2e-6 after 2048, 9e-6 after 8192, relative), so an accumulator
+// holds at most 512 products with fp32 output and 4096 with bf16, whose half step is 2e-3 at least; the epilogue joins such
+// runs, rounded to nearest, while the next one is under way.  Runs are cut evenly, since a tile is finished under the first
+// run of the next one: with 1024 products the MMAs waited for the epilogue (8192 x 20480 x 5120, gelu, pre: 1261 us, now
+// 1145 to 1160; the product alone 1088 to 1105, cuBLAS' 1080).
 //
-// SPLIT > 1: where there are fewer tiles than pairs, a cluster of SPLIT pairs takes one tile, each pair a part of K.  The
-// pairs' sums meet in shared memory: each pair finishes a part of the rows, for which the others send it theirs
-// through the cluster's network, into the ring that the products no longer need, and adds them in the order of the
-// parts.  No workspace, no atomics, no waiting on memory.
+// Where there are fewer tiles than SMs, a cluster takes one tile and each pair (or CTA) of it a part of K.  The sums
+// meet in shared memory: no workspace, no atomics, no waiting on memory (tile_epilogue).
 //
 // Every mbarrier wait is bounded by the caller's budget; on expiry the CTA raises the timeout flag, drains its copies
 // and MMAs (bounded again) and frees its TMEM.
 #include <algorithm>
+
 
 #include "act.cuh"
 #include "nvfp4_device.cuh"
@@ -49,6 +54,10 @@ struct GemmActParams {
     int32_t M, N;
     int32_t stages, run;    // of K, and of an accumulator
     int32_t np, nq, wq;     // feature tiles, row tiles and their width
+    int32_t split, per;     // parts of K; chunks of 16 rows that a part finishes at most
+    int32_t part_stages, longer;   // of a part, and how many have one more
+    int32_t ring;           // one CTA per tile: stages of the ring
+    uint32_t tmem_cols;
     int32_t act, out_fp32, res_fp32;
     int32_t pairs;          // D, pre and the residual can be taken two features at a time
     uint32_t* flags;
@@ -66,11 +75,14 @@ struct GemmActSmem {        // behind the stages
     uint32_t consumed, runs;       // leader: stages and accumulators that the MMA issuer has committed
     uint32_t stage_tx[kGaStages];  // bytes per CTA of the last use of each stage
 };
+constexpr int kGaClusterStages = 4;                      // where an inbox takes the room of two
+constexpr int kInbox = 96 * 1024;                        // of a part's CTA: the sums of up to 3 (pairs) or 7 others
 constexpr int kGaSmem = kGaRing + (int)sizeof(GemmActSmem) + 1024;
-static_assert(kGaSmem <= 232448, "shared memory");
+constexpr int kGaClusterSmem = kGaClusterStages * kGaStageBytes + kInbox + (int)sizeof(GemmActSmem) + 1024;
+static_assert(kGaSmem <= 232448 && kGaClusterSmem <= 232448, "shared memory");
 
 struct GemmActMaps {
-    CUtensorMap p, q[3];    // features; rows in boxes of 32, 64 and 128
+    CUtensorMap p, q;       // features in boxes of 128; rows in boxes of a tile's (a pair's: half)
 };
 
 struct GaTile {
@@ -111,22 +123,30 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
 // bf16 words hold two features of a row, so neighbouring lanes trade: a lane packs its feature of rows i and i + 1,
 // and of its own word and its neighbour's the even lane keeps row i's halves, the odd one row i + 1's.
 // ---------------------------------------------------------------------------------------
+// In a loop that moves the values along, 8 at a time: a launch of few tiles runs each of these instructions once or twice, and
+// fetches them for that.
 template <int ACT>
-__device__ __forceinline__ void act16(float* v, bool wide) {
-    if (wide) {
+__device__ __forceinline__ void act16(float* v) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        float w[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = act::wide<ACT>(v[i]);
-    } else {
+        for (int j = 0; j < 8; ++j) w[j] = v[j];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) act::pair<ACT>(v[i], v[i + 1]);
+        for (int j = 0; j < 8; j += 2) act::pair<ACT>(w[j], w[j + 1]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = v[j + 8];
+            v[j + 8] = w[j];
+        }
     }
 }
-__device__ __forceinline__ void act16(int act, float* v, bool wide) {
+__device__ __forceinline__ void act16(int act, float* v) {
     switch (act) {
-        case kActRelu: act16<kActRelu>(v, wide); break;
-        case kActRelu2: act16<kActRelu2>(v, wide); break;
-        case kActGelu: act16<kActGelu>(v, wide); break;
-        case kActSilu: act16<kActSilu>(v, wide); break;
+        case kActRelu: act16<kActRelu>(v); break;
+        case kActRelu2: act16<kActRelu2>(v); break;
+        case kActGelu: act16<kActGelu>(v); break;
+        case kActSilu: act16<kActSilu>(v); break;
     }
 }
 // the trade, its own inverse: halves {own row i, own row i + 1} <-> {feature even, feature odd} of row i + odd
@@ -139,97 +159,222 @@ __device__ __forceinline__ void put_words(uint16_t* at, int64_t ld, const float*
     for (int i = 0; i < 16; i += 2, at += 2 * ld) *reinterpret_cast<uint32_t*>(at) = traded(f32x2_to_bf16x2(v[i], v[i + 1]), select);
 }
 
-// v: sums of rows row0 .. row0 + 15 of feature f.  All of the rows and of the warp's 32 features exist, and leading
-// dimensions are even.
-__device__ __forceinline__ void finish16(float* v, const GemmActParams& p, int row0, int f, float bias) {
+// v: sums of rows row0 .. row0 + 15 of feature f, the first n of which exist.  whole: all 16 do and all of the warp's 32
+// features, and leading dimensions are even; else each lane takes its own feature, element by element.
+__device__ __forceinline__ void finish16(float* v, const GemmActParams& p, int row0, int n, int f, float bias, bool whole) {
     const int odd = threadIdx.x & 1, fe = f - odd;
     const uint32_t select = odd ? 0x3276u : 0x5410u;
+    const bool in = f < p.N;
     // the residual first: its loads are under way during the rest
     float w[16];
+    const bool words = whole && !p.res_fp32;
     if (p.residual) {
-        if (p.res_fp32) {
-            const float* r = reinterpret_cast<const float*>(p.residual) + row0 * p.ldr + f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i, r += p.ldr) w[i] = *r;
-        } else {
+        if (words) {
             const uint16_t* r = reinterpret_cast<const uint16_t*>(p.residual) + (row0 + odd) * p.ldr + fe;
 #pragma unroll
             for (int i = 0; i < 8; ++i, r += 2 * p.ldr) w[i] = __uint_as_float(*reinterpret_cast<const uint32_t*>(r));
+        } else if (whole) {
+            const float* r = reinterpret_cast<const float*>(p.residual) + row0 * p.ldr + f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, r += p.ldr) w[i] = *r;
+        } else if (p.res_fp32) {
+            const float* r = reinterpret_cast<const float*>(p.residual) + row0 * p.ldr + f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, r += p.ldr) w[i] = in && i < n ? *r : 0.0f;
+        } else {
+            const uint16_t* r = reinterpret_cast<const uint16_t*>(p.residual) + row0 * p.ldr + f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, r += p.ldr) w[i] = in && i < n ? __uint_as_float((uint32_t)*r << 16) : 0.0f;
         }
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] += bias;
-    if (p.pre) put_words(p.pre + (row0 + odd) * p.ldpre + fe, p.ldpre, v, select);
-    act16(p.act, v, p.out_fp32);
-    if (p.residual) {
-        if (p.res_fp32) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] += w[i];
+    if (p.pre) {
+        if (whole) {
+            put_words(p.pre + (row0 + odd) * p.ldpre + fe, p.ldpre, v, select);
         } else {
+            uint16_t* at = p.pre + row0 * p.ldpre + f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, at += p.ldpre)
+                if (in && i < n) *at = (uint16_t)f32x2_to_bf16x2(v[i], 0.0f);
+        }
+    }
+    act16(p.act, v);
+    if (p.residual) {
+        if (words) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t u = traded(__float_as_uint(w[i]), select);
                 v[2 * i] += bf16_lo(u);
                 v[2 * i + 1] += bf16_hi(u);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += w[i];
         }
     }
     if (p.out_fp32) {
         float* at = reinterpret_cast<float*>(p.d) + row0 * p.ldd + f;
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i, at += p.ldd) *at = v[i];
-    } else {
+            for (int i = 0; i < 16; ++i, at += p.ldd) *at = v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i, at += p.ldd)
+                if (in && i < n) *at = v[i];
+        }
+    } else if (whole) {
         put_words(reinterpret_cast<uint16_t*>(p.d) + (row0 + odd) * p.ldd + fe, p.ldd, v, select);
+    } else {
+        uint16_t* at = reinterpret_cast<uint16_t*>(p.d) + row0 * p.ldd + f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i, at += p.ldd)
+            if (in && i < n) *at = (uint16_t)f32x2_to_bf16x2(v[i], 0.0f);
     }
 }
 
-// The same at the edges of the output, or where a leading dimension is odd: the first n rows, element by element
-__device__ __noinline__ void finish_edge(float v0, float v1, float v2, float v3, const GemmActParams& p, int64_t row0, int n, int f, float bias) {
-    float v[4] = {v0 + bias, v1 + bias, v2 + bias, v3 + bias};
-    if (f >= p.N) return;
+// ---------------------------------------------------------------------------------------
+// A tile's epilogue, for the warps of both kernels below.  The warp's TMEM lanes start at `lanes`, its columns (rows of
+// the output) are the chunks of 16 numbered group, group + G, ...
+//
+// Sums of several runs are joined in registers and put back where the last run stood, so that the tile is finished from
+// TMEM, 16 columns at a time: with 64 sums of a lane still in registers, those of the epilogue do not fit, and what is
+// spilled goes to L2 with the output (8192 x 20480 x 5120: 1235 us, without 1107).
+//
+// CLUSTER: the tile's K is cut into `split` parts.  Chunk c is finished by part c % split, to which the others send their
+// sums of it, through the cluster's network, to [sender][c / split][row][feature] at `inbox`; they are added in the order of the
+// parts.  Every warp of the cluster comes by, for the barriers: one that each has arrived at when it began (no
+// sums before their CTA runs), one behind the sends.
+// ---------------------------------------------------------------------------------------
+constexpr uint32_t kChunkBytes = 16 * 128 * 4;
+struct EpilogueTile {
+    int q0, qn, f;           // first row, rows, this lane's feature
+    int group, runs;         // the warp's first chunk; accumulators of the tile
+    int split, part, per;    // per: chunks of a part at most
+    uint32_t rank_step, rank0;   // part s stands at cluster rank s * rank_step + rank0
+    uint32_t inbox;          // shared::cta address, plus 4 bytes for each feature before this lane's
+    uint32_t lanes, buf_cols;
+};
+template <int G, bool CLUSTER, class Ready, class Release>
+__device__ __forceinline__ bool tile_epilogue(const GemmActParams& p, const EpilogueTile& e, bool works, int& it, const Ready& ready, const Release& release) {
+    bool ok = true;
+    if (works) {
+        if (e.runs > 1) {
+            float acc[64];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (i >= n) break;
-        const int64_t row = row0 + i;
-        if (p.pre) p.pre[row * p.ldpre + f] = (uint16_t)f32x2_to_bf16x2(v[i], 0.0f);
-        float y;
-        if (p.out_fp32) {
-            y = act::wide(p.act, v[i]);
+            for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+            for (int r = 0; r < e.runs; ++r) {
+                if (!(ok = ready())) break;
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    const int at = 16 * (e.group + G * (h >> 1)) + 8 * (h & 1);
+                    if (at >= e.qn) break;
+                    float v[8];
+                    tmem_ld8(e.lanes + e.buf_cols * (it & 1) + (uint32_t)at, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[8 * h + i] += v[i];
+                }
+                if (r + 1 < e.runs) release();
+            }
+            if (ok) {
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    const int at = 16 * (e.group + G * (h >> 1)) + 8 * (h & 1);
+                    if (at >= e.qn) break;
+                    tmem_st8(e.lanes + e.buf_cols * (it & 1) + (uint32_t)at, acc + 8 * h);
+                }
+                tmem_st_wait();
+            }
         } else {
-            float z = y = v[i];
-            switch (p.act) {
-                case kActRelu: act::pair<kActRelu>(y, z); break;
-                case kActRelu2: act::pair<kActRelu2>(y, z); break;
-                case kActGelu: act::pair<kActGelu>(y, z); break;
-                case kActSilu: act::pair<kActSilu>(y, z); break;
+            ok = ready();
+        }
+    }
+    const uint32_t from = e.lanes + e.buf_cols * (it & 1);
+    if constexpr (CLUSTER) {
+        __syncwarp();
+        cluster_wait();
+        if (works && ok) {
+            int owner = e.group, row = 0;   // c % split, c / split
+#pragma unroll 1
+            for (int c = e.group; 16 * c < e.qn; c += G, owner += G) {
+                while (owner >= e.split) {
+                    owner -= e.split;
+                    ++row;
+                }
+                if (owner == e.part) continue;
+                float v[16];
+                tmem_ld16(from + (uint32_t)(16 * c), v);
+                const int slot = e.part < owner ? e.part : e.part - 1;
+                const uint32_t at = map_rank(e.inbox + (uint32_t)(slot * e.per + row) * kChunkBytes, (uint32_t)owner * e.rank_step + e.rank0);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) st_cluster_f32(at + 512u * i, v[i]);
             }
         }
-        if (p.residual)
-            y += p.res_fp32 ? reinterpret_cast<const float*>(p.residual)[row * p.ldr + f]
-                            : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p.residual)[row * p.ldr + f] << 16);
-        if (p.out_fp32) reinterpret_cast<float*>(p.d)[row * p.ldd + f] = y;
-        else reinterpret_cast<uint16_t*>(p.d)[row * p.ldd + f] = (uint16_t)f32x2_to_bf16x2(y, 0.0f);
+        tc_fence_before();
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        tc_fence_after();
     }
+    if (!works || !ok) return ok;
+    const float bias = p.bias && e.f < p.N ? p.bias[e.f] : 0.0f;
+    const bool whole = p.pairs && (e.f & ~31) + 32 <= p.N;
+    // in a cluster the part's own chunks, part, part + split, ..., are dealt out anew over the warps of a lane quarter
+    const int step = CLUSTER ? G * e.split : G;
+    int row = e.group;
+#pragma unroll 1
+    for (int c = CLUSTER ? e.part + e.group * e.split : e.group; 16 * c < e.qn; c += step, row += G) {
+        float v[16];
+        tmem_ld16(from + (uint32_t)(16 * c), v);
+        tmem_ld_wait();
+        if constexpr (CLUSTER) {
+            float own[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                own[i] = v[i];
+                v[i] = e.part == 0 ? own[i] : 0.0f;
+            }
+#pragma unroll 1
+            for (int slot = 0; slot < e.split - 1; ++slot) {
+                const uint32_t at = e.inbox + (uint32_t)(slot * e.per + row) * kChunkBytes;
+                float w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(at + 512u * i));
+                const bool mine = slot + 1 == e.part;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    v[i] += w[i];
+                    if (mine) v[i] += own[i];
+                }
+            }
+        }
+        finish16(v, p, e.q0 + 16 * c, e.qn - 16 * c, e.f, bias, whole && 16 * c + 16 <= e.qn);
+    }
+    return true;
 }
 
 // ---------------------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------------------
-template <int SPLIT>
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_constant__ GemmActMaps maps, const __grid_constant__ GemmActParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    GemmActSmem& sm = *reinterpret_cast<GemmActSmem*>(smem + kGaRing);
+    // in a cluster of several pairs: four stages, and the inbox behind them
+    constexpr int kStages = CLUSTER ? kGaClusterStages : kGaStages;
+    GemmActSmem& sm = *reinterpret_cast<GemmActSmem*>(smem + kStages * kGaStageBytes + (CLUSTER ? kInbox : 0));
     volatile uint32_t* abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = cluster_rank(), rank = crank & 1u, leader = crank & ~1u;
-    const int part = (int)(crank >> 1);                            // of K
-    const int unit = blockIdx.x / (2 * SPLIT), units = gridDim.x / (2 * SPLIT);
+    const int split = CLUSTER ? p.split : 1, part = CLUSTER ? (int)(crank >> 1) : 0;   // of K
+    const int unit = CLUSTER ? (int)blockIdx.x / (2 * split) : (int)blockIdx.x >> 1, units = CLUSTER ? (int)gridDim.x / (2 * split) : (int)gridDim.x >> 1;
     const int tiles = p.np * p.nq;
-    const int s0 = (int)((int64_t)p.stages * part / SPLIT), s1 = (int)((int64_t)p.stages * (part + 1) / SPLIT);
+    const int s0 = CLUSTER ? part * p.part_stages + min(part, p.longer) : 0, s1 = CLUSTER ? s0 + p.part_stages + (part < p.longer) : p.stages;
 
     if (threadIdx.x == 8 * 32) {
-        for (int s = 0; s < kGaStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&sm.full[s]), 1);
             mbar_init(smem_u32(&sm.empty[s]), 1);
             sm.stage_tx[s] = 0;
@@ -247,7 +392,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
         sm.runs = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&maps.p);
-        prefetch_map(&maps.q[2]);
+        prefetch_map(&maps.q);
     }
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "r"(512)
@@ -261,6 +406,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
     griddep_wait();
     griddep_launch();
     cluster_wait();     // and the others'
+    if (CLUSTER) cluster_arrive_relaxed();   // for the epilogue
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     const int run = p.run;   // stages per accumulator
@@ -276,8 +422,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
             for (int t = unit; ok && t < tiles; t += units) {
                 const GaTile c = ga_tile(p, t);
                 const int half = c.n >> 1, p0 = c.p0 + (int)rank * 128, q0 = c.q0 + (int)rank * half;
-                const int qbox = half <= 32 ? 0 : half <= 64 ? 1 : 2;
-                const uint32_t tx = (uint32_t)(kGaOpBytes + (4096 << qbox));
+                const uint32_t tx = (uint32_t)(kGaOpBytes + 64 * p.wq);   // rows of the box past the tile's are not used
                 for (int k = s0; k < s1; ++k) {
                     if (!mbar_wait(empty + 8u * s, parity, abort_flag, p.flags, p.budget_ns)) {
                         ok = false;
@@ -287,18 +432,18 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
                     sm.stage_tx[s] = tx;
                     const uint32_t dst = base + (uint32_t)(s * kGaStageBytes), bar = leader_full + 8u * s;
                     ++g;
-                    if (++s == kGaStages) {
+                    if (++s == kStages) {
                         s = 0;
                         parity ^= 1u;
                     }
                     tma_load_2d_pair(dst, &maps.p, k * kGaK, p0, bar);
-                    tma_load_2d_pair(dst + kGaOpBytes, &maps.q[qbox], k * kGaK, q0, bar);
+                    tma_load_2d_pair(dst + kGaOpBytes, &maps.q, k * kGaK, q0, bar);
                 }
             }
             sm.issued = (uint32_t)g;   // read by the drain, after the cluster barrier
             // the releases of the last stages, which the leader's MMAs signal in both CTAs, land before the end
-            for (int k = max(0, g - kGaStages); ok && k < g; ++k)
-                ok = mbar_wait(empty + 8u * (k % kGaStages), (uint32_t)(k / kGaStages) & 1u, abort_flag, p.flags, p.budget_ns);
+            for (int k = max(0, g - kStages); ok && k < g; ++k)
+                ok = mbar_wait(empty + 8u * (k % kStages), (uint32_t)(k / kStages) & 1u, abort_flag, p.flags, p.budget_ns);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -338,7 +483,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
                             add = 1;
                             commit_pair(empty + 8u * s, leader);
                             ++consumed;
-                            if (++s == kGaStages) {
+                            if (++s == kStages) {
                                 s = 0;
                                 parity ^= 1u;
                             }
@@ -360,7 +505,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
             for (int t = unit; ok && t < tiles; t += units) {
                 for (int k = s0; k < s1; k += run, ++it) {
                     // a cluster's one tile: its last accumulator is read behind barriers that this warp takes part in
-                    if (SPLIT > 1 && k + run >= s1) break;
+                    if (CLUSTER && k + run >= s1) break;
                     if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sm.edrained[it & 1]), (uint32_t)(it >> 1) & 1u, abort_flag,
                                                            p.flags, p.budget_ns))) {
                         ok = false;
@@ -373,126 +518,41 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
         }
     }
     // ------------------------------- epilogue (both CTAs) ------------------------------------
-    // Warps 2-17: the warp's TMEM lanes are 32 q .. 32 q + 31, its columns 16 from c0 and from every 64 further.
-    // Sums that take several runs (or parts) are joined in registers and put back where the last run stood, so that
-    // the tile is finished from TMEM, 16 columns at a time: with the 64 sums of a warp still in registers, those of
-    // the epilogue do not fit, and what is spilled goes to L2 with the output (8192 x 20480 x 5120: 1235 us).
+    // Warps 2-17, four to a TMEM lane quarter
     const bool epilogue = warp >= 2;
-    const int q = warp & 3, c0 = ((warp - 2) >> 2) * 16;
-    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    const int q = warp & 3;
+    EpilogueTile e;
+    e.group = (warp - 2) >> 2;
+    e.runs = 1;
+    for (int k = s0 + run; k < s1; k += run) ++e.runs;
+    e.split = split;
+    e.part = part;
+    e.per = p.per;
+    e.rank_step = 2;
+    e.rank0 = rank;
+    e.inbox = smem_u32(smem) + kStages * kGaStageBytes + (uint32_t)(q * 32 + lane) * 4u;
+    e.lanes = tmem + ((uint32_t)(q * 32) << 16);
+    e.buf_cols = 256;
     int it = 0;
-    bool ok = true;
-    // with SPLIT > 1 every warp comes by once, for the cluster's barriers
-    for (int t = unit; (epilogue || SPLIT > 1) && ok && t < tiles; t += units) {
+    const auto ready = [&]() {   // the next accumulator is complete
+        const bool full = mbar_wait(smem_u32(&sm.tfull[it & 1]), (uint32_t)(it >> 1) & 1u, abort_flag, p.flags, p.budget_ns);
+        if (!__all_sync(0xFFFFFFFFu, full)) return false;
+        tc_fence_after();
+        return true;
+    };
+    const auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(rank == 0 ? &sm.tempty[it & 1] : &sm.edrained[it & 1]));
+        ++it;
+    };
+    for (int t = unit; (epilogue || CLUSTER) && t < tiles; t += units) {   // a cluster: one tile
         const GaTile c = ga_tile(p, t);
-        const auto ready = [&]() {   // the next accumulator is complete
-            const bool full = mbar_wait(smem_u32(&sm.tfull[it & 1]), (uint32_t)(it >> 1) & 1u, abort_flag, p.flags, p.budget_ns);
-            if (!__all_sync(0xFFFFFFFFu, full)) return false;
-            tc_fence_after();
-            return true;
-        };
-        const auto release = [&]() {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(rank == 0 ? &sm.tempty[it & 1] : &sm.edrained[it & 1]));
-            ++it;
-        };
-        if (SPLIT > 1 || s1 - s0 > run) {
-            float acc[64];
-#pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-            if (epilogue)
-                for (int k = s0; k < s1; k += run) {
-                    if (!(ok = ready())) break;
-#pragma unroll
-                    for (int h = 0; h < 8; ++h) {
-                        const int at = c0 + 64 * (h >> 1) + 8 * (h & 1);
-                        if (at >= c.qn) break;
-                        float v[8];
-                        tmem_ld8(lanes + 256u * (it & 1) + (uint32_t)at, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[8 * h + i] += v[i];
-                    }
-                    if (k + run < s1) release();
-                }
-            if constexpr (SPLIT > 1) {
-                // chunk (c0 / 16) + 4 h of 16 rows is finished by part (c0 / 16 + h) % SPLIT, in whose shared memory the
-                // others' sums of it stand at [sender][h * 4 / SPLIT + c0 / 16 / SPLIT][row][feature]
-                constexpr uint32_t kChunk = 16 * 128 * 4;
-                const int group = c0 >> 4;
-                const uint32_t mine = (uint32_t)(q * 32 + lane) * 4u;
-                const auto place = [&](int owner, int sender, int h) {
-                    const int slot = sender < owner ? sender : sender - 1;
-                    return smem_u32(smem) + (uint32_t)(slot * (16 / SPLIT) + h * (4 / SPLIT) + group / SPLIT) * kChunk + mine;
-                };
-                __syncwarp();
-                cluster_arrive();
-                cluster_wait();      // the products of all parts are done: the rings are free
-                if (epilogue && ok) {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const int owner = (group + h) % SPLIT;
-                        if (c0 + 64 * h >= c.qn || owner == part) continue;
-                        const uint32_t at = map_rank(place(owner, part, h), (uint32_t)(2 * owner) + rank);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) st_cluster_f32(at + 512u * i, acc[16 * h + i]);
-                    }
-                }
-                __syncwarp();
-                cluster_arrive();
-                cluster_wait();      // and what each part finishes is there
-                if (epilogue && ok) {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        if (c0 + 64 * h >= c.qn || (group + h) % SPLIT != part) continue;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float sum = 0.0f;
-#pragma unroll
-                            for (int s = 0; s < SPLIT; ++s) {   // in the order of the parts
-                                float v = acc[16 * h + i];
-                                if (s != part) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(place(part, s, h) + 512u * i));
-                                sum = s == 0 ? v : sum + v;
-                            }
-                            acc[16 * h + i] = sum;
-                        }
-                    }
-                }
-            }
-            if (epilogue && ok) {
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    const int at = c0 + 64 * (h >> 1) + 8 * (h & 1);
-                    if (at >= c.qn) break;
-                    tmem_st8(lanes + 256u * (it & 1) + (uint32_t)at, acc + 8 * h);
-                }
-                tmem_st_wait();
-            }
-        } else {
-            ok = ready();
-        }
-        if (!epilogue || !ok) continue;
-        const int f = c.p0 + (int)rank * 128 + q * 32 + lane;
-        const float bias = p.bias && f < p.N ? p.bias[f] : 0.0f;
-        const bool whole = p.pairs && f - lane + 32 <= p.N;
-#pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-            const int at = c0 + 64 * h;
-            if (at >= c.qn) break;
-            if (SPLIT > 1 && ((c0 >> 4) + h) % SPLIT != part) continue;
-            float v[16];
-            tmem_ld16(lanes + 256u * (it & 1) + (uint32_t)at, v);
-            tmem_ld_wait();
-            if (whole && at + 16 <= c.qn) {
-                finish16(v, p, c.q0 + at, f, bias);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    if (at + i < c.qn) finish_edge(v[i], v[i + 1], v[i + 2], v[i + 3], p, c.q0 + at + i, c.qn - (at + i), f, bias);
-            }
-        }
-        release();
+        e.q0 = c.q0;
+        e.qn = c.qn;
+        e.f = c.p0 + (int)rank * 128 + q * 32 + lane;
+        if (!tile_epilogue<4, CLUSTER>(p, e, epilogue, it, ready, release)) break;
+        if (!CLUSTER) release();
     }
 
     // Each warp hands an abort that it has seen to the pair's leader.  No arrival may land in a CTA that has ended: those that
@@ -513,19 +573,19 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
         // producer is at most a ring ahead of the MMAs, so only the last uses of its stages can be outstanding; a stage that only
         // the other CTA issued has its arrival made here, one that only the leader issued has the other's bytes cancelled.
         const uint32_t consumed = ld_cluster_u32(map_rank(smem_u32(&sm.consumed), leader)), runs = ld_cluster_u32(map_rank(smem_u32(&sm.runs), leader));
-        for (int k = max(0, (int)consumed - kGaStages); k < (int)consumed; ++k)
-            mbar_wait(smem_u32(&sm.empty[k % kGaStages]), (uint32_t)(k / kGaStages) & 1u, abort_flag, p.flags, kGaDrainNs, false);
+        for (int k = max(0, (int)consumed - kStages); k < (int)consumed; ++k)
+            mbar_wait(smem_u32(&sm.empty[k % kStages]), (uint32_t)(k / kStages) & 1u, abort_flag, p.flags, kGaDrainNs, false);
         for (int i = max(0, (int)runs - 2); i < (int)runs; ++i)
             mbar_wait(smem_u32(&sm.tfull[i & 1]), (uint32_t)(i >> 1) & 1u, abort_flag, p.flags, kGaDrainNs, false);
         if (rank == 0) {
             const int gl = (int)sm.issued, gp = (int)ld_cluster_u32(map_rank(smem_u32(&sm.issued), leader + 1)), gm = max(gl, gp);
-            for (int k = max(0, gm - kGaStages); k < gm; ++k) {
-                const int s = k % kGaStages;
+            for (int k = max(0, gm - kStages); k < gm; ++k) {
+                const int s = k % kStages;
                 const uint32_t bar = smem_u32(&sm.full[s]);
                 const uint32_t tx = k < gl ? sm.stage_tx[s] : ld_cluster_u32(map_rank(smem_u32(&sm.stage_tx[s]), leader + 1));
                 if (k >= gl) mbar_expect_tx(bar, tx);
                 else if (k >= gp) mbar_complete_tx(bar, tx);
-                mbar_wait(bar, (uint32_t)(k / kGaStages) & 1u, abort_flag, p.flags, kGaDrainNs, false);
+                mbar_wait(bar, (uint32_t)(k / kStages) & 1u, abort_flag, p.flags, kGaDrainNs, false);
             }
         }
     }
@@ -535,6 +595,201 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// tiles too few or too small for the SM pairs: one CTA per tile of 128 features x up to 128 rows, two CTAs per SM
+//
+// What bounds such a product is how fast an SM takes in operands (64 bytes a cycle from L2: 300 cycles for a stage of 128
+// features and 32 rows, whose MMAs take 64), and the fixed cost of a launch.  So the tiles are small, a cluster of up to 8
+// CTAs cuts K, every SM takes a share, and there is as little set-up as possible: no pairs, no cluster barriers unless K is cut,
+// the first loads issued before the CTA's other warps are ready.
+// Warps: 0 producer, 1 MMA issuer, 2-9 epilogue.
+// ---------------------------------------------------------------------------------------
+constexpr int kGmRing = 96 * 1024;
+constexpr int kGmMaxStages = 5;
+constexpr int kGmEpiWarps = 8;
+constexpr int kGmThreads = 64 + 32 * kGmEpiWarps;
+constexpr int kGmMaxRows = 128, kGmMaxSplit = 8;
+struct GemmMidSmem {
+    uint64_t full[kGmMaxStages], empty[kGmMaxStages], tfull[2], tempty[2], done;
+    uint32_t tmem, abort;
+};
+constexpr int kGmSmem = kGmRing + (int)sizeof(GemmMidSmem) + 1024;
+constexpr int kGmClusterSmem = kGmSmem + kInbox;
+static_assert(2 * (kGmSmem + 1024) <= 232448 && kGmClusterSmem <= 232448, "two CTAs per SM, one of a cluster");
+
+__device__ __forceinline__ uint32_t cluster_x() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void mma_bf16_single(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit_single(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kernel(const __grid_constant__ GemmActMaps maps, const __grid_constant__ GemmActParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    GemmMidSmem& sm = *reinterpret_cast<GemmMidSmem*>(smem + kGmRing + (CLUSTER ? kInbox : 0));
+    volatile uint32_t* abort_flag = &sm.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = CLUSTER ? p.split : 1, part = CLUSTER ? (int)cluster_rank() : 0;
+    // neighbours share the features' rows of B
+    const int q0 = (int)(CLUSTER ? cluster_x() : blockIdx.x) * p.wq, p0 = 128 * (int)blockIdx.y, qn = min(p.wq, p.M - q0);
+    const int s0 = CLUSTER ? part * p.part_stages + min(part, p.longer) : 0, s1 = CLUSTER ? s0 + p.part_stages + (part < p.longer) : p.stages;
+    const int run = p.run;
+    const int n = (qn + 15) & ~15;                       // the MMA's N
+    const uint32_t stage_bytes = (uint32_t)(kGaOpBytes + 128 * p.wq);
+    const int ring = p.ring;
+    const uint32_t base = smem_u32(smem), full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
+    const uint32_t cols = p.tmem_cols;                   // two accumulators (one, where one run serves)
+
+    int g = s0, s = 0;                                   // the producer's next stage, its slot
+    const auto load = [&]() {
+        mbar_expect_tx(full + 8u * s, stage_bytes);
+        tma_load_2d(base + s * stage_bytes, &maps.p, g * kGaK, p0, full + 8u * s);
+        tma_load_2d(base + s * stage_bytes + kGaOpBytes, &maps.q, g * kGaK, q0, full + 8u * s);
+        ++g;
+        if (++s == ring) s = 0;
+    };
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int i = 0; i < ring; ++i) {
+                mbar_init(full + 8u * i, 1);
+                mbar_init(empty + 8u * i, 1);
+            }
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&sm.tfull[b]), 1);
+                mbar_init(smem_u32(&sm.tempty[b]), kGmEpiWarps);
+            }
+            mbar_init(smem_u32(&sm.done), 1);
+            sm.abort = 0u;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            fence_async_smem();
+            griddep_wait();
+            for (int i = 0; i < ring && g < s1; ++i) load();
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    griddep_wait();
+    griddep_launch();
+    __syncthreads();
+    if (CLUSTER) cluster_arrive_relaxed();   // for the epilogue
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem, buf_cols = cols >> 1;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t parity = 0;     // of the slots' first release
+            bool ok = true;
+            while (ok && g < s1) {
+                const bool wrap = s + 1 == ring;
+                ok = mbar_wait(empty + 8u * s, parity, abort_flag, p.flags, p.budget_ns);
+                if (!ok) break;
+                load();
+                if (wrap) parity ^= 1u;
+            }
+            // every copy lands, and every release of the MMAs, before the CTA ends
+            const int issued = g - s0;
+            for (int k = max(0, issued - ring); k < issued; ++k) {
+                const uint32_t ph = (uint32_t)(k / ring) & 1u;
+                mbar_wait(full + 8u * (k % ring), ph, abort_flag, p.flags, kGaDrainNs, false);
+                if (ok) ok = mbar_wait(empty + 8u * (k % ring), ph, abort_flag, p.flags, p.budget_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            const uint64_t pdesc = desc_k_major(base), qdesc = desc_k_major(base + kGaOpBytes);
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            int it = 0, slot = 0;
+            uint32_t parity = 0;
+            bool ok = true;
+            for (int k = s0; ok && k < s1; ++it) {
+                const int end = min(s1, k + run);
+                if (!mbar_wait(smem_u32(&sm.tempty[it & 1]), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, p.flags, p.budget_ns)) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + buf_cols * (it & 1);
+                uint32_t add = 0;
+                for (; k < end; ++k) {
+                    ok = mbar_wait(full + 8u * slot, parity, abort_flag, p.flags, p.budget_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t off = (uint64_t)((slot * stage_bytes) >> 4);
+#pragma unroll
+                    for (int j = 0; j < kGaK / 16; ++j) mma_bf16_single(acc, pdesc + off + 2 * j, qdesc + off + 2 * j, idesc, j ? 1u : add);
+                    add = 1;
+                    commit_single(empty + 8u * slot);
+                    if (++slot == ring) {
+                        slot = 0;
+                        parity ^= 1u;
+                    }
+                }
+                if (ok) commit_single(smem_u32(&sm.tfull[it & 1]));
+            }
+            commit_single(smem_u32(&sm.done));
+            mbar_wait(smem_u32(&sm.done), 0u, abort_flag, p.flags, kGaDrainNs, false);
+        }
+        __syncwarp();
+    }
+    // epilogue: warps 2-9, two to a TMEM lane quarter
+    const int q = warp & 3;
+    EpilogueTile e;
+    e.q0 = q0;
+    e.qn = qn;
+    e.f = p0 + q * 32 + lane;
+    e.group = (warp - 2) >> 2;
+    e.runs = 1;
+    for (int k = s0 + run; k < s1; k += run) ++e.runs;
+    e.split = split;
+    e.part = part;
+    e.per = p.per;
+    e.rank_step = 1;
+    e.rank0 = 0;
+    e.inbox = base + kGmRing + (uint32_t)(q * 32 + lane) * 4u;
+    e.lanes = tmem + ((uint32_t)(q * 32) << 16);
+    e.buf_cols = buf_cols;
+    int it = 0;
+    const auto ready = [&]() {
+        const bool done = mbar_wait(smem_u32(&sm.tfull[it & 1]), (uint32_t)(it >> 1) & 1u, abort_flag, p.flags, p.budget_ns);
+        if (!__all_sync(0xFFFFFFFFu, done)) return false;
+        tc_fence_after();
+        return true;
+    };
+    const auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.tempty[it & 1]));
+        ++it;
+    };
+    if (warp >= 2 || CLUSTER) tile_epilogue<2, CLUSTER>(p, e, warp >= 2, it, ready, release);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
     }
 }
 
@@ -625,7 +880,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) gemm_act_few_kernel(co
             for (int w = 0; w < WARPS; ++w) s += part[w][r][i & 15];
             if (p.e.bias) s += p.e.bias[f];
             if (p.e.pre) p.e.pre[(int64_t)row * p.e.ldpre + f] = (uint16_t)f32x2_to_bf16x2(s, 0.0f);
-            s = act::wide(p.e.act, s);
+            s = act::one(p.e.act, s);
             if (p.e.residual) {
                 const int64_t at = (int64_t)row * p.e.ldr + f;
                 s += p.e.res_fp32 ? reinterpret_cast<const float*>(p.e.residual)[at]
@@ -645,49 +900,88 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) gemm_act_few_kernel(co
 constexpr int kGfRows = 16;      // rows up to which the kernel for few is taken
 constexpr int kGfLongK = 2048;   // a K from which 16 warps cut it, where one wave of CTAs holds the launch
 
-template <int SPLIT>
-static cudaError_t launch_pairs(const GemmActMaps& maps, const GemmActParams& p, int clusters, cudaStream_t s) {
-    static std::atomic<uint64_t> attr{0};
-    auto kern = gemm_act_kernel<SPLIT>;
-    if (cudaError_t e = host::ensure_smem(reinterpret_cast<const void*>(kern), kGaSmem, attr)) return e;
+template <class Kernel>
+static cudaError_t launch_ga(Kernel kern, int bytes, std::atomic<uint64_t>& attr, int cluster, int threads, int64_t blocks,
+                             unsigned rows, const GemmActMaps& maps, const GemmActParams& p, cudaStream_t s) {
+    if (cudaError_t e = host::ensure_smem(reinterpret_cast<const void*>(kern), bytes, attr)) return e;
     cudaLaunchAttribute at[2] = {};
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = 2 * SPLIT;
+    at[1].val.clusterDim.x = (unsigned)cluster;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(2 * SPLIT * clusters));
-    cfg.blockDim = dim3(kGaThreads);
-    cfg.dynamicSmemBytes = kGaSmem;
+    cfg.gridDim = dim3((unsigned)blocks, rows);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
+// The kernel, the row tiles' width w and the parts of K, by an estimate of the time in ns, whose terms are fitted to
+// measurements of every width and split at 20 shapes from 17 x 256 x 64 to 1024 x 5120 x 5120:
+//   a stage of 64 products takes a CTA the time its operands need, (128 + w) * 128 bytes at 122 bytes a ns, a pair of CTAs
+//   180 + 0.26 w, or 1.465 w for the MMAs; all SMs together take 12000 bytes a ns from L2, and memory gives 6000, 75 to
+//   one SM (operands of more than 100 MB do not stay in L2);
+//   a launch takes 2900 + 19 w (one CTA per tile), 3800 + 150 split + 14 w (K cut over CTAs), 5000 + 8 w (pairs) or 4600 + 26 w (K
+//   cut over pairs) besides; clusters that do not fit at once have cost 20 us a wave.
+// Estimate / fastest measured (us): 64 x 1280 x 5120 7.9 / 8.1 (one CTA per tile, 6 parts; one pair 18.3), 333 x 1288 x 5120
+// 12.4 / 12.5 (4 parts; pairs in 3 parts 14.1), 500 x 5120 x 5120 29 / 28.6 (pairs), 64 x 20480 x 5120 39 / 39.3 (one CTA per
+// tile; pairs 53), 2088 x 376 x 504 5.7 / 5.7 (pairs 7.6).
 struct GaPlan {
+    bool single;     // one CTA per tile
     int split, wq;
 };
-// The row tiles' width and the parts of K: the least of waves x (stages x a stage's cycles + a tile's fixed ones)
+static int even(int64_t rows, int64_t tiles, int step) { return (int)(((rows + tiles - 1) / tiles + step - 1) / step * step); }
 static GaPlan ga_plan(int64_t M, int64_t N, int64_t stages, int sms) {
-    const int64_t np = (N + 255) / 256;
-    const int fit[3] = {sms / 2, sms / 4 - 1, sms / 8 - 1};   // clusters of 2, 4 and 8 CTAs at once
-    GaPlan best{1, 256};
+    GaPlan best{false, 1, 256};
     double least = 1e300;
-    for (int i = 0; i < 3; ++i) {
-        const int split = 1 << i;
-        if (split > stages || fit[i] < 1) break;
-        for (int w = 256; w >= 32; w -= 32) {
-            const int64_t nq = (M + w - 1) / w;
-            const int wq = (int)(((M + nq - 1) / nq + 31) / 32 * 32);
-            if (wq != w && w < 256) continue;   // an even cut of that many tiles has been seen
-            const double waves = (double)((np * nq + fit[i] - 1) / fit[i]);
-            const double cycles = std::max(320.0, 256.0 + wq) * (double)((stages + split - 1) / split) + (split > 1 ? 2500.0 : 1000.0);
-            if (waves * cycles < least) {
-                least = waves * cycles;
-                best = GaPlan{split, wq};
-            }
+    const auto take = [&](bool single, int split, int wq, double ns) {
+        if (ns < least) {
+            least = ns;
+            best = GaPlan{single, split, wq};
+        }
+    };
+    const int64_t np2 = (N + 255) / 256, np1 = (N + 127) / 128;
+    const double bytes = 128.0 * (double)(M + N) * (double)stages, memory_ns = bytes / 6000.0;
+    const bool resident = bytes < 100e6;
+    int64_t seen = 0;
+    for (int w = 256; w >= 32; w -= 32) {
+        const int64_t nq = (M + w - 1) / w, tiles = np2 * nq;
+        if (nq == seen) continue;   // the same even cut
+        seen = nq;
+        const int wq = even(M, nq, 32);
+        const double per_sm = 128.0 * (128 + wq / 2);
+        for (int split = 1; split <= 4 && split <= stages; ++split) {
+            const int64_t fit = split == 1 ? sms / 2 : sms / (2 * split) - (split > 2 ? 2 : 1);   // clusters at once
+            if (fit < 1 || (split > 1 && tiles > fit)) break;
+            const double part = (double)((stages + split - 1) / split);
+            const auto wave = [&](int64_t now) {
+                const double stage = std::max({180.0 + 0.26 * wq, 1.465 * wq, (double)(now * 2 * split) * per_sm / 12000.0, resident ? 0.0 : per_sm / 75.0});
+                return std::max(part * stage, memory_ns * (double)now / (double)tiles);
+            };
+            const int64_t full = tiles / fit, rest = tiles % fit;
+            take(false, split, wq, (full ? (double)full * wave(fit) : 0.0) + (rest ? wave(rest) : 0.0) +
+                                       (split > 1 ? 4600.0 + 26.0 * wq : 5000.0 + 8.0 * wq));
+        }
+    }
+    seen = 0;
+    for (int w = kGmMaxRows; w >= 16; w -= 16) {
+        const int64_t nq = (M + w - 1) / w;
+        if (nq == seen) continue;
+        if (np1 * nq > 4 * sms) break;
+        seen = nq;
+        const int wq = even(M, nq, 16);
+        const double per_sm = 128.0 * (128 + wq);
+        for (int split = 1; split <= kGmMaxSplit && split <= stages; ++split) {
+            const int64_t ctas = np1 * nq * split;
+            if (split > 1 && ctas > sms - sms / 16) break;
+            const double waves = (double)((ctas + sms - 1) / sms), now = (double)std::min<int64_t>(ctas, sms);
+            const double stage = std::max({per_sm / 122.0, now * per_sm / 12000.0, resident ? 0.0 : per_sm / 75.0 / std::min(waves, 2.0)});
+            take(true, split, wq, std::max(waves * (double)((stages + split - 1) / split) * stage, memory_ns) +
+                                      (split > 1 ? 3800.0 + 150.0 * split + 14.0 * wq : 2900.0 + 19.0 * wq));
         }
     }
     return best;
@@ -732,22 +1026,29 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
     const int64_t runs = (part + most - 1) / most;
     p.run = (int32_t)((part + runs - 1) / runs);
     p.wq = plan.wq;
-    p.np = (int32_t)((g.N + 255) / 256);
+    p.split = plan.split;
+    p.per = ((plan.wq + 15) / 16 + plan.split - 1) / plan.split;
+    p.part_stages = (int32_t)(stages / plan.split);
+    p.longer = (int32_t)(stages % plan.split);
+    p.np = (int32_t)((g.N + (plan.single ? 127 : 255)) / (plan.single ? 128 : 256));
     p.nq = (int32_t)((g.M + plan.wq - 1) / plan.wq);
     GemmActMaps maps;
     const int64_t bdims[2] = {g.K, g.N}, bstrides[1] = {g.ldb}, adims[2] = {g.K, g.M}, astrides[1] = {g.lda};
-    const uint32_t bbox[2] = {64, 128};
-    if (!host::bf16_map(&maps.p, g.b, 2, bdims, bstrides, bbox)) return cudaErrorInvalidValue;
-    for (int i = 0; i < 3; ++i) {
-        const uint32_t abox[2] = {64, 32u << i};
-        if (!host::bf16_map(&maps.q[i], g.a, 2, adims, astrides, abox)) return cudaErrorInvalidValue;
-    }
+    const uint32_t bbox[2] = {64, 128}, abox[2] = {64, (uint32_t)(plan.single ? plan.wq : plan.wq / 2)};
+    if (!host::bf16_map(&maps.p, g.b, 2, bdims, bstrides, bbox) || !host::bf16_map(&maps.q, g.a, 2, adims, astrides, abox))
+        return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)p.np * p.nq;
-    switch (plan.split) {
-        case 1: return launch_pairs<1>(maps, p, (int)std::min<int64_t>(tiles, sms / 2), s);
-        case 2: return launch_pairs<2>(maps, p, (int)tiles, s);
-        default: return launch_pairs<4>(maps, p, (int)tiles, s);
+    static std::atomic<uint64_t> attr[4];
+    const int split = plan.split;
+    if (plan.single) {
+        p.ring = std::min(kGmMaxStages, kGmRing / (kGaOpBytes + 128 * plan.wq));
+        p.tmem_cols = 64;   // two accumulators
+        while ((int)p.tmem_cols < 2 * plan.wq) p.tmem_cols <<= 1;
+        return split > 1 ? launch_ga(gemm_act_mid_kernel<true>, kGmClusterSmem, attr[0], split, kGmThreads, p.nq * split, p.np, maps, p, s)
+                         : launch_ga(gemm_act_mid_kernel<false>, kGmSmem, attr[1], 1, kGmThreads, p.nq, p.np, maps, p, s);
     }
+    return split > 1 ? launch_ga(gemm_act_kernel<true>, kGaClusterSmem, attr[2], 2 * split, kGaThreads, 2 * tiles * split, 1, maps, p, s)
+                     : launch_ga(gemm_act_kernel<false>, kGaSmem, attr[3], 2, kGaThreads, 2 * std::min<int64_t>(tiles, sms / 2), 1, maps, p, s);
 }
 
 // ---------------------------------------------------------------------------------------
