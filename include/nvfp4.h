@@ -511,7 +511,7 @@ nvfp4_status nvfp4_combine_bwd(const void* dy, int64_t lddy, const void* ys, int
  * fp32 with leading dimension ldd.  act: relu2 is max(h, 0)^2, gelu the erf form, silu h / (1 + e^-h).
  * Everything after the sums is fp32, act taken of the unrounded h (gelu and silu err by less than
  * 2^-20 |h|), D rounded once; the sums are joined from runs of at most 512 products (bf16 output: 4096) in
- * fp32 registers, rounded to nearest, since the tensor core truncates as it accumulates (2^-18 of the sum after 4096).  A row's result depends on that row alone, in an order of summation
+ * fp32 registers, rounded to nearest, since the tensor core truncates as it accumulates (by 2^-15 of the products' magnitudes at most in 4096).  A row's result depends on that row alone, in an order of summation
  * that M, N, K choose.  D may be the residual (one address, leading dimension and type); nothing else overlaps.
  * Shape rules: M >= 0 (0: no-op), N >= 1, K >= 8, K % 8 == 0; lda >= K, ldb >= K, multiples of 8;
  * ldd, ldr, ldpre >= N; sizes up to 2^30, ceil(M / 32) * ceil(N / 256) up to 2^28; pointers 16-byte

@@ -177,6 +177,13 @@ def _check(status: int, what: str):
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _raw_stream(dev: int, stream):
+    """A stream's handle; without one, that of the current stream of device `dev`."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _RAW_STREAM(dev) if _RAW_STREAM is not None else torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
@@ -830,7 +837,7 @@ def _act_bwd(dy, lddy, pre, act, out, dbias, accumulate, scratch, stream):
     for t in (dy, pre if reads else None, out, dbias, scratch if need else None):
         if t is not None and t.get_device() != dev:
             _elsewhere(dev, t)
-    raw = stream.cuda_stream if stream is not None else _stream()
+    raw = _raw_stream(dev, stream)
     st = _lib().nvfp4_act_bwd(dy.data_ptr(), lddy, pre.data_ptr() if reads else None, ldpre, rows, n, act,
                               None if out is None else out.data_ptr(), 0 if out is None else _row_stride(out, "out"),
                               None if dbias is None else dbias.data_ptr(), 1 if accumulate else 0,
@@ -893,7 +900,7 @@ class LinearActBF16:
 # ---------------------------------------------------------------------------------------
 # routing of tokens to experts, and their rows into the experts' order and back
 # ---------------------------------------------------------------------------------------
-@dataclass
+@dataclass(frozen=True)
 class Routes:
     """A route's buffers (owned by torch): what nvfp4_route writes, and the grouped products, nvfp4_dispatch
     and nvfp4_combine take."""
@@ -902,20 +909,30 @@ class Routes:
     rows: torch.Tensor           # int32 [tokens][k]: the row of each choice in the experts' order, -1 for none
     sources: torch.Tensor        # int32 [tokens * k]: token * k + choice of each row, -1 behind the last
     offsets: torch.Tensor        # int32 [experts + 1]: expert e owns rows [offsets[e], offsets[e + 1])
-    scratch: torch.Tensor | None = None   # of nvfp4_route; routes whose calls may overlap have one each
+    scratch: torch.Tensor | None = None   # of nvfp4_route, which needs it; routes whose calls may overlap have one each
 
     def __post_init__(self):
         shape = self.experts.shape
         if len(shape) != 2:
             raise ValueError("experts: int32 [tokens][k]")
-        self.tokens, self.k = shape
-        self.count = self.offsets.numel() - 1
-        self.index = self.experts.get_device()
+        count = self.offsets.numel() - 1
+        index = self.experts.get_device()
         for name, dtype, want in (("experts", torch.int32, shape), ("weights", torch.float32, shape), ("rows", torch.int32, shape),
-                                  ("sources", torch.int32, (shape[0] * shape[1],)), ("offsets", torch.int32, (self.count + 1,))):
+                                  ("sources", torch.int32, (shape[0] * shape[1],)), ("offsets", torch.int32, (count + 1,))):
             t = getattr(self, name)
-            if t.dtype is not dtype or t.shape != want or not t.is_contiguous() or t.get_device() != self.index:
+            if t.dtype is not dtype or t.shape != want or not t.is_contiguous() or t.get_device() != index:
                 raise ValueError(f"{name}: contiguous {dtype} {list(want)}, all on one device")
+        t = self.scratch
+        if t is not None and (t.dtype is not torch.uint8 or not t.is_contiguous() or t.get_device() != index):
+            raise ValueError("scratch: contiguous uint8 on the same device")
+        # the fields do not change, so neither do these
+        for name, value in (("tokens", shape[0]), ("k", shape[1]), ("count", count), ("index", index), ("rows_addr", self.rows.data_ptr()),
+                            ("weights_addr", self.weights.data_ptr()), ("experts_addr", self.experts.data_ptr()),
+                            ("outputs", (self.experts.data_ptr(), self.weights.data_ptr(), self.rows.data_ptr(), self.sources.data_ptr(),
+                                         self.offsets.data_ptr(), None if t is None else t.data_ptr())),
+                            ("scratch_bytes", 0 if t is None else t.numel()), ("args", CRouteArgs())):
+            object.__setattr__(self, name, value)
+        object.__setattr__(self, "args_ref", ctypes.byref(self.args))
 
     @staticmethod
     def empty(tokens: int, experts: int, k: int, device=None) -> "Routes":
@@ -927,14 +944,15 @@ class Routes:
 
 
 def _logits(x: torch.Tensor):
-    """A [tokens][experts] tensor's dtype code and row stride."""
-    if x.dtype is not torch.float32 and x.dtype is not torch.bfloat16 or x.dim() != 2:
+    """A [tokens][experts] tensor's dtype code, row stride and sizes."""
+    dtype = x.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16 or x.dim() != 2:
         raise TypeError("expected fp32 or bf16 [tokens][experts]")
     row, col = x.stride()
     tokens, experts = x.shape
     if col != 1 and experts > 1:
         raise ValueError("inner dimension must be contiguous")
-    return OUT_FP32 if x.dtype is torch.float32 else OUT_BF16, row if tokens > 1 else -(-experts // 8) * 8
+    return OUT_FP32 if dtype is torch.float32 else OUT_BF16, row if tokens > 1 else -(-experts // 8) * 8, tokens, experts
 
 
 def nvfp4_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None, groups: int = 1,
@@ -947,8 +965,7 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, bias: 
     `groups` runs of experts, a group counting as its best expert or as the sum of its two best.  weights: scale *
     score, with renormalize over the sum of the chosen.  valid: bool [tokens], False for padding, which chooses
     nobody.  Ties go to the lowest index; experts of logit -inf are never chosen."""
-    dtype, ld = _logits(logits)
-    tokens, experts = logits.shape
+    dtype, ld, tokens, experts = _logits(logits)
     if out is None:
         if stream is None:
             out = Routes.empty(tokens, experts, k, logits.device)
@@ -957,8 +974,8 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, bias: 
                 out = Routes.empty(tokens, experts, k, logits.device)
     elif out.tokens != tokens or out.k != k or out.count != experts:
         raise ValueError(f"out: Routes of {tokens} tokens, {experts} experts, k = {k}")
-    if out.scratch is None:
-        out.scratch = _empty((max(_lib().nvfp4_route_scratch_bytes(experts), 16),), torch.uint8, logits.device, stream)
+    elif out.scratch_bytes < 592 * experts and out.scratch_bytes < _lib().nvfp4_route_scratch_bytes(experts):
+        raise ValueError("out: Routes without a scratch of nvfp4_route_scratch_bytes(experts) (Routes.empty has one)")
     dev = _CUR_DEVICE()
     if logits.get_device() != dev or out.index != dev:
         _elsewhere(dev, logits, out.experts)
@@ -972,10 +989,9 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, bias: 
             raise ValueError("valid: contiguous bool [tokens] on the logits' device")
         valid_addr = valid.data_ptr()
     ws_addr, raw = _call_context(dev, ws, stream)
-    args = CRouteArgs(k, score, groups, top_groups, group_top, 1 if renormalize else 0, scale, 0)
-    st = _lib().nvfp4_route(logits.data_ptr(), dtype, ld, tokens, experts, ctypes.byref(args), bias_addr, valid_addr,
-                            out.experts.data_ptr(), out.weights.data_ptr(), out.rows.data_ptr(), out.sources.data_ptr(),
-                            out.offsets.data_ptr(), out.scratch.data_ptr(), ws_addr, raw)
+    a = out.args
+    a.k, a.score, a.groups, a.top_groups, a.group_top, a.renormalize, a.scale = k, score, groups, top_groups, group_top, renormalize, scale
+    st = _lib().nvfp4_route(logits.data_ptr(), dtype, ld, tokens, experts, out.args_ref, bias_addr, valid_addr, *out.outputs, ws_addr, raw)
     if st:
         _check(st, "nvfp4_route")
     return out
@@ -985,8 +1001,7 @@ def nvfp4_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, routes: Routes
                     renormalize: bool = True, scale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The gradient of the logits (of their type) from that of the weights of a route with the same score,
     renormalize and scale."""
-    dtype, ld = _logits(logits)
-    tokens, experts = logits.shape
+    dtype, ld, tokens, experts = _logits(logits)
     if routes.tokens != tokens or routes.count != experts:
         raise ValueError("routes: of these logits")
     if dweights.dtype is not torch.float32 or dweights.shape != routes.experts.shape or not dweights.is_contiguous():
@@ -999,10 +1014,10 @@ def nvfp4_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, routes: Routes
     dev = _CUR_DEVICE()
     if logits.get_device() != dev or routes.index != dev or dweights.get_device() != dev or out.get_device() != dev:
         _elsewhere(dev, logits, routes.experts, dweights, out)
-    raw = stream.cuda_stream if stream is not None else _stream()
+    raw = _raw_stream(dev, stream)
     args = CRouteArgs(routes.k, score, 1, 1, 1, 1 if renormalize else 0, scale, 0)
     st = _lib().nvfp4_route_bwd(dweights.data_ptr(), logits.data_ptr(), dtype, ld, tokens, experts, ctypes.byref(args),
-                                routes.experts.data_ptr(), out.data_ptr(), ldd, raw)
+                                routes.experts_addr, out.data_ptr(), ldd, raw)
     if st:
         _check(st, "nvfp4_route_bwd")
     return out
@@ -1025,8 +1040,8 @@ def nvfp4_dispatch(x: torch.Tensor, routes: Routes, out: torch.Tensor | None = N
     dev = _CUR_DEVICE()
     if x.get_device() != dev or routes.index != dev or out.get_device() != dev:
         _elsewhere(dev, x, routes.rows, out)
-    raw = stream.cuda_stream if stream is not None else _stream()
-    st = _lib().nvfp4_dispatch(x.data_ptr(), ldx, tokens, d, routes.rows.data_ptr(), routes.k, out.data_ptr(), ldo, out.shape[0], raw)
+    raw = _raw_stream(dev, stream)
+    st = _lib().nvfp4_dispatch(x.data_ptr(), ldx, tokens, d, routes.rows_addr, routes.k, out.data_ptr(), ldo, out.shape[0], raw)
     if st:
         _check(st, "nvfp4_dispatch")
     return out
@@ -1060,9 +1075,9 @@ def nvfp4_combine(ys: torch.Tensor, routes: Routes, residual: torch.Tensor | Non
         _elsewhere(dev, residual)
     if ys.get_device() != dev or routes.index != dev or out.get_device() != dev:
         _elsewhere(dev, ys, routes.rows, out)
-    raw = stream.cuda_stream if stream is not None else _stream()
-    st = _lib().nvfp4_combine(ys.data_ptr(), ldys, OUT_FP32 if ys.dtype is torch.float32 else OUT_BF16, total, routes.rows.data_ptr(),
-                              routes.weights.data_ptr() if weighted else None, routes.k,
+    raw = _raw_stream(dev, stream)
+    st = _lib().nvfp4_combine(ys.data_ptr(), ldys, OUT_FP32 if ys.dtype is torch.float32 else OUT_BF16, total, routes.rows_addr,
+                              routes.weights_addr if weighted else None, routes.k,
                               residual.data_ptr() if residual is not None else None, ldr, out.data_ptr(), ldo,
                               OUT_FP32 if out.dtype is torch.float32 else OUT_BF16, tokens, d, raw)
     if st:
@@ -1093,9 +1108,9 @@ def nvfp4_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, routes: Routes, dys: t
     dev = _CUR_DEVICE()
     if dy.get_device() != dev or ys.get_device() != dev or routes.index != dev or dys.get_device() != dev or dweights.get_device() != dev:
         _elsewhere(dev, dy, ys, routes.rows, dys, dweights)
-    raw = stream.cuda_stream if stream is not None else _stream()
+    raw = _raw_stream(dev, stream)
     st = _lib().nvfp4_combine_bwd(dy.data_ptr(), lddy, ys.data_ptr(), ldys, OUT_FP32 if ys.dtype is torch.float32 else OUT_BF16, total,
-                                  routes.rows.data_ptr(), routes.weights.data_ptr(), routes.k, dys.data_ptr(), lddys,
+                                  routes.rows_addr, routes.weights_addr, routes.k, dys.data_ptr(), lddys,
                                   dweights.data_ptr(), tokens, d, raw)
     if st:
         _check(st, "nvfp4_combine_bwd")

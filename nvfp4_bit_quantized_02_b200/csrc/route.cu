@@ -10,17 +10,20 @@
 // e^(l - max) / sum, for the sigmoid e^(min(l, 0) - max) / (1 + e^-|l|) / sum, the maxima over the chosen.
 //
 // A warp takes a token.  Its lanes hold the experts in ascending order, a group on a power of two of lanes
-// (32 / groups), so that what is reduced within a group stays within neighbouring lanes and the lowest lane
-// with a value holds the lowest index.  Values are compared as unsigned words that order as they do.
+// (32 / groups), so that what is reduced within a group stays within neighbouring lanes and a lower lane holds lower
+// indices.  The k-th largest of the lanes' largest values bounds the k-th largest of all from below: what is not under it (a dozen
+// of 256 for k = 8) is gathered, one candidate a lane, and each candidate's place is the number of those before it.  That is a
+// third of the instructions of k rounds of "largest of all, then remove it", which bounded the kernel.
 //
 // The choice is that of the definition in fp64.  Where c is the logit itself its order is exact.  Otherwise c
-// is evaluated in fp32 (the error bound stands at kTau), and a token whose order is not certain, because
-// two neighbours in it lie closer than the bound, is decided again in fp64 (choose_slow): about 1 token in 300
-// of 256 experts with sigmoid scores.
+// is evaluated in fp32 (the error bound stands at kTauSigmoid), and where two neighbours in the order lie closer than the bound
+// the candidates near it are compared in fp64 (about 1 token in 1000 of 256 experts with sigmoid scores), as are groups whose
+// scores are too close (groups_slow).  More than 32 candidates, that is, many equal values, are looked through one by one
+// (choose_slow).
 //
 // Rows: a warp takes neighbouring tokens and counts each expert's choices as it goes, so that a choice's rank
 // among the warp's is there at once; the ranks are joined over the block's warps, and over the blocks by a
-// second kernel, which reads every block's counts.  No atomics: the order is that of the tokens.
+// second kernel, which reads every block's counts.  No atomics on memory: the order is that of the tokens.
 // One block does it all for few tokens.
 #include <cuda_runtime.h>
 
@@ -51,10 +54,12 @@ constexpr float kTauC = 4.7683716e-7f;         // 2^-21
 struct RouteKernelParams {
     RouteProblem r;
     int32_t size;        // experts per group
-    int32_t lanes;       // of a group, a power of two
+    int32_t lanes_log2;  // lanes of a group, a power of two
     int32_t per_lane;    // experts of a lane
     int32_t vec;         // a lane's logits can be read 16 bytes at a time
     int32_t block_tokens, warp_tokens;
+    int32_t stride;      // of the warps' counts: odd
+    int32_t held;        // choices that shared memory keeps, 0: they are read back from rows and chosen
 };
 
 __device__ __forceinline__ uint32_t order_key(float c) {   // ascends with c; 0 for none
@@ -83,66 +88,74 @@ __device__ __forceinline__ void merge_top2(F& a1, F& a2, F b1, F b2) {
 // Whether the group of this lane is among the top_groups best, the lowest index first among equals
 template <typename F>
 __device__ __forceinline__ bool group_stays(F score, const RouteKernelParams& p, int lane) {
-    const int g = lane / p.lanes;
+    const int g = lane >> p.lanes_log2;
     int before = 0;
+#pragma unroll 4
     for (int i = 0; i < p.r.groups; ++i) {
-        const F other = __shfl_sync(kAll, score, i * p.lanes);
-        before += other > score || (other == score && i < g);
+        const F other = __shfl_sync(kAll, score, i << p.lanes_log2);
+        before += i < g ? other >= score : other > score;
     }
     return before < p.r.top_groups && score > (F)kNone && g < p.r.groups;
 }
 
-// The choice in fp64: lane j returns the j-th expert, or -1.  Nothing is kept: each pick looks through the
-// row for what comes next in order behind the one before.
+// c in fp64; the softmax's largest logit and sum
+__device__ __forceinline__ double value64(const RouteKernelParams& p, float l, int e, float top, double sum) {
+    if (!(l > kNone)) return (double)kNone;
+    const double s = p.r.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / sum;
+    const double c = p.r.bias ? s + (double)__ldg(p.r.bias + e) : s;
+    return c == c ? c : (double)kNone;
+}
 template <typename T>
-__device__ __noinline__ int choose_slow(const RouteKernelParams& p, const T* row, float top) {
-    const int lane = threadIdx.x & 31, g = lane / p.lanes, first = (lane % p.lanes) * p.per_lane;
-    const int count = g < p.r.groups ? max(0, min(p.per_lane, p.size - first)) : 0, e0 = g * p.size + first;
-    double sum = 1.0;
-    const auto value = [&](int e) {
+__device__ __noinline__ double sum64(const RouteKernelParams& p, const T* row, float top) {
+    double part = 0.0;
+    for (int e = threadIdx.x & 31; e < p.r.experts; e += 32) {
         const float l = logit_of(raw_logit(row, e));
-        if (!(l > kNone)) return (double)kNone;
-        const double s = p.r.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / sum;
-        const double c = p.r.bias ? s + (double)__ldg(p.r.bias + e) : s;
-        return c == c ? c : (double)kNone;
-    };
-    if (!p.r.sigmoid) {
-        double part = 0.0;
-        for (int i = 0; i < count; ++i) {
-            const float l = logit_of(raw_logit(row, e0 + i));
-            if (l > kNone) part += exp((double)l - (double)top);
-        }
-        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
-        sum = part;
+        if (l > kNone) part += exp((double)l - (double)top);
     }
-    bool open = true;
-    if (p.r.groups > 1) {
-        double a1 = kNone, a2 = kNone;
-        for (int i = 0; i < count; ++i) merge_top2(a1, a2, value(e0 + i), (double)kNone);
-        for (int o = 1; o < p.lanes; o <<= 1) merge_top2(a1, a2, __shfl_xor_sync(kAll, a1, o), __shfl_xor_sync(kAll, a2, o));
-        open = group_stays(p.r.group_top == 2 ? a1 + a2 : a1, p, lane);
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
+    return part;
+}
+
+// The groups' choice in fp64
+template <typename T>
+__device__ __noinline__ bool groups_slow(const RouteKernelParams& p, const T* row, float top) {
+    const int lane = threadIdx.x & 31, g = lane >> p.lanes_log2, first = (lane & ((1 << p.lanes_log2) - 1)) * p.per_lane;
+    const int count = g < p.r.groups ? max(0, min(p.per_lane, p.size - first)) : 0, e0 = g * p.size + first;
+    const double sum = p.r.sigmoid ? 1.0 : sum64(p, row, top);
+    double a1 = kNone, a2 = kNone;
+    for (int i = 0; i < count; ++i) merge_top2(a1, a2, value64(p, logit_of(raw_logit(row, e0 + i)), e0 + i, top, sum), (double)kNone);
+    for (int o = 1; o < 1 << p.lanes_log2; o <<= 1) merge_top2(a1, a2, __shfl_xor_sync(kAll, a1, o), __shfl_xor_sync(kAll, a2, o));
+    return group_stays(p.r.group_top == 2 ? a1 + a2 : a1, p, lane);
+}
+
+// The experts' choice in fp64 within the groups that stay: lane j returns the j-th expert, or -1
+template <int VMAX, typename T>
+__device__ __noinline__ int choose_slow(const RouteKernelParams& p, const T* row, float top, bool stays) {
+    const int lane = threadIdx.x & 31, g = lane >> p.lanes_log2, first = (lane & ((1 << p.lanes_log2) - 1)) * p.per_lane;
+    const int count = stays ? max(0, min(p.per_lane, p.size - first)) : 0, e0 = g * p.size + first;
+    const double sum = p.r.sigmoid || !p.r.bias ? 1.0 : sum64(p, row, top);
+    double c[VMAX];
+    for (int i = 0; i < count; ++i) {
+        const float l = logit_of(raw_logit(row, e0 + i));
+        c[i] = p.r.bias ? value64(p, l, e0 + i, top, sum) : (double)l;
     }
-    // without a bias the groups alone go by scores, the experts by their logits
-    const auto order = [&](int e) { return p.r.bias ? value(e) : (double)logit_of(raw_logit(row, e)); };
     int mine = -1, last_e = -1;
     double last = INFINITY;
-    for (int j = 0; j < p.r.k; ++j) {
+    for (int j = 0; j < p.r.k; ++j) {   // what comes next in order behind the one before
         double best = kNone;
         int at = -1;
-        if (open)
-            for (int i = 0; i < count; ++i) {
-                const int e = e0 + i;
-                const double c = order(e);
-                if ((c < last || (c == last && e > last_e)) && c > best) {
-                    best = c;
-                    at = e;
-                }
+        for (int i = 0; i < count; ++i) {
+            const int e = e0 + i;
+            if ((c[i] < last || (c[i] == last && e > last_e)) && c[i] > best) {
+                best = c[i];
+                at = e;
             }
+        }
         for (int o = 16; o > 0; o >>= 1) {
-            const double c = __shfl_xor_sync(kAll, best, o);
+            const double b = __shfl_xor_sync(kAll, best, o);
             const int e = __shfl_xor_sync(kAll, at, o);
-            if (e >= 0 && (at < 0 || c > best || (c == best && e < at))) {
-                best = c;
+            if (e >= 0 && (at < 0 || b > best || (b == best && e < at))) {
+                best = b;
                 at = e;
             }
         }
@@ -152,6 +165,23 @@ __device__ __noinline__ int choose_slow(const RouteKernelParams& p, const T* row
         last_e = at;
     }
     return mine;
+}
+
+// One candidate a lane, the first `count` lanes, in ascending order of their indices: the place of each in descending
+// order of c, the lowest index first among equals
+template <typename F>
+__device__ __forceinline__ int place_of(F c, int count, int lane) {
+    int before = 0;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) before += __shfl_sync(kAll, c, i) > c;
+    // equals have come to one place
+    return before + __popc(__match_any_sync(kAll, lane < count ? before : 64) & ((1u << lane) - 1u));
+}
+template <typename T>
+__device__ __noinline__ int places_slow(const RouteKernelParams& p, const T* row, int e, float top, int count) {
+    const double sum = p.r.sigmoid ? 1.0 : sum64(p, row, top);
+    const int lane = threadIdx.x & 31;
+    return place_of(lane < count ? value64(p, logit_of(raw_logit(row, e)), e, top, sum) : (double)kNone, count, lane);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -175,143 +205,235 @@ __device__ __forceinline__ float chosen_weight(const RouteProblem& r, float l, f
     float v = held ? expf(z - most) : 0.0f;
     if (r.sigmoid && held) v /= 1.0f + expf(-fabsf(l));
     const float all = warp_sum(v);
-    return held ? r.scale * (v / all) : 0.0f;
+    return held ? r.scale * __fdividef(v, all) : 0.0f;   // all: 1 to 32
 }
 
-// VMAX: experts of a lane at most; T: the logits' type
+struct RouteWarp {       // a warp's candidates, then the same in order: c, the expert
+    float2 found[32], sorted[32];
+};
+
+// VMAX: experts of a lane at most; T: the logits' type.  WARPS: at most
 template <int VMAX, int WARPS, typename T>
-__global__ void __launch_bounds__(32 * WARPS) route_choose_kernel(const RouteKernelParams p) {
+__global__ void __launch_bounds__(32 * WARPS) route_choose_kernel(const __grid_constant__ RouteKernelParams p) {
     extern __shared__ int32_t smem[];
-    int32_t* counts = smem;                               // [WARPS][experts]
-    int32_t* base = smem + WARPS * p.r.experts;           // [experts + 1]: one block's offsets
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ RouteWarp scratch[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int k = p.r.k, E = p.r.experts;
-    for (int i = threadIdx.x; i < WARPS * E; i += 32 * WARPS) counts[i] = 0;
-    __syncthreads();
+    int32_t* counts = smem;                               // [warps][stride]
+    int32_t* base = smem + warps * p.stride;              // [experts + 1]: one block's offsets
+    uint32_t* held = reinterpret_cast<uint32_t*>(base + E + 1);   // rank << 11 | expert + 1 of the block's choices
+    RouteWarp& own = scratch[warp];
+    for (int i = threadIdx.x; i < warps * p.stride; i += blockDim.x) counts[i] = 0;
     ptx::griddep_launch();
     const int t0 = blockIdx.x * p.block_tokens, t1 = min(p.r.tokens, t0 + p.block_tokens);
-    const int g = lane / p.lanes, first = (lane % p.lanes) * p.per_lane, e0 = g * p.size + first;
+    const int g = lane >> p.lanes_log2, first = (lane & ((1 << p.lanes_log2) - 1)) * p.per_lane, e0 = g * p.size + first;
     const int count = g < p.r.groups ? max(0, min(p.per_lane, p.size - first)) : 0;
     const bool by_logit = !p.r.bias;
     const bool scores = !by_logit || (p.r.groups > 1 && p.r.group_top == 2);
+    const bool soft = !p.r.sigmoid && (scores || !p.r.renormalize);
     bool odd = false;
-    int32_t* mine_counts = counts + warp * E;
+    int32_t* mine_counts = counts + warp * p.stride;
+    // the bias, -inf for what is none whatever its logit
+    const auto bias_of = [&](int i) {
+        float b = i < count ? 0.0f : kNone;
+        if (p.r.bias && i < count) b = __ldg(p.r.bias + e0 + i);
+        return b == b ? b : kNone;
+    };
+    float bias[VMAX <= 8 ? VMAX : 1];
+    if constexpr (VMAX <= 8) {
+#pragma unroll
+        for (int i = 0; i < VMAX; ++i) bias[i] = bias_of(i);
+    }
+    const auto load = [&](int t, float (&l)[VMAX]) {   // places without an expert: -inf
+        const T* row = reinterpret_cast<const T*>(p.r.logits) + (int64_t)t * p.r.ld;
+        if (p.vec) {
+            constexpr int per = 16 / (int)sizeof(T);
+            constexpr uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+#pragma unroll
+            for (int i = 0; i < VMAX; i += per) {
+                uint4 v = make_uint4(none, none, none, none);
+                if (i < count) v = __ldg(reinterpret_cast<const uint4*>(row + e0 + i));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < per && i + j < VMAX; ++j)
+                    l[i + j] = sizeof(T) == 4 ? __uint_as_float(w[j & 3]) : (j & 1 ? bf16_hi(w[(j >> 1) & 3]) : bf16_lo(w[(j >> 1) & 3]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VMAX; ++i) l[i] = i < count ? raw_logit(row, e0 + i) : kNone;
+        }
+    };
     const int w1 = min(t1, t0 + (warp + 1) * p.warp_tokens);
-    for (int t = t0 + warp * p.warp_tokens; t < w1; ++t) {
+    int t = t0 + warp * p.warp_tokens;
+    float next[VMAX <= 8 ? VMAX : 1];   // the next token's logits, on their way
+    if constexpr (VMAX <= 8) {
+        if (t < w1) load(t, next);
+    }
+    __syncthreads();
+    for (; t < w1; ++t) {
+        float l[VMAX];
+        if constexpr (VMAX <= 8) {
+#pragma unroll
+            for (int i = 0; i < VMAX; ++i) l[i] = next[i];
+            if (t + 1 < w1) load(t + 1, next);
+        } else {
+            load(t, l);
+        }
         int mine = -1;
         float weight = 0.0f;
         if (!p.r.valid || __ldg(p.r.valid + t)) {
             const T* row = reinterpret_cast<const T*>(p.r.logits) + (int64_t)t * p.r.ld;
-            float l[VMAX];
-            if (p.vec) {
-                constexpr int per = 16 / (int)sizeof(T);
+            bool strange = false;   // NaN or an infinity, here where there is no expert too
 #pragma unroll
-                for (int i = 0; i < VMAX; i += per) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (i < count) v = __ldg(reinterpret_cast<const uint4*>(row + e0 + i));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < VMAX; ++i) strange |= !(fabsf(l[i]) <= FLT_MAX);
+            if (strange) {
 #pragma unroll
-                    for (int j = 0; j < per && i + j < VMAX; ++j)
-                        l[i + j] = sizeof(T) == 4 ? __uint_as_float(w[j & 3]) : (j & 1 ? bf16_hi(w[(j >> 1) & 3]) : bf16_lo(w[(j >> 1) & 3]));
+                for (int i = 0; i < VMAX; ++i) {
+                    odd |= !(l[i] <= FLT_MAX);
+                    l[i] = logit_of(l[i]);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < VMAX; ++i) l[i] = i < count ? raw_logit(row, e0 + i) : 0.0f;
             }
-            float top = kNone;
-#pragma unroll
-            for (int i = 0; i < VMAX; ++i) {
-                const bool in = i < count;
-                odd |= in && !(l[i] <= FLT_MAX);
-                l[i] = in ? logit_of(l[i]) : kNone;
-                top = fmaxf(top, l[i]);
-            }
-            float sum = 1.0f;
-            const bool soft = !p.r.sigmoid && (scores || !p.r.renormalize);
+            float top = 0.0f, sum = 1.0f;
             if (soft) {
+                top = kNone;
+#pragma unroll
+                for (int i = 0; i < VMAX; ++i) top = fmaxf(top, l[i]);
                 top = warp_max(top);
+                if (!(top > kNone)) top = 0.0f;   // no expert at all
                 sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < VMAX; ++i) sum += l[i] > kNone ? __expf(l[i] - top) : 0.0f;
+                for (int i = 0; i < VMAX; ++i) sum += __expf(l[i] - top);
                 sum = warp_sum(sum);
             }
-            // c, and what of it the groups go by
-            uint32_t key[VMAX];
-            bool certain = true;
+            // c, and the lane's largest two
+            float c[VMAX];
             const float tau = p.r.sigmoid ? kTauSigmoid : kTauSoftmax / sum;
             if (scores) {
                 const float per_sum = 1.0f / sum;
+                const auto bias_at = [&](int i) { return VMAX <= 8 ? bias[VMAX <= 8 ? i : 0] : bias_of(i); };
+                if (p.r.sigmoid) {
 #pragma unroll
-                for (int i = 0; i < VMAX; ++i) {
-                    float c = p.r.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - top) * per_sum;
-                    if (p.r.bias && i < count) c += __ldg(p.r.bias + e0 + i);
-                    key[i] = l[i] > kNone ? order_key(c) : 0u;
+                    for (int i = 0; i < VMAX; ++i) c[i] = __fdividef(1.0f, 1.0f + __expf(-l[i])) + bias_at(i);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VMAX; ++i) c[i] = fmaf(__expf(l[i] - top), per_sum, bias_at(i));
+                }
+                if (strange) {
+#pragma unroll
+                    for (int i = 0; i < VMAX; ++i) c[i] = l[i] > kNone && c[i] == c[i] ? c[i] : kNone;
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < VMAX; ++i) key[i] = order_key(l[i]);
+                for (int i = 0; i < VMAX; ++i) c[i] = l[i];
             }
+            bool stays = g < p.r.groups;
+            float a1 = kNone, a2 = kNone;
             if (p.r.groups > 1) {
-                float a1 = kNone, a2 = kNone;
 #pragma unroll
-                for (int i = 0; i < VMAX; ++i) merge_top2(a1, a2, key_value(key[i]), kNone);
-                for (int o = 1; o < p.lanes; o <<= 1) merge_top2(a1, a2, __shfl_xor_sync(kAll, a1, o), __shfl_xor_sync(kAll, a2, o));
-                const float score = p.r.group_top == 2 ? a1 + a2 : a1;
-                const bool stays = group_stays(score, p, lane);
+                for (int i = 0; i < VMAX; ++i) {
+                    a2 = fmaxf(a2, fminf(a1, c[i]));
+                    a1 = fmaxf(a1, c[i]);
+                }
+                float b1 = a1, b2 = a2;
+                for (int o = 1; o < 1 << p.lanes_log2; o <<= 1) {
+                    const float d1 = __shfl_xor_sync(kAll, b1, o), d2 = __shfl_xor_sync(kAll, b2, o);
+                    b2 = fmaxf(fminf(b1, d1), fmaxf(b2, d2));
+                    b1 = fmaxf(b1, d1);
+                }
+                const float score = p.r.group_top == 2 ? b1 + b2 : b1;
+                stays = group_stays(score, p, lane);
                 if (scores) {
                     const uint32_t least = __reduce_min_sync(kAll, stays ? order_key(score) : kAll);
                     const uint32_t most = __reduce_max_sync(kAll, stays || g >= p.r.groups ? 0u : order_key(score));
                     const float lo = key_value(least);
                     // a sum of two errs by both, and by its rounding
-                    if (most && least != kAll) certain = lo - key_value(most) > 2.0f * (tau + kTauC * fabsf(lo));
+                    if (most && least != kAll && !(lo - key_value(most) > 2.0f * (tau + kTauC * fabsf(lo)))) stays = groups_slow(p, row, top);
                 }
-#pragma unroll
-                for (int i = 0; i < VMAX; ++i) key[i] = !stays ? 0u : by_logit ? order_key(l[i]) : key[i];
-            }
-            uint32_t best = 0;
-#pragma unroll
-            for (int i = 0; i < VMAX; ++i) best = max(best, key[i]);
-            // k picks, and where the order is that of c in fp32 one more, to see its distance
-            float last = INFINITY;
-            int last_e = -1;
-            const int picks = by_logit ? k : k + 1;
-            for (int j = 0; j < picks && certain; ++j) {
-                const uint32_t most = __reduce_max_sync(kAll, best);
-                if (!most) break;
-                const int winner = __ffs(__ballot_sync(kAll, best == most)) - 1;
-                int at = 0;
-                if (lane == winner) {
-                    bool found = false;
-                    best = 0;
+                if (by_logit && scores) {   // the groups went by scores, the experts go by logits
+                    a1 = a2 = kNone;
 #pragma unroll
                     for (int i = 0; i < VMAX; ++i) {
-                        const bool here = !found && key[i] == most;
-                        found |= here;
-                        if (here) {
-                            at = i;
-                            key[i] = 0;
-                        }
-                        best = max(best, key[i]);
+                        c[i] = l[i];
+                        a2 = fmaxf(a2, fminf(a1, c[i]));
+                        a1 = fmaxf(a1, c[i]);
                     }
-                    at += e0;
                 }
-                at = __shfl_sync(kAll, at, winner);
+                if (!stays) a1 = a2 = kNone;
+            } else {
+#pragma unroll
+                for (int i = 0; i < VMAX; ++i) a1 = fmaxf(a1, c[i]);
+            }
+            // a bound that as many values reach as are wanted: k, and where c has errors one more, to see its distance
+            const int wanted = by_logit ? k : k + 1;
+            uint32_t x = order_key(a1), y = p.r.groups > 1 ? order_key(a2) : 0u, bound = 0;
+#pragma unroll 4
+            for (int j = 0; j < wanted; ++j) {   // 0: fewer than that, so all that there are
+                bound = __reduce_max_sync(kAll, x);
+                if (x == bound) {
+                    x = y;
+                    y = 0;
+                }
+            }
+            float at_least = bound ? key_value(bound) : -FLT_MAX;
+            int all = 0;
+            const auto gather = [&]() {   // what reaches at_least, one a lane, in ascending order of the experts
+                int n = 0;
+                const float least = stays ? at_least : __int_as_float(0x7FC00000);   // NaN: nothing reaches it
+#pragma unroll
+                for (int i = 0; i < VMAX; ++i) n += c[i] >= least;
+                int before = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(kAll, before, o);
+                    if (lane >= o) before += u;
+                }
+                all = __shfl_sync(kAll, before, 31);
+                if (all > 32) return make_float2(kNone, 0.0f);
+                float2* to = own.found + (before - n);
+#pragma unroll
+                for (int i = 0; i < VMAX; ++i)
+                    if (c[i] >= least) *to++ = make_float2(c[i], __int_as_float(e0 + i));
+                __syncwarp();
+                return lane < all ? own.found[lane] : make_float2(kNone, 0.0f);
+            };
+            float2 found = gather();
+            float logit = kNone;
+            if (all <= 32) {
+                int place = place_of(found.x, all, lane);
+                if (lane < all) own.sorted[place] = found;
+                __syncwarp();
+                float2 at = own.sorted[lane];
                 if (!by_logit) {
-                    const float c = key_value(most);
-                    if (j > 0 && !(last - c > tau + kTauC * fabsf(last))) {
-                        // the same logit and bias give the same c: the lower index came first
-                        certain = j < k && raw_logit(row, at) == raw_logit(row, last_e) && __ldg(p.r.bias + at) == __ldg(p.r.bias + last_e);
+                    const float2 behind = own.sorted[min(lane + 1, 31)];
+                    const int e1 = __float_as_int(at.y), e2 = __float_as_int(behind.y);
+                    bool close = lane < k && lane + 1 < all && !(at.x - behind.x > tau + kTauC * fabsf(at.x));
+                    // the same logit and bias give the same c, and the lower index came first
+                    if (close && lane + 1 < k) close = raw_logit(row, e1) != raw_logit(row, e2) || __ldg(p.r.bias + e1) != __ldg(p.r.bias + e2);
+                    if (__any_sync(kAll, close)) {
+                        // all that may be among the first k, compared in fp64
+                        const float last = own.sorted[min(k, all) - 1].x;
+                        at_least = fminf(at_least, last - 2.0f * (tau + kTauC * fabsf(last)));
+                        __syncwarp();
+                        found = gather();
+                        if (all <= 32) {
+                            place = places_slow(p, row, __float_as_int(found.y), top, all);
+                            if (lane < all) own.sorted[place] = found;
+                            __syncwarp();
+                            at = own.sorted[lane];
+                        }
                     }
-                    last = c;
-                    last_e = at;
                 }
-                if (lane == j && j < k) mine = at;
+                if (all <= 32 && lane < k && lane < all) {
+                    mine = __float_as_int(at.y);
+                    logit = by_logit ? at.x : logit_of(raw_logit(row, mine));
+                }
+                __syncwarp();
             }
-            if (!certain) {
-                if (p.r.sigmoid) top = 0.0f;
-                mine = choose_slow(p, row, top);
+            if (all > 32) {
+                mine = choose_slow<VMAX>(p, row, top, stays);
+                logit = mine >= 0 ? logit_of(raw_logit(row, mine)) : kNone;
             }
-            weight = chosen_weight(p.r, mine >= 0 ? logit_of(raw_logit(row, mine)) : kNone, top, sum);
+            weight = chosen_weight(p.r, logit, top, sum);
         }
         int rank = 0;
         if (mine >= 0) rank = mine_counts[mine]++;   // a token's experts differ
@@ -320,25 +442,26 @@ __global__ void __launch_bounds__(32 * WARPS) route_choose_kernel(const RouteKer
             const int64_t at = (int64_t)t * k + lane;
             p.r.chosen[at] = mine;
             p.r.weights[at] = weight;
-            p.r.rows[at] = rank;
+            if (p.held) held[(t - t0) * k + lane] = (uint32_t)rank << 11 | (uint32_t)(mine + 1);
+            else p.r.rows[at] = rank;
         }
     }
     if (__any_sync(kAll, odd) && lane == 0) atomicOr(p.r.flags, kFlagNonFinite);
     __syncthreads();
     // ranks within the block: the warps before
-    for (int e = threadIdx.x; e < E; e += 32 * WARPS) {
+    const bool alone = gridDim.x == 1;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int before = 0;
 #pragma unroll 8
-        for (int w = 0; w < WARPS; ++w) {
-            const int c = counts[w * E + e];
-            counts[w * E + e] = before;
+        for (int w = 0; w < warps; ++w) {
+            const int c = counts[w * p.stride + e];
+            counts[w * p.stride + e] = before;
             before += c;
         }
-        if (gridDim.x == 1) base[e] = before;
+        if (alone) base[e] = before;
         else p.r.scratch[(int64_t)blockIdx.x * E + e] = before;
     }
     __syncthreads();
-    const bool alone = gridDim.x == 1;
     if (alone) {
         if (warp == 0) {   // the offsets: lane by lane a run of experts
             const int per = (E + 31) / 32, lo = min(E, lane * per), hi = min(E, lo + per);
@@ -364,22 +487,23 @@ __global__ void __launch_bounds__(32 * WARPS) route_choose_kernel(const RouteKer
         }
         __syncthreads();
     }
-    const int64_t c0 = (int64_t)t0 * k, c1 = (int64_t)t1 * k;
-    for (int64_t i = c0 + threadIdx.x; i < c1; i += 32 * WARPS) {
-        const int e = p.r.chosen[i];
-        const int w = (int)((uint32_t)(i - c0) / (uint32_t)(k * p.warp_tokens));   // a block's choices: less than 2^30
+    const int64_t c0 = (int64_t)t0 * k;
+    const int choices = max(0, t1 - t0) * k, per_warp = k * p.warp_tokens;   // of a block: less than 2^30
+    for (int i = threadIdx.x; i < choices; i += blockDim.x) {
+        const uint32_t h = p.held ? held[i] : 0u;
+        const int e = p.held ? (int)(h & 2047u) - 1 : p.r.chosen[c0 + i];
         int row = -1;
         if (e >= 0) {
-            row = p.r.rows[i] + counts[w * E + e];
+            row = (p.held ? (int)(h >> 11) : p.r.rows[c0 + i]) + counts[(int)((uint32_t)i / (uint32_t)per_warp) * p.stride + e];
             if (alone) {
                 row += base[e];
-                p.r.sources[row] = (int32_t)i;
+                p.r.sources[row] = (int32_t)(c0 + i);
             }
         }
-        p.r.rows[i] = row;
+        p.r.rows[c0 + i] = row;
     }
     if (alone)
-        for (int64_t i = base[E] + threadIdx.x; i < c1; i += 32 * WARPS) p.r.sources[i] = -1;
+        for (int i = base[E] + threadIdx.x; i < choices; i += blockDim.x) p.r.sources[i] = -1;
 }
 
 constexpr int kPlaceThreads = 1024;
@@ -391,14 +515,21 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteK
     for (int e = threadIdx.x; e < E; e += kPlaceThreads) total[e] = before[e] = 0;
     __syncthreads();
     ptx::griddep_wait();
-    int wide = 32;
-    while (wide < E) wide <<= 1;
-    const int e = threadIdx.x & (wide - 1), parts = kPlaceThreads / wide;
+    const int t0 = blockIdx.x * p.block_tokens, t1 = min(p.r.tokens, t0 + p.block_tokens);
+    const int64_t c0 = (int64_t)t0 * k + threadIdx.x, c1 = (int64_t)t1 * k;
+    // the block's first choices are on their way during the sums
+    const int chosen0 = c0 < c1 ? __ldcg(p.r.chosen + c0) : -1, rank0 = c0 < c1 ? __ldcg(p.r.rows + c0) : 0;
+    int wide = 32, shift = 5;
+    while (wide < E) {
+        wide <<= 1;
+        ++shift;
+    }
+    const int e = threadIdx.x & (wide - 1), parts = kPlaceThreads >> shift;
     if (e < E) {
         int all = 0, prior = 0;
-#pragma unroll 8
-        for (int b = threadIdx.x / wide; b < blocks; b += parts) {
-            const int c = __ldcg(p.r.scratch + (int64_t)b * E + e);
+#pragma unroll 20
+        for (int b = threadIdx.x >> shift; b < blocks; b += parts) {
+            const int c = __ldcg(p.r.scratch + b * E + e);
             all += c;
             prior += b < (int)blockIdx.x ? c : 0;
         }
@@ -428,11 +559,10 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteK
     __syncthreads();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i <= E; i += kPlaceThreads) p.r.offsets[i] = total[i];
-    const int t0 = blockIdx.x * p.block_tokens, t1 = min(p.r.tokens, t0 + p.block_tokens);
-    for (int64_t i = (int64_t)t0 * k + threadIdx.x; i < (int64_t)t1 * k; i += kPlaceThreads) {
-        const int c = __ldcg(p.r.chosen + i);
+    for (int64_t i = c0; i < c1; i += kPlaceThreads) {
+        const int c = i == c0 ? chosen0 : __ldcg(p.r.chosen + i);
         if (c < 0) continue;
-        const int row = __ldcg(p.r.rows + i) + before[c];
+        const int row = (i == c0 ? rank0 : __ldcg(p.r.rows + i)) + before[c];
         p.r.rows[i] = row;
         p.r.sources[row] = (int32_t)i;
     }
@@ -462,6 +592,15 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteBwd p) {
     if (t >= p.r.tokens) return;
     const T* row = reinterpret_cast<const T*>(p.r.logits) + (int64_t)t * p.r.ld;
     T* out = reinterpret_cast<T*>(p.dlogits) + (int64_t)t * p.ldd;
+    const bool whole = !p.r.renormalize && !p.r.sigmoid;
+    constexpr int per = 16 / (int)sizeof(T);
+    if (!whole) {   // the zeros are under way during the rest
+        if (p.vec) {
+            for (int i = lane * per; i < E; i += 32 * per) *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int i = lane; i < E; i += 32) put_logit(out, i, 0.0f);
+        }
+    }
     int mine = -1;
     float g = 0.0f;
     if (lane < k) {
@@ -472,7 +611,6 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteBwd p) {
     const float l = mine >= 0 ? logit_of(raw_logit(row, mine)) : kNone;
     const bool held = l > kNone;
     float d = 0.0f;
-    const bool whole = !p.r.renormalize && !p.r.sigmoid;
     if (p.r.renormalize) {
         const float z = p.r.sigmoid ? fminf(l, 0.0f) : l, most = warp_max(held ? z : kNone);
         float n = held ? expf(z - most) : 0.0f;
@@ -487,14 +625,9 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteBwd p) {
         const float small = expf(-fabsf(l)), one = 1.0f + small;
         d = held ? g * (small / one) / one : 0.0f;
     }
-    const int per = 16 / (int)sizeof(T);
-    if (!whole || !__any_sync(kAll, held)) {
-        if (p.vec) {
-            for (int i = lane * per; i < E; i += 32 * per) *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
-        } else {
-            for (int i = lane; i < E; i += 32) put_logit(out, i, 0.0f);
-        }
-    } else {
+    if (whole && !__any_sync(kAll, held)) {
+        for (int i = lane; i < E; i += 32) put_logit(out, i, 0.0f);
+    } else if (whole) {
         float top = kNone;
         for (int i = lane; i < E; i += 32) top = fmaxf(top, logit_of(raw_logit(row, i)));
         top = warp_max(top);
@@ -513,45 +646,49 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteBwd p) {
 // ---------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------
+constexpr int kRouteHeld = 8192;   // choices of a block that shared memory keeps
+
 template <int VMAX, int WARPS, typename T>
-static cudaError_t launch_choose(const RouteKernelParams& p, int blocks, cudaStream_t s) {
+static cudaError_t launch_choose(const RouteKernelParams& p, int blocks, int warps, cudaStream_t s) {
     static std::atomic<uint64_t> attr{0};
     auto kern = route_choose_kernel<VMAX, WARPS, T>;
-    const int bytes = (WARPS * p.r.experts + p.r.experts + 1) * 4;
-    if (cudaError_t e = host::ensure_smem(reinterpret_cast<const void*>(kern), (WARPS * kMaxExperts + kMaxExperts + 1) * 4, attr)) return e;
-    kern<<<blocks, 32 * WARPS, bytes, s>>>(p);
+    if (cudaError_t e = host::ensure_smem(reinterpret_cast<const void*>(kern), (WARPS * (kMaxExperts + 1) + kMaxExperts + 1 + kRouteHeld) * 4, attr)) return e;
+    kern<<<blocks, 32 * warps, (warps * p.stride + p.r.experts + 1 + p.held) * 4, s>>>(p);
     return cudaGetLastError();
 }
+static int most_warps(int per_lane) { return per_lane <= 8 ? 32 : per_lane <= 16 ? 16 : 8; }
 template <typename T>
-static cudaError_t launch_choose(const RouteKernelParams& p, int blocks, cudaStream_t s) {
+static cudaError_t launch_choose(const RouteKernelParams& p, int blocks, int warps, cudaStream_t s) {
     const int v = p.per_lane;
-    if (v <= 1) return launch_choose<1, 32, T>(p, blocks, s);
-    if (v <= 2) return launch_choose<2, 32, T>(p, blocks, s);
-    if (v <= 4) return launch_choose<4, 32, T>(p, blocks, s);
-    if (v <= 8) return launch_choose<8, 32, T>(p, blocks, s);
-    if (v <= 16) return launch_choose<16, 16, T>(p, blocks, s);
-    return launch_choose<64, 8, T>(p, blocks, s);
+    if (v <= 1) return launch_choose<1, 32, T>(p, blocks, warps, s);
+    if (v <= 2) return launch_choose<2, 32, T>(p, blocks, warps, s);
+    if (v <= 4) return launch_choose<4, 32, T>(p, blocks, warps, s);
+    if (v <= 8) return launch_choose<8, 32, T>(p, blocks, warps, s);
+    if (v <= 16) return launch_choose<16, 16, T>(p, blocks, warps, s);
+    return launch_choose<64, 8, T>(p, blocks, warps, s);
 }
-
-constexpr int kAloneTokens = 256;   // tokens that one block takes by itself
 
 cudaError_t launch_route(const RouteProblem& r, cudaStream_t s) {
     RouteKernelParams p{};
     p.r = r;
     p.size = r.experts / r.groups;
-    int wide = 1;
-    while (wide < r.groups) wide <<= 1;
-    p.lanes = 32 / wide;
-    p.per_lane = (p.size + p.lanes - 1) / p.lanes;
+    p.lanes_log2 = 5;
+    while ((32 >> p.lanes_log2) < r.groups) --p.lanes_log2;
+    const int lanes = 1 << p.lanes_log2;
+    p.per_lane = (p.size + lanes - 1) / lanes;
     const int esz = r.bf16 ? 2 : 4;
     p.vec = p.per_lane * esz % 16 == 0 && p.size % p.per_lane == 0 && r.ld * esz % 16 == 0;
-    const int warps = p.per_lane <= 8 ? 32 : p.per_lane <= 16 ? 16 : 8;
-    int blocks = 1;
-    if (r.tokens > kAloneTokens) blocks = std::min(kRouteBlocks, (r.tokens + warps - 1) / warps);
+    int warps = most_warps(p.per_lane), blocks = 1;
+    // One block by itself as long as a warp takes one token: 16 tokens of 64 experts 4.8 us, 64 tokens 7.2, and 6.8 with two
+    // kernels; of 256 experts 6.5, 11.1 and 10.3.
+    if (r.tokens > warps) blocks = std::min(kRouteBlocks, (r.tokens + warps - 1) / warps);
+    else warps = std::max(1, r.tokens);
     p.block_tokens = std::max(1, (r.tokens + blocks - 1) / blocks);
     blocks = std::max(1, (r.tokens + p.block_tokens - 1) / p.block_tokens);
     p.warp_tokens = (p.block_tokens + warps - 1) / warps;
-    if (cudaError_t e = r.bf16 ? launch_choose<uint16_t>(p, blocks, s) : launch_choose<float>(p, blocks, s)) return e;
+    p.stride = r.experts | 1;
+    p.held = (int64_t)p.block_tokens * r.k <= kRouteHeld ? p.block_tokens * r.k : 0;
+    if (cudaError_t e = r.bf16 ? launch_choose<uint16_t>(p, blocks, warps, s) : launch_choose<float>(p, blocks, warps, s)) return e;
     if (blocks == 1) return cudaSuccess;
     cudaLaunchAttribute pdl{};
     pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
