@@ -930,7 +930,7 @@ class Routes:
                             ("weights_addr", self.weights.data_ptr()), ("experts_addr", self.experts.data_ptr()),
                             ("outputs", (self.experts.data_ptr(), self.weights.data_ptr(), self.rows.data_ptr(), self.sources.data_ptr(),
                                          self.offsets.data_ptr(), None if t is None else t.data_ptr())),
-                            ("scratch_bytes", 0 if t is None else t.numel()), ("args", CRouteArgs())):
+                            ("ready", t is not None and t.numel() >= _lib().nvfp4_route_scratch_bytes(count)), ("args", CRouteArgs())):
             object.__setattr__(self, name, value)
         object.__setattr__(self, "args_ref", ctypes.byref(self.args))
 
@@ -974,7 +974,7 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, bias: 
                 out = Routes.empty(tokens, experts, k, logits.device)
     elif out.tokens != tokens or out.k != k or out.count != experts:
         raise ValueError(f"out: Routes of {tokens} tokens, {experts} experts, k = {k}")
-    elif out.scratch_bytes < 592 * experts and out.scratch_bytes < _lib().nvfp4_route_scratch_bytes(experts):
+    elif not out.ready:
         raise ValueError("out: Routes without a scratch of nvfp4_route_scratch_bytes(experts) (Routes.empty has one)")
     dev = _CUR_DEVICE()
     if logits.get_device() != dev or out.index != dev:
@@ -1015,7 +1015,7 @@ def nvfp4_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, routes: Routes
     if logits.get_device() != dev or routes.index != dev or dweights.get_device() != dev or out.get_device() != dev:
         _elsewhere(dev, logits, routes.experts, dweights, out)
     raw = _raw_stream(dev, stream)
-    args = CRouteArgs(routes.k, score, 1, 1, 1, 1 if renormalize else 0, scale, 0)
+    args = CRouteArgs(routes.k, score, 1, 1, 1, 1 if renormalize else 0, scale, 0)   # not the routes' own: two calls may read them at once
     st = _lib().nvfp4_route_bwd(dweights.data_ptr(), logits.data_ptr(), dtype, ld, tokens, experts, ctypes.byref(args),
                                 routes.experts_addr, out.data_ptr(), ldd, raw)
     if st:

@@ -18,7 +18,7 @@
 
 namespace nvfp4 {
 
-constexpr int kMoveThreads = 128;
+constexpr int kMoveThreads = 128, kCombineThreads = 256;
 
 // How the 16-byte pieces (8 elements) of the token rows are dealt out: a block takes `pieces` pieces of one
 // token (grid.y cuts its row), or whole rows of `tokens` tokens.
@@ -36,6 +36,11 @@ __device__ __forceinline__ int64_t row_of(const TokenRows& m, int64_t choice) {
 __device__ __forceinline__ void widen(const uint4& v, float (&f)[8]) {
     f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
     f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ void widen(const uint4 (&v)[1], float (&f)[8]) { widen(v[0], f); }   // 8 elements as loaded: bf16
+__device__ __forceinline__ void widen(const uint4 (&v)[2], float (&f)[8]) {                      // or fp32
+    f[0] = __uint_as_float(v[0].x); f[1] = __uint_as_float(v[0].y); f[2] = __uint_as_float(v[0].z); f[3] = __uint_as_float(v[0].w);
+    f[4] = __uint_as_float(v[1].x); f[5] = __uint_as_float(v[1].y); f[6] = __uint_as_float(v[1].z); f[7] = __uint_as_float(v[1].w);
 }
 __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
     return make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]), f32x2_to_bf16x2(f[6], f[7]));
@@ -79,71 +84,134 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const TokenRows 
     }
 }
 
-template <bool YS32, bool Y32>
-__global__ void __launch_bounds__(kMoveThreads) combine_kernel(const Combine c, const MoveGrid g) {
+// A block takes a piece of one token's row (narrow rows: a row of threads for each of several tokens), so that the rows and
+// weights of its choices are looked up once; the loads of J choices and U pieces are issued
+// before the first is used.  8192 tokens x 2 x 5120, bf16 rows with a residual: 69 us (4.8 TB/s).
+template <int J, int U, bool YS32, bool Y32>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Combine c, int pieces) {
+    constexpr int Q = YS32 ? 2 : 1;
     const TokenRows& m = c.m;
-    const int64_t t0 = (int64_t)blockIdx.x * g.tokens;
-    const int v0 = blockIdx.y * g.pieces, width = min(g.pieces, g.vecs - v0);
-    const int tokens = (int)min((int64_t)g.tokens, m.tokens - t0);
-    for (int i = threadIdx.x; i < tokens * width; i += kMoveThreads) {
-        const int a = i / width, col = 8 * (v0 + i - a * width);
-        const int64_t t = t0 + a;
-        float y[8] = {};
-        if (c.residual) load8<Y32, true>(c.residual, t * c.ldr + col, y);
-        for (int j = 0; j < m.k; ++j) {
-            const int64_t r = row_of(m, t * m.k + j);
-            if (r < 0) continue;
-            const float w = m.weights ? __ldg(m.weights + t * m.k + j) : 1.0f;
-            float f[8];
-            load8<YS32>(c.ys, r * c.ldys + col, f);
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= m.tokens) return;
+    const int end = min((int)(blockIdx.y + 1) * pieces, (int)(m.d >> 3));
+    int64_t r[J];
+    float w[J];
+    const auto look_up = [&](int j0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = fmaf(w, f[e], y[e]);
+        for (int j = 0; j < J; ++j) {
+            const bool in = j0 + j < m.k;
+            r[j] = in ? row_of(m, t * m.k + j0 + j) : -1;
+            w[j] = in && m.weights ? __ldg(m.weights + t * m.k + j0 + j) : 1.0f;
         }
-        store8<Y32>(c.y, t * c.ldy + col, y);
+    };
+    look_up(0);
+    for (int v0 = blockIdx.y * pieces + threadIdx.x; v0 < end; v0 += U * blockDim.x) {
+        float y[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u * blockDim.x;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[u][e] = 0.0f;
+            if (c.residual && v < end) load8<Y32, true>(c.residual, t * c.ldr + 8 * v, y[u]);
+        }
+        for (int j0 = 0; j0 < m.k; j0 += J) {
+            if (m.k > J) look_up(j0);
+            uint4 f[U][J][Q];
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int v = v0 + u * blockDim.x;
+                    if (r[j] >= 0 && v < end) {
+                        const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(c.ys) + (r[j] * c.ldys + 8 * v) * (YS32 ? 4 : 2));
+#pragma unroll
+                        for (int h = 0; h < Q; ++h) f[u][j][h] = __ldg(q + h);
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (r[j] >= 0) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {   // past the end: what is in the registers, and is not stored
+                        float x[8];
+                        widen(f[u][j], x);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[u][e] = fmaf(w[j], x[e], y[u][e]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u * blockDim.x;
+            if (v < end) store8<Y32>(c.y, t * c.ldy + 8 * v, y[u]);
+        }
     }
 }
 
-// One block per token
-constexpr int kGradThreads = 128;
+// One block per token, as many threads as its row has pieces, up to 256 (narrow rows: up to 32 threads a token, several tokens a
+// block).  The loads of up to 8 choices' rows are issued before the first is used.
+constexpr int kGradThreads = 256;
 template <int KMAX, bool YS32>
 __global__ void __launch_bounds__(kGradThreads) combine_bwd_kernel(const CombineBwd c) {
+    constexpr int J = KMAX < 8 ? KMAX : 8, Q = YS32 ? 2 : 1;
     __shared__ float part[kGradThreads / 32][KMAX];
     const TokenRows& m = c.m;
-    const int64_t t = blockIdx.x;
-    const int vecs = (int)(m.d >> 3), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float dot[KMAX];
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool in = t < m.tokens;
+    const int vecs = (int)(m.d >> 3), lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    for (int j0 = 0; j0 < m.k; j0 += J) {
+        int64_t r[J];
+        float w[J], dot[J];
 #pragma unroll
-    for (int j = 0; j < KMAX; ++j) dot[j] = 0.0f;
-    for (int v = threadIdx.x; v < vecs; v += kGradThreads) {
-        float g[8];
-        load8<false>(c.dy, t * c.lddy + 8 * v, g);
+        for (int j = 0; j < J; ++j) {
+            const bool choice = in && j0 + j < m.k;
+            r[j] = choice ? row_of(m, t * m.k + j0 + j) : -1;
+            w[j] = choice ? __ldg(m.weights + t * m.k + j0 + j) : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (int v = threadIdx.x; v < vecs && in; v += blockDim.x) {
+            const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(c.dy + t * c.lddy) + v);
+            uint4 f[J][Q];
 #pragma unroll
-        for (int j = 0; j < KMAX; ++j) {
-            const int64_t r = j < m.k ? row_of(m, t * m.k + j) : -1;
-            if (r < 0) continue;
-            const float w = __ldg(m.weights + t * m.k + j);
-            float f[8], o[8];
-            load8<YS32>(c.ys, r * c.ldys + 8 * v, f);
+            for (int j = 0; j < J; ++j)
+                if (r[j] >= 0) {
+                    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(c.ys) + (r[j] * c.ldys + 8 * v) * (YS32 ? 4 : 2));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dot[j] = fmaf(g[e], f[e], dot[j]);
-                o[e] = w * g[e];
+                    for (int h = 0; h < Q; ++h) f[j][h] = __ldg(q + h);
+                }
+            float g[8];
+            widen(g4, g);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (r[j] >= 0) {
+                    float x[8], o[8];
+                    widen(f[j], x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dot[j] = fmaf(g[e], x[e], dot[j]);
+                        o[e] = w[j] * g[e];
+                    }
+                    store8<false>(c.dys, r[j] * c.lddys + 8 * v, o);
+                }
+        }
+        __syncwarp();
+        const int span = min((int)blockDim.x, 32);   // lanes of a token in a warp, a power of two
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (j0 + j >= m.k) break;
+            for (int o = span >> 1; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
+            if (blockDim.x <= 32) {
+                if (threadIdx.x == 0 && in) c.dweights[t * m.k + j0 + j] = dot[j];
+            } else if (lane == 0) {
+                part[warp][j0 + j] = dot[j];
             }
-            store8<false>(c.dys, r * c.lddys + 8 * v, o);
         }
     }
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-        if (j >= m.k) break;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
-        if (lane == 0) part[warp][j] = dot[j];
-    }
+    if (blockDim.x <= 32) return;
     __syncthreads();
     if (threadIdx.x < m.k) {
         float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kGradThreads / 32; ++w) s += part[w][threadIdx.x];
+        for (int i = 0; i < warps; ++i) s += part[i][threadIdx.x];
         c.dweights[t * m.k + threadIdx.x] = s;
     }
 }
@@ -174,23 +242,50 @@ cudaError_t launch_dispatch(const TokenRows& m, const uint16_t* x, int64_t ldx, 
     return cudaGetLastError();
 }
 
-cudaError_t launch_combine(const Combine& c, cudaStream_t s) {
-    MoveGrid g;
-    const dim3 grid = move_grid(c.m, g);
-    if (c.ys_fp32) {
-        if (c.y_fp32) combine_kernel<true, true><<<grid, kMoveThreads, 0, s>>>(c, g);
-        else combine_kernel<true, false><<<grid, kMoveThreads, 0, s>>>(c, g);
-    } else {
-        if (c.y_fp32) combine_kernel<false, true><<<grid, kMoveThreads, 0, s>>>(c, g);
-        else combine_kernel<false, false><<<grid, kMoveThreads, 0, s>>>(c, g);
+// Threads for `vecs` pieces: as even a cut into rounds of at most `most` threads as warps allow; up to 32 pieces a power of two
+// of threads, and as many tokens as make 128
+static dim3 even_threads(int vecs, int most) {
+    if (vecs <= 32) {
+        unsigned x = 1;
+        while ((int)x < vecs) x <<= 1;
+        return dim3(x, 128 / x);
     }
+    const int rounds = (vecs + most - 1) / most, each = (vecs + rounds - 1) / rounds;
+    return dim3((unsigned)((each + 31) / 32 * 32));
+}
+template <int J>
+static void launch_combine(const Combine& c, cudaStream_t s) {
+    const int vecs = (int)(c.m.d / 8);
+    // few tokens: their rows cut over blocks, a piece a thread
+    const int64_t want = (8 * host::sm_count() + c.m.tokens - 1) / c.m.tokens;
+    const int cuts = (int)std::max<int64_t>(1, std::min<int64_t>((vecs + 127) / 128, want));
+    const int pieces = (vecs + cuts - 1) / cuts;
+    const bool two = !c.ys_fp32 && pieces > 128;   // pieces a thread at a time
+    const dim3 threads = even_threads(two ? (pieces + 1) / 2 : pieces, kCombineThreads);
+    const dim3 grid((unsigned)((c.m.tokens + threads.y - 1) / threads.y), (unsigned)((vecs + pieces - 1) / pieces));
+    if (c.ys_fp32) {
+        if (c.y_fp32) combine_kernel<J, 1, true, true><<<grid, threads, 0, s>>>(c, pieces);
+        else combine_kernel<J, 1, true, false><<<grid, threads, 0, s>>>(c, pieces);
+    } else if (two) {
+        if (c.y_fp32) combine_kernel<J, 2, false, true><<<grid, threads, 0, s>>>(c, pieces);
+        else combine_kernel<J, 2, false, false><<<grid, threads, 0, s>>>(c, pieces);
+    } else {
+        if (c.y_fp32) combine_kernel<J, 1, false, true><<<grid, threads, 0, s>>>(c, pieces);
+        else combine_kernel<J, 1, false, false><<<grid, threads, 0, s>>>(c, pieces);
+    }
+}
+cudaError_t launch_combine(const Combine& c, cudaStream_t s) {
+    if (c.m.k <= 2) launch_combine<2>(c, s);
+    else launch_combine<4>(c, s);
     return cudaGetLastError();
 }
 
 template <int KMAX>
 static void launch_combine_bwd(const CombineBwd& c, cudaStream_t s) {
-    if (c.ys_fp32) combine_bwd_kernel<KMAX, true><<<(unsigned)c.m.tokens, kGradThreads, 0, s>>>(c);
-    else combine_bwd_kernel<KMAX, false><<<(unsigned)c.m.tokens, kGradThreads, 0, s>>>(c);
+    const dim3 threads = even_threads((int)(c.m.d / 8), kGradThreads);   // more than 32, the bound of k, or several tokens
+    const unsigned blocks = (unsigned)((c.m.tokens + threads.y - 1) / threads.y);
+    if (c.ys_fp32) combine_bwd_kernel<KMAX, true><<<blocks, threads, 0, s>>>(c);
+    else combine_bwd_kernel<KMAX, false><<<blocks, threads, 0, s>>>(c);
 }
 cudaError_t launch_combine_bwd(const CombineBwd& c, cudaStream_t s) {
     const int k = c.m.k;
