@@ -188,3 +188,70 @@ def test_no_tokens():
     assert m.nvfp4_dispatch(e, r).shape == (0, 16) and m.nvfp4_combine(e, r).shape == (0, 16)
     dys, dw = m.nvfp4_combine_bwd(e, e, r)
     assert dys.shape == (0, 16) and dw.shape == (0, 2)
+
+
+# (24 MB and more for combine, 16 for its gradient: warps that stay, where a call of 400 tokens goes by blocks)
+LARGE = [(2100, 2, 2056), (13003, 1, 520), (4001, 4, 1288), (2900, 3, 1032), (2300, 2, 2816), (601, 2, 10504)]
+
+
+@pytest.mark.parametrize("padded", [0.0, 0.25])
+@pytest.mark.parametrize("size", LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_combine_of_many_tokens(size, padded):
+    """Many tokens against 64 bits and, bit for bit, against the same tokens a few hundred at a time."""
+    m = nv()
+    T, k, d = size
+    r = _routes(T, 40, k, T, padded)
+    rc = _cuda(r)
+    live = int(r.offsets[-1])
+    wide = torch.full((T * k, d + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:live, :d] = _rand((live, d), 2).cuda()
+    ys = wide[:, :d]
+    for dtype in (torch.bfloat16, torch.float32):
+        residual = _rand((T, d), 3, dtype).cuda()
+        for res, weighted in ((residual, True), (None, False)):
+            terms = torch.zeros(T, d, dtype=torch.float64, device="cuda") if res is None else res.double()
+            size_ = terms.abs()
+            for j in range(k):
+                held = rc.rows[:, j] >= 0
+                term = torch.where(held[:, None], ys[rc.rows[:, j].clamp(min=0).long()].double(), 0.0)
+                term = term * rc.weights[:, j, None].double() if weighted else term
+                terms, size_ = terms + term, size_ + term.abs()
+            back = torch.full((T, d + 8), 7.0, dtype=dtype, device="cuda")
+            y = m.nvfp4_combine(ys, rc, residual=res, out=back[:, :d], weighted=weighted)
+            assert (back[:, d:] == 7).all()
+            tol = _gamma(k + 1) * size_ + _half(dtype) * (terms.abs() + _gamma(k + 1) * size_) + 2.0 ** -130
+            assert ((y.double() - terms).abs() <= tol).all()
+            for t in range(0, T, 400):
+                part = [v[t:t + 400].contiguous() for v in (rc.experts, rc.weights, rc.rows)]
+                part = m.Routes(*part, rc.sources[:part[0].numel()], rc.offsets)
+                few = m.nvfp4_combine(ys, part, residual=None if res is None else res[t:t + 400], out_dtype=dtype, weighted=weighted)
+                assert torch.equal(few, y[t:t + 400])
+            if res is not None:
+                held = res.clone()
+                assert torch.equal(m.nvfp4_combine(ys, rc, residual=held, out=held), y)
+
+
+@pytest.mark.parametrize("padded", [0.0, 0.25])
+@pytest.mark.parametrize("size", LARGE + [(530, 8, 1032), (900, 5, 2064)], ids=lambda s: "x".join(map(str, s)))
+def test_combine_gradient_of_many_tokens(size, padded):
+    m = nv()
+    T, k, d = size
+    r = _routes(T, 40, k, T, padded)
+    rc = _cuda(r)
+    live = int(r.offsets[-1])
+    ys = torch.full((T * k, d + 8), float("nan"), dtype=torch.bfloat16, device="cuda")[:, :d]
+    ys[:live] = _rand((live, d), 4).cuda()
+    dy = torch.zeros(T, d + 16, dtype=torch.bfloat16, device="cuda")[:, :d]
+    dy.copy_(_rand((T, d), 5))
+    dys = torch.full((T * k, d + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((T, k), 7.0, device="cuda")
+    m.nvfp4_combine_bwd(dy, ys, rc, dys=dys[:, :d], dweights=dw)
+    assert (dys[live:] == 7).all() and (dys[:, d:] == 7).all() and (dw[rc.rows < 0] == 0).all()
+    choice = rc.sources[:live].long()
+    want = rc.weights.double().view(-1)[choice][:, None] * dy.double()[choice // k]
+    assert ((dys[:live, :d].double() - want).abs() <= 2.0 ** -8 * (1 + 2.0 ** -8) * want.abs() + 2.0 ** -130).all()
+    products = dy.double()[choice // k] * ys[:live].double()
+    assert ((dw.double().view(-1)[choice] - products.sum(1)).abs() <= _gamma(d) * products.abs().sum(1) + 2.0 ** -130).all()
+    again = torch.full((T * k, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.empty(T, k, device="cuda")
+    m.nvfp4_combine_bwd(dy, ys, rc, dys=again[0], dweights=again[1])
+    assert torch.equal(again[0][:live], dys[:live, :d]) and torch.equal(again[1], dw)
