@@ -802,7 +802,7 @@ nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b,
 }
 
 size_t nvfp4_route_scratch_bytes(int experts) {
-    return experts >= 1 && experts <= kMaxExperts ? (size_t)kRouteBlocks * experts * sizeof(int32_t) : 0;
+    return experts >= 1 && experts <= kMaxExperts ? (size_t)kRouteBlocks * route_count_stride(experts) * sizeof(int32_t) : 0;
 }
 
 static bool is_dtype(nvfp4_dtype t) { return t == NVFP4_OUT_BF16 || t == NVFP4_OUT_FP32; }

@@ -157,6 +157,7 @@ cudaError_t launch_wgrad_grouped(const GroupedWgrad& g, cudaStream_t s);
 // Routing of tokens to experts (the arguments of nvfp4_route, checked)
 constexpr int kRouteMaxK = 32, kRouteMaxGroups = 32;
 constexpr int kRouteBlocks = 148;   // counts [blocks][experts] of the scratch
+__host__ __device__ constexpr int route_count_stride(int experts) { return (experts + 3) & ~3; }   // of a block's, read four at a time
 struct RouteProblem {
     const void* logits;
     int64_t ld;

@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(32 * WARPS) route_choose_kernel(const __grid_c
             before += c;
         }
         if (alone) base[e] = before;
-        else p.r.scratch[(int64_t)blockIdx.x * E + e] = before;
+        else p.r.scratch[blockIdx.x * route_count_stride(E) + e] = before;
     }
     __syncthreads();
     if (alone) {
@@ -519,22 +519,29 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteK
     const int64_t c0 = (int64_t)t0 * k + threadIdx.x, c1 = (int64_t)t1 * k;
     // the block's first choices are on their way during the sums
     const int chosen0 = c0 < c1 ? __ldcg(p.r.chosen + c0) : -1, rank0 = c0 < c1 ? __ldcg(p.r.rows + c0) : 0;
-    int wide = 32, shift = 5;
-    while (wide < E) {
+    // four experts of every parts-th block a thread
+    int wide = 8, shift = 3;
+    while (4 * wide < E) {
         wide <<= 1;
         ++shift;
     }
-    const int e = threadIdx.x & (wide - 1), parts = kPlaceThreads >> shift;
+    const int e = 4 * (threadIdx.x & (wide - 1)), parts = kPlaceThreads >> shift;
     if (e < E) {
-        int all = 0, prior = 0;
-#pragma unroll 20
+        int4 all = make_int4(0, 0, 0, 0), prior = all;
+#pragma unroll 10
         for (int b = threadIdx.x >> shift; b < blocks; b += parts) {
-            const int c = __ldcg(p.r.scratch + b * E + e);
-            all += c;
-            prior += b < (int)blockIdx.x ? c : 0;
+            const int4 c = __ldcg(reinterpret_cast<const int4*>(p.r.scratch + b * route_count_stride(E) + e));
+            const int m = b < (int)blockIdx.x ? -1 : 0;
+            all.x += c.x; all.y += c.y; all.z += c.z; all.w += c.w;
+            prior.x += c.x & m; prior.y += c.y & m; prior.z += c.z & m; prior.w += c.w & m;
         }
-        atomicAdd(&total[e], all);     // whole numbers: no order to depend on
-        atomicAdd(&before[e], prior);
+        const int a4[4] = {all.x, all.y, all.z, all.w}, p4[4] = {prior.x, prior.y, prior.z, prior.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (e + i >= E) break;            // what a row of counts has behind the last expert is nobody's
+            atomicAdd(&total[e + i], a4[i]);  // whole numbers: no order to depend on
+            atomicAdd(&before[e + i], p4[i]);
+        }
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -656,14 +663,15 @@ static cudaError_t launch_choose(const RouteKernelParams& p, int blocks, int war
     kern<<<blocks, 32 * warps, (warps * p.stride + p.r.experts + 1 + p.held) * 4, s>>>(p);
     return cudaGetLastError();
 }
-static int most_warps(int per_lane) { return per_lane <= 8 ? 32 : per_lane <= 16 ? 16 : 8; }
+// 28 of 8 experts a lane: 72 registers and no more rounds for 16384 tokens (softmax, 256 experts: 20.5 us, with 32 21.6, with 24 21.7)
+static int most_warps(int per_lane) { return per_lane <= 4 ? 32 : per_lane <= 8 ? 28 : per_lane <= 16 ? 16 : 8; }
 template <typename T>
 static cudaError_t launch_choose(const RouteKernelParams& p, int blocks, int warps, cudaStream_t s) {
     const int v = p.per_lane;
     if (v <= 1) return launch_choose<1, 32, T>(p, blocks, warps, s);
     if (v <= 2) return launch_choose<2, 32, T>(p, blocks, warps, s);
     if (v <= 4) return launch_choose<4, 32, T>(p, blocks, warps, s);
-    if (v <= 8) return launch_choose<8, 32, T>(p, blocks, warps, s);
+    if (v <= 8) return launch_choose<8, 28, T>(p, blocks, warps, s);
     if (v <= 16) return launch_choose<16, 16, T>(p, blocks, warps, s);
     return launch_choose<64, 8, T>(p, blocks, warps, s);
 }
@@ -679,11 +687,13 @@ cudaError_t launch_route(const RouteProblem& r, cudaStream_t s) {
     const int esz = r.bf16 ? 2 : 4;
     p.vec = p.per_lane * esz % 16 == 0 && p.size % p.per_lane == 0 && r.ld * esz % 16 == 0;
     int warps = most_warps(p.per_lane), blocks = 1;
-    // One block by itself as long as a warp takes one token: 16 tokens of 64 experts 4.8 us, 64 tokens 7.2, and 6.8 with two
-    // kernels; of 256 experts 6.5, 11.1 and 10.3.
-    if (r.tokens > warps) blocks = std::min(kRouteBlocks, (r.tokens + warps - 1) / warps);
-    else warps = std::max(1, r.tokens);
+    // One block by itself as long as a warp takes one token: 28 tokens of 256 experts 7.3 us, 40 by two kernels 7.2; 8 tokens 5.3 and
+    // 8.0.  More tokens go over as many blocks as leave each 8 (of 512 experts and more: a token for each of its warps), since joining the
+    // warps' counts is what a block of few tokens spends its time on: 300 tokens of 256 experts by blocks of 28 9.9 us, of 8 7.8.
+    const int least = p.per_lane <= 8 ? 8 : warps;
+    if (r.tokens > warps) blocks = std::min(kRouteBlocks, (r.tokens + least - 1) / least);
     p.block_tokens = std::max(1, (r.tokens + blocks - 1) / blocks);
+    warps = std::min(warps, p.block_tokens);
     blocks = std::max(1, (r.tokens + p.block_tokens - 1) / p.block_tokens);
     p.warp_tokens = (p.block_tokens + warps - 1) / warps;
     p.stride = r.experts | 1;
