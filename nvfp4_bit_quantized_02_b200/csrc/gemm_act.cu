@@ -825,73 +825,79 @@ __device__ __forceinline__ void gf_mma(float (&c)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NG: groups of 8 rows in one pass over the weights; with more rows there are more passes (their weights then come from L2)
+// the products of one chunk's fragments with the rows' own at k: `x` is row g of the first group
+template <int NG>
+__device__ __forceinline__ void gf_chunk(const GemmActFewParams& p, float (&acc)[NG][4], const uint16_t* x, int k, int g, bool in0, bool in1,
+                                         const uint4& a00, const uint4& a01, const uint4& a10, const uint4& a11) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+        const bool row = 8 * i + g < p.e.M;
+        const uint16_t* xi = x + (int64_t)(8 * i) * p.lda + k;
+        const uint4 b0 = row && in0 ? __ldg(reinterpret_cast<const uint4*>(xi)) : zero;
+        const uint4 b1 = row && in1 ? __ldg(reinterpret_cast<const uint4*>(xi + 32)) : zero;
+        gf_mma(acc[i], a00.x, a10.x, a00.y, a10.y, b0.x, b0.y);
+        gf_mma(acc[i], a00.z, a10.z, a00.w, a10.w, b0.z, b0.w);
+        gf_mma(acc[i], a01.x, a11.x, a01.y, a11.y, b1.x, b1.y);
+        gf_mma(acc[i], a01.z, a11.z, a01.w, a11.w, b1.z, b1.w);
+    }
+}
+// the warps' sums (part[warp][row][feature], padded) joined, and the outputs of 16 features from f0 on
+template <int NG, int WARPS>
+__device__ __forceinline__ void gf_finish(const GemmActParams& e, const float (&part)[WARPS][NG * 8][17], int f0) {
+    for (int i = threadIdx.x; i < 16 * e.M; i += 32 * WARPS) {
+        const int f = f0 + (i & 15), row = i >> 4;
+        if (f >= e.N) continue;
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) s += part[w][row][i & 15];
+        if (e.bias) s += e.bias[f];
+        if (e.pre) e.pre[(int64_t)row * e.ldpre + f] = (uint16_t)f32x2_to_bf16x2(s, 0.0f);
+        s = act::one(e.act, s);
+        if (e.residual) {
+            const int64_t at = (int64_t)row * e.ldr + f;
+            s += e.res_fp32 ? reinterpret_cast<const float*>(e.residual)[at]
+                            : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(e.residual)[at] << 16);
+        }
+        const int64_t at = (int64_t)row * e.ldd + f;
+        if (e.out_fp32) reinterpret_cast<float*>(e.d)[at] = s;
+        else reinterpret_cast<uint16_t*>(e.d)[at] = (uint16_t)f32x2_to_bf16x2(s, 0.0f);
+    }
+}
+
+// NG: groups of 8 rows
 template <int NG, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) gemm_act_few_kernel(const GemmActFewParams p) {
-    __shared__ float part[WARPS][NG * 8][17];   // [warp][row][feature], padded
+    __shared__ float part[WARPS][NG * 8][17];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int f0 = blockIdx.x * 16, N = p.e.N;
     // features past the end read the last one
     const uint16_t* w0 = p.b + (int64_t)min(f0 + g, N - 1) * p.ldb + 8 * t;
     const uint16_t* w1 = p.b + (int64_t)min(f0 + g + 8, N - 1) * p.ldb + 8 * t;
+    const uint16_t* x = p.a + (int64_t)g * p.lda + 8 * t;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int lo = 0; lo < p.e.M; lo += 8 * NG) {
-        const int rows = min(8 * NG, p.e.M - lo), groups = (rows + 7) >> 3;
-        const uint16_t* x = p.a + (int64_t)(lo + g) * p.lda + 8 * t;   // row g of each group
-        // runs of kGfRun products, joined in the warp's own part of shared memory (registers are full)
+    // runs of kGfRun products, joined in the warp's own part of shared memory (registers are full)
 #pragma unroll 1
-        for (int k = 64 * warp, run = 0; run == 0 || k < p.K; ++run) {
-            const int end = min(p.K, k + kGfRun * WARPS);
-            float acc[NG][4] = {};
+    for (int k = 64 * warp, run = 0; run == 0 || k < p.K; ++run) {
+        const int end = min(p.K, k + kGfRun * WARPS);
+        float acc[NG][4] = {};
 #pragma unroll 1
-            for (; k < end; k += 64 * WARPS) {
-                const bool in0 = k + 8 * t < p.K, in1 = k + 32 + 8 * t < p.K;
-                const uint4 a00 = in0 ? gf_stream(w0 + k) : zero, a01 = in1 ? gf_stream(w0 + k + 32) : zero;
-                const uint4 a10 = in0 ? gf_stream(w1 + k) : zero, a11 = in1 ? gf_stream(w1 + k + 32) : zero;
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    if (i >= groups) break;
-                    const bool row = 8 * i + g < rows;
-                    const uint16_t* xi = x + (int64_t)(8 * i) * p.lda + k;
-                    const uint4 b0 = row && in0 ? __ldg(reinterpret_cast<const uint4*>(xi)) : zero;
-                    const uint4 b1 = row && in1 ? __ldg(reinterpret_cast<const uint4*>(xi + 32)) : zero;
-                    gf_mma(acc[i], a00.x, a10.x, a00.y, a10.y, b0.x, b0.y);
-                    gf_mma(acc[i], a00.z, a10.z, a00.w, a10.w, b0.z, b0.w);
-                    gf_mma(acc[i], a01.x, a11.x, a01.y, a11.y, b1.x, b1.y);
-                    gf_mma(acc[i], a01.z, a11.z, a01.w, a11.w, b1.z, b1.w);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                if (i >= groups) break;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float& s = part[warp][8 * i + 2 * t + (j & 1)][g + 4 * (j & 2)];
-                    s = run == 0 ? acc[i][j] : s + acc[i][j];
-                }
-            }
+        for (; k < end; k += 64 * WARPS) {
+            const bool in0 = k + 8 * t < p.K, in1 = k + 32 + 8 * t < p.K;
+            const uint4 a00 = in0 ? gf_stream(w0 + k) : zero, a01 = in1 ? gf_stream(w0 + k + 32) : zero;
+            const uint4 a10 = in0 ? gf_stream(w1 + k) : zero, a11 = in1 ? gf_stream(w1 + k + 32) : zero;
+            gf_chunk<NG>(p, acc, x, k, g, in0, in1, a00, a01, a10, a11);
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 16 * rows; i += 32 * WARPS) {
-            const int f = f0 + (i & 15), r = i >> 4, row = lo + r;
-            if (f >= N) continue;
-            float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) s += part[w][r][i & 15];
-            if (p.e.bias) s += p.e.bias[f];
-            if (p.e.pre) p.e.pre[(int64_t)row * p.e.ldpre + f] = (uint16_t)f32x2_to_bf16x2(s, 0.0f);
-            s = act::one(p.e.act, s);
-            if (p.e.residual) {
-                const int64_t at = (int64_t)row * p.e.ldr + f;
-                s += p.e.res_fp32 ? reinterpret_cast<const float*>(p.e.residual)[at]
-                                  : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p.e.residual)[at] << 16);
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float& s = part[warp][8 * i + 2 * t + (j & 1)][g + 4 * (j & 2)];
+                s = run == 0 ? acc[i][j] : s + acc[i][j];
             }
-            const int64_t at = (int64_t)row * p.e.ldd + f;
-            if (p.e.out_fp32) reinterpret_cast<float*>(p.e.d)[at] = s;
-            else reinterpret_cast<uint16_t*>(p.e.d)[at] = (uint16_t)f32x2_to_bf16x2(s, 0.0f);
-        }
-        __syncthreads();   // the next pass writes `part` again
     }
+    __syncthreads();
+    gf_finish<NG, WARPS>(p.e, part, f0);
 }
 
 // ---------------------------------------------------------------------------------------

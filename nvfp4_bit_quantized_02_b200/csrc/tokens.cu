@@ -227,17 +227,6 @@ __global__ void __launch_bounds__(kGradThreads) combine_bwd_kernel(const Combine
 // ---------------------------------------------------------------------------------------
 constexpr int kRing = 4, kRingWarps = 4;
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory"); }
-__device__ __forceinline__ uint4 take16(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-    return v;
-}
-
 struct RingGrid {
     int32_t rounds;        // of 32 pieces, of a unit
     int32_t cuts;          // units of a token
@@ -299,17 +288,17 @@ __global__ void __launch_bounds__(32 * kRingWarps) combine_ring_kernel(const Com
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (j < k) {
-                    if (r[j] >= 0) copy16(to, ys + (int64_t)r[j] * c.ldys + 8 * v);
+                    if (r[j] >= 0) ptx::copy16(to, ys + (int64_t)r[j] * c.ldys + 8 * v);
                     to += kSlot;
                 }
             }
             if (c.residual) {
                 const uint8_t* from = reinterpret_cast<const uint8_t*>(c.residual) + (in.t * c.ldr + 8 * v) * (Y32 ? 4 : 2);
 #pragma unroll
-                for (int q = 0; q < R; ++q) copy16(to + q * kSlot, from + 16 * q);
+                for (int q = 0; q < R; ++q) ptx::copy16(to + q * kSlot, from + 16 * q);
             }
         }
-        copies_end();
+        ptx::copies_end();
         if (++in.round == g.rounds) {
             in.round = 0;
             advance(in.t, in.cut);
@@ -325,7 +314,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) combine_ring_kernel(const Com
     weights(follow(out, used_next), w_next);
     for (int s = 0; out.t < m.tokens; s = s + 1 == kRing ? 0 : s + 1) {
         ask(s == 0 ? kRing - 1 : s - 1);
-        copies_wait();
+        ptx::copies_wait<kRing - 1>();
         const int v = (out.cut * g.rounds + out.round) * 32 + lane;
         if (v < vecs) {
             uint32_t at = own + s * stage;
@@ -333,13 +322,13 @@ __global__ void __launch_bounds__(32 * kRingWarps) combine_ring_kernel(const Com
             if (c.residual) {
                 uint4 f[R];
 #pragma unroll
-                for (int q = 0; q < R; ++q) f[q] = take16(at + (k + q) * kSlot);
+                for (int q = 0; q < R; ++q) f[q] = ptx::take16(at + (k + q) * kSlot);
                 widen(f, y);
             }
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (used[j] >= 0) {
-                    widen(take16(at + j * kSlot), x);
+                    widen(ptx::take16(at + j * kSlot), x);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] = fmaf(w[j], x[e], y[e]);
                 }
@@ -386,13 +375,13 @@ __global__ void __launch_bounds__(256) combine_bwd_ring_kernel(const CombineBwd 
         const int v = in_round * (int)blockDim.x + (int)threadIdx.x;
         if (in < m.tokens && v < vecs) {
             uint32_t to = own + s * stage;
-            copy16(to, c.dy + in * c.lddy + 8 * v);
+            ptx::copy16(to, c.dy + in * c.lddy + 8 * v);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                if (r[j] >= 0) copy16(to + (1 + j) * slot, ys + (int64_t)r[j] * c.ldys + 8 * v);
+                if (r[j] >= 0) ptx::copy16(to + (1 + j) * slot, ys + (int64_t)r[j] * c.ldys + 8 * v);
             }
         }
-        copies_end();
+        ptx::copies_end();
         if (++in_round == rounds) {
             in_round = 0;
             in += gridDim.x;
@@ -409,17 +398,17 @@ __global__ void __launch_bounds__(256) combine_bwd_ring_kernel(const CombineBwd 
     weights(out + gridDim.x, w_next);
     for (int s = 0; out < m.tokens; s = s + 1 == kRing ? 0 : s + 1) {
         ask(s == 0 ? kRing - 1 : s - 1);
-        copies_wait();
+        ptx::copies_wait<kRing - 1>();
         const int v = round * (int)blockDim.x + (int)threadIdx.x;
         if (v < vecs) {
             const uint32_t at = own + s * stage;
             float g[8];
-            widen(take16(at), g);
+            widen(ptx::take16(at), g);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (used[j] >= 0) {
                     float x[8], o[8];
-                    widen(take16(at + (1 + j) * slot), x);
+                    widen(ptx::take16(at + (1 + j) * slot), x);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         dot[j] = fmaf(g[e], x[e], dot[j]);
