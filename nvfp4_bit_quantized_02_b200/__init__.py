@@ -926,13 +926,9 @@ class Routes:
         if t is not None and (t.dtype is not torch.uint8 or not t.is_contiguous() or t.get_device() != index):
             raise ValueError("scratch: contiguous uint8 on the same device")
         # the fields do not change, so neither do these
-        for name, value in (("tokens", shape[0]), ("k", shape[1]), ("count", count), ("index", index), ("rows_addr", self.rows.data_ptr()),
-                            ("weights_addr", self.weights.data_ptr()), ("experts_addr", self.experts.data_ptr()),
-                            ("outputs", (self.experts.data_ptr(), self.weights.data_ptr(), self.rows.data_ptr(), self.sources.data_ptr(),
-                                         self.offsets.data_ptr(), None if t is None else t.data_ptr())),
-                            ("ready", t is not None and t.numel() >= _lib().nvfp4_route_scratch_bytes(count)), ("args", CRouteArgs())):
+        for name, value in (("tokens", shape[0]), ("k", shape[1]), ("count", count), ("index", index),
+                            ("ready", t is not None and t.numel() >= _lib().nvfp4_route_scratch_bytes(count))):
             object.__setattr__(self, name, value)
-        object.__setattr__(self, "args_ref", ctypes.byref(self.args))
 
     @staticmethod
     def empty(tokens: int, experts: int, k: int, device=None) -> "Routes":
@@ -989,9 +985,10 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = SCORE_SOFTMAX, bias: 
             raise ValueError("valid: contiguous bool [tokens] on the logits' device")
         valid_addr = valid.data_ptr()
     ws_addr, raw = _call_context(dev, ws, stream)
-    a = out.args
-    a.k, a.score, a.groups, a.top_groups, a.group_top, a.renormalize, a.scale = k, score, groups, top_groups, group_top, renormalize, scale
-    st = _lib().nvfp4_route(logits.data_ptr(), dtype, ld, tokens, experts, out.args_ref, bias_addr, valid_addr, *out.outputs, ws_addr, raw)
+    args = CRouteArgs(k, score, groups, top_groups, group_top, renormalize, scale, 0)
+    st = _lib().nvfp4_route(logits.data_ptr(), dtype, ld, tokens, experts, ctypes.byref(args), bias_addr, valid_addr,
+                            out.experts.data_ptr(), out.weights.data_ptr(), out.rows.data_ptr(), out.sources.data_ptr(),
+                            out.offsets.data_ptr(), out.scratch.data_ptr(), ws_addr, raw)
     if st:
         _check(st, "nvfp4_route")
     return out
@@ -1015,9 +1012,9 @@ def nvfp4_route_bwd(dweights: torch.Tensor, logits: torch.Tensor, routes: Routes
     if logits.get_device() != dev or routes.index != dev or dweights.get_device() != dev or out.get_device() != dev:
         _elsewhere(dev, logits, routes.experts, dweights, out)
     raw = _raw_stream(dev, stream)
-    args = CRouteArgs(routes.k, score, 1, 1, 1, 1 if renormalize else 0, scale, 0)   # not the routes' own: two calls may read them at once
+    args = CRouteArgs(routes.k, score, 1, 1, 1, renormalize, scale, 0)
     st = _lib().nvfp4_route_bwd(dweights.data_ptr(), logits.data_ptr(), dtype, ld, tokens, experts, ctypes.byref(args),
-                                routes.experts_addr, out.data_ptr(), ldd, raw)
+                                routes.experts.data_ptr(), out.data_ptr(), ldd, raw)
     if st:
         _check(st, "nvfp4_route_bwd")
     return out
@@ -1041,7 +1038,7 @@ def nvfp4_dispatch(x: torch.Tensor, routes: Routes, out: torch.Tensor | None = N
     if x.get_device() != dev or routes.index != dev or out.get_device() != dev:
         _elsewhere(dev, x, routes.rows, out)
     raw = _raw_stream(dev, stream)
-    st = _lib().nvfp4_dispatch(x.data_ptr(), ldx, tokens, d, routes.rows_addr, routes.k, out.data_ptr(), ldo, out.shape[0], raw)
+    st = _lib().nvfp4_dispatch(x.data_ptr(), ldx, tokens, d, routes.rows.data_ptr(), routes.k, out.data_ptr(), ldo, out.shape[0], raw)
     if st:
         _check(st, "nvfp4_dispatch")
     return out
@@ -1076,8 +1073,8 @@ def nvfp4_combine(ys: torch.Tensor, routes: Routes, residual: torch.Tensor | Non
     if ys.get_device() != dev or routes.index != dev or out.get_device() != dev:
         _elsewhere(dev, ys, routes.rows, out)
     raw = _raw_stream(dev, stream)
-    st = _lib().nvfp4_combine(ys.data_ptr(), ldys, OUT_FP32 if ys.dtype is torch.float32 else OUT_BF16, total, routes.rows_addr,
-                              routes.weights_addr if weighted else None, routes.k,
+    st = _lib().nvfp4_combine(ys.data_ptr(), ldys, OUT_FP32 if ys.dtype is torch.float32 else OUT_BF16, total, routes.rows.data_ptr(),
+                              routes.weights.data_ptr() if weighted else None, routes.k,
                               residual.data_ptr() if residual is not None else None, ldr, out.data_ptr(), ldo,
                               OUT_FP32 if out.dtype is torch.float32 else OUT_BF16, tokens, d, raw)
     if st:
@@ -1110,7 +1107,7 @@ def nvfp4_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, routes: Routes, dys: t
         _elsewhere(dev, dy, ys, routes.rows, dys, dweights)
     raw = _raw_stream(dev, stream)
     st = _lib().nvfp4_combine_bwd(dy.data_ptr(), lddy, ys.data_ptr(), ldys, OUT_FP32 if ys.dtype is torch.float32 else OUT_BF16, total,
-                                  routes.rows_addr, routes.weights_addr, routes.k, dys.data_ptr(), lddys,
+                                  routes.rows.data_ptr(), routes.weights.data_ptr(), routes.k, dys.data_ptr(), lddys,
                                   dweights.data_ptr(), tokens, d, raw)
     if st:
         _check(st, "nvfp4_combine_bwd")
