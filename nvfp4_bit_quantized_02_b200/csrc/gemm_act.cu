@@ -865,9 +865,9 @@ __device__ __forceinline__ void gf_finish(const GemmActParams& e, const float (&
     }
 }
 
-// NG: groups of 8 rows
-template <int NG, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) gemm_act_few_kernel(const GemmActFewParams p) {
+// NG: groups of 8 rows; PER_SM: CTAs of an SM.  With three of 8 warps a thread has the registers for two chunks of weights in flight
+template <int NG, int WARPS, int PER_SM>
+__global__ void __launch_bounds__(32 * WARPS, PER_SM) gemm_act_few_kernel(const GemmActFewParams p) {
     __shared__ float part[WARPS][NG * 8][17];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int f0 = blockIdx.x * 16, N = p.e.N;
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) gemm_act_few_kernel(co
     for (int k = 64 * warp, run = 0; run == 0 || k < p.K; ++run) {
         const int end = min(p.K, k + kGfRun * WARPS);
         float acc[NG][4] = {};
-#pragma unroll 1
+#pragma unroll(PER_SM * WARPS <= 24 ? 2 : 1)
         for (; k < end; k += 64 * WARPS) {
             const bool in0 = k + 8 * t < p.K, in1 = k + 32 + 8 * t < p.K;
             const uint4 a00 = in0 ? gf_stream(w0 + k) : zero, a01 = in1 ? gf_stream(w0 + k + 32) : zero;
@@ -1015,11 +1015,15 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
         const unsigned blocks = (unsigned)((g.N + 15) / 16);
         const bool long_k = g.K >= kGfLongK && blocks <= 2u * host::sm_count();
         if (g.M <= 8) {
-            if (long_k) gemm_act_few_kernel<1, 16><<<blocks, 512, 0, s>>>(f);
-            else gemm_act_few_kernel<1, 8><<<blocks, 256, 0, s>>>(f);
+            // Three CTAs per SM, unless four need fewer waves, one or two: 1 x 20480 x 5120 35.2 us, with four 38.5; 1 x 10240 x 5120 21.4,
+            // 23.8; 1 x 5120 x 20480 36.5, 41.8; but 1 x 8192 x 4096 (512 CTAs) 16.6, 13.7 and 1 x 16384 x 2048 15.5, 13.9.
+            const unsigned sms = (unsigned)host::sm_count(), four = (blocks + 4 * sms - 1) / (4 * sms), three = (blocks + 3 * sms - 1) / (3 * sms);
+            if (long_k) gemm_act_few_kernel<1, 16, 2><<<blocks, 512, 0, s>>>(f);
+            else if (four <= 2 && four < three) gemm_act_few_kernel<1, 8, 4><<<blocks, 256, 0, s>>>(f);
+            else gemm_act_few_kernel<1, 8, 3><<<blocks, 256, 0, s>>>(f);
         } else {
-            if (long_k) gemm_act_few_kernel<2, 16><<<blocks, 512, 0, s>>>(f);
-            else gemm_act_few_kernel<2, 8><<<blocks, 256, 0, s>>>(f);
+            if (long_k) gemm_act_few_kernel<2, 16, 2><<<blocks, 512, 0, s>>>(f);
+            else gemm_act_few_kernel<2, 8, 4><<<blocks, 256, 0, s>>>(f);
         }
         return cudaGetLastError();
     }
