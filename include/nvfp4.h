@@ -517,6 +517,8 @@ nvfp4_status nvfp4_combine_bwd(const void* dy, int64_t lddy, const void* ys, int
  * ldd, ldr, ldpre >= N; sizes up to 2^30, ceil(M / 32) * ceil(N / 256) up to 2^28; pointers 16-byte
  * aligned (bias 4-byte).  Even leading dimensions of D, pre and the residual let a bf16 D take whole words.
  * ws receives the timeout flag.
+ * nvfp4_bf16_gemm_act_kn: the same with B [K][N], its rows ldb >= N apart (h = A . B + bias): with dh and a layer's weight, the
+ * layer's input gradient.
  *
  * nvfp4_act_bwd: dh = dy * act'(pre) in bf16 (dh may be NULL, or dy itself) and dbias[f] (+)= the sum over the rows
  * of dy * act'(pre) before its rounding, in fp32 in a fixed order (dbias may be NULL; accumulate = 1 adds to what it
@@ -536,6 +538,10 @@ nvfp4_status nvfp4_bf16_gemm_act(const void* a, int64_t lda, const void* b, int6
                                  const float* bias, nvfp4_act act, const void* residual, int64_t ldr,
                                  nvfp4_dtype residual_dtype, void* pre, int64_t ldpre, void* d, int64_t ldd,
                                  nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream);
+nvfp4_status nvfp4_bf16_gemm_act_kn(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                                    const float* bias, nvfp4_act act, const void* residual, int64_t ldr,
+                                    nvfp4_dtype residual_dtype, void* pre, int64_t ldpre, void* d, int64_t ldd,
+                                    nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream);
 size_t nvfp4_act_bwd_scratch_bytes(int64_t n);
 nvfp4_status nvfp4_act_bwd(const void* dy, int64_t lddy, const void* pre, int64_t ldpre, int64_t rows, int64_t n,
                            nvfp4_act act, void* dh, int64_t lddh, float* dbias, int accumulate, void* scratch,

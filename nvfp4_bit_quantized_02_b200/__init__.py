@@ -122,6 +122,7 @@ def _lib():
             "nvfp4_combine": ([vp, i64, i32, i64, vp, vp, i32, vp, i64, vp, i64, i32, i64, i64, vp], i32),
             "nvfp4_combine_bwd": ([vp, i64, vp, i64, i32, i64, vp, vp, i32, vp, i64, vp, i64, i64, vp], i32),
             "nvfp4_bf16_gemm_act": ([vp, i64, vp, i64, i64, i64, i64, vp, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp], i32),
+            "nvfp4_bf16_gemm_act_kn": ([vp, i64, vp, i64, i64, i64, i64, vp, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp], i32),
             "nvfp4_act_bwd_scratch_bytes": ([i64], c.c_size_t),
             "nvfp4_act_bwd": ([vp, i64, vp, i64, i64, i64, i32, vp, i64, vp, i32, vp, vp], i32),
             "nvfp4_amax": ([vp, i64, i64, i64, i32, u64, vp, vp], i32),
@@ -754,13 +755,14 @@ def _row_stride(x: torch.Tensor, what: str):
 
 def nvfp4_bf16_gemm_act(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None, act: int = ACT_NONE,
                         residual: torch.Tensor | None = None, pre: torch.Tensor | None = None, out_dtype=torch.bfloat16,
-                        out: torch.Tensor | None = None, ws: Workspace | None = None, stream=None) -> torch.Tensor:
-    """out = act(a . b^T + bias) + residual for bf16 a [M][K], b [N][K] (fp32 accumulation, one rounding).  bias:
-    fp32 [N]; residual: bf16 or fp32 [M][N], may be out; pre: bf16 [M][N], receives a . b^T + bias for nvfp4_act_bwd."""
+                        out: torch.Tensor | None = None, ws: Workspace | None = None, stream=None, b_kn: bool = False) -> torch.Tensor:
+    """out = act(a . b^T + bias) + residual for bf16 a [M][K], b [N][K] (fp32 accumulation, one rounding), with b_kn
+    act(a . b + bias) + residual for b [K][N].  bias: fp32 [N]; residual: bf16 or fp32 [M][N], may be out; pre: bf16
+    [M][N], receives the product + bias for nvfp4_act_bwd."""
     if a.dtype is not torch.bfloat16 or b.dtype is not torch.bfloat16 or a.dim() != 2 or b.dim() != 2:
-        raise TypeError("expected bf16 a [M][K] and b [N][K]")
+        raise TypeError("expected bf16 a [M][K] and b [N][K] (with b_kn [K][N])")
     M, K = a.shape
-    N, Kb = b.shape
+    Kb, N = b.shape if b_kn else b.shape[::-1]
     if Kb != K:
         raise ValueError("a and b need the same K")
     a_row, a_col = a.stride()
@@ -795,9 +797,10 @@ def nvfp4_bf16_gemm_act(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | N
         if t is not None and t.get_device() != dev:
             _elsewhere(dev, *(u for u in (a, b, out, bias, residual, pre) if u is not None))
     ws_addr, raw = _call_context(dev, ws, stream)
-    st = _lib().nvfp4_bf16_gemm_act(a.data_ptr(), a_row if M > 1 else K, b.data_ptr(), b_row if N > 1 else K, M, N, K, bias_addr, act,
-                                    res_addr, ldr, res_fp32, pre_addr, ldpre, out.data_ptr(), ldd,
-                                    OUT_FP32 if out_dtype is torch.float32 else OUT_BF16, ws_addr, raw)
+    L = _lib()
+    st = (L.nvfp4_bf16_gemm_act_kn if b_kn else L.nvfp4_bf16_gemm_act)(
+        a.data_ptr(), a_row if M > 1 else K, b.data_ptr(), b_row if b_kn or N > 1 else K, M, N, K, bias_addr, act, res_addr, ldr, res_fp32,
+        pre_addr, ldpre, out.data_ptr(), ldd, OUT_FP32 if out_dtype is torch.float32 else OUT_BF16, ws_addr, raw)
     if st:
         _check(st, "nvfp4_bf16_gemm_act")
     return out
@@ -892,7 +895,7 @@ class LinearActBF16:
             raise ValueError(f"dw: [{self.n}][{self.d}]")
         _act_bwd(dy, _row_stride(dy, "dy"), pre, self.act, self.dh, dbias, accumulate, self.scratch, stream)
         dh = dy if self.dh is None else self.dh
-        dx = nvfp4_bf16_gemm_grouped(dh, w.unsqueeze(0), self.offsets, b_kn=True, out=dx, ws=self.ws, stream=stream)
+        dx = nvfp4_bf16_gemm_act(dh, w, out=dx, ws=self.ws, stream=stream, b_kn=True)
         nvfp4_bf16_wgrad_grouped(dh, x, self.offsets, out=dw.unsqueeze(0), accumulate=accumulate, ws=self.ws, stream=stream)
         return dx, dw, dbias
 

@@ -967,12 +967,11 @@ nvfp4_status nvfp4_combine_bwd(const void* dy, int64_t lddy, const void* ys, int
 
 static bool is_act(nvfp4_act a) { return a >= NVFP4_ACT_NONE && a <= NVFP4_ACT_SILU; }
 
-nvfp4_status nvfp4_bf16_gemm_act(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
-                                 const float* bias, nvfp4_act act, const void* residual, int64_t ldr,
-                                 nvfp4_dtype residual_dtype, void* pre, int64_t ldpre, void* d, int64_t ldd,
-                                 nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream) {
+static nvfp4_status gemm_act(bool b_kn, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                             const float* bias, nvfp4_act act, const void* residual, int64_t ldr, nvfp4_dtype residual_dtype,
+                             void* pre, int64_t ldpre, void* d, int64_t ldd, nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream) {
     if (!is_dtype(out_dtype) || !is_act(act) || (residual && !is_dtype(residual_dtype))) return NVFP4_ERR_ARG;
-    if (M < 0 || N < 1 || K < 8 || K % 8 || lda < K || ldb < K || ldd < N) return NVFP4_ERR_SHAPE;
+    if (M < 0 || N < 1 || K < 8 || K % 8 || lda < K || ldb < (b_kn ? N : K) || ldd < N) return NVFP4_ERR_SHAPE;
     if ((residual && ldr < N) || (pre && ldpre < N)) return NVFP4_ERR_SHAPE;
     if (M > kMaxDim || N > kMaxDim || K > kMaxDim || lda > kMaxDim || ldb > kMaxDim || ldd > kMaxDim ||
         (residual && ldr > kMaxDim) || (pre && ldpre > kMaxDim) || ((M + 31) / 32) * ((N + 255) / 256) > (int64_t)1 << 28)
@@ -1002,9 +1001,23 @@ nvfp4_status nvfp4_bf16_gemm_act(const void* a, int64_t lda, const void* b, int6
     g.act = act;
     g.out_fp32 = out_dtype == NVFP4_OUT_FP32;
     g.res_fp32 = residual && residual_dtype == NVFP4_OUT_FP32;
+    g.b_kn = b_kn;
     g.flags = &ws_of(ws)->flags;
     g.budget_ns = g_budget_ns.load();
     return from_cuda(launch_gemm_act(g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_bf16_gemm_act(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                                 const float* bias, nvfp4_act act, const void* residual, int64_t ldr,
+                                 nvfp4_dtype residual_dtype, void* pre, int64_t ldpre, void* d, int64_t ldd,
+                                 nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream) {
+    return gemm_act(false, a, lda, b, ldb, M, N, K, bias, act, residual, ldr, residual_dtype, pre, ldpre, d, ldd, out_dtype, ws, stream);
+}
+nvfp4_status nvfp4_bf16_gemm_act_kn(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                                    const float* bias, nvfp4_act act, const void* residual, int64_t ldr,
+                                    nvfp4_dtype residual_dtype, void* pre, int64_t ldpre, void* d, int64_t ldd,
+                                    nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream) {
+    return gemm_act(true, a, lda, b, ldb, M, N, K, bias, act, residual, ldr, residual_dtype, pre, ldpre, d, ldd, out_dtype, ws, stream);
 }
 
 size_t nvfp4_act_bwd_scratch_bytes(int64_t n) {

@@ -45,6 +45,9 @@ constexpr int kGaRunK = 512, kGaRunBf16 = 4096;          // products per accumul
 constexpr int kGaBand = 8;                               // row tiles swept together along the features (L2 reuse)
 constexpr uint64_t kGaDrainNs = 2000000000ull;           // teardown waits, whatever the caller's budget
 
+// B [K][N]: a CTA's 128 features of 64 products are two blocks of 64 x 64, the MMA's MN-major layout (both read zeros past the ends)
+constexpr uint32_t kGaKnBlock = 8192, kGaKnStep = 2048 >> 4;
+
 struct GemmActParams {
     const float* bias;
     const void* residual;
@@ -60,6 +63,7 @@ struct GemmActParams {
     uint32_t tmem_cols;
     int32_t act, out_fp32, res_fp32;
     int32_t pairs;          // D, pre and the residual can be taken two features at a time
+    int32_t b_kn;           // B is [K][N]
     uint32_t* flags;
     uint64_t budget_ns;
 };
@@ -436,7 +440,12 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
                         s = 0;
                         parity ^= 1u;
                     }
-                    tma_load_2d_pair(dst, &maps.p, k * kGaK, p0, bar);
+                    if (p.b_kn) {
+                        tma_load_2d_pair(dst, &maps.p, p0, k * kGaK, bar);
+                        tma_load_2d_pair(dst + kGaKnBlock, &maps.p, p0 + 64, k * kGaK, bar);
+                    } else {
+                        tma_load_2d_pair(dst, &maps.p, k * kGaK, p0, bar);
+                    }
                     tma_load_2d_pair(dst + kGaOpBytes, &maps.q, k * kGaK, q0, bar);
                 }
             }
@@ -451,8 +460,9 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
             // ------------------------------- MMA issuer (leader) -----------------------------
             if (elect_one()) {
                 const uint32_t base = smem_u32(smem);
-                const uint64_t pdesc = desc_k_major(base), qdesc = desc_k_major(base + kGaOpBytes);
-                constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(256 >> 4) << 24);
+                const uint64_t pdesc = p.b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base), qdesc = desc_k_major(base + kGaOpBytes);
+                const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.b_kn << 15) | ((uint32_t)(256 >> 4) << 24);
+                const uint32_t pstep = p.b_kn ? kGaKnStep : 2;   // 16 products further
                 int it = 0, s = 0;
                 uint32_t parity = 0, consumed = 0;   // of the slot's `full`; stages committed
                 const uint32_t full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
@@ -479,7 +489,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
                             const uint64_t off = (uint64_t)((uint32_t)(s * kGaStageBytes) >> 4);
 #pragma unroll
                             for (int j = 0; j < kGaK / 16; ++j)   // products past K are zero
-                                mma_bf16_pair(acc, pdesc + off + 2 * j, qdesc + off + 2 * j, idesc, j ? 1u : add);
+                                mma_bf16_pair(acc, pdesc + off + pstep * j, qdesc + off + 2 * j, idesc, j ? 1u : add);
                             add = 1;
                             commit_pair(empty + 8u * s, leader);
                             ++consumed;
@@ -664,7 +674,12 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
     int g = s0, s = 0;                                   // the producer's next stage, its slot
     const auto load = [&]() {
         mbar_expect_tx(full + 8u * s, stage_bytes);
-        tma_load_2d(base + s * stage_bytes, &maps.p, g * kGaK, p0, full + 8u * s);
+        if (p.b_kn) {
+            tma_load_2d(base + s * stage_bytes, &maps.p, p0, g * kGaK, full + 8u * s);
+            tma_load_2d(base + s * stage_bytes + kGaKnBlock, &maps.p, p0 + 64, g * kGaK, full + 8u * s);
+        } else {
+            tma_load_2d(base + s * stage_bytes, &maps.p, g * kGaK, p0, full + 8u * s);
+        }
         tma_load_2d(base + s * stage_bytes + kGaOpBytes, &maps.q, g * kGaK, q0, full + 8u * s);
         ++g;
         if (++s == ring) s = 0;
@@ -722,8 +737,9 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
         __syncwarp();
     } else if (warp == 1) {
         if (elect_one()) {
-            const uint64_t pdesc = desc_k_major(base), qdesc = desc_k_major(base + kGaOpBytes);
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            const uint64_t pdesc = p.b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base), qdesc = desc_k_major(base + kGaOpBytes);
+            const uint32_t pstep = p.b_kn ? kGaKnStep : 2;   // 16 products further
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.b_kn << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
             int it = 0, slot = 0;
             uint32_t parity = 0;
             bool ok = true;
@@ -739,7 +755,7 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
                     tc_fence_after();
                     const uint64_t off = (uint64_t)((slot * stage_bytes) >> 4);
 #pragma unroll
-                    for (int j = 0; j < kGaK / 16; ++j) mma_bf16_single(acc, pdesc + off + 2 * j, qdesc + off + 2 * j, idesc, j ? 1u : add);
+                    for (int j = 0; j < kGaK / 16; ++j) mma_bf16_single(acc, pdesc + off + pstep * j, qdesc + off + 2 * j, idesc, j ? 1u : add);
                     add = 1;
                     commit_single(empty + 8u * slot);
                     if (++slot == ring) {
@@ -903,7 +919,7 @@ __global__ void __launch_bounds__(32 * WARPS, PER_SM) gemm_act_few_kernel(const 
 // ---------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------
-constexpr int kGfRows = 16;      // rows up to which the kernel for few is taken
+constexpr int kGfRows = 16;      // rows up to which the kernel for few is taken (B [N][K])
 constexpr int kGfLongK = 2048;   // a K from which 16 warps cut it, where one wave of CTAs holds the launch
 
 template <class Kernel>
@@ -1010,7 +1026,8 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
     p.pairs = (g.out_fp32 || g.ldd % 2 == 0) && (!g.pre || g.ldpre % 2 == 0) && (!g.residual || g.ldr % 2 == 0);
     p.flags = g.flags;
     p.budget_ns = g.budget_ns;
-    if (g.M <= kGfRows) {
+    p.b_kn = g.b_kn;
+    if (g.M <= kGfRows && !g.b_kn) {
         const GemmActFewParams f{g.a, g.b, g.lda, g.ldb, (int32_t)g.K, p};
         const unsigned blocks = (unsigned)((g.N + 15) / 16);
         const bool long_k = g.K >= kGfLongK && blocks <= 2u * host::sm_count();
@@ -1043,8 +1060,8 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
     p.np = (int32_t)((g.N + (plan.single ? 127 : 255)) / (plan.single ? 128 : 256));
     p.nq = (int32_t)((g.M + plan.wq - 1) / plan.wq);
     GemmActMaps maps;
-    const int64_t bdims[2] = {g.K, g.N}, bstrides[1] = {g.ldb}, adims[2] = {g.K, g.M}, astrides[1] = {g.lda};
-    const uint32_t bbox[2] = {64, 128}, abox[2] = {64, (uint32_t)(plan.single ? plan.wq : plan.wq / 2)};
+    const int64_t bdims[2] = {g.b_kn ? g.N : g.K, g.b_kn ? g.K : g.N}, bstrides[1] = {g.ldb}, adims[2] = {g.K, g.M}, astrides[1] = {g.lda};
+    const uint32_t bbox[2] = {64, g.b_kn ? (uint32_t)kGaK : 128u}, abox[2] = {64, (uint32_t)(plan.single ? plan.wq : plan.wq / 2)};
     if (!host::bf16_map(&maps.p, g.b, 2, bdims, bstrides, bbox) || !host::bf16_map(&maps.q, g.a, 2, adims, astrides, abox))
         return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)p.np * p.nq;

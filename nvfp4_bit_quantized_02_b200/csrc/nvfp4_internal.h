@@ -225,6 +225,7 @@ struct GemmAct {
     int64_t M, N, K;
     int act;
     bool out_fp32, res_fp32;
+    bool b_kn;                  // B is [K][N]: D = act(A . B + bias) + residual
     uint32_t* flags;
     uint64_t budget_ns;
 };

@@ -64,3 +64,17 @@ def test_binding_refuses(L):
                  lambda: nv.nvfp4_act_bwd(a.float(), a, nv.ACT_GELU)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_gemm_act_kn_refuses(L):
+    ok = dict(a=P, lda=64, b=P, ldb=128, M=32, N=128, K=64, bias=P, act=3, residual=P, ldr=128, res=0, pre=P, ldpre=128, d=P, ldd=128,
+              out=0, ws=P, stream=None)
+    for want, change in [(4, dict(out=2)), (4, dict(act=5)), (3, dict(M=-1)), (3, dict(N=0)), (3, dict(K=60)), (3, dict(lda=56)),
+                         (3, dict(ldb=120)), (3, dict(ldd=127)), (10, dict(ldb=BIG)), (5, dict(ws=None)), (1, dict(b=None)),
+                         (2, dict(b=ctypes.c_void_p(72))), (2, dict(ldb=132))]:
+        assert L.nvfp4_bf16_gemm_act_kn(*{**ok, **change}.values()) == want, change
+    import nvfp4_bit_quantized_02_b200 as nv
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    for call in (lambda: nv.nvfp4_bf16_gemm_act(bf(6, 16), bf(24, 16), b_kn=True), lambda: nv.nvfp4_bf16_gemm_act(bf(6, 16), bf(24, 16).t(), b_kn=True)):
+        with pytest.raises(ValueError):
+            call()
