@@ -519,6 +519,9 @@ nvfp4_status nvfp4_combine_bwd(const void* dy, int64_t lddy, const void* ys, int
  * ws receives the timeout flag.
  * nvfp4_bf16_gemm_act_kn: the same with B [K][N], its rows ldb >= N apart (h = A . B + bias): with dh and a layer's weight, the
  * layer's input gradient.
+ * nvfp4_bf16_wgrad: out[n][d] (+)= dy[rows][n]^T . x[rows][d], a layer's weight gradient, with bf16 operands and fp32 output (leading
+ * dimension ldo), by the same kernels and joins.  Shape rules: rows >= 0 (0: zeros unless accumulated), n, d >= 1; lddy >= n, ldx >= d,
+ * multiples of 8; ldo >= d; limits and alignment as above.
  *
  * nvfp4_act_bwd: dh = dy * act'(pre) in bf16 (dh may be NULL, or dy itself) and dbias[f] (+)= the sum over the rows
  * of dy * act'(pre) before its rounding, in fp32 in a fixed order (dbias may be NULL; accumulate = 1 adds to what it
@@ -542,6 +545,8 @@ nvfp4_status nvfp4_bf16_gemm_act_kn(const void* a, int64_t lda, const void* b, i
                                     const float* bias, nvfp4_act act, const void* residual, int64_t ldr,
                                     nvfp4_dtype residual_dtype, void* pre, int64_t ldpre, void* d, int64_t ldd,
                                     nvfp4_dtype out_dtype, void* ws, nvfp4_stream_t stream);
+nvfp4_status nvfp4_bf16_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t rows, int64_t n, int64_t d, float* out,
+                              int64_t ldo, int accumulate, void* ws, nvfp4_stream_t stream);
 size_t nvfp4_act_bwd_scratch_bytes(int64_t n);
 nvfp4_status nvfp4_act_bwd(const void* dy, int64_t lddy, const void* pre, int64_t ldpre, int64_t rows, int64_t n,
                            nvfp4_act act, void* dh, int64_t lddh, float* dbias, int accumulate, void* scratch,

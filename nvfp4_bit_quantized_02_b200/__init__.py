@@ -11,7 +11,7 @@ The functions carry the C names: ``nvfp4_quantize``, ``nvfp4_quantize_dual``,
 ``nvfp4_linear_bwd``, ``nvfp4_gelu_fwd``, ``nvfp4_gelu_bwd``, ``nvfp4_poll``, for layers with one weight
 per expert ``nvfp4_bf16_gemm_grouped`` and ``nvfp4_bf16_wgrad_grouped``, around them ``nvfp4_route``,
 ``nvfp4_dispatch`` and ``nvfp4_combine`` with their gradients, for dense layers with bias, activation and
-residual ``nvfp4_bf16_gemm_act`` and ``nvfp4_act_bwd``, for the weight update
+residual ``nvfp4_bf16_gemm_act``, ``nvfp4_act_bwd`` and ``nvfp4_bf16_wgrad``, for the weight update
 ``nvfp4_adamw_step``, and for data-parallel token shards ``nvfp4_amax``, ``nvfp4_quantize_dual_shard`` (and ``nvfp4_quantize_dual_dp``, which
 all-reduces the amax between them).
 """
@@ -123,6 +123,7 @@ def _lib():
             "nvfp4_combine_bwd": ([vp, i64, vp, i64, i32, i64, vp, vp, i32, vp, i64, vp, i64, i64, vp], i32),
             "nvfp4_bf16_gemm_act": ([vp, i64, vp, i64, i64, i64, i64, vp, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp], i32),
             "nvfp4_bf16_gemm_act_kn": ([vp, i64, vp, i64, i64, i64, i64, vp, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, vp], i32),
+            "nvfp4_bf16_wgrad": ([vp, i64, vp, i64, i64, i64, i64, vp, i64, i32, vp, vp], i32),
             "nvfp4_act_bwd_scratch_bytes": ([i64], c.c_size_t),
             "nvfp4_act_bwd": ([vp, i64, vp, i64, i64, i64, i32, vp, i64, vp, i32, vp, vp], i32),
             "nvfp4_amax": ([vp, i64, i64, i64, i32, u64, vp, vp], i32),
@@ -806,6 +807,34 @@ def nvfp4_bf16_gemm_act(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | N
     return out
 
 
+def nvfp4_bf16_wgrad(dy: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None, accumulate: bool = False,
+                     ws: Workspace | None = None, stream=None) -> torch.Tensor:
+    """dy^T . x (fp32 [n][d]) for bf16 dy [rows][n] and x [rows][d], a layer's weight gradient; accumulate adds it to out."""
+    if dy.dtype is not torch.bfloat16 or x.dtype is not torch.bfloat16:
+        raise TypeError("expected bf16 dy [rows][n] and x [rows][d]")
+    lddy, ldx = _row_stride(dy, "dy"), _row_stride(x, "x")
+    rows, n = dy.shape
+    d = x.shape[1]
+    if x.shape[0] != rows:
+        raise ValueError("dy and x need the same rows")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = _empty((n, d), torch.float32, dy.device, stream)
+    elif out.dtype is not torch.float32 or out.shape != (n, d):
+        raise ValueError("out: fp32 [n][d]")
+    ldo = _row_stride(out, "out")
+    dev = _CUR_DEVICE()
+    if dy.get_device() != dev or x.get_device() != dev or out.get_device() != dev:
+        _elsewhere(dev, dy, x, out)
+    ws_addr, raw = _call_context(dev, ws, stream)
+    st = _lib().nvfp4_bf16_wgrad(dy.data_ptr(), lddy if rows > 1 else -(-n // 8) * 8, x.data_ptr(), ldx if rows > 1 else -(-d // 8) * 8, rows,
+                                 n, d, out.data_ptr(), ldo, 1 if accumulate else 0, ws_addr, raw)
+    if st:
+        _check(st, "nvfp4_bf16_wgrad")
+    return out
+
+
 def nvfp4_act_bwd(dy: torch.Tensor, pre: torch.Tensor | None, act: int, out: torch.Tensor | None = None,
                   dbias: torch.Tensor | None = None, accumulate: bool = False, scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dy * act'(pre) (bf16 [rows][n]; out may be dy) and, where dbias (fp32 [n]) is given, its sum over the rows, which
@@ -896,7 +925,13 @@ class LinearActBF16:
         _act_bwd(dy, _row_stride(dy, "dy"), pre, self.act, self.dh, dbias, accumulate, self.scratch, stream)
         dh = dy if self.dh is None else self.dh
         dx = nvfp4_bf16_gemm_act(dh, w, out=dx, ws=self.ws, stream=stream, b_kn=True)
-        nvfp4_bf16_wgrad_grouped(dh, x, self.offsets, out=dw.unsqueeze(0), accumulate=accumulate, ws=self.ws, stream=stream)
+        # The grouped kernel walks a tile's whole T on one SM pair but writes and adds larger gradients faster (us, it and the
+        # other, stored / added): 16384 x 256 x 256 61.9, 15.6 / 62.1, 16.2; 8192 x 1000 x 1000 57, 49 / 57, 52; 3974 x 208 x 2384
+        # 25, 16 / 25, 17; 500 x 1280 x 5120 17.2, 14.6 / 20, 22; 2000 x 2048 x 2048 19.9, 20.5 / 21, 25; 4096 x 5120 x 5120 160, 166 / 166, 189.
+        if self.n * self.d <= 1 << 21:
+            nvfp4_bf16_wgrad(dh, x, out=dw, accumulate=accumulate, ws=self.ws, stream=stream)
+        else:
+            nvfp4_bf16_wgrad_grouped(dh, x, self.offsets, out=dw.unsqueeze(0), accumulate=accumulate, ws=self.ws, stream=stream)
         return dx, dw, dbias
 
 

@@ -1020,6 +1020,41 @@ nvfp4_status nvfp4_bf16_gemm_act_kn(const void* a, int64_t lda, const void* b, i
     return gemm_act(true, a, lda, b, ldb, M, N, K, bias, act, residual, ldr, residual_dtype, pre, ldpre, d, ldd, out_dtype, ws, stream);
 }
 
+nvfp4_status nvfp4_bf16_wgrad(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t rows, int64_t n, int64_t d, float* out,
+                              int64_t ldo, int accumulate, void* ws, nvfp4_stream_t stream) {
+    if (accumulate != 0 && accumulate != 1) return NVFP4_ERR_ARG;
+    if (rows < 0 || n < 1 || d < 1 || lddy < n || ldx < d || ldo < d) return NVFP4_ERR_SHAPE;
+    if (rows > kMaxDim || n > kMaxDim || d > kMaxDim || lddy > kMaxDim || ldx > kMaxDim || ldo > kMaxDim ||
+        ((n + 31) / 32) * ((d + 255) / 256) > (int64_t)1 << 28)
+        return NVFP4_ERR_LIMIT;
+    if (!ws) return NVFP4_ERR_WORKSPACE;
+    if (!out || (rows > 0 && (!dy || !x))) return NVFP4_ERR_NULL;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(out) || lddy % 8 || ldx % 8) return NVFP4_ERR_ALIGN;
+    if (nvfp4_status st = check_device()) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows == 0) return accumulate ? NVFP4_OK : from_cuda(cudaMemset2DAsync(out, ldo * sizeof(float), 0, d * sizeof(float), n, s));
+    GemmAct g{};
+    g.a = reinterpret_cast<const uint16_t*>(dy);
+    g.b = reinterpret_cast<const uint16_t*>(x);
+    g.d = out;
+    g.lda = lddy;
+    g.ldb = ldx;
+    g.ldd = ldo;
+    g.M = n;
+    g.N = d;
+    g.K = rows;
+    g.out_fp32 = true;
+    if (accumulate) {   // what it holds is the residual
+        g.residual = out;
+        g.ldr = ldo;
+        g.res_fp32 = true;
+    }
+    g.a_km = g.b_kn = true;
+    g.flags = &ws_of(ws)->flags;
+    g.budget_ns = g_budget_ns.load();
+    return from_cuda(launch_gemm_act(g, s));
+}
+
 size_t nvfp4_act_bwd_scratch_bytes(int64_t n) {
     return n > 0 && n <= kMaxDim ? (size_t)kActBwdRuns * (size_t)n * sizeof(float) : 0;
 }

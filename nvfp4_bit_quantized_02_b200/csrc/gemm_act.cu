@@ -45,8 +45,11 @@ constexpr int kGaRunK = 512, kGaRunBf16 = 4096;          // products per accumul
 constexpr int kGaBand = 8;                               // row tiles swept together along the features (L2 reuse)
 constexpr uint64_t kGaDrainNs = 2000000000ull;           // teardown waits, whatever the caller's budget
 
-// B [K][N]: a CTA's 128 features of 64 products are two blocks of 64 x 64, the MMA's MN-major layout (both read zeros past the ends)
+// Operands with K outermost: 64 features or rows of 64 products are a block of 64 x 64, the MMA's MN-major layout (zeros past the ends)
 constexpr uint32_t kGaKnBlock = 8192, kGaKnStep = 2048 >> 4;
+__host__ __device__ constexpr uint32_t ga_row_bytes(bool a_km, int rows) {   // of a stage
+    return a_km ? kGaKnBlock * (uint32_t)((rows + 63) / 64) : 2u * kGaK * (uint32_t)rows;
+}
 
 struct GemmActParams {
     const float* bias;
@@ -63,7 +66,7 @@ struct GemmActParams {
     uint32_t tmem_cols;
     int32_t act, out_fp32, res_fp32;
     int32_t pairs;          // D, pre and the residual can be taken two features at a time
-    int32_t b_kn;           // B is [K][N]
+    int32_t b_kn, a_km;     // B is [K][N], A is [K][M]
     uint32_t* flags;
     uint64_t budget_ns;
 };
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
             for (int t = unit; ok && t < tiles; t += units) {
                 const GaTile c = ga_tile(p, t);
                 const int half = c.n >> 1, p0 = c.p0 + (int)rank * 128, q0 = c.q0 + (int)rank * half;
-                const uint32_t tx = (uint32_t)(kGaOpBytes + 64 * p.wq);   // rows of the box past the tile's are not used
+                const uint32_t tx = (uint32_t)kGaOpBytes + ga_row_bytes(p.a_km, p.wq >> 1);   // rows of the box past the tile's are not used
                 for (int k = s0; k < s1; ++k) {
                     if (!mbar_wait(empty + 8u * s, parity, abort_flag, p.flags, p.budget_ns)) {
                         ok = false;
@@ -446,7 +449,12 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
                     } else {
                         tma_load_2d_pair(dst, &maps.p, k * kGaK, p0, bar);
                     }
-                    tma_load_2d_pair(dst + kGaOpBytes, &maps.q, k * kGaK, q0, bar);
+                    if (p.a_km) {
+                        tma_load_2d_pair(dst + kGaOpBytes, &maps.q, q0, k * kGaK, bar);
+                        if (p.wq > 128) tma_load_2d_pair(dst + kGaOpBytes + kGaKnBlock, &maps.q, q0 + 64, k * kGaK, bar);
+                    } else {
+                        tma_load_2d_pair(dst + kGaOpBytes, &maps.q, k * kGaK, q0, bar);
+                    }
                 }
             }
             sm.issued = (uint32_t)g;   // read by the drain, after the cluster barrier
@@ -460,9 +468,10 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
             // ------------------------------- MMA issuer (leader) -----------------------------
             if (elect_one()) {
                 const uint32_t base = smem_u32(smem);
-                const uint64_t pdesc = p.b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base), qdesc = desc_k_major(base + kGaOpBytes);
-                const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.b_kn << 15) | ((uint32_t)(256 >> 4) << 24);
-                const uint32_t pstep = p.b_kn ? kGaKnStep : 2;   // 16 products further
+                const uint64_t pdesc = p.b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base);
+                const uint64_t qdesc = p.a_km ? desc_mn_major(base + kGaOpBytes, kGaKnBlock) : desc_k_major(base + kGaOpBytes);
+                const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.b_kn << 15) | ((uint32_t)p.a_km << 16) | ((uint32_t)(256 >> 4) << 24);
+                const uint32_t pstep = p.b_kn ? kGaKnStep : 2, qstep = p.a_km ? kGaKnStep : 2;   // 16 products further
                 int it = 0, s = 0;
                 uint32_t parity = 0, consumed = 0;   // of the slot's `full`; stages committed
                 const uint32_t full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
@@ -489,7 +498,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
                             const uint64_t off = (uint64_t)((uint32_t)(s * kGaStageBytes) >> 4);
 #pragma unroll
                             for (int j = 0; j < kGaK / 16; ++j)   // products past K are zero
-                                mma_bf16_pair(acc, pdesc + off + pstep * j, qdesc + off + 2 * j, idesc, j ? 1u : add);
+                                mma_bf16_pair(acc, pdesc + off + pstep * j, qdesc + off + qstep * j, idesc, j ? 1u : add);
                             add = 1;
                             commit_pair(empty + 8u * s, leader);
                             ++consumed;
@@ -666,7 +675,7 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
     const int s0 = CLUSTER ? part * p.part_stages + min(part, p.longer) : 0, s1 = CLUSTER ? s0 + p.part_stages + (part < p.longer) : p.stages;
     const int run = p.run;
     const int n = (qn + 15) & ~15;                       // the MMA's N
-    const uint32_t stage_bytes = (uint32_t)(kGaOpBytes + 128 * p.wq);
+    const uint32_t stage_bytes = (uint32_t)kGaOpBytes + ga_row_bytes(p.a_km, p.wq);
     const int ring = p.ring;
     const uint32_t base = smem_u32(smem), full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
     const uint32_t cols = p.tmem_cols;                   // two accumulators (one, where one run serves)
@@ -680,7 +689,12 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
         } else {
             tma_load_2d(base + s * stage_bytes, &maps.p, g * kGaK, p0, full + 8u * s);
         }
-        tma_load_2d(base + s * stage_bytes + kGaOpBytes, &maps.q, g * kGaK, q0, full + 8u * s);
+        if (p.a_km) {
+            tma_load_2d(base + s * stage_bytes + kGaOpBytes, &maps.q, q0, g * kGaK, full + 8u * s);
+            if (p.wq > 64) tma_load_2d(base + s * stage_bytes + kGaOpBytes + kGaKnBlock, &maps.q, q0 + 64, g * kGaK, full + 8u * s);
+        } else {
+            tma_load_2d(base + s * stage_bytes + kGaOpBytes, &maps.q, g * kGaK, q0, full + 8u * s);
+        }
         ++g;
         if (++s == ring) s = 0;
     };
@@ -737,9 +751,10 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
         __syncwarp();
     } else if (warp == 1) {
         if (elect_one()) {
-            const uint64_t pdesc = p.b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base), qdesc = desc_k_major(base + kGaOpBytes);
-            const uint32_t pstep = p.b_kn ? kGaKnStep : 2;   // 16 products further
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.b_kn << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            const uint64_t pdesc = p.b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base);
+                const uint64_t qdesc = p.a_km ? desc_mn_major(base + kGaOpBytes, kGaKnBlock) : desc_k_major(base + kGaOpBytes);
+            const uint32_t pstep = p.b_kn ? kGaKnStep : 2, qstep = p.a_km ? kGaKnStep : 2;   // 16 products further
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.b_kn << 15) | ((uint32_t)p.a_km << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
             int it = 0, slot = 0;
             uint32_t parity = 0;
             bool ok = true;
@@ -755,7 +770,7 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
                     tc_fence_after();
                     const uint64_t off = (uint64_t)((slot * stage_bytes) >> 4);
 #pragma unroll
-                    for (int j = 0; j < kGaK / 16; ++j) mma_bf16_single(acc, pdesc + off + pstep * j, qdesc + off + 2 * j, idesc, j ? 1u : add);
+                    for (int j = 0; j < kGaK / 16; ++j) mma_bf16_single(acc, pdesc + off + pstep * j, qdesc + off + qstep * j, idesc, j ? 1u : add);
                     add = 1;
                     commit_single(empty + 8u * slot);
                     if (++slot == ring) {
@@ -1027,7 +1042,8 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
     p.flags = g.flags;
     p.budget_ns = g.budget_ns;
     p.b_kn = g.b_kn;
-    if (g.M <= kGfRows && !g.b_kn) {
+    p.a_km = g.a_km;
+    if (g.M <= kGfRows && !g.b_kn && !g.a_km) {
         const GemmActFewParams f{g.a, g.b, g.lda, g.ldb, (int32_t)g.K, p};
         const unsigned blocks = (unsigned)((g.N + 15) / 16);
         const bool long_k = g.K >= kGfLongK && blocks <= 2u * host::sm_count();
@@ -1060,15 +1076,15 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
     p.np = (int32_t)((g.N + (plan.single ? 127 : 255)) / (plan.single ? 128 : 256));
     p.nq = (int32_t)((g.M + plan.wq - 1) / plan.wq);
     GemmActMaps maps;
-    const int64_t bdims[2] = {g.b_kn ? g.N : g.K, g.b_kn ? g.K : g.N}, bstrides[1] = {g.ldb}, adims[2] = {g.K, g.M}, astrides[1] = {g.lda};
-    const uint32_t bbox[2] = {64, g.b_kn ? (uint32_t)kGaK : 128u}, abox[2] = {64, (uint32_t)(plan.single ? plan.wq : plan.wq / 2)};
+    const int64_t bdims[2] = {g.b_kn ? g.N : g.K, g.b_kn ? g.K : g.N}, bstrides[1] = {g.ldb}, adims[2] = {g.a_km ? g.M : g.K, g.a_km ? g.K : g.M}, astrides[1] = {g.lda};
+    const uint32_t bbox[2] = {64, g.b_kn ? (uint32_t)kGaK : 128u}, abox[2] = {64, g.a_km ? (uint32_t)kGaK : (uint32_t)(plan.single ? plan.wq : plan.wq / 2)};
     if (!host::bf16_map(&maps.p, g.b, 2, bdims, bstrides, bbox) || !host::bf16_map(&maps.q, g.a, 2, adims, astrides, abox))
         return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)p.np * p.nq;
     static std::atomic<uint64_t> attr[4];
     const int split = plan.split;
     if (plan.single) {
-        p.ring = std::min(kGmMaxStages, kGmRing / (kGaOpBytes + 128 * plan.wq));
+        p.ring = std::min(kGmMaxStages, kGmRing / (kGaOpBytes + (int)ga_row_bytes(g.a_km, plan.wq)));
         p.tmem_cols = 64;   // two accumulators
         while ((int)p.tmem_cols < 2 * plan.wq) p.tmem_cols <<= 1;
         return split > 1 ? launch_ga(gemm_act_mid_kernel<true>, kGmClusterSmem, attr[0], split, kGmThreads, p.nq * split, p.np, maps, p, s)

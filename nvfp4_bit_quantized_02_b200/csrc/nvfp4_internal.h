@@ -225,7 +225,7 @@ struct GemmAct {
     int64_t M, N, K;
     int act;
     bool out_fp32, res_fp32;
-    bool b_kn;                  // B is [K][N]: D = act(A . B + bias) + residual
+    bool b_kn, a_km;            // B is [K][N] (D = act(A . B + bias) + residual); A is [K][M]
     uint32_t* flags;
     uint64_t budget_ns;
 };

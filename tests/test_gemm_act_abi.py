@@ -78,3 +78,21 @@ def test_gemm_act_kn_refuses(L):
     for call in (lambda: nv.nvfp4_bf16_gemm_act(bf(6, 16), bf(24, 16), b_kn=True), lambda: nv.nvfp4_bf16_gemm_act(bf(6, 16), bf(24, 16).t(), b_kn=True)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_wgrad_refuses(L):
+    ok = dict(dy=P, lddy=64, x=P, ldx=128, rows=32, n=64, d=128, out=P, ldo=128, accumulate=0, ws=P, stream=None)
+    for want, change in [(4, dict(accumulate=2)), (3, dict(rows=-1)), (3, dict(n=0)), (3, dict(d=0)), (3, dict(lddy=56)), (3, dict(ldx=120)),
+                         (3, dict(ldo=127)), (10, dict(rows=BIG)), (10, dict(n=BIG, lddy=BIG)), (10, dict(ldo=BIG)), (10, dict(ldx=BIG)),
+                         (5, dict(ws=None)), (1, dict(dy=None)), (1, dict(x=None)), (1, dict(out=None)), (2, dict(dy=ctypes.c_void_p(72))),
+                         (2, dict(x=ctypes.c_void_p(72))), (2, dict(out=ctypes.c_void_p(72))), (2, dict(lddy=68)), (2, dict(ldx=132))]:
+        assert L.nvfp4_bf16_wgrad(*{**ok, **change}.values()) == want, change
+    import nvfp4_bit_quantized_02_b200 as nv
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    for call in (lambda: nv.nvfp4_bf16_wgrad(bf(6, 16), bf(5, 16)), lambda: nv.nvfp4_bf16_wgrad(bf(6, 16), bf(6, 24), accumulate=True),
+                 lambda: nv.nvfp4_bf16_wgrad(bf(6, 16), bf(6, 24), out=torch.zeros(24, 16)), lambda: nv.nvfp4_bf16_wgrad(bf(16, 6).t(), bf(6, 24)),
+                 lambda: nv.nvfp4_bf16_wgrad(bf(6, 16), bf(6, 24), out=bf(16, 24))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        nv.nvfp4_bf16_wgrad(torch.zeros(6, 16), bf(6, 24))
