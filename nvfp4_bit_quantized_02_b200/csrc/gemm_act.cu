@@ -662,9 +662,11 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-template <bool CLUSTER>
+// KOUT: operands with K outermost, by p.b_kn and p.a_km (333 x 1288 x 5120 takes 0.4 us longer where they are looked up)
+template <bool CLUSTER, bool KOUT>
 __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kernel(const __grid_constant__ GemmActMaps maps, const __grid_constant__ GemmActParams p) {
     extern __shared__ uint8_t smem_raw[];
+    const bool b_kn = KOUT && p.b_kn, a_km = KOUT && p.a_km;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     GemmMidSmem& sm = *reinterpret_cast<GemmMidSmem*>(smem + kGmRing + (CLUSTER ? kInbox : 0));
     volatile uint32_t* abort_flag = &sm.abort;
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
     const int s0 = CLUSTER ? part * p.part_stages + min(part, p.longer) : 0, s1 = CLUSTER ? s0 + p.part_stages + (part < p.longer) : p.stages;
     const int run = p.run;
     const int n = (qn + 15) & ~15;                       // the MMA's N
-    const uint32_t stage_bytes = (uint32_t)kGaOpBytes + ga_row_bytes(p.a_km, p.wq);
+    const uint32_t stage_bytes = (uint32_t)kGaOpBytes + ga_row_bytes(a_km, p.wq);
     const int ring = p.ring;
     const uint32_t base = smem_u32(smem), full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
     const uint32_t cols = p.tmem_cols;                   // two accumulators (one, where one run serves)
@@ -683,13 +685,13 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
     int g = s0, s = 0;                                   // the producer's next stage, its slot
     const auto load = [&]() {
         mbar_expect_tx(full + 8u * s, stage_bytes);
-        if (p.b_kn) {
+        if (b_kn) {
             tma_load_2d(base + s * stage_bytes, &maps.p, p0, g * kGaK, full + 8u * s);
             tma_load_2d(base + s * stage_bytes + kGaKnBlock, &maps.p, p0 + 64, g * kGaK, full + 8u * s);
         } else {
             tma_load_2d(base + s * stage_bytes, &maps.p, g * kGaK, p0, full + 8u * s);
         }
-        if (p.a_km) {
+        if (a_km) {
             tma_load_2d(base + s * stage_bytes + kGaOpBytes, &maps.q, q0, g * kGaK, full + 8u * s);
             if (p.wq > 64) tma_load_2d(base + s * stage_bytes + kGaOpBytes + kGaKnBlock, &maps.q, q0 + 64, g * kGaK, full + 8u * s);
         } else {
@@ -751,10 +753,10 @@ __global__ void __launch_bounds__(kGmThreads, CLUSTER ? 1 : 2) gemm_act_mid_kern
         __syncwarp();
     } else if (warp == 1) {
         if (elect_one()) {
-            const uint64_t pdesc = p.b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base);
-                const uint64_t qdesc = p.a_km ? desc_mn_major(base + kGaOpBytes, kGaKnBlock) : desc_k_major(base + kGaOpBytes);
-            const uint32_t pstep = p.b_kn ? kGaKnStep : 2, qstep = p.a_km ? kGaKnStep : 2;   // 16 products further
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.b_kn << 15) | ((uint32_t)p.a_km << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            const uint64_t pdesc = b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base);
+                const uint64_t qdesc = a_km ? desc_mn_major(base + kGaOpBytes, kGaKnBlock) : desc_k_major(base + kGaOpBytes);
+            const uint32_t pstep = b_kn ? kGaKnStep : 2, qstep = a_km ? kGaKnStep : 2;   // 16 products further
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_kn << 15) | ((uint32_t)a_km << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
             int it = 0, slot = 0;
             uint32_t parity = 0;
             bool ok = true;
@@ -1042,7 +1044,7 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
     p.flags = g.flags;
     p.budget_ns = g.budget_ns;
     p.b_kn = g.b_kn;
-    p.a_km = g.a_km;
+    p.a_km = g.a_km;   // only with b_kn
     if (g.M <= kGfRows && !g.b_kn && !g.a_km) {
         const GemmActFewParams f{g.a, g.b, g.lda, g.ldb, (int32_t)g.K, p};
         const unsigned blocks = (unsigned)((g.N + 15) / 16);
@@ -1081,14 +1083,17 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
     if (!host::bf16_map(&maps.p, g.b, 2, bdims, bstrides, bbox) || !host::bf16_map(&maps.q, g.a, 2, adims, astrides, abox))
         return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)p.np * p.nq;
-    static std::atomic<uint64_t> attr[4];
+    static std::atomic<uint64_t> attr[6];
     const int split = plan.split;
     if (plan.single) {
         p.ring = std::min(kGmMaxStages, kGmRing / (kGaOpBytes + (int)ga_row_bytes(g.a_km, plan.wq)));
         p.tmem_cols = 64;   // two accumulators
         while ((int)p.tmem_cols < 2 * plan.wq) p.tmem_cols <<= 1;
-        return split > 1 ? launch_ga(gemm_act_mid_kernel<true>, kGmClusterSmem, attr[0], split, kGmThreads, p.nq * split, p.np, maps, p, s)
-                         : launch_ga(gemm_act_mid_kernel<false>, kGmSmem, attr[1], 1, kGmThreads, p.nq, p.np, maps, p, s);
+        if (split > 1)
+            return g.b_kn ? launch_ga(gemm_act_mid_kernel<true, true>, kGmClusterSmem, attr[4], split, kGmThreads, p.nq * split, p.np, maps, p, s)
+                          : launch_ga(gemm_act_mid_kernel<true, false>, kGmClusterSmem, attr[0], split, kGmThreads, p.nq * split, p.np, maps, p, s);
+        return g.b_kn ? launch_ga(gemm_act_mid_kernel<false, true>, kGmSmem, attr[5], 1, kGmThreads, p.nq, p.np, maps, p, s)
+                      : launch_ga(gemm_act_mid_kernel<false, false>, kGmSmem, attr[1], 1, kGmThreads, p.nq, p.np, maps, p, s);
     }
     return split > 1 ? launch_ga(gemm_act_kernel<true>, kGaClusterSmem, attr[2], 2 * split, kGaThreads, 2 * tiles * split, 1, maps, p, s)
                      : launch_ga(gemm_act_kernel<false>, kGaSmem, attr[3], 2, kGaThreads, 2 * std::min<int64_t>(tiles, sms / 2), 1, maps, p, s);
