@@ -365,9 +365,11 @@ __device__ __forceinline__ bool tile_epilogue(const GemmActParams& p, const Epil
 // ---------------------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------------------
-template <bool CLUSTER>
+// KOUT: operands with K outermost, by p.b_kn and p.a_km (looked up in every call, they cost 8192 x 20480 x 5120 10 us of 1137)
+template <bool CLUSTER, bool KOUT>
 __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_constant__ GemmActMaps maps, const __grid_constant__ GemmActParams p) {
     extern __shared__ uint8_t smem_raw[];
+    const bool b_kn = KOUT && p.b_kn, a_km = KOUT && p.a_km;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // in a cluster of several pairs: four stages, and the inbox behind them
     constexpr int kStages = CLUSTER ? kGaClusterStages : kGaStages;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
             for (int t = unit; ok && t < tiles; t += units) {
                 const GaTile c = ga_tile(p, t);
                 const int half = c.n >> 1, p0 = c.p0 + (int)rank * 128, q0 = c.q0 + (int)rank * half;
-                const uint32_t tx = (uint32_t)kGaOpBytes + ga_row_bytes(p.a_km, p.wq >> 1);   // rows of the box past the tile's are not used
+                const uint32_t tx = (uint32_t)kGaOpBytes + ga_row_bytes(a_km, p.wq >> 1);   // rows of the box past the tile's are not used
                 for (int k = s0; k < s1; ++k) {
                     if (!mbar_wait(empty + 8u * s, parity, abort_flag, p.flags, p.budget_ns)) {
                         ok = false;
@@ -443,13 +445,13 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
                         s = 0;
                         parity ^= 1u;
                     }
-                    if (p.b_kn) {
+                    if (b_kn) {
                         tma_load_2d_pair(dst, &maps.p, p0, k * kGaK, bar);
                         tma_load_2d_pair(dst + kGaKnBlock, &maps.p, p0 + 64, k * kGaK, bar);
                     } else {
                         tma_load_2d_pair(dst, &maps.p, k * kGaK, p0, bar);
                     }
-                    if (p.a_km) {
+                    if (a_km) {
                         tma_load_2d_pair(dst + kGaOpBytes, &maps.q, q0, k * kGaK, bar);
                         if (p.wq > 128) tma_load_2d_pair(dst + kGaOpBytes + kGaKnBlock, &maps.q, q0 + 64, k * kGaK, bar);
                     } else {
@@ -468,10 +470,10 @@ __global__ void __launch_bounds__(kGaThreads, 1) gemm_act_kernel(const __grid_co
             // ------------------------------- MMA issuer (leader) -----------------------------
             if (elect_one()) {
                 const uint32_t base = smem_u32(smem);
-                const uint64_t pdesc = p.b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base);
-                const uint64_t qdesc = p.a_km ? desc_mn_major(base + kGaOpBytes, kGaKnBlock) : desc_k_major(base + kGaOpBytes);
-                const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.b_kn << 15) | ((uint32_t)p.a_km << 16) | ((uint32_t)(256 >> 4) << 24);
-                const uint32_t pstep = p.b_kn ? kGaKnStep : 2, qstep = p.a_km ? kGaKnStep : 2;   // 16 products further
+                const uint64_t pdesc = b_kn ? desc_mn_major(base, kGaKnBlock) : desc_k_major(base);
+                const uint64_t qdesc = a_km ? desc_mn_major(base + kGaOpBytes, kGaKnBlock) : desc_k_major(base + kGaOpBytes);
+                const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_kn << 15) | ((uint32_t)a_km << 16) | ((uint32_t)(256 >> 4) << 24);
+                const uint32_t pstep = b_kn ? kGaKnStep : 2, qstep = a_km ? kGaKnStep : 2;   // 16 products further
                 int it = 0, s = 0;
                 uint32_t parity = 0, consumed = 0;   // of the slot's `full`; stages committed
                 const uint32_t full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
@@ -1083,7 +1085,7 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
     if (!host::bf16_map(&maps.p, g.b, 2, bdims, bstrides, bbox) || !host::bf16_map(&maps.q, g.a, 2, adims, astrides, abox))
         return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)p.np * p.nq;
-    static std::atomic<uint64_t> attr[6];
+    static std::atomic<uint64_t> attr[8];
     const int split = plan.split;
     if (plan.single) {
         p.ring = std::min(kGmMaxStages, kGmRing / (kGaOpBytes + (int)ga_row_bytes(g.a_km, plan.wq)));
@@ -1095,8 +1097,12 @@ cudaError_t launch_gemm_act(const GemmAct& g, cudaStream_t s) {
         return g.b_kn ? launch_ga(gemm_act_mid_kernel<false, true>, kGmSmem, attr[5], 1, kGmThreads, p.nq, p.np, maps, p, s)
                       : launch_ga(gemm_act_mid_kernel<false, false>, kGmSmem, attr[1], 1, kGmThreads, p.nq, p.np, maps, p, s);
     }
-    return split > 1 ? launch_ga(gemm_act_kernel<true>, kGaClusterSmem, attr[2], 2 * split, kGaThreads, 2 * tiles * split, 1, maps, p, s)
-                     : launch_ga(gemm_act_kernel<false>, kGaSmem, attr[3], 2, kGaThreads, 2 * std::min<int64_t>(tiles, sms / 2), 1, maps, p, s);
+    if (split > 1)
+        return g.b_kn ? launch_ga(gemm_act_kernel<true, true>, kGaClusterSmem, attr[6], 2 * split, kGaThreads, 2 * tiles * split, 1, maps, p, s)
+                      : launch_ga(gemm_act_kernel<true, false>, kGaClusterSmem, attr[2], 2 * split, kGaThreads, 2 * tiles * split, 1, maps, p, s);
+    const int64_t blocks = 2 * std::min<int64_t>(tiles, sms / 2);
+    return g.b_kn ? launch_ga(gemm_act_kernel<false, true>, kGaSmem, attr[7], 2, kGaThreads, blocks, 1, maps, p, s)
+                  : launch_ga(gemm_act_kernel<false, false>, kGaSmem, attr[3], 2, kGaThreads, blocks, 1, maps, p, s);
 }
 
 // ---------------------------------------------------------------------------------------
