@@ -412,7 +412,9 @@ __global__ void __launch_bounds__(32 * WARPS) route_choose_kernel(const __grid_c
                     if (__any_sync(kAll, close)) {
                         // all that may be among the first k, compared in fp64
                         const float last = own.sorted[min(k, all) - 1].x;
-                        at_least = fminf(at_least, last - 2.0f * (tau + kTauC * fabsf(last)));
+                        // (next to the lowest number the difference is -inf, which places without an expert and experts that may
+                        // not be chosen would reach too)
+                        at_least = fmaxf(fminf(at_least, last - 2.0f * (tau + kTauC * fabsf(last))), -FLT_MAX);
                         __syncwarp();
                         found = gather();
                         if (all <= 32) {

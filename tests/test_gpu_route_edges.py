@@ -1,0 +1,52 @@
+"""Routing at the ends of its range, against the definition in 64 bits (the reference and the tolerances are those of the
+other tests of the route): biases of the type's lowest value."""
+import pytest
+import torch
+
+from gpu_helpers import nv
+from test_gpu_route import INF, _bias, _logits, check
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = torch.finfo(torch.float32).min
+
+
+def _masked_bias(E, left, seed, value=LOWEST):
+    """A balance bias that switches all experts but `left` of them off."""
+    bias = _bias(E, seed)
+    off = torch.randperm(E, generator=torch.Generator().manual_seed(seed))[left:]
+    bias[off] = value
+    return bias
+
+
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(7, 4), (16, 4), (24, 5), (30, 8), (31, 31), (32, 8), (33, 8), (64, 6), (256, 8)])
+def test_experts_switched_off_by_the_lowest_bias(E, k, sigmoid):
+    """c = s + the lowest number is that number, in 64 bits too: eligible, all alike, chosen by index where fewer than k experts are
+    left.  The last token's logits end where the buffer does."""
+    x = _logits(70, E, E)
+    gone = x.clone()
+    gone[::2, ::3] = -INF                  # never chosen
+    gone[5] = -INF
+    for left in (0, 1, k - 1, k):
+        bias = _masked_bias(E, left, left)
+        for logits in (x, gone, x.bfloat16()):
+            check(logits, k, sigmoid=sigmoid, bias=bias)
+        check(x[:1], k, sigmoid=sigmoid, bias=bias, renormalize=False)
+    near = _masked_bias(E, 1, 3)
+    near[near == LOWEST] = torch.tensor(LOWEST).nextafter(torch.tensor(0.0))   # and next to it
+    near[0] = LOWEST
+    check(gone, k, sigmoid=sigmoid, bias=near)
+    never = _masked_bias(E, 2, 4)
+    never[1::4] = -INF                     # beside biases that may not be chosen
+    check(gone, k, sigmoid=sigmoid, bias=never)
+
+
+# with lanes or whole groups of lanes that have no expert
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top_groups", [(30, 8, 5, 2), (64, 8, 8, 3), (24, 6, 3, 2), (20, 6, 10, 4), (63, 12, 9, 5), (96, 9, 32, 6)])
+def test_groups_with_experts_switched_off_by_the_lowest_bias(E, k, groups, top_groups, sigmoid):
+    x = _logits(70, E, E)
+    x[::3, ::4] = -INF
+    for left in (0, 2, k, E // 2):
+        check(x, k, sigmoid=sigmoid, bias=_masked_bias(E, left, left), groups=groups, top_groups=top_groups)
