@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(32 * WARPS) route_choose_kernel(const __grid_c
                     b2 = fmaxf(fminf(b1, d1), fmaxf(b2, d2));
                     b1 = fmaxf(b1, d1);
                 }
-                const float score = p.r.group_top == 2 ? b1 + b2 : b1;
+                // a sum of two that are no less than the lowest number is above -inf: it is held there, where groups are as close as can be
+                const float score = p.r.group_top == 1 ? b1 : b2 > kNone ? fmaxf(b1 + b2, -FLT_MAX) : kNone;
                 stays = group_stays(score, p, lane);
                 if (scores) {
                     const uint32_t least = __reduce_min_sync(kAll, stays ? order_key(score) : kAll);

@@ -1,5 +1,5 @@
 """Routing at the ends of its range, against the definition in 64 bits (the reference and the tolerances are those of the
-other tests of the route): biases of the type's lowest value."""
+other tests of the route): biases of the type's lowest value, sums of two of them as the scores of groups."""
 import pytest
 import torch
 
@@ -50,3 +50,29 @@ def test_groups_with_experts_switched_off_by_the_lowest_bias(E, k, groups, top_g
     x[::3, ::4] = -INF
     for left in (0, 2, k, E // 2):
         check(x, k, sigmoid=sigmoid, bias=_masked_bias(E, left, left), groups=groups, top_groups=top_groups)
+
+
+def _masked_groups(E, groups, left, seed, value=LOWEST):
+    """A balance bias that switches all groups but `left` off."""
+    bias = _bias(E, seed).view(groups, -1)
+    bias[torch.randperm(groups, generator=torch.Generator().manual_seed(seed))[left:]] = value
+    return bias.flatten()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", [LOWEST, -LOWEST], ids=["lowest", "largest"])
+@pytest.mark.parametrize("E,k,groups,top_groups", [(64, 12, 8, 3), (30, 8, 5, 2), (24, 24, 4, 4), (256, 8, 8, 4), (63, 12, 9, 5), (64, 9, 32, 6)])
+def test_groups_whose_two_largest_add_to_more_than_fp32_holds(E, k, groups, top_groups, value, sigmoid):
+    """Twice the lowest number is above -inf in 64 bits: such a group stays, behind the others and the lowest index first."""
+    x = _logits(70, E, E)
+    gone = x.clone()
+    gone[::2, ::3] = -INF
+    gone[5] = -INF
+    for left in range(top_groups + 1):
+        bias = _masked_groups(E, groups, left, left, value)
+        for logits in (x, gone):
+            check(logits, k, sigmoid=sigmoid, bias=bias, groups=groups, top_groups=top_groups, group_top=2)
+        bias.view(groups, -1)[:, 0] = 0.125        # one expert of each is left: sums of the number itself
+        check(gone, k, sigmoid=sigmoid, bias=bias, groups=groups, top_groups=top_groups, group_top=2)
+        bias[E // 2:] = -INF                       # and groups that cannot stay
+        check(gone, k, sigmoid=sigmoid, bias=bias, groups=groups, top_groups=top_groups, group_top=2)
