@@ -344,11 +344,11 @@ __global__ void __launch_bounds__(32 * WARPS) route_choose_kernel(const __grid_c
                 const float score = p.r.group_top == 1 ? b1 : b2 > kNone ? fmaxf(b1 + b2, -FLT_MAX) : kNone;
                 stays = group_stays(score, p, lane);
                 if (scores) {
-                    const uint32_t least = __reduce_min_sync(kAll, stays ? order_key(score) : kAll);
-                    const uint32_t most = __reduce_max_sync(kAll, stays || g >= p.r.groups ? 0u : order_key(score));
-                    const float lo = key_value(least);
-                    // a sum of two errs by both, and by its rounding
-                    if (most && least != kAll && !(lo - key_value(most) > 2.0f * (tau + kTauC * fabsf(lo)))) stays = groups_slow(p, row, top);
+                    // what a score may err by: a sum of two by both and by its rounding, relative to the larger of them, since they may cancel
+                    const float err = p.r.group_top == 1 ? 0.5f * tau + kTauC * fabsf(b1) : tau + kTauC * fmaxf(fabsf(b1), fabsf(b2));
+                    const uint32_t least = __reduce_min_sync(kAll, stays ? order_key(score - err) : kAll);
+                    const uint32_t most = __reduce_max_sync(kAll, stays || g >= p.r.groups ? 0u : order_key(score + err));
+                    if (most && least != kAll && !(key_value(least) > key_value(most))) stays = groups_slow(p, row, top);
                 }
                 if (by_logit && scores) {   // the groups went by scores, the experts go by logits
                     a1 = a2 = kNone;

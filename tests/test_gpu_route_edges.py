@@ -1,5 +1,6 @@
 """Routing at the ends of its range, against the definition in 64 bits (the reference and the tolerances are those of the
-other tests of the route): biases of the type's lowest value, sums of two of them as the scores of groups."""
+other tests of the route): biases of the type's lowest value, sums of two of them as the scores of groups,
+sums that cancel."""
 import pytest
 import torch
 
@@ -76,3 +77,18 @@ def test_groups_whose_two_largest_add_to_more_than_fp32_holds(E, k, groups, top_
         check(gone, k, sigmoid=sigmoid, bias=bias, groups=groups, top_groups=top_groups, group_top=2)
         bias[E // 2:] = -INF                       # and groups that cannot stay
         check(gone, k, sigmoid=sigmoid, bias=bias, groups=groups, top_groups=top_groups, group_top=2)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups", [(32, 8, 4), (96, 6, 2), (64, 32, 9)])
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e30])
+def test_groups_whose_two_largest_cancel(size, E, groups, top_groups, sigmoid):
+    """A large bias on one expert of each group and its opposite on the others: the sum has the size of the scores, its error in
+    fp32 that of the biases."""
+    x = _logits(2000, E, groups)
+    bias = torch.full((groups, E // groups), -size)
+    bias[:, 1] = size
+    for k in (1, top_groups):
+        check(x, k, sigmoid=sigmoid, bias=bias.flatten(), groups=groups, top_groups=top_groups, group_top=2)
+    bias[1::2] = _bias(E // 2, 1).view(-1, E // groups)          # beside groups of ordinary biases
+    check(x, top_groups, sigmoid=sigmoid, bias=bias.flatten(), groups=groups, top_groups=top_groups, group_top=2)
