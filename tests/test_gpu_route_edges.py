@@ -92,3 +92,20 @@ def test_groups_whose_two_largest_cancel(size, E, groups, top_groups, sigmoid):
         check(x, k, sigmoid=sigmoid, bias=bias.flatten(), groups=groups, top_groups=top_groups, group_top=2)
     bias[1::2] = _bias(E // 2, 1).view(-1, E // groups)          # beside groups of ordinary biases
     check(x, top_groups, sigmoid=sigmoid, bias=bias.flatten(), groups=groups, top_groups=top_groups, group_top=2)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+def test_more_choices_than_a_block_keeps(sigmoid):
+    """A long packed batch: 1352 tokens x 8 of each of 148 blocks, whose ranks go through `rows` (a block's shared memory keeps 8192)."""
+    T, E, k = 200000, 16, 8
+    valid = torch.arange(T) % 7 != 3
+    valid[150000:160000] = False
+    check(_logits(T, E, 1), k, sigmoid=sigmoid, valid=valid, bias=_bias(E, 1))
+
+
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top_groups", [(256, 20, 1, 1), (256, 24, 1, 1), (256, 32, 1, 1), (64, 32, 1, 1), (512, 8, 8, 1), (1024, 32, 4, 2)])
+def test_more_candidates_than_lanes(E, k, groups, top_groups, sigmoid):
+    """Many choices of few values a lane: most tokens have more than 32 values above the bound."""
+    for n, (dtype, bias) in enumerate([(torch.float32, True), (torch.bfloat16, False)]):
+        check(_logits(300, E, E + n, dtype), k, sigmoid=sigmoid, bias=_bias(E, n) if bias else None, groups=groups, top_groups=top_groups, group_top=2)
