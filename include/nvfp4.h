@@ -434,7 +434,7 @@ nvfp4_status nvfp4_bf16_wgrad_grouped(const void* a, int64_t lda, const void* b,
  *   its largest c (group_top 1), or the sum of its two largest (group_top 2; without a bias c is s
  *   there), and the top_groups groups of highest score stay, the lowest index first among equals;
  *   the k experts of largest c in what stays are chosen, in descending order, the lowest index first
- *   among equals.  c is compared as evaluated in fp64, whatever the logits' type.
+ *   among equals.  c and the groups' scores are compared as evaluated in fp64, whatever the logits' type.
  *   weight = scale * s, with renormalize scale * s / (the sum of s over the chosen).
  * An expert whose logit is -inf or NaN, or whose c is -inf or NaN, is never chosen (its s is 0, so
  * masking by -inf takes it out of the softmax; masking by the type's lowest value leaves it eligible),

@@ -880,7 +880,8 @@ def _act_bwd(dy, lddy, pre, act, out, dbias, accumulate, scratch, stream):
 
 class LinearActBF16:
     """The BF16 layer y = act(x w^T + bias) + residual of T rows (x [T][d], w [n][d] bf16, bias fp32 [n]), with the
-    buffers of its backward pass.  Its workspace holds the device flags of its calls (nvfp4_poll(layer.ws))."""
+    buffers of its backward pass (which calls on two streams may not share).  d is a multiple of 8; bwd needs n to be one
+    too.  Its workspace holds the device flags of its calls (nvfp4_poll(layer.ws))."""
 
     def __init__(self, T: int, d: int, n: int, act: int = ACT_GELU, device=None):
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
@@ -927,7 +928,8 @@ class LinearActBF16:
         dx = nvfp4_bf16_gemm_act(dh, w, out=dx, ws=self.ws, stream=stream, b_kn=True)
         # The grouped kernel walks a tile's whole T on one SM pair but writes and adds larger gradients faster (us, it and the
         # other, stored / added): 16384 x 256 x 256 61.9, 15.6 / 62.1, 16.2; 8192 x 1000 x 1000 57, 49 / 57, 52; 3974 x 208 x 2384
-        # 25, 16 / 25, 17; 500 x 1280 x 5120 17.2, 14.6 / 20, 22; 2000 x 2048 x 2048 19.9, 20.5 / 21, 25; 4096 x 5120 x 5120 160, 166 / 166, 189.
+        # 25, 16 / 25, 17; 2000 x 2048 x 2048 19.9, 20.5 / 21, 25; 4096 x 5120 x 5120 160, 166 / 166, 189.  Beside the border they
+        # take turns: 500 x 1280 x 5120 (2^22.6 weights) 15.7 to 17.2, 14.6 stored, 17.1 to 20, 18.3 to 22 added.
         if self.n * self.d <= 1 << 21:
             nvfp4_bf16_wgrad(dh, x, out=dw, accumulate=accumulate, ws=self.ws, stream=stream)
         else:
@@ -1085,8 +1087,8 @@ def nvfp4_dispatch(x: torch.Tensor, routes: Routes, out: torch.Tensor | None = N
 def nvfp4_combine(ys: torch.Tensor, routes: Routes, residual: torch.Tensor | None = None, out_dtype=torch.bfloat16,
                   out: torch.Tensor | None = None, weighted: bool = True, stream=None) -> torch.Tensor:
     """out[token] = residual[token] + sum of weight * ys[row] over the token's choices (ys [tokens * k][d] bf16 or
-    fp32, out and residual [tokens][d] of one type).  weighted=False takes every weight as 1: the gradient of
-    nvfp4_dispatch.  out may be the residual."""
+    fp32, out and residual [tokens][d] of one type, out_dtype where neither is given).  weighted=False takes every
+    weight as 1: the gradient of nvfp4_dispatch.  out may be the residual."""
     if ys.dtype is not torch.bfloat16 and ys.dtype is not torch.float32:
         raise TypeError("expected bf16 or fp32 rows")
     ldys = _row_stride(ys, "ys")

@@ -972,9 +972,13 @@ static cudaError_t launch_ga(Kernel kern, int bytes, std::atomic<uint64_t>& attr
 //   one SM (operands of more than 100 MB do not stay in L2);
 //   a launch takes 2900 + 19 w (one CTA per tile), 3800 + 150 split + 14 w (K cut over CTAs), 5000 + 8 w (pairs) or 4600 + 26 w (K
 //   cut over pairs) besides; clusters that do not fit at once have cost 20 us a wave.
-// Estimate / fastest measured (us): 64 x 1280 x 5120 7.9 / 8.1 (one CTA per tile, 6 parts; one pair 18.3), 333 x 1288 x 5120
-// 12.4 / 12.5 (4 parts; pairs in 3 parts 14.1), 500 x 5120 x 5120 29 / 28.6 (pairs), 64 x 20480 x 5120 39 / 39.3 (one CTA per
-// tile; pairs 53), 2088 x 376 x 504 5.7 / 5.7 (pairs 7.6).
+// Estimate / measured of what it chooses (us): 64 x 1280 x 5120 7.7 / 7.9 (one CTA per tile, 5 parts; one pair 18.3), 333 x 1288 x
+// 5120 12.7 / 12.6 (3 parts; in 4, 0.1 less in a sweep; pairs in 3 parts 14.1), 500 x 5120 x 5120 29.5 / 28.7 (pairs), 1000 x 1280 x
+// 5120 21.1 / 18.6 (pairs in 2 parts), 2000 x 2568 x 1288 19.6 / 22.6 (pairs), 2088 x 376 x 504 5.7 / 5.6 (one CTA per tile; pairs 7.6),
+// 64 x 20480 x 5120 52.6 / 41.4 (one CTA per tile, 160 of them, counted as two whole waves; pairs 53).
+// With K outermost the terms are the same, and the estimate is short: whole blocks of 64 are loaded (w = 48 loads 64), and
+// clusters of 8 CTAs may not all fit at once.  16384 rows of 256 x 256 11.6 / 16.1, 8192 of 1000 x 1000 23.3 / 48.3, 3974 of 208 x
+// 2384 11.9 / 13.9.
 struct GaPlan {
     bool single;     // one CTA per tile
     int split, wq;

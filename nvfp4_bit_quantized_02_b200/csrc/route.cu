@@ -18,8 +18,10 @@
 // The choice is that of the definition in fp64.  Where c is the logit itself its order is exact.  Otherwise c
 // is evaluated in fp32 (the error bound stands at kTauSigmoid), and where two neighbours in the order lie closer than the bound
 // the candidates near it are compared in fp64 (about 1 token in 1000 of 256 experts with sigmoid scores), as are groups whose
-// scores are too close (groups_slow).  More than 32 candidates, that is, many equal values, are looked through one by one
-// (choose_slow).
+// scores are too close (groups_slow).  More than 32 candidates are looked through one by one, in fp64 (choose_slow): many equal
+// values, or more wanted than the lanes that stay give to the bound (one value each, with groups two).  Random logits, 16384
+// tokens: 256 experts 21 us with k = 8, 112 with 20 (17 % of the tokens), 203 with 24 (91 %), 269 with 32 (all); 512 experts
+// with k = 8 55 us in the 4 best of 8 groups, 221 in the best one (4 lanes: all).
 //
 // Rows: a warp takes neighbouring tokens and counts each expert's choices as it goes, so that a choice's rank
 // among the warp's is there at once; the ranks are joined over the block's warps, and over the blocks by a
@@ -205,7 +207,7 @@ __device__ __forceinline__ float chosen_weight(const RouteProblem& r, float l, f
     float v = held ? expf(z - most) : 0.0f;
     if (r.sigmoid && held) v /= 1.0f + expf(-fabsf(l));
     const float all = warp_sum(v);
-    return held ? r.scale * __fdividef(v, all) : 0.0f;   // all: 1 to 32
+    return held ? r.scale * __fdividef(v, all) : 0.0f;   // all: 0.5 to 32 (a sigmoid's largest term is 1 / (1 + e^-|l|))
 }
 
 struct RouteWarp {       // a warp's candidates, then the same in order: c, the expert
@@ -666,7 +668,9 @@ static cudaError_t launch_choose(const RouteKernelParams& p, int blocks, int war
     kern<<<blocks, 32 * warps, (warps * p.stride + p.r.experts + 1 + p.held) * 4, s>>>(p);
     return cudaGetLastError();
 }
-// 28 of 8 experts a lane: 72 registers and no more rounds for 16384 tokens (softmax, 256 experts: 20.5 us, with 32 21.6, with 24 21.7)
+// 28 of 8 experts a lane: 72 registers, where 32 leave 64 and spill (16384 tokens of 256 experts, softmax: 20.5 us, with 32 21.6, with
+// 24 21.7).  32 save a round from 4145 to 4736 tokens, among others, which is worth what the spills cost: 4144 tokens 12.4 to 12.6 us, 12.8
+// to 13.3 with 32; 4700 13.6 to 14.7, 13.3 to 13.7; 9000 16.5 to 17.7, 16.8 to 16.9.
 static int most_warps(int per_lane) { return per_lane <= 4 ? 32 : per_lane <= 8 ? 28 : per_lane <= 16 ? 16 : 8; }
 template <typename T>
 static cudaError_t launch_choose(const RouteKernelParams& p, int blocks, int warps, cudaStream_t s) {
