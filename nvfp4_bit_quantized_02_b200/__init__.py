@@ -907,10 +907,10 @@ class LinearActBF16:
     def bwd(self, x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, pre: torch.Tensor | None = None, dx: torch.Tensor | None = None,
             dw: torch.Tensor | None = None, dbias: torch.Tensor | None = None, accumulate: bool = False, stream=None):
         """dx [T][d] bf16, dw [n][d] and dbias [n] fp32 (accumulate: both added to; they must be given).  The residual's
-        gradient is dy."""
+        gradient is dy.  A refused call adds nothing."""
         self._shapes(x, w, dy, pre)
-        if dy.dtype is not torch.bfloat16:
-            raise TypeError("expected bf16 dy")
+        if dy.dtype is not torch.bfloat16 or x.dtype is not torch.bfloat16 or w.dtype is not torch.bfloat16:
+            raise TypeError("expected bf16 x, w and dy")
         if self.act != ACT_NONE and (pre is None or pre.dtype is not torch.bfloat16):
             raise TypeError("expected bf16 pre")
         if accumulate and (dw is None or dbias is None):
@@ -919,10 +919,24 @@ class LinearActBF16:
             dbias = _empty((self.n,), torch.float32, dy.device, stream)
         elif dbias.dtype is not torch.float32 or dbias.shape != (self.n,) or not dbias.is_contiguous():
             raise ValueError("dbias: contiguous fp32 [n]")
+        cut = self.n * self.d <= 1 << 21   # which of the weight gradients, see below
+        if self.d % 8 and not cut:
+            raise ValueError("d: a multiple of 8")
         if dw is None:
             dw = _empty((self.n, self.d), torch.float32, dy.device, stream)
-        elif dw.shape != (self.n, self.d):
-            raise ValueError(f"dw: [{self.n}][{self.d}]")
+        elif dw.dtype is not torch.float32 or dw.shape != (self.n, self.d) or (_row_stride(dw, "dw") % 4 and not cut):
+            raise ValueError(f"dw: fp32 [{self.n}][{self.d}]" + ("" if cut else ", rows of whole 16 bytes"))
+        if dx is not None and (dx.shape != x.shape or dx.dtype is not torch.bfloat16 and dx.dtype is not torch.float32):
+            raise ValueError(f"dx: bf16 or fp32 [{self.T}][{self.d}]")
+        if accumulate:   # what the products would refuse is refused here, before anything is added to dbias
+            dev = _CUR_DEVICE()
+            for name, t, step in (("x", x, 8), ("w", w, 8), ("dw", dw, 1), ("dx", dx, 1)):
+                if t is None:
+                    continue
+                if t.get_device() != dev:
+                    _elsewhere(dev, t)
+                if (_row_stride(t, name) % step and t.shape[0] > 1) or t.data_ptr() % 16:
+                    raise ValueError(f"{name}: 16-byte aligned" + (", rows of whole 16 bytes" if step == 8 else ""))
         _act_bwd(dy, _row_stride(dy, "dy"), pre, self.act, self.dh, dbias, accumulate, self.scratch, stream)
         dh = dy if self.dh is None else self.dh
         dx = nvfp4_bf16_gemm_act(dh, w, out=dx, ws=self.ws, stream=stream, b_kn=True)
@@ -930,7 +944,7 @@ class LinearActBF16:
         # other, stored / added): 16384 x 256 x 256 61.9, 15.6 / 62.1, 16.2; 8192 x 1000 x 1000 57, 49 / 57, 52; 3974 x 208 x 2384
         # 25, 16 / 25, 17; 2000 x 2048 x 2048 19.9, 20.5 / 21, 25; 4096 x 5120 x 5120 160, 166 / 166, 189.  Beside the border they
         # take turns: 500 x 1280 x 5120 (2^22.6 weights) 15.7 to 17.2, 14.6 stored, 17.1 to 20, 18.3 to 22 added.
-        if self.n * self.d <= 1 << 21:
+        if cut:
             nvfp4_bf16_wgrad(dh, x, out=dw, accumulate=accumulate, ws=self.ws, stream=stream)
         else:
             nvfp4_bf16_wgrad_grouped(dh, x, self.offsets, out=dw.unsqueeze(0), accumulate=accumulate, ws=self.ws, stream=stream)

@@ -65,3 +65,30 @@ def test_waits_of_the_weight_gradient_run_out(rows, n, d):
     ws = m.Workspace()
     out = torch.empty(n, d, device="cuda")
     _expires(lambda: m.nvfp4_bf16_wgrad(dy, x, out=out, ws=ws), ws)
+
+
+@pytest.mark.parametrize("T,d,n", [(40, 72, 64), (40, 1288, 2048)])
+def test_refused_backward_calls_add_nothing(T, d, n):
+    """On both sides of the rule that chooses the weight gradient's kernel."""
+    m = nv()
+    g = torch.Generator().manual_seed(1)
+    x, w, dy = (torch.randn(*s, generator=g).bfloat16().cuda() for s in ((T, d), (n, d), (T, n)))
+    layer = m.LinearActBF16(T, d, n, act=m.ACT_RELU)
+    pre = torch.randn(T, n, generator=g).bfloat16().cuda()
+    shifted = lambda t, by: torch.zeros(t.shape[0], t.shape[1] + 16, dtype=t.dtype, device="cuda")[:, by:by + t.shape[1]]
+    odd = lambda t: torch.zeros(t.shape[0], t.shape[1] + 3, dtype=t.dtype, device="cuda")[:, :t.shape[1]]
+    f32 = torch.zeros(n, d, device="cuda")
+    cases = [dict(x=x.float()), dict(w=w.float()), dict(dy=dy.float()), dict(pre=pre.float()), dict(x=odd(x)), dict(w=odd(w)), dict(dy=odd(dy)),
+             dict(pre=odd(pre)), dict(x=shifted(x, 1)), dict(w=shifted(w, 3)), dict(dy=shifted(dy, 1)), dict(x=x.cpu()), dict(w=w.cpu()),
+             dict(dw=f32.bfloat16()), dict(dw=f32.cpu()), dict(dw=shifted(f32, 1)), dict(dw=f32.t()), dict(dx=x.half()), dict(dx=x[:, 8:]),
+             dict(dx=shifted(x, 1)), dict(dx=x.cpu())]
+    if n * d > 1 << 21:
+        cases.append(dict(dw=odd(f32)))
+    for change in cases:
+        dw, db = torch.full((n, d), 3.0, device="cuda"), torch.full((n,), 5.0, device="cuda")
+        args = dict(x=x, w=w, dy=dy, pre=pre, dw=dw, dbias=db, accumulate=True) | change
+        with pytest.raises((TypeError, ValueError, m.NVFP4Error)):
+            layer.bwd(**args)
+        assert (dw == 3).all() and (db == 5).all(), list(change)
+    layer.bwd(x, w, dy, pre, dx=shifted(x, 8), dw=shifted(f32, 4))
+    assert m.nvfp4_poll(layer.ws) == 0
